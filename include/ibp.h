@@ -427,6 +427,121 @@ int ibp_query(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, int64_t
 int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, int64_t n_rows,
                     int64_t row_elems, int dtype, ibp_stats *d_stats, ibp_stream_t s);
 
+/* ---- 8-bit paged key/value cache ------------------------------------------------
+ * A lossy companion of the codec for the K/V rows it stores ("System integration":
+ * offloaded inference keeps the KV cache as rows of tokens; the cache below is the
+ * library's, the paper has no counterpart): the rows of the tokens attention reads on
+ * the GPU are held in 8 bits an element with one scale for each page and head.
+ *
+ * Layout. At most 65535 sequences and 4096 heads. K codes, V codes: [n_pages][n_heads][page_tokens][head_dim] bytes, each
+ * (page, head) one contiguous tile; scales: [n_pages][n_heads] floats. Token t of
+ * sequence b lies in slot t % page_tokens of page d_table[b*table_stride +
+ * t / page_tokens]; its value is code * scale. page_tokens is 16, 32, 64 or 128,
+ * head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
+ * page_tokens tokens (its capacity, at most 2^30). No two entries that name a page in
+ * use may name the same one in a call that writes pages; entries past a sequence's last
+ * page are never read.
+ *
+ * Quantisation of a page's tile whose largest finite magnitude is a: scale = a * (1 /
+ * qmax) (qmax 127 for IBP_KV_INT8, 448 for IBP_KV_E4M3) held in [2^-100, 2^120], or 0
+ * when a is 0; code = value * (1 / scale), rounded to nearest even and saturated to +-qmax. A
+ * NaN becomes code 0, an infinity the largest code of its sign. All of it is IEEE
+ * single precision, so equal inputs give equal codes.
+ *
+ * Device-detected errors of these calls: a page id outside [0, n_pages), a length
+ * outside [0, capacity] (it is clamped) or offsets that do not rise within [0, n_rows]
+ * record IBP_ERR_INDEX in *d_status; tokens of such a page are skipped (not written, not
+ * attended, read as zeros). */
+typedef enum { IBP_KV_INT8 = 0, IBP_KV_E4M3 = 1 } ibp_kv_code;
+
+typedef struct {
+  void *k_codes, *v_codes;   /* device, 16-byte aligned */
+  float *k_scales, *v_scales; /* device */
+  const int32_t *d_table;    /* device, [batch][table_stride], table_cols of each row used */
+  const int32_t *d_lens;     /* device, [batch]: tokens held by each sequence */
+  int64_t n_pages, table_stride;
+  int32_t batch, table_cols, n_heads, page_tokens, head_dim;
+  int32_t code;              /* ibp_kv_code */
+} ibp_kv_cache;
+
+/* New K and V rows of the sequences, one after another: row r of K starts at k +
+ * r*k_row_stride elements, its head h k_head_stride elements further (strides whole
+ * multiples of 16 bytes, the elements of a head contiguous). Sequence b owns rows
+ * d_cu[b] .. d_cu[b+1] - 1; d_cu null: n_rows / batch rows each. */
+typedef struct {
+  const void *k, *v;         /* device, 16-byte aligned, IBP_FP32, IBP_FP16 or IBP_BF16 */
+  const int32_t *d_cu;       /* device, [batch + 1], or null */
+  int64_t n_rows;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int32_t dtype;
+} ibp_kv_rows;
+
+/* Append: sequence b's rows become its tokens d_lens[b], d_lens[b] + 1, ... in the pages
+ * its table names. A page that already holds tokens keeps its scale s unless the new
+ * rows need a larger one s'; the codes there then become round(code * (s / s')). A page
+ * whose first slot is written starts a new scale. d_new_lens (nullable, [batch], not
+ * d_lens itself) receives the lengths after the call; d_lens is not changed. Rows past
+ * the capacity are dropped with IBP_ERR_INDEX. Calling it again with the same lengths
+ * and rows leaves the pages as they are. Asynchronous on s, one launch. */
+int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
+                  int32_t *d_status, ibp_stream_t s);
+
+/* Read back: token d_begin[b] + i (d_begin null: i) of every sequence b, i < n_out, as
+ * values rounded once to dtype into k_out and v_out ([batch][n_out][n_heads][head_dim],
+ * either may be null; 16-byte aligned device memory): rows the codec's calls take.
+ * Tokens at or past the length (or before 0) are written as zeros. */
+int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out, void *k_out,
+                void *v_out, int dtype, int32_t *d_status, ibp_stream_t s);
+
+/* Query rows of the sequences and what attention writes for them. Sequence b owns rows
+ * d_cu[b] .. d_cu[b+1] - 1 (d_cu null: max_q rows each, n_rows = batch * max_q), at most
+ * max_q of them; with n of them, row i stands at position d_lens[b] - n + i (the rows'
+ * own keys are in the cache already) and sees the tokens up to and including it.
+ * q_heads is a multiple of n_heads; query heads g*q_heads/n_heads .. share K/V head g.
+ * dtype IBP_FP16 or IBP_BF16 (of q and out). Strides in elements, whole multiples of
+ * 16 bytes. */
+typedef struct {
+  const void *q;             /* device, 16-byte aligned */
+  void *out;                 /* device, 16-byte aligned, rows and heads strided */
+  float *d_lse;              /* nullable, [n_rows][q_heads]: log of the sum of exponentials */
+  const int32_t *d_cu;       /* nullable */
+  const float *d_weights_in; /* nullable, [batch][n_heads][weights_stride] */
+  float *d_weights;          /* nullable, same shape; may be d_weights_in itself */
+  int64_t n_rows, max_q, weights_stride;
+  int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+  int32_t q_heads, dtype;
+  float scale, decay;
+} ibp_kv_query;
+
+/* Attention over the cache: out = sum_t p_t v_t with p = softmax over the tokens a row
+ * sees of scale * q . k_t, sums and statistics in single precision; a row that sees
+ * nothing gives zeros and lse = -inf. d_weights (weights_stride >= the capacity): for t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is
+ * null) + the sum of p_t over the rows and query heads of (b, h), in a fixed order;
+ * entries at or past the length are left alone. d_scratch: the size
+ * ibp_kv_attention_scratch_bytes gives for the same cache and query shapes (16-byte
+ * aligned; smaller: IBP_ERR_ARG), overwritten. Asynchronous on s, capturable. */
+int ibp_kv_attention_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
+                                   int32_t q_heads, int with_weights, size_t *bytes);
+int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void *d_scratch,
+                     size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
+
+/* Eviction by accumulated weight: of every sequence b and head h longer than budget,
+ * keeps the last `recent` tokens and, of the others, the budget - recent with the
+ * largest d_weights[b][h][t] (equal weights: the lowest t first; a NaN counts as the
+ * lowest); a shorter sequence keeps all. The kept tokens, in their order, become tokens
+ * 0, 1, ... of dst (same heads, page size, head size, code and batch; pages distinct
+ * from the source's; capacity >= the smaller of budget and the source's): values
+ * code * scale requantised page by page. dst->d_lens is not read. d_new_lens [batch]
+ * receives min(length, budget); d_new_weights (nullable, [batch][n_heads]
+ * [new_weights_stride], new_weights_stride >= budget) the kept weights, then zeros;
+ * d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old positions, then -1.
+ * 0 <= recent <= budget, budget >= 1. Asynchronous on s, two launches. */
+int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes);
+int ibp_kv_evict(const ibp_kv_cache *cache, const float *d_weights, int64_t weights_stride,
+                 int64_t budget, int64_t recent, const ibp_kv_cache *dst, int32_t *d_new_lens,
+                 float *d_new_weights, int64_t new_weights_stride, int32_t *d_kept,
+                 void *d_scratch, size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
+
 /* Measurement helper, not part of the codec: streams `bytes` (a multiple of 16)
  * from src (device or registered host memory) with 16-byte loads across the whole
  * GPU and writes one XOR checksum word to *d_sink, so a caller can time the plain

@@ -20,7 +20,9 @@ decompress_gather_sized (only each row's used bytes), decompress_gather_batched
 (several tables in one launch), decompress_range (rows in order). Next to them: the
 packed store (pack_offsets, pack, decompress_gather_packed) and per-position or
 block-position metadata (build_meta_positions, build_meta_block_positions,
-compress_positions, decompress_gather_positions). ``offload.py`` streams compressed
+compress_positions, decompress_gather_positions). Beside the codec, an 8-bit paged
+key/value cache for the K/V rows it stores: KVCache, kv_append, kv_read, kv_attention,
+kv_evict (``kvcache.py`` manages one). ``offload.py`` streams compressed
 tensors through device buffers; ``sharded.py`` builds the metadata of a table spread
 over several processes.
 """
@@ -35,6 +37,7 @@ import torch
 from . import build_lib
 
 FP32, FP16, BF16, W8 = 0, 1, 2, 3
+KV_INT8, KV_E4M3 = 0, 1
 OK = 0
 ERR_ARG, ERR_DTYPE, ERR_UNSUPPORTED, ERR_CUDA, ERR_INDEX, ERR_CORRUPT, ERR_META, ERR_TIMEOUT = (
     -1, -2, -3, -4, -5, -6, -7, -8)
@@ -68,6 +71,37 @@ class Stats(ctypes.Structure):
                 ("total_bits", ctypes.c_int64)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    """ibp_kv_cache"""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("d_table", ctypes.c_void_p), ("d_lens", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("table_cols", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("code", ctypes.c_int32)]
+
+
+class KVRows(ctypes.Structure):
+    """ibp_kv_rows"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("d_cu", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class KVQuery(ctypes.Structure):
+    """ibp_kv_query"""
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("d_lse", ctypes.c_void_p),
+                ("d_cu", ctypes.c_void_p), ("d_weights_in", ctypes.c_void_p),
+                ("d_weights", ctypes.c_void_p), ("n_rows", ctypes.c_int64),
+                ("max_q", ctypes.c_int64), ("weights_stride", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("decay", ctypes.c_float)]
+
+
 SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp_build_meta",
            "ibp_compress", "ibp_decompress_gather", "ibp_query", "ibp_probe_read",
            "ibp_build_meta_noalloc", "ibp_meta_select_scratch_bytes", "ibp_build_meta_select",
@@ -76,7 +110,9 @@ SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp
            "ibp_compress_positions", "ibp_decompress_gather_positions",
            "ibp_decompress_gather_sized", "ibp_decompress_gather_batched", "ibp_meta_count",
            "ibp_meta_finalize", "ibp_build_meta_block_positions", "ibp_gather_dedup_scratch_bytes",
-           "ibp_decompress_gather_dedup", "ibp_query_async")
+           "ibp_decompress_gather_dedup", "ibp_query_async", "ibp_kv_append", "ibp_kv_read",
+           "ibp_kv_attention_scratch_bytes", "ibp_kv_attention", "ibp_kv_evict_scratch_bytes",
+           "ibp_kv_evict")
 
 # declared in include/ibp_testing.h (a testing hook, not part of the codec)
 TESTING_SYMBOLS = ("ibp_testing_set_wait_limit_ns", "ibp_testing_withhold_plans")
@@ -134,6 +170,14 @@ def load() -> ctypes.CDLL:
     lib.ibp_pack.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, i64, vp, vp, u64, vp, vp, vp, vp]
     lib.ibp_decompress_gather_packed.argtypes = [vp, u64, vp, i64, i64, i32, u32, vp, vp, vp, i64,
                                                  vp, vp, vp]
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    lib.ibp_kv_append.argtypes = [vp, vp, vp, vp, vp]
+    lib.ibp_kv_read.argtypes = [vp, vp, i64, vp, vp, i32, vp, vp]
+    lib.ibp_kv_attention_scratch_bytes.argtypes = [vp, i64, i64, i32, i32, szp]
+    lib.ibp_kv_attention.argtypes = [vp, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.ibp_kv_evict_scratch_bytes.argtypes = [vp, i64, szp]
+    lib.ibp_kv_evict.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, ctypes.c_size_t,
+                                 vp, vp]
     for name in SYMBOLS[1:]:
         getattr(lib, name).restype = i32
     lib.ibp_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -488,6 +532,187 @@ def query_async(bitmask: torch.Tensor, row_bits: torch.Tensor, n_rows: int, row_
 def read_stats(stats: torch.Tensor) -> Stats:
     host = stats.detach().to("cpu").contiguous().view(torch.uint8).numpy().tobytes()
     return Stats.from_buffer_copy(host[:ctypes.sizeof(Stats)])
+
+
+_KV_CODES = {torch.int8: KV_INT8}
+if hasattr(torch, "float8_e4m3fn"):
+    _KV_CODES[torch.float8_e4m3fn] = KV_E4M3
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+class KVCache:
+    """Handle of an 8-bit paged key/value cache (``ibp_kv_cache``): the tensors it is
+    made of, which the caller owns and keeps where they are.
+
+    k_codes, v_codes: [n_pages, n_heads, page_tokens, head_dim], int8 or float8_e4m3fn;
+    k_scales, v_scales: [n_pages, n_heads] float32; table: [batch, columns] int32 page ids
+    (unused entries are not read); lens: [batch] int32 tokens held. page_tokens is 16, 32,
+    64 or 128, head_dim 64 or 128. Several handles may share the page pools."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor,
+                 v_scales: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+        if k_codes.dim() != 4 or k_codes.shape != v_codes.shape or \
+                k_codes.dtype != v_codes.dtype or k_codes.dtype not in _KV_CODES:
+            raise ValueError("k_codes and v_codes must be int8 or float8_e4m3fn tensors "
+                             "[n_pages, n_heads, page_tokens, head_dim]")
+        if any(s.shape != k_codes.shape[:2] or s.dtype != torch.float32
+               for s in (k_scales, v_scales)):
+            raise ValueError("k_scales and v_scales must be float32 [n_pages, n_heads]")
+        if table.dim() != 2 or table.dtype != torch.int32 or \
+                (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be int32 [batch, columns], its rows contiguous")
+        if lens.dtype != torch.int32 or lens.shape != table.shape[:1]:
+            raise ValueError("lens must be int32 [batch]")
+        for t in (k_codes, v_codes, k_scales, v_scales, lens):
+            if not t.is_contiguous():
+                raise ValueError("codes, scales and lens must be contiguous")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, \
+            v_scales
+        self.table, self.lens = table, lens
+        n, h, p, d = k_codes.shape
+        stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        self.batch, self.n_heads, self.page_tokens, self.head_dim = table.shape[0], h, p, d
+        self.capacity = table.shape[1] * p
+        self.struct = KVCacheStruct(_at(k_codes), _at(v_codes), _at(k_scales), _at(v_scales),
+                                    _at(table), _at(lens), n, stride, table.shape[0],
+                                    table.shape[1], h, p, d, _KV_CODES[k_codes.dtype])
+        self.address = ctypes.addressof(self.struct)
+
+
+def _head_rows(t: torch.Tensor, cache: KVCache, heads: int, what: str) -> tuple[int, int]:
+    """Row and head strides of [n_rows, heads, head_dim] rows (elements of a head contiguous)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim or \
+            (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [n_rows, {heads}, {cache.head_dim}] with the elements "
+                         "of a head contiguous")
+    if t.shape[0] <= 1 and not t.numel():
+        return heads * cache.head_dim, cache.head_dim
+    return (t.stride(0) if t.shape[0] > 1 else heads * cache.head_dim,
+            t.stride(1) if heads > 1 else cache.head_dim)
+
+
+def _int32(t: torch.Tensor | None, n: int, what: str):
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {n} entries")
+    return _at(t)
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor | None = None,
+              new_lens: torch.Tensor | None = None, status: torch.Tensor | None = None,
+              stream=None) -> None:
+    """ibp_kv_append: quantise rows ``k`` and ``v`` ([n_rows, n_heads, head_dim]; sequence
+    b owns rows cu[b]..cu[b+1]-1, or n_rows/batch each) into the pages behind
+    ``cache.lens``; ``new_lens`` receives the lengths after the call."""
+    kr, kh = _head_rows(k, cache, cache.n_heads, "k")
+    vr, vh = _head_rows(v, cache, cache.n_heads, "v")
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one dtype and row count")
+    rows = KVRows(_at(k), _at(v), _int32(cu, cache.batch + 1, "cu"), k.shape[0], kr, kh, vr, vh,
+                  dtype_code(k))
+    _check(load().ibp_kv_append(cache.address, ctypes.addressof(rows),
+                                _int32(new_lens, cache.batch, "new_lens"), _at(status),
+                                _raw_stream(stream)), "ibp_kv_append")
+
+
+def kv_read(cache: KVCache, k_out: torch.Tensor | None, v_out: torch.Tensor | None,
+            begin: torch.Tensor | None = None, status: torch.Tensor | None = None,
+            stream=None) -> None:
+    """ibp_kv_read: tokens begin[b] (0 when None) and on of every sequence as values into
+    ``k_out`` and ``v_out`` ([batch, n_out, n_heads, head_dim], either may be None); zeros
+    past the length."""
+    given = [t for t in (k_out, v_out) if t is not None]
+    if not given:
+        return
+    for t in given:
+        if t.dim() != 4 or not t.is_contiguous() or t.dtype != given[0].dtype or \
+                t.shape != (cache.batch, given[0].shape[1], cache.n_heads, cache.head_dim):
+            raise ValueError("k_out and v_out must be contiguous [batch, n_out, n_heads, "
+                             "head_dim] tensors of one dtype")
+    _check(load().ibp_kv_read(cache.address, _int32(begin, cache.batch, "begin"),
+                              given[0].shape[1], _at(k_out), _at(v_out), dtype_code(given[0]),
+                              _at(status), _raw_stream(stream)), "ibp_kv_read")
+
+
+def kv_attention_scratch_bytes(cache: KVCache, n_rows: int, max_q: int, q_heads: int,
+                               with_weights: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ibp_kv_attention_scratch_bytes(cache.address, int(n_rows), int(max_q),
+                                                 int(q_heads), int(bool(with_weights)),
+                                                 ctypes.byref(out)),
+           "ibp_kv_attention_scratch_bytes")
+    return out.value
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scale: float,
+                 scratch: torch.Tensor, cu_q: torch.Tensor | None = None,
+                 max_q: int | None = None, lse: torch.Tensor | None = None,
+                 weights: torch.Tensor | None = None, weights_in: torch.Tensor | None = None,
+                 decay: float = 1.0, status: torch.Tensor | None = None, stream=None) -> None:
+    """ibp_kv_attention: softmax(scale * q k) v of the query rows ``q`` ([n_rows, q_heads,
+    head_dim], float16 or bfloat16; sequence b owns rows cu_q[b]..cu_q[b+1]-1, at most
+    ``max_q`` of them, the last of which stands at its last token) into ``out``; ``lse``
+    [n_rows, q_heads] float32; ``weights`` [batch, n_heads, >= capacity] float32 receives
+    decay * weights_in + the probabilities summed over rows and shared heads."""
+    n, heads = q.shape[0], q.shape[1]
+    qr, qh = _head_rows(q, cache, heads, "q")
+    orow, oh = _head_rows(out, cache, heads, "out")
+    if out.dtype != q.dtype or out.shape[0] != n:
+        raise ValueError("out must have q's dtype and shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * heads or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [n_rows, q_heads]")
+    stride = 0
+    if weights is not None:
+        stride = weights.shape[-1]
+        for t in (weights, weights_in):
+            if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
+                                  t.shape != (cache.batch, cache.n_heads, stride)):
+                raise ValueError("weights must be contiguous float32 [batch, n_heads, stride]")
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("cu_q needs max_q, the most rows that a sequence has")
+        max_q = n // max(cache.batch, 1)
+    query = KVQuery(_at(q), _at(out), _at(lse), _int32(cu_q, cache.batch + 1, "cu_q"),
+                    _at(weights_in), _at(weights), n, max_q, stride, qr, qh, orow, oh, heads,
+                    dtype_code(q), scale, decay)
+    _check(load().ibp_kv_attention(cache.address, ctypes.addressof(query), _at(scratch),
+                                   scratch.numel() * scratch.element_size(), _at(status),
+                                   _raw_stream(stream)), "ibp_kv_attention")
+
+
+def kv_evict_scratch_bytes(cache: KVCache, budget: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ibp_kv_evict_scratch_bytes(cache.address, int(budget), ctypes.byref(out)),
+           "ibp_kv_evict_scratch_bytes")
+    return out.value
+
+
+def kv_evict(cache: KVCache, weights: torch.Tensor, budget: int, recent: int, dst: KVCache,
+             scratch: torch.Tensor, new_weights: torch.Tensor | None = None,
+             kept: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             stream=None) -> None:
+    """ibp_kv_evict: the last ``recent`` tokens and the budget - recent of the largest
+    ``weights`` ([batch, n_heads, >= capacity] float32) of every longer sequence and head,
+    requantised into ``dst``'s pages; ``dst.lens`` receives the new lengths,
+    ``new_weights`` ([batch, n_heads, >= budget]) and ``kept`` ([batch, n_heads, budget]
+    int32) the kept tokens' weights and old positions."""
+    for t in (weights, new_weights):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 3 or
+                              t.shape[:2] != (cache.batch, cache.n_heads)):
+            raise ValueError("weights must be contiguous float32 [batch, n_heads, stride]")
+    _check(load().ibp_kv_evict(
+        cache.address, _at(weights), weights.shape[2], int(budget), int(recent), dst.address,
+        _at(dst.lens), _at(new_weights), 0 if new_weights is None else new_weights.shape[2],
+        _int32(kept, cache.batch * cache.n_heads * int(budget), "kept"), _at(scratch),
+        scratch.numel() * scratch.element_size(), _at(status), _raw_stream(stream)),
+        "ibp_kv_evict")
 
 
 def probe_read(src: torch.Tensor, sink: torch.Tensor, nbytes: int | None = None,

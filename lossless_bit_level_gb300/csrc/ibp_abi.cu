@@ -19,10 +19,8 @@ namespace {
 constexpr int64_t MAX_ROW_ELEMS = int64_t(1) << 20;
 constexpr int BATCH_JOBS_MAX_CHECK = 256;  // job flags kept on the stack up to this many
 
-enum class Where { device_only, device_or_host };
+}  // namespace
 
-// Device memory, managed memory, or (when allowed) page-locked host memory that
-// CUDA has mapped; anything else is rejected before a kernel could fault on it.
 bool pointer_ok(const void *p, Where where, size_t align) {
   if (!p || (reinterpret_cast<uintptr_t>(p) % align) != 0) return false;
   cudaPointerAttributes attr;
@@ -37,6 +35,8 @@ bool pointer_ok(const void *p, Where where, size_t align) {
     default: return false;
   }
 }
+
+namespace {
 
 bool in_device_memory(const void *p) {
   cudaPointerAttributes attr;

@@ -34,6 +34,11 @@ struct DeviceInfo {
 };
 int device_info(DeviceInfo *out);
 
+// Device memory, managed memory, or (when allowed) page-locked host memory that
+// CUDA has mapped; anything else is rejected before a kernel could fault on it.
+enum class Where { device_only, device_or_host };
+bool pointer_ok(const void *p, Where where, size_t align);
+
 int launch_build_meta(const void *rows, int64_t n_words, int dtype, double T, uint32_t block_elems,
                       int64_t n_elems, ibp_meta *d_meta, void *d_scratch, cudaStream_t s);
 // The positional population count of the preprocessing stage: clears the 32
