@@ -1,9 +1,15 @@
 // Attention over the 8-bit paged key/value cache (declared in include/ibp.h).
 //
-// out = sum_t p_t v_t, p = softmax of scale * q . k_t over the tokens a row sees. One
-// pass over the keys with the running maximum m and sum l of the softmax:
-//   m' = max(m, x), l' = l 2^(m - m') + 2^(x - m'), o' = o 2^(m - m') + 2^(x - m') v
-// with x in units of log2(e).
+// out = sum_t p_t v_t, p = softmax of scale * q . k_t over the tokens a row sees, in one
+// pass over the keys: with x = scale * log2(e) * q . k_t, a running reference m and
+//   l = sum 2^(x - m),  o = sum 2^(x + log2 s_v - mv) c_v   (c_v: codes, s_v: their scale)
+// both are multiplied by 2^(old - new) whenever a reference rises, and the output is
+// o 2^(mv - m) / l. The value scale enters the exponent, with a reference mv of its own,
+// so that the second product's factors stay within fp16 whatever the scales of the
+// pages are; a reference only rises once a score passes it by 2^8 (a vote a slab instead
+// of a maximum across lanes; fp16 and fp32 have the room).
+#include <algorithm>
+
 #include "ibp_kv_device.cuh"
 
 namespace ibp {
@@ -12,192 +18,800 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr int WARPS = 4;
+constexpr float NONE = -1e30f;  // reference of a row that has seen no token yet
 
-template <int DT, int N>
-__device__ __forceinline__ void load_few(const char *p, float *x) {
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(p + 2 * i);
-    if constexpr (DT == IBP_BF16) {
-      x[i] = __uint_as_float(u << 16);
-      x[i + 1] = __uint_as_float(u & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    }
+constexpr int TILE = 64;      // tokens a stage holds
+constexpr int SLAB = 16;      // tokens a warp takes at a time; never more than one page
+constexpr int CONSUMERS = 4;  // warps that compute; one more fetches
+constexpr int THREADS = 32 * (CONSUMERS + 1);
+constexpr int MAX_BATCH = 1024;  // sequences of one launch (their tile counts are in shared memory)
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements held one row to four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Codes to fp16, exactly. int8: the byte of code + 128 below 0x64 is 1024 + 128 + code.
+template <int CODE>
+__device__ __forceinline__ uint32_t code_bias(uint32_t w) {
+  return CODE == IBP_KV_INT8 ? w ^ 0x80808080u : w;
+}
+// Bytes 0, 1 (HIGH = 0) or 2, 3 of a biased word as two fp16.
+template <int CODE, int HIGH>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  if constexpr (CODE == IBP_KV_INT8) {
+    const uint32_t u = __byte_perm(w, 0x64646464u, HIGH ? 0x4342 : 0x4140);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    uint32_t y;
+    const uint16_t x = HIGH ? (uint16_t)(w >> 16) : (uint16_t)w;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return y;
   }
 }
 
-template <int CODE, int N>
-__device__ __forceinline__ void load_codes(const char *p, float *x) {
-  const uint32_t w = N == 4 ? *reinterpret_cast<const uint32_t *>(p)
-                            : *reinterpret_cast<const uint16_t *>(p);
-  float y[4];
-  kv_decode4<CODE>(w, y);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = y[i];
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory");
 }
 
-// One CTA per (query row, query head, sequence); its warps take every fourth key.
-template <int D, int DT, int CODE>
-__global__ void __launch_bounds__(32 * WARPS)
-    kv_attention_kernel(ibp_kv_cache c, ibp_kv_query q, float *lse2, int32_t *status) {
-  constexpr int N = D / 32;
-  __shared__ float sm_o[WARPS][D], sm_m[WARPS], sm_l[WARPS];
+// How a launch is divided. A (sequence, K/V head, block of MB query rows) is a segment
+// of ceil(length / TILE) tiles; all tiles of all segments are laid end to end and every
+// CTA takes an equal stretch, so a batch of any mix of lengths fills the GPU and a
+// segment is joined from as many CTAs as it took.
+struct Split {
+  int64_t total;
+  int ctas;  // that have work: every one of them has a tile at least
+  __device__ __forceinline__ Split(int64_t tiles, int launched)
+      : total(tiles), ctas((int)min((int64_t)launched, tiles)) {}
+  __device__ __forceinline__ int64_t start(int cta) const { return total * cta / ctas; }
+  // the CTA whose stretch holds tile x
+  __device__ __forceinline__ int owner(int64_t x) const {
+    return (int)(((x + 1) * ctas - 1) / total);
+  }
+};
+
+struct AttentionArgs {
+  ibp_kv_cache c;
+  ibp_kv_query q;
+  int32_t *status;
+  uint64_t wait_ns;
+  int b0, batch, ctas, score_cols;
+  int64_t *prefix;  // [batch + 1] tiles before each sequence
+  float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
+  float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
+  float *scores;    // [n_rows][q_heads][score_cols], or null
+};
+
+struct Sequence {
+  int64_t row0;  // its first query row
+  int n, len;    // query rows, tokens
+};
+
+__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, int32_t *status) {
+  Sequence s;
+  int64_t lo, hi;
+  kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + b, status, &lo, &hi);
+  if (hi - lo > a.q.max_q) {
+    report(status, IBP_ERR_INDEX);
+    hi = lo + a.q.max_q;
+  }
+  s.row0 = lo;
+  s.n = (int)(hi - lo);
+  s.len = kv_len(a.c, a.b0 + b, status);
+  return s;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
+
+// A tile's place: segment (b, head, block) and tile number.
+struct Place {
+  int b, seg, tile;
+};
+template <int MB>
+__device__ __forceinline__ int blocks_of(int n, int group) {
+  return (n * group + MB - 1) / MB;
+}
+
+__device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, int64_t x) {
+  int lo = 0, hi = batch;  // the last b with prefix[b] <= x (empty ones come before it)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <int D, int NT, int WQ>
+struct Shape {
+  static constexpr int WK = CONSUMERS / WQ;     // warps that share a tile's tokens
+  static constexpr int MB = 8 * NT * WQ;        // query rows of a segment
+  static constexpr int STAGES = 4;
+  static constexpr int stage_bytes = 2 * TILE * D;
+  static constexpr int slabs = TILE / SLAB;
+  static constexpr int merge_floats = CONSUMERS * 8 * NT * D;
+  static constexpr size_t part_floats = (size_t)MB * (D + 4);
+  static constexpr size_t smem = (size_t)STAGES * stage_bytes + merge_floats * 4 +
+                                 3 * CONSUMERS * 8 * NT * 4 + STAGES * slabs * 12 +
+                                 (2 * STAGES) * 8 + (MAX_BATCH + 1) * 8 + 16;
+};
+
+template <int D, int CODE, int DT, int NT, int WQ, bool SCORES>
+__global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_constant__ AttentionArgs a) {
+  using S = Shape<D, NT, WQ>;
+  constexpr int MB = S::MB, WK = S::WK, ST = S::STAGES, NS = S::slabs, J = D / 64, MT = D / 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char *stages = smem;
+  float *merge = reinterpret_cast<float *>(smem + ST * S::stage_bytes);
+  float *st_m = merge + S::merge_floats, *st_mv = st_m + CONSUMERS * 8 * NT,
+        *st_l = st_mv + CONSUMERS * 8 * NT;
+  float *slab_ks = st_l + CONSUMERS * 8 * NT, *slab_lv = slab_ks + ST * NS;
+  int *slab_n = reinterpret_cast<int *>(slab_lv + ST * NS);
+  uint64_t *full = reinterpret_cast<uint64_t *>(slab_n + ST * NS), *freed = full + ST;
+  int64_t *prefix = reinterpret_cast<int64_t *>(freed + ST);
+  volatile int *abort = reinterpret_cast<volatile int *>(prefix + MAX_BATCH + 1);
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qh = blockIdx.y, group = q.q_heads / c.n_heads, head = qh / group;
-  const char *kc = static_cast<const char *>(c.k_codes), *vc = static_cast<const char *>(c.v_codes);
-  for (int b = blockIdx.z; b < c.batch; b += gridDim.z) {
-    int64_t lo, hi;
-    kv_row_range(q.d_cu, q.n_rows, q.max_q, b, status, &lo, &hi);
-    const int64_t n = hi - lo, i = blockIdx.x;
-    if (n > q.max_q) report(status, IBP_ERR_INDEX);
-    if (i >= n) continue;
-    const int len = kv_len(c, b, status);
-    const int limit = (int)max((int64_t)0, len - n + i + 1);
-    float qv[N], o[N] = {}, m = -INFINITY, l = 0.0f;
-    load_few<DT, N>(static_cast<const char *>(q.q) +
-                        2 * ((lo + i) * q.q_row_stride + qh * q.q_head_stride + lane * N),
-                    qv);
-    for (int t = warp; t < limit; t += WARPS) {
-      const int page = kv_page(c, b, t / c.page_tokens, status);
-      if (page < 0) continue;
-      const int64_t at = kv_tile(c, page, head) + (t % c.page_tokens) * D + lane * N;
-      const int64_t st = (int64_t)page * c.n_heads + head;
-      float k[N], v[N], x = 0.0f;
-      load_codes<CODE, N>(kc + at, k);
-      load_codes<CODE, N>(vc + at, v);
-#pragma unroll
-      for (int e = 0; e < N; ++e) x = fmaf(qv[e], k[e], x);
-      for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(FULL, x, w);
-      x *= __ldg(c.k_scales + st) * (q.scale * LOG2E);
-      const float to = fmaxf(m, x), keep = exp2f(m - to), p = exp2f(x - to);
-      const float pv = p * __ldg(c.v_scales + st);
-      m = to;
-      l = l * keep + p;
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = o[e] * keep + pv * v[e];
+  const ibp_kv_cache &c = a.c;
+  const int group = a.q.q_heads / c.n_heads, cta = blockIdx.x;
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&freed[i], CONSUMERS);
     }
-    if (lane == 0) {
-      sm_m[warp] = m;
-      sm_l[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) sm_o[warp][lane * N + e] = o[e];
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sm_m[w]);
-    if (top == -INFINITY) top = 0.0f;
-    for (int w = 0; w < WARPS; ++w) sum += sm_l[w] * exp2f(sm_m[w] - top);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const int64_t row = (lo + i) * q.q_heads + qh;
-    if (threadIdx.x < D / 2) {
-      float y[2] = {};
-      for (int w = 0; w < WARPS; ++w)
-        for (int e = 0; e < 2; ++e)
-          y[e] += sm_o[w][2 * threadIdx.x + e] * exp2f(sm_m[w] - top);
-      uint32_t *out = reinterpret_cast<uint32_t *>(
-          static_cast<char *>(q.out) + 2 * ((lo + i) * q.out_row_stride + qh * q.out_head_stride));
-      out[threadIdx.x] = pack2<DT>(y[0] * inv, y[1] * inv);
-    }
-    if (threadIdx.x == 0) {
-      const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
-      lse2[row] = z;
-      if (q.d_lse) q.d_lse[row] = z * LN2;
-    }
-    __syncthreads();
+    *abort = 0;
+    mbar_init_fence();
   }
-}
-
-// weights[t] = decay * weights_in[t] + the sum over rows and heads of 2^(x - lse2).
-template <int D, int DT, int CODE>
-__global__ void __launch_bounds__(128)
-    kv_weights_kernel(ibp_kv_cache c, ibp_kv_query q, const float *lse2, int32_t *status) {
-  const int head = blockIdx.y, group = q.q_heads / c.n_heads;
-  for (int b = blockIdx.z; b < c.batch; b += gridDim.z) {
-    int64_t lo, hi;
-    kv_row_range(q.d_cu, q.n_rows, q.max_q, b, status, &lo, &hi);
-    const int len = kv_len(c, b, status), t = blockIdx.x * 128 + threadIdx.x;
-    if (t >= len) continue;
-    const int page = kv_page(c, b, t / c.page_tokens, status);
-    float k[D], sum = 0.0f;
-    if (page >= 0) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(
-          static_cast<const char *>(c.k_codes) + kv_tile(c, page, head) + (t % c.page_tokens) * D);
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) {
-        const uint4 w = p[e];
-        kv_decode4<CODE>(w.x, k + 16 * e);
-        kv_decode4<CODE>(w.y, k + 16 * e + 4);
-        kv_decode4<CODE>(w.z, k + 16 * e + 8);
-        kv_decode4<CODE>(w.w, k + 16 * e + 12);
+  if (warp == CONSUMERS) {  // tiles before each sequence
+    int64_t base = 0;
+    for (int k0 = 0; k0 < a.batch; k0 += 32) {
+      const int b = k0 + lane;
+      int64_t tiles = 0;
+      if (b < a.batch) {
+        const Sequence s = sequence_of(a, b, cta == 0 ? a.status : nullptr);
+        tiles = (int64_t)c.n_heads * blocks_of<MB>(s.n, group) * tiles_of(s.len);
       }
-      const float f = __ldg(c.k_scales + (int64_t)page * c.n_heads + head) * (q.scale * LOG2E);
-      for (int64_t i = 0; i < min(hi - lo, q.max_q); ++i) {
-        if (t >= len - (hi - lo) + i + 1) continue;
-        for (int g = 0; g < group; ++g) {
-          const int qh = head * group + g;
-          const char *row = static_cast<const char *>(q.q) +
-                            2 * ((lo + i) * q.q_row_stride + qh * q.q_head_stride);
-          float x = 0.0f;
-#pragma unroll
-          for (int e = 0; e < D; e += 4) {
-            float y[4];
-            load_few<DT, 4>(row + 2 * e, y);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) x = fmaf(y[w], k[e + w], x);
-          }
-          sum += exp2f(x * f - lse2[(lo + i) * q.q_heads + qh]);
+      int64_t sum = tiles;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, sum, o);
+        if (lane >= o) sum += y;
+      }
+      if (b < a.batch) prefix[b] = base + sum - tiles;
+      base += __shfl_sync(FULL, sum, 31);
+    }
+    if (lane == 0) prefix[a.batch] = base;
+  }
+  __syncthreads();
+  const int64_t total = prefix[a.batch];
+  if (cta == 0)
+    for (int b = threadIdx.x; b <= a.batch; b += THREADS) a.prefix[b] = prefix[b];
+  const Split split(total, a.ctas);
+  if (cta >= split.ctas) return;
+  const int64_t lo = split.start(cta), hi = split.start(cta + 1);
+
+  if (warp == CONSUMERS) {
+    // ---- the fetching warp: a lane looks up one piece (the part of a page that lies
+    // in one tile) of the next 32, one batch ahead of the copies
+    const int PP = min(c.page_tokens, TILE), NP = TILE / PP;
+    const char *kc = static_cast<const char *>(c.k_codes), *vc = static_cast<const char *>(c.v_codes);
+    const int64_t pieces = (hi - lo) * NP;
+    struct Piece {
+      int64_t at;  // byte offset of its codes, or -1
+      float ks, lv;
+      int n;       // tokens of it that the sequence holds
+    };
+    auto look_up = [&](int64_t e) {
+      Piece p = {-1, 0.0f, 0.0f, 0};
+      if (e >= pieces) return p;
+      const int64_t x = lo + e / NP;
+      const int b = find_sequence(prefix, a.batch, x);
+      const int len = kv_len(c, a.b0 + b, nullptr), nt = tiles_of(len);
+      const int64_t local = x - prefix[b], per_head = (prefix[b + 1] - prefix[b]) / c.n_heads;
+      const int head = (int)(local / per_head), tile = (int)(local % nt);
+      const int t = tile * TILE + (int)(e % NP) * PP;
+      if (t >= len) return p;
+      const int page = kv_page(c, a.b0 + b, t / c.page_tokens, a.status);
+      if (page < 0) return p;
+      const int64_t si = (int64_t)page * c.n_heads + head;
+      p.at = kv_tile(c, page, head) + (int64_t)(t % c.page_tokens) * D;
+      p.ks = __ldg(c.k_scales + si);
+      p.lv = log2f(__ldg(c.v_scales + si));
+      p.n = min(len - t, PP);
+      return p;
+    };
+    Piece next = look_up(lane), now = next;
+    bool ok = true;
+    int64_t i = 0;
+    for (; i < hi - lo && ok; ++i) {
+      const int s = (int)(i % ST), e = (int)((i * NP) & 31);
+      if (e == 0) {
+        now = next;
+        next = look_up(i * NP + 32 + lane);
+      }
+      if (i >= ST) ok = mbar_wait(&freed[s], (uint32_t)((i / ST) & 1) ^ 1u, abort, a.wait_ns);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      const int64_t at = __shfl_sync(FULL, now.at, e + lane % NP);
+      const float ks = __shfl_sync(FULL, now.ks, e + lane % NP);
+      const float lv = __shfl_sync(FULL, now.lv, e + lane % NP);
+      const int n = __shfl_sync(FULL, now.n, e + lane % NP);
+      const unsigned some = __ballot_sync(FULL, lane < NP && at >= 0);
+      if (lane < NP) {
+        for (int k = 0; k < PP / SLAB; ++k) {
+          const int slab = s * NS + lane * (PP / SLAB) + k;
+          slab_ks[slab] = ks;
+          slab_lv[slab] = lv;
+          slab_n[slab] = min(max(n - k * SLAB, 0), SLAB);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(some) * 2 * PP * D));
+      __syncwarp();
+      if (lane < NP && at >= 0) {
+        unsigned char *to = stages + s * S::stage_bytes + lane * PP * D;
+        bulk_load(to, kc + at, PP * D, &full[s]);
+        bulk_load(to + TILE * D, vc + at, PP * D, &full[s]);
+      }
     }
-    const int64_t at = ((int64_t)b * c.n_heads + head) * q.weights_stride + t;
-    q.d_weights[at] = (q.d_weights_in ? q.decay * q.d_weights_in[at] : 0.0f) + sum;
+    if (!ok) {
+      if (lane == 0) {
+        report(a.status, IBP_ERR_TIMEOUT);
+        *abort = 1;
+      }
+      // no copy may land after this CTA is gone
+      for (int64_t k = i > ST ? i - ST : 0; k < i; ++k)
+        mbar_wait(&full[k % ST], (uint32_t)((k / ST) & 1), nullptr, a.wait_ns);
+    }
+    return;
+  }
+
+  // ---- computing warps: S^T = K q^T (16 tokens x 8 NT rows), then O^T += V^T P^T
+  const int wq = warp % WQ, wk = warp / WQ, g = lane >> 2, t4 = lane & 3;
+  bool dead = false;  // a wait ran out: the rest is gone through without waiting or computing,
+                      // so that no warp is missed at a barrier
+  int64_t x = lo, i = 0;
+  int b = find_sequence(prefix, a.batch, lo);
+  while (x < hi) {
+    while (x >= prefix[b + 1]) ++b;
+    const Sequence sq = sequence_of(a, b, nullptr);
+    const int nt = tiles_of(sq.len), blocks = blocks_of<MB>(sq.n, group);
+    const int64_t local = x - prefix[b];
+    const int seg = (int)(local / nt), tile0 = (int)(local % nt);
+    const int count = (int)min((int64_t)(nt - tile0), hi - x);
+    const int head = seg / blocks, r0 = (seg % blocks) * MB, rows = min(MB, sq.n * group - r0);
+    const bool active = wq * 8 * NT < rows;
+
+    // query rows as the second operand: lane (g, t) holds 16 consecutive elements of row g
+    uint32_t qb[NT][MT][2];
+    float rowc[NT][2];
+    int limit[NT][2], least = 0x7FFFFFFF;
+    float *score[NT][2];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const int r = wq * 8 * NT + 8 * k + g;
+      const bool live = r < rows;
+      const int rr = r0 + r;
+      const char *src = static_cast<const char *>(a.q.q) +
+                        2 * ((sq.row0 + rr / group) * a.q.q_row_stride +
+                             (head * group + rr % group) * a.q.q_head_stride);
+      float big = 0.0f, y[J][16];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[j][e] = 0.0f;
+        if (live) load16<DT>(src + 2 * 16 * (t4 + 4 * j), y[j]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) big = fmaxf(big, fabsf(y[j][e]));
+      }
+      float up = 1.0f, down = 1.0f;
+      if constexpr (DT == IBP_BF16) {
+        // bf16 rows in fp16: brought to a largest magnitude in [1, 2) by a power of two,
+        // which the score's factor takes back; elements 2^-16 of it and up stay exact
+        big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
+        const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 120);
+        up = __uint_as_float((uint32_t)(127 - e) << 23);
+        down = __uint_as_float((uint32_t)(127 + e) << 23);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          qb[k][4 * j + e][0] = pack2<IBP_FP16>(y[j][4 * e] * up, y[j][4 * e + 1] * up);
+          qb[k][4 * j + e][1] = pack2<IBP_FP16>(y[j][4 * e + 2] * up, y[j][4 * e + 3] * up);
+        }
+      const float factor = down * (a.q.scale * LOG2E);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int col = wq * 8 * NT + 8 * k + 2 * t4 + w, cc = r0 + col;
+        rowc[k][w] = __shfl_sync(FULL, factor, (2 * t4 + w) * 4);
+        limit[k][w] = col < rows ? max(sq.len - sq.n + cc / group + 1, 0) : 0x7FFFFFFF;
+        least = min(least, limit[k][w]);
+        if constexpr (SCORES)
+          score[k][w] = col < rows ? a.scores + ((sq.row0 + cc / group) * a.q.q_heads + head * group +
+                                                 cc % group) * a.score_cols
+                                   : nullptr;
+      }
+    }
+    for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(FULL, least, o));
+
+    float o[NT][MT][4], m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        m[k][w] = mv[k][w] = NONE;
+        l[k][w] = 0.0f;
+      }
+#pragma unroll
+      for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][n][e] = 0.0f;
+    }
+
+    for (int tile = tile0; tile < tile0 + count; ++tile, ++i) {
+      const int s = (int)(i % ST);
+      if (!dead && !__all_sync(FULL, mbar_wait(&full[s], (uint32_t)((i / ST) & 1), abort, a.wait_ns))) {
+        dead = true;
+        if (lane == 0) {
+          report(a.status, IBP_ERR_TIMEOUT);
+          *abort = 1;
+        }
+      }
+      const unsigned char *kt = stages + s * S::stage_bytes, *vt = kt + TILE * D;
+      for (int slab = wk; active && !dead && slab < NS; slab += WK) {
+        const int t0 = tile * TILE + slab * SLAB;
+        if (t0 >= sq.len) break;
+        const int held = slab_n[s * NS + slab];  // 0: its page is not there
+        const float ks = slab_ks[s * NS + slab], lv = slab_lv[s * NS + slab];
+        const bool whole = held == SLAB && t0 + SLAB <= least;
+
+        float acc[NT][4];
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint4 ra = *reinterpret_cast<const uint4 *>(kt + (slab * SLAB + g) * D + 16 * (t4 + 4 * j));
+          const uint4 rb = *reinterpret_cast<const uint4 *>(kt + (slab * SLAB + g + 8) * D + 16 * (t4 + 4 * j));
+          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t ua = code_bias<CODE>(wa[e]), ub = code_bias<CODE>(wb[e]);
+            const uint32_t a0 = code_pair<CODE, 0>(ua), a1 = code_pair<CODE, 0>(ub),
+                           a2 = code_pair<CODE, 1>(ua), a3 = code_pair<CODE, 1>(ub);
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+              mma16816(acc[k], a0, a1, a2, a3, qb[k][4 * j + e][0], qb[k][4 * j + e][1]);
+          }
+        }
+        // scores of tokens g, g + 8 and rows 2t, 2t + 1
+        bool rise = false;
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const float f = rowc[k][w] * ks;
+            acc[k][w] *= f;
+            acc[k][w + 2] *= f;
+            if (!whole) {
+              const int seen = min(limit[k][w] - t0, held);
+              if (g >= seen) acc[k][w] = -INFINITY;
+              if (g + 8 >= seen) acc[k][w + 2] = -INFINITY;
+            }
+            const float top = fmaxf(acc[k][w], acc[k][w + 2]);
+            rise |= top > m[k][w] + 8.0f || top + lv > mv[k][w] + 8.0f;
+            if constexpr (SCORES) {
+              if (score[k][w]) {
+                score[k][w][t0 + g] = acc[k][w];
+                score[k][w][t0 + g + 8] = acc[k][w + 2];
+              }
+            }
+          }
+        }
+        if (__any_sync(FULL, rise)) {
+#pragma unroll
+          for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              float top = fmaxf(acc[k][w], acc[k][w + 2]);
+              for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, sh));
+              const float mn = fmaxf(m[k][w], top), mvn = fmaxf(mv[k][w], top + lv);
+              const float fl = exp2_fast(m[k][w] - mn), fo = exp2_fast(mv[k][w] - mvn);
+              m[k][w] = mn;
+              mv[k][w] = mvn;
+              l[k][w] *= fl;
+#pragma unroll
+              for (int n = 0; n < MT; ++n) {
+                o[k][n][w] *= fo;
+                o[k][n][w + 2] *= fo;
+              }
+            }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[k][e & 1] += exp2_fast(acc[k][e] - m[k][e & 1]);
+            p[e] = exp2_fast(acc[k][e] + (lv - mv[k][e & 1]));
+          }
+          pb[k][0] = transpose8(pack2<IBP_FP16>(p[0], p[1]));
+          pb[k][1] = transpose8(pack2<IBP_FP16>(p[2], p[3]));
+        }
+        // values: lane (g, t) holds D/8 consecutive elements of tokens 2t, 2t+1, 2t+8, 2t+9
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 2 * t4 + (e & 1) + 8 * (e >> 1);
+          const unsigned char *p = vt + (slab * SLAB + row) * D + g * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            v[e][0] = w.x; v[e][1] = w.y;
+          }
+          if (held < SLAB && row >= held)  // what lies past the length is not a number of ours
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) v[e][w] = 0u;
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t u0 = code_bias<CODE>(v[0][w]), u1 = code_bias<CODE>(v[1][w]);
+          const uint32_t u2 = code_bias<CODE>(v[2][w]), u3 = code_bias<CODE>(v[3][w]);
+          const uint32_t p01 = __byte_perm(u0, u1, 0x5140), p23 = __byte_perm(u0, u1, 0x7362);
+          const uint32_t q01 = __byte_perm(u2, u3, 0x5140), q23 = __byte_perm(u2, u3, 0x7362);
+          const uint32_t a0 = code_pair<CODE, 0>(p01), a1 = code_pair<CODE, 1>(p01),
+                         a2 = code_pair<CODE, 0>(q01), a3 = code_pair<CODE, 1>(q01);
+          const uint32_t b0 = code_pair<CODE, 0>(p23), b1 = code_pair<CODE, 1>(p23),
+                         b2 = code_pair<CODE, 0>(q23), b3 = code_pair<CODE, 1>(q23);
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            mma16816(o[k][2 * w], a0, a1, a2, a3, pb[k][0], pb[k][1]);
+            mma16816(o[k][2 * w + 1], b0, b1, b2, b3, pb[k][0], pb[k][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&freed[s]);
+    }
+
+    // ---- join the warps' results of this stretch, then finish the segment or leave a part
+    const bool first = x == lo, done = tile0 == 0 && count == nt;
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float sum = l[k][w];
+        for (int sh = 4; sh < 32; sh <<= 1) sum += __shfl_xor_sync(FULL, sum, sh);
+        const int r = 8 * k + 2 * t4 + w, at = warp * 8 * NT + r;
+        if (g == 0) {
+          st_m[at] = m[k][w];
+          st_mv[at] = mv[k][w];
+          st_l[at] = sum;
+        }
+        // elements g*D/8 .. of row r, in 16-byte pieces that the row's number scatters
+        float4 *to = reinterpret_cast<float4 *>(merge + at * D);
+#pragma unroll
+        for (int n = 0; n < MT / 2; ++n)
+          to[(g * (D / 32) + n) ^ (t4 & 3)] = make_float4(o[k][2 * n][w], o[k][2 * n][w + 2],
+                                                         o[k][2 * n + 1][w], o[k][2 * n + 1][w + 2]);
+      }
+    consumer_sync();
+    float *part = a.part + ((int64_t)cta * 2 + (first ? 0 : 1)) * S::part_floats;
+    for (int u = threadIdx.x; u < rows * (D / 4); u += 32 * CONSUMERS) {
+      const int r = u / (D / 4), piece = u % (D / 4);
+      const int in = r % (8 * NT);
+      float top = NONE, topv = NONE;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const int at = (k * WQ + r / (8 * NT)) * 8 * NT + in;
+        top = fmaxf(top, st_m[at]);
+        topv = fmaxf(topv, st_mv[at]);
+      }
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const int at = (k * WQ + r / (8 * NT)) * 8 * NT + in;
+        const float4 z = reinterpret_cast<const float4 *>(merge + at * D)[piece ^ ((in >> 1) & 3)];
+        const float f = exp2_fast(st_mv[at] - topv);
+        y.x += z.x * f;
+        y.y += z.y * f;
+        y.z += z.z * f;
+        y.w += z.w * f;
+        sum += st_l[at] * exp2_fast(st_m[at] - top);
+      }
+      if (done) {
+        const int rr = r0 + r;
+        const int64_t row = sq.row0 + rr / group;
+        const int qh = head * group + rr % group;
+        const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
+        *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
+                                   2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
+            make_uint2(pack2<DT>(y.x * f, y.y * f), pack2<DT>(y.z * f, y.w * f));
+        if (piece == 0) {
+          const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
+          if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
+          if constexpr (SCORES) a.lse2[row * a.q.q_heads + qh] = z;
+        }
+      } else {
+        reinterpret_cast<float4 *>(part)[r * (D / 4) + piece] = y;
+        if (piece == 0)
+          reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(top, topv, sum, 0.0f);
+      }
+    }
+    consumer_sync();
+    x += count;
   }
 }
 
-template <int D, int DT, int CODE>
-int launch_for(const ibp_kv_cache &c, const ibp_kv_query &q, void *scratch, int32_t *status,
-               cudaStream_t s) {
-  float *lse2 = static_cast<float *>(scratch);
-  const unsigned z = (unsigned)c.batch;
-  kv_attention_kernel<D, DT, CODE>
-      <<<dim3((unsigned)q.max_q, (unsigned)q.q_heads, z), 32 * WARPS, 0, s>>>(c, q, lse2, status);
-  if (q.d_weights) {
-    const unsigned tiles = (unsigned)((c.table_cols * c.page_tokens + 127) / 128);
-    kv_weights_kernel<D, DT, CODE>
-        <<<dim3(tiles, (unsigned)c.n_heads, z), 128, 0, s>>>(c, q, lse2, status);
-  }
-  return cudaGetLastError() == cudaSuccess ? IBP_OK : IBP_ERR_CUDA;
+// Where the parts of a segment lie.
+struct Parts {
+  Split split;
+  int64_t start;    // the segment's first tile
+  int first, last;  // CTAs
+};
+template <int MB>
+__device__ __forceinline__ Parts parts_of(const AttentionArgs &a, int b, const Sequence &s, int head,
+                                          int block, int group) {
+  Parts p = {Split(a.prefix[a.batch], a.ctas), 0, 0, 0};
+  const int nt = tiles_of(s.len);
+  p.start = a.prefix[b] + ((int64_t)head * blocks_of<MB>(s.n, group) + block) * nt;
+  p.first = p.split.owner(p.start);
+  p.last = p.split.owner(p.start + nt - 1);
+  return p;
+}
+template <int MB, int D>
+__device__ __forceinline__ const float *part_at(const AttentionArgs &a, const Parts &p, int cta) {
+  const int second = p.split.start(cta) < p.start;
+  return a.part + ((int64_t)cta * 2 + second) * ((int64_t)MB * (D + 4));
 }
 
-template <int D, int DT>
-int launch_code(const ibp_kv_cache &c, const ibp_kv_query &q, void *scratch, int32_t *status,
-                cudaStream_t s) {
-  return c.code == IBP_KV_INT8 ? launch_for<D, DT, IBP_KV_INT8>(c, q, scratch, status, s)
-                               : launch_for<D, DT, IBP_KV_E4M3>(c, q, scratch, status, s);
+// (m, mv, l) of one row over all parts, in the order of the CTAs.
+template <int MB, int D>
+__device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &p, int r) {
+  float4 y = make_float4(NONE, NONE, 0.0f, 0.0f);
+  for (int k = p.first; k <= p.last; ++k) {
+    const float4 z = reinterpret_cast<const float4 *>(part_at<MB, D>(a, p, k) + MB * D)[r];
+    const float m = fmaxf(y.x, z.x);
+    y.z = y.z * exp2_fast(y.x - m) + z.z * exp2_fast(z.x - m);
+    y.x = m;
+    y.y = fmaxf(y.y, z.y);
+  }
+  return y;
+}
+
+constexpr int FINISH_THREADS = 128;
+constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
+
+// Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
+// sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
+template <int D, int DT, int MB, bool SCORES>
+__global__ void __launch_bounds__(FINISH_THREADS)
+    kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
+  __shared__ float4 stat[MB];
+  const int b = blockIdx.z, head = blockIdx.y;
+  const int group = a.q.q_heads / a.c.n_heads;
+  grid_dependency_wait();
+  const Sequence s = sequence_of(a, b, nullptr);
+  const int all = s.n * group;
+  if ((int)blockIdx.x < row_blocks) {
+    const int r0 = blockIdx.x * MB, rows = min(MB, all - r0);
+    if (rows <= 0) return;
+    Parts p = {Split(1, 1), 0, 0, 0};
+    if (s.len > 0) {
+      p = parts_of<MB>(a, b, s, head, blockIdx.x, group);
+      if (p.first == p.last) return;
+      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) stat[r] = join_row<MB, D>(a, p, r);
+      __syncthreads();
+    }
+    for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
+      const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
+      const int64_t row = s.row0 + rr / group;
+      const int qh = head * group + rr % group;
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f, top = 0.0f;
+      if (s.len > 0) {
+        const float4 st = stat[r];
+        sum = st.z;
+        top = st.x;
+        for (int k = p.first; k <= p.last; ++k) {
+          const float *part = part_at<MB, D>(a, p, k);
+          const float f = exp2_fast(reinterpret_cast<const float4 *>(part + MB * D)[r].y - st.y);
+          const float4 z = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
+          y.x += z.x * f;
+          y.y += z.y * f;
+          y.z += z.z * f;
+          y.w += z.w * f;
+        }
+        const float f = sum > 0.0f ? exp2_fast(st.y - st.x) / sum : 0.0f;
+        y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+      }
+      *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
+                                 2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
+          make_uint2(pack2<DT>(y.x, y.y), pack2<DT>(y.z, y.w));
+      if (piece == 0 && a.q.d_lse)
+        a.q.d_lse[row * a.q.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
+    }
+    return;
+  }
+  if constexpr (SCORES) {
+    const int t = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
+    if (((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS >= s.len) return;
+    float sum[4] = {};
+    float *lse2 = reinterpret_cast<float *>(stat);
+    for (int r0 = 0; r0 < all; r0 += MB) {
+      const int rows = min(MB, all - r0);
+      const Parts p = parts_of<MB>(a, b, s, head, r0 / MB, group);
+      __syncthreads();
+      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) {
+        const int rr = r0 + r;
+        const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
+        float z;
+        if (p.first == p.last) {
+          z = a.lse2[row];
+        } else {
+          const float4 st = join_row<MB, D>(a, p, r);
+          z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
+        }
+        lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
+      }
+      __syncthreads();
+      if (t < s.len)
+        for (int r = 0; r < rows; ++r) {
+          const int rr = r0 + r;
+          const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
+          const float4 z = *reinterpret_cast<const float4 *>(a.scores + row * a.score_cols + t);
+          sum[0] += exp2_fast(z.x - lse2[r]);
+          sum[1] += exp2_fast(z.y - lse2[r]);
+          sum[2] += exp2_fast(z.z - lse2[r]);
+          sum[3] += exp2_fast(z.w - lse2[r]);
+        }
+    }
+    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < s.len)
+        a.q.d_weights[at + e] =
+            (a.q.d_weights_in ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f) + sum[e];
+  }
+}
+
+// ---- host side -------------------------------------------------------------------
+
+int score_cols_of(const ibp_kv_cache &c) {
+  return (c.table_cols * c.page_tokens + TILE - 1) / TILE * TILE;
+}
+
+// Query rows of a segment: the fewest that hold a sequence's rows of one K/V head.
+int rows_of(int64_t max_rows) {
+  return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
+}
+
+constexpr int MAX_CTAS = 1024;
+
+struct Layout {
+  size_t prefix, part, lse2, scores, bytes;
+};
+Layout layout_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, bool weights) {
+  const int mb = rows_of(max_q * (q_heads / c.n_heads));
+  Layout y;
+  y.prefix = 0;
+  y.part = ((MAX_BATCH + 1) * sizeof(int64_t) + 255) / 256 * 256;
+  y.lse2 = y.part + (size_t)MAX_CTAS * 2 * mb * (c.head_dim + 4) * sizeof(float);
+  y.scores = y.lse2 + (weights ? ((size_t)n_rows * q_heads * sizeof(float) + 255) / 256 * 256 : 0);
+  y.bytes = y.scores + (weights ? (size_t)n_rows * q_heads * score_cols_of(c) * sizeof(float) : 0);
+  return y;
+}
+
+template <int D, int CODE, int DT, int NT, int WQ, bool SCORES>
+int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
+  using S = Shape<D, NT, WQ>;
+  auto kernel = kv_attend_kernel<D, CODE, DT, NT, WQ, SCORES>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem) !=
+      cudaSuccess)
+    return IBP_ERR_CUDA;
+  const int group = a.q.q_heads / a.c.n_heads;
+  const int64_t blocks = (a.q.max_q * group + S::MB - 1) / S::MB;
+  const int64_t most = (int64_t)a.batch * a.c.n_heads * blocks * (a.score_cols / TILE);
+  a.ctas = (int)std::min<int64_t>(std::min(2 * dev.sm_count, MAX_CTAS), std::max<int64_t>(most, 1));
+  kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+  const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
+  if (launch_dependent(kv_finish_kernel<D, DT, S::MB, SCORES>,
+                       dim3((unsigned)(blocks + chunks), (unsigned)a.c.n_heads, (unsigned)a.batch),
+                       dim3(FINISH_THREADS), 0, s, a, (int)blocks) != cudaSuccess)
+    return IBP_ERR_CUDA;
+  return IBP_OK;
+}
+
+template <int D, int CODE, int DT>
+int launch_rows(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  const bool w = a.q.d_weights != nullptr;
+  switch (rows_of(a.q.max_q * (a.q.q_heads / a.c.n_heads))) {
+    case 8:
+      return w ? launch_shape<D, CODE, DT, 1, 1, true>(a, dev, s)
+               : launch_shape<D, CODE, DT, 1, 1, false>(a, dev, s);
+    case 16:
+      return w ? launch_shape<D, CODE, DT, 2, 1, true>(a, dev, s)
+               : launch_shape<D, CODE, DT, 2, 1, false>(a, dev, s);
+    case 32:
+      return w ? launch_shape<D, CODE, DT, 2, 2, true>(a, dev, s)
+               : launch_shape<D, CODE, DT, 2, 2, false>(a, dev, s);
+    default:
+      return w ? launch_shape<D, CODE, DT, 2, 4, true>(a, dev, s)
+               : launch_shape<D, CODE, DT, 2, 4, false>(a, dev, s);
+  }
 }
 
 template <int D>
-int launch_dtype(const ibp_kv_cache &c, const ibp_kv_query &q, void *scratch, int32_t *status,
-                 cudaStream_t s) {
-  return q.dtype == IBP_BF16 ? launch_code<D, IBP_BF16>(c, q, scratch, status, s)
-                             : launch_code<D, IBP_FP16>(c, q, scratch, status, s);
+int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (a.c.code == IBP_KV_INT8)
+    return a.q.dtype == IBP_BF16 ? launch_rows<D, IBP_KV_INT8, IBP_BF16>(a, dev, s)
+                                 : launch_rows<D, IBP_KV_INT8, IBP_FP16>(a, dev, s);
+  return a.q.dtype == IBP_BF16 ? launch_rows<D, IBP_KV_E4M3, IBP_BF16>(a, dev, s)
+                               : launch_rows<D, IBP_KV_E4M3, IBP_FP16>(a, dev, s);
 }
 
 }  // namespace
 
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,
                                   int q_heads, bool with_weights) {
-  return ((size_t)n_rows * q_heads * sizeof(float) + 15) / 16 * 16;
+  return layout_of(c, n_rows, max_q, q_heads, with_weights).bytes;
 }
 
 int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
                         int32_t *d_status, cudaStream_t s) {
-  return c.head_dim == 64 ? launch_dtype<64>(c, q, d_scratch, d_status, s)
-                          : launch_dtype<128>(c, q, d_scratch, d_status, s);
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  const Layout y = layout_of(c, q.n_rows, q.max_q, q.q_heads, q.d_weights != nullptr);
+  char *base = static_cast<char *>(d_scratch);
+  AttentionArgs a;
+  a.c = c;
+  a.q = q;
+  a.status = d_status;
+  a.wait_ns = gather_wait_limit_ns();
+  a.score_cols = score_cols_of(c);
+  a.prefix = reinterpret_cast<int64_t *>(base + y.prefix);
+  a.part = reinterpret_cast<float *>(base + y.part);
+  a.lse2 = reinterpret_cast<float *>(base + y.lse2);
+  a.scores = q.d_weights ? reinterpret_cast<float *>(base + y.scores) : nullptr;
+  for (a.b0 = 0; a.b0 < c.batch; a.b0 += MAX_BATCH) {
+    a.batch = std::min(c.batch - a.b0, MAX_BATCH);
+    if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
+      return rc;
+  }
+  return IBP_OK;
 }
 
 }  // namespace ibp
