@@ -24,7 +24,7 @@ constexpr int TILE = 64;      // tokens a stage holds
 constexpr int SLAB = 16;      // tokens a warp takes at a time; never more than one page
 constexpr int CONSUMERS = 4;  // warps that compute; one more fetches
 constexpr int THREADS = 32 * (CONSUMERS + 1);
-constexpr int MAX_BATCH = 1024;  // sequences of one launch (their tile counts are in shared memory)
+constexpr int MAX_BATCH = 256;  // sequences of one launch (their tile counts are in shared memory)
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -76,6 +76,11 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   }
 }
 
+// Orders this thread's shared-memory accesses before later bulk copies into the same place.
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory");
 }
@@ -102,7 +107,6 @@ struct AttentionArgs {
   int32_t *status;
   uint64_t wait_ns;
   int b0, batch, ctas, score_cols;
-  int64_t *prefix;  // [batch + 1] tiles before each sequence
   float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
   float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
   float *scores;    // [n_rows][q_heads][score_cols], or null
@@ -149,30 +153,36 @@ __device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, i
 
 template <int D, int NT, int WQ>
 struct Shape {
-  static constexpr int WK = CONSUMERS / WQ;     // warps that share a tile's tokens
-  static constexpr int MB = 8 * NT * WQ;        // query rows of a segment
-  static constexpr int STAGES = 4;
+  static constexpr int MB = 8 * NT * WQ;  // query rows of a segment
+  // NT = 1 runs three CTAs on an SM (12 computing warps), NT = 2 two for its registers
+  static constexpr int per_sm = NT == 1 ? 3 : 2;
+  static constexpr int STAGES = NT == 1 ? 4 : 6;
   static constexpr int stage_bytes = 2 * TILE * D;
   static constexpr int slabs = TILE / SLAB;
-  static constexpr int merge_floats = CONSUMERS * 8 * NT * D;
   static constexpr size_t part_floats = (size_t)MB * (D + 4);
-  static constexpr size_t smem = (size_t)STAGES * stage_bytes + merge_floats * 4 +
-                                 3 * CONSUMERS * 8 * NT * 4 + STAGES * slabs * 12 +
+  static constexpr size_t smem = (size_t)STAGES * stage_bytes + STAGES * slabs * 16 +
+                                 3 * CONSUMERS * 8 * 4 +
                                  (2 * STAGES) * 8 + (MAX_BATCH + 1) * 8 + 16;
 };
 
+// What a consumer needs to know of 16 tokens in a stage.
+struct __align__(16) SlabInfo {
+  float ks, lv;  // key scale, log2 of the value scale
+  int n;         // tokens held (0: the page is not there)
+  int unused;
+};
+
 template <int D, int CODE, int DT, int NT, int WQ, bool SCORES>
-__global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_constant__ AttentionArgs a) {
+__global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
+    kv_attend_kernel(const __grid_constant__ AttentionArgs a) {
   using S = Shape<D, NT, WQ>;
-  constexpr int MB = S::MB, WK = S::WK, ST = S::STAGES, NS = S::slabs, J = D / 64, MT = D / 16;
+  constexpr int MB = S::MB, ST = S::STAGES, NS = S::slabs, J = D / 64, MT = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char *stages = smem;
-  float *merge = reinterpret_cast<float *>(smem + ST * S::stage_bytes);
-  float *st_m = merge + S::merge_floats, *st_mv = st_m + CONSUMERS * 8 * NT,
-        *st_l = st_mv + CONSUMERS * 8 * NT;
-  float *slab_ks = st_l + CONSUMERS * 8 * NT, *slab_lv = slab_ks + ST * NS;
-  int *slab_n = reinterpret_cast<int *>(slab_lv + ST * NS);
-  uint64_t *full = reinterpret_cast<uint64_t *>(slab_n + ST * NS), *freed = full + ST;
+  SlabInfo *slabs = reinterpret_cast<SlabInfo *>(smem + ST * S::stage_bytes);
+  float *st_m = reinterpret_cast<float *>(slabs + ST * NS), *st_mv = st_m + CONSUMERS * 8,
+        *st_l = st_mv + CONSUMERS * 8;
+  uint64_t *full = reinterpret_cast<uint64_t *>(st_l + CONSUMERS * 8), *freed = full + ST;
   int64_t *prefix = reinterpret_cast<int64_t *>(freed + ST);
   volatile int *abort = reinterpret_cast<volatile int *>(prefix + MAX_BATCH + 1);
 
@@ -209,8 +219,6 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
   }
   __syncthreads();
   const int64_t total = prefix[a.batch];
-  if (cta == 0)
-    for (int b = threadIdx.x; b <= a.batch; b += THREADS) a.prefix[b] = prefix[b];
   const Split split(total, a.ctas);
   if (cta >= split.ctas) return;
   const int64_t lo = split.start(cta), hi = split.start(cta + 1);
@@ -264,10 +272,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
       const unsigned some = __ballot_sync(FULL, lane < NP && at >= 0);
       if (lane < NP) {
         for (int k = 0; k < PP / SLAB; ++k) {
-          const int slab = s * NS + lane * (PP / SLAB) + k;
-          slab_ks[slab] = ks;
-          slab_lv[slab] = lv;
-          slab_n[slab] = min(max(n - k * SLAB, 0), SLAB);
+          const SlabInfo info = {ks, lv, min(max(n - k * SLAB, 0), SLAB), 0};
+          slabs[s * NS + lane * (PP / SLAB) + k] = info;
         }
       }
       __syncwarp();
@@ -292,11 +298,12 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
   }
 
   // ---- computing warps: S^T = K q^T (16 tokens x 8 NT rows), then O^T += V^T P^T
-  const int wq = warp % WQ, wk = warp / WQ, g = lane >> 2, t4 = lane & 3;
+  const int g = lane >> 2, t4 = lane & 3;
   bool dead = false;  // a wait ran out: the rest is gone through without waiting or computing,
                       // so that no warp is missed at a barrier
-  int64_t x = lo, i = 0;
-  int b = find_sequence(prefix, a.batch, lo);
+  int64_t x = lo;
+  int b = find_sequence(prefix, a.batch, lo), s = 0;
+  uint32_t phase = 0;
   while (x < hi) {
     while (x >= prefix[b + 1]) ++b;
     const Sequence sq = sequence_of(a, b, nullptr);
@@ -305,6 +312,9 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
     const int seg = (int)(local / nt), tile0 = (int)(local % nt);
     const int count = (int)min((int64_t)(nt - tile0), hi - x);
     const int head = seg / blocks, r0 = (seg % blocks) * MB, rows = min(MB, sq.n * group - r0);
+    // as many warps side by side along the rows as these need, the others along a tile
+    const int wqn = rows <= 8 * NT ? 1 : WQ >= 2 && rows <= 16 * NT ? 2 : WQ;
+    const int wq = warp % wqn, wk = warp / wqn, wkn = CONSUMERS / wqn;
     const bool active = wq * 8 * NT < rows;
 
     // query rows as the second operand: lane (g, t) holds 16 consecutive elements of row g
@@ -354,9 +364,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
         limit[k][w] = col < rows ? max(sq.len - sq.n + cc / group + 1, 0) : 0x7FFFFFFF;
         least = min(least, limit[k][w]);
         if constexpr (SCORES)
-          score[k][w] = col < rows ? a.scores + ((sq.row0 + cc / group) * a.q.q_heads + head * group +
-                                                 cc % group) * a.score_cols
-                                   : nullptr;
+          score[k][w] = a.scores + ((sq.row0 + cc / group) * a.q.q_heads + head * group +
+                                    cc % group) * a.score_cols;
       }
     }
     for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(FULL, least, o));
@@ -375,9 +384,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
         for (int e = 0; e < 4; ++e) o[k][n][e] = 0.0f;
     }
 
-    for (int tile = tile0; tile < tile0 + count; ++tile, ++i) {
-      const int s = (int)(i % ST);
-      if (!dead && !__all_sync(FULL, mbar_wait(&full[s], (uint32_t)((i / ST) & 1), abort, a.wait_ns))) {
+    for (int tile = tile0;; ++tile) {
+      if (!dead && !__all_sync(FULL, mbar_wait(&full[s], phase, abort, a.wait_ns))) {
         dead = true;
         if (lane == 0) {
           report(a.status, IBP_ERR_TIMEOUT);
@@ -385,13 +393,10 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
         }
       }
       const unsigned char *kt = stages + s * S::stage_bytes, *vt = kt + TILE * D;
-      for (int slab = wk; active && !dead && slab < NS; slab += WK) {
+      for (int slab = wk; active && !dead && slab < NS; slab += wkn) {
         const int t0 = tile * TILE + slab * SLAB;
         if (t0 >= sq.len) break;
-        const int held = slab_n[s * NS + slab];  // 0: its page is not there
-        const float ks = slab_ks[s * NS + slab], lv = slab_lv[s * NS + slab];
-        const bool whole = held == SLAB && t0 + SLAB <= least;
-
+        const SlabInfo info = slabs[s * NS + slab];
         float acc[NT][4];
 #pragma unroll
         for (int k = 0; k < NT; ++k)
@@ -399,8 +404,9 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
           for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          const uint4 ra = *reinterpret_cast<const uint4 *>(kt + (slab * SLAB + g) * D + 16 * (t4 + 4 * j));
-          const uint4 rb = *reinterpret_cast<const uint4 *>(kt + (slab * SLAB + g + 8) * D + 16 * (t4 + 4 * j));
+          const unsigned char *at = kt + (slab * SLAB + g) * D + 16 * (t4 + 4 * j);
+          const uint4 ra = *reinterpret_cast<const uint4 *>(at);
+          const uint4 rb = *reinterpret_cast<const uint4 *>(at + 8 * D);
           const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -413,29 +419,29 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
           }
         }
         // scores of tokens g, g + 8 and rows 2t, 2t + 1
+        const bool whole = info.n == SLAB && t0 + SLAB <= least;
         bool rise = false;
 #pragma unroll
-        for (int k = 0; k < NT; ++k) {
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const float f = rowc[k][w] * ks;
-            acc[k][w] *= f;
-            acc[k][w + 2] *= f;
+            const float f = rowc[k][w] * info.ks;
+            float y0 = acc[k][w] * f, y1 = acc[k][w + 2] * f;
             if (!whole) {
-              const int seen = min(limit[k][w] - t0, held);
-              if (g >= seen) acc[k][w] = -INFINITY;
-              if (g + 8 >= seen) acc[k][w + 2] = -INFINITY;
+              const int seen = min(limit[k][w] - t0, info.n);
+              if (g >= seen) y0 = -INFINITY;
+              if (g + 8 >= seen) y1 = -INFINITY;
             }
-            const float top = fmaxf(acc[k][w], acc[k][w + 2]);
-            rise |= top > m[k][w] + 8.0f || top + lv > mv[k][w] + 8.0f;
+            acc[k][w] = y0;
+            acc[k][w + 2] = y1;
+            rise |= fmaxf(y0, y1) > fminf(m[k][w], mv[k][w] - info.lv) + 8.0f;
             if constexpr (SCORES) {
-              if (score[k][w]) {
-                score[k][w][t0 + g] = acc[k][w];
-                score[k][w][t0 + g + 8] = acc[k][w + 2];
+              if (wq * 8 * NT + 8 * k + 2 * t4 + w < rows) {
+                score[k][w][t0 + g] = y0;
+                score[k][w][t0 + g + 8] = y1;
               }
             }
           }
-        }
         if (__any_sync(FULL, rise)) {
 #pragma unroll
           for (int k = 0; k < NT; ++k)
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
             for (int w = 0; w < 2; ++w) {
               float top = fmaxf(acc[k][w], acc[k][w + 2]);
               for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, sh));
-              const float mn = fmaxf(m[k][w], top), mvn = fmaxf(mv[k][w], top + lv);
+              const float mn = fmaxf(m[k][w], top), mvn = fmaxf(mv[k][w], top + info.lv);
               const float fl = exp2_fast(m[k][w] - mn), fo = exp2_fast(mv[k][w] - mvn);
               m[k][w] = mn;
               mv[k][w] = mvn;
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             l[k][e & 1] += exp2_fast(acc[k][e] - m[k][e & 1]);
-            p[e] = exp2_fast(acc[k][e] + (lv - mv[k][e & 1]));
+            p[e] = exp2_fast(acc[k][e] + (info.lv - mv[k][e & 1]));
           }
           pb[k][0] = transpose8(pack2<IBP_FP16>(p[0], p[1]));
           pb[k][1] = transpose8(pack2<IBP_FP16>(p[2], p[3]));
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
             const uint2 w = *reinterpret_cast<const uint2 *>(p);
             v[e][0] = w.x; v[e][1] = w.y;
           }
-          if (held < SLAB && row >= held)  // what lies past the length is not a number of ours
+          if (!whole && row >= info.n)  // what lies past the length is not a number of ours
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) v[e][w] = 0u;
         }
@@ -501,76 +507,91 @@ __global__ void __launch_bounds__(THREADS, 2) kv_attend_kernel(const __grid_cons
           }
         }
       }
+      if (tile == tile0 + count - 1) break;  // the last one's stage is kept for the join
       __syncwarp();
       if (lane == 0) mbar_arrive(&freed[s]);
+      if (++s == ST) {
+        s = 0;
+        phase ^= 1u;
+      }
     }
 
-    // ---- join the warps' results of this stretch, then finish the segment or leave a part
+    // ---- join the warps' results of this stretch in the last tile's stage (its 2 * TILE *
+    // D bytes hold 8 rows of every warp), then finish the segment or leave a part
     const bool first = x == lo, done = tile0 == 0 && count == nt;
+    float *part = a.part + ((int64_t)cta * 2 + (first ? 0 : 1)) * S::part_floats;
+    float *merge = reinterpret_cast<float *>(stages + s * S::stage_bytes);
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int k = 0; k < NT; ++k) {
+      consumer_sync();
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         float sum = l[k][w];
         for (int sh = 4; sh < 32; sh <<= 1) sum += __shfl_xor_sync(FULL, sum, sh);
-        const int r = 8 * k + 2 * t4 + w, at = warp * 8 * NT + r;
+        const int at = warp * 8 + 2 * t4 + w;
         if (g == 0) {
           st_m[at] = m[k][w];
           st_mv[at] = mv[k][w];
           st_l[at] = sum;
         }
-        // elements g*D/8 .. of row r, in 16-byte pieces that the row's number scatters
+        // elements g*D/8 .. of the row, in 16-byte pieces that the row's number scatters
         float4 *to = reinterpret_cast<float4 *>(merge + at * D);
 #pragma unroll
         for (int n = 0; n < MT / 2; ++n)
-          to[(g * (D / 32) + n) ^ (t4 & 3)] = make_float4(o[k][2 * n][w], o[k][2 * n][w + 2],
-                                                         o[k][2 * n + 1][w], o[k][2 * n + 1][w + 2]);
+          to[(g * (D / 32) + n) ^ t4] = make_float4(o[k][2 * n][w], o[k][2 * n][w + 2],
+                                                   o[k][2 * n + 1][w], o[k][2 * n + 1][w + 2]);
       }
-    consumer_sync();
-    float *part = a.part + ((int64_t)cta * 2 + (first ? 0 : 1)) * S::part_floats;
-    for (int u = threadIdx.x; u < rows * (D / 4); u += 32 * CONSUMERS) {
-      const int r = u / (D / 4), piece = u % (D / 4);
-      const int in = r % (8 * NT);
-      float top = NONE, topv = NONE;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) {
-        const int at = (k * WQ + r / (8 * NT)) * 8 * NT + in;
-        top = fmaxf(top, st_m[at]);
-        topv = fmaxf(topv, st_mv[at]);
-      }
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) {
-        const int at = (k * WQ + r / (8 * NT)) * 8 * NT + in;
-        const float4 z = reinterpret_cast<const float4 *>(merge + at * D)[piece ^ ((in >> 1) & 3)];
-        const float f = exp2_fast(st_mv[at] - topv);
-        y.x += z.x * f;
-        y.y += z.y * f;
-        y.z += z.z * f;
-        y.w += z.w * f;
-        sum += st_l[at] * exp2_fast(st_m[at] - top);
-      }
-      if (done) {
-        const int rr = r0 + r;
-        const int64_t row = sq.row0 + rr / group;
-        const int qh = head * group + rr % group;
-        const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
-        *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
-                                   2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
-            make_uint2(pack2<DT>(y.x * f, y.y * f), pack2<DT>(y.z * f, y.w * f));
-        if (piece == 0) {
-          const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
-          if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
-          if constexpr (SCORES) a.lse2[row * a.q.q_heads + qh] = z;
+      consumer_sync();
+      for (int u = threadIdx.x; u < wqn * 8 * (D / 4); u += 32 * CONSUMERS) {
+        const int in = u / (D / 4) % 8, side = u / (D / 4) / 8, piece = u % (D / 4);
+        const int r = side * 8 * NT + 8 * k + in;
+        if (r >= rows) continue;
+        float top = NONE, topv = NONE;
+        for (int i = 0; i < wkn; ++i) {
+          const int at = (i * wqn + side) * 8 + in;
+          top = fmaxf(top, st_m[at]);
+          topv = fmaxf(topv, st_mv[at]);
         }
-      } else {
-        reinterpret_cast<float4 *>(part)[r * (D / 4) + piece] = y;
-        if (piece == 0)
-          reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(top, topv, sum, 0.0f);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+        for (int i = 0; i < wkn; ++i) {
+          const int at = (i * wqn + side) * 8 + in;
+          const float4 z = reinterpret_cast<const float4 *>(merge + at * D)[piece ^ (in >> 1)];
+          const float f = exp2_fast(st_mv[at] - topv);
+          y.x += z.x * f;
+          y.y += z.y * f;
+          y.z += z.z * f;
+          y.w += z.w * f;
+          sum += st_l[at] * exp2_fast(st_m[at] - top);
+        }
+        if (done) {
+          const int rr = r0 + r;
+          const int64_t row = sq.row0 + rr / group;
+          const int qh = head * group + rr % group;
+          const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
+          *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
+                                     2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
+              make_uint2(pack2<DT>(y.x * f, y.y * f), pack2<DT>(y.z * f, y.w * f));
+          if (piece == 0) {
+            const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
+            if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
+            if constexpr (SCORES) a.lse2[row * a.q.q_heads + qh] = z;
+          }
+        } else {
+          reinterpret_cast<float4 *>(part)[r * (D / 4) + piece] = y;
+          if (piece == 0)
+            reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(top, topv, sum, 0.0f);
+        }
       }
     }
     consumer_sync();
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&freed[s]);
+    if (++s == ST) {
+      s = 0;
+      phase ^= 1u;
+    }
     x += count;
   }
 }
@@ -582,31 +603,40 @@ struct Parts {
   int first, last;  // CTAs
 };
 template <int MB>
-__device__ __forceinline__ Parts parts_of(const AttentionArgs &a, int b, const Sequence &s, int head,
-                                          int block, int group) {
-  Parts p = {Split(a.prefix[a.batch], a.ctas), 0, 0, 0};
+__device__ __forceinline__ Parts parts_of(const AttentionArgs &a, const int64_t *prefix,
+                                          const Sequence &s, int head, int block, int group) {
+  Parts p = {Split(prefix[1], a.ctas), 0, 0, 0};
   const int nt = tiles_of(s.len);
-  p.start = a.prefix[b] + ((int64_t)head * blocks_of<MB>(s.n, group) + block) * nt;
+  p.start = prefix[0] + ((int64_t)head * blocks_of<MB>(s.n, group) + block) * nt;
   p.first = p.split.owner(p.start);
   p.last = p.split.owner(p.start + nt - 1);
   return p;
 }
+// Only a segment's first CTA can have held another segment before it.
 template <int MB, int D>
 __device__ __forceinline__ const float *part_at(const AttentionArgs &a, const Parts &p, int cta) {
-  const int second = p.split.start(cta) < p.start;
+  const int second = cta == p.first ? p.split.start(cta) < p.start : 0;
   return a.part + ((int64_t)cta * 2 + second) * ((int64_t)MB * (D + 4));
 }
 
-// (m, mv, l) of one row over all parts, in the order of the CTAs.
+// (m, mv, l) of one row over all parts: a warp's lanes take every 32nd part, then a
+// fixed tree.
 template <int MB, int D>
 __device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &p, int r) {
   float4 y = make_float4(NONE, NONE, 0.0f, 0.0f);
-  for (int k = p.first; k <= p.last; ++k) {
+  for (int k = p.first + (int)(threadIdx.x & 31); k <= p.last; k += 32) {
     const float4 z = reinterpret_cast<const float4 *>(part_at<MB, D>(a, p, k) + MB * D)[r];
     const float m = fmaxf(y.x, z.x);
     y.z = y.z * exp2_fast(y.x - m) + z.z * exp2_fast(z.x - m);
     y.x = m;
     y.y = fmaxf(y.y, z.y);
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    const float zx = __shfl_xor_sync(FULL, y.x, o), zl = __shfl_xor_sync(FULL, y.z, o);
+    const float m = fmaxf(y.x, zx);
+    y.y = fmaxf(y.y, __shfl_xor_sync(FULL, y.y, o));
+    y.z = y.z * exp2_fast(y.x - m) + zl * exp2_fast(zx - m);
+    y.x = m;
   }
   return y;
 }
@@ -617,24 +647,43 @@ constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
 // Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
 // sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
 template <int D, int DT, int MB, bool SCORES>
-__global__ void __launch_bounds__(FINISH_THREADS)
+__global__ void __launch_bounds__(FINISH_THREADS, 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
-  __shared__ float4 stat[MB];
+  __shared__ float lse2[MB];
+  __shared__ int64_t prefix[2];  // tiles before sequence b and in all
   const int b = blockIdx.z, head = blockIdx.y;
   const int group = a.q.q_heads / a.c.n_heads;
-  grid_dependency_wait();
+  // what follows from the lengths alone is worked out before the attending kernel ends
+  // (whatever wrote the lengths ended before that one began)
   const Sequence s = sequence_of(a, b, nullptr);
   const int all = s.n * group;
+  if (threadIdx.x < 32) {
+    int64_t before = 0, total = 0;
+    for (int k = threadIdx.x; k < a.batch; k += 32) {
+      const Sequence other = sequence_of(a, k, nullptr);
+      const int64_t tiles = (int64_t)a.c.n_heads * blocks_of<MB>(other.n, group) * tiles_of(other.len);
+      total += tiles;
+      if (k < b) before += tiles;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(FULL, before, o);
+      total += __shfl_xor_sync(FULL, total, o);
+    }
+    if (threadIdx.x == 0) {
+      prefix[0] = before;
+      prefix[1] = total;
+    }
+  }
+  __syncthreads();
   if ((int)blockIdx.x < row_blocks) {
     const int r0 = blockIdx.x * MB, rows = min(MB, all - r0);
     if (rows <= 0) return;
     Parts p = {Split(1, 1), 0, 0, 0};
     if (s.len > 0) {
-      p = parts_of<MB>(a, b, s, head, blockIdx.x, group);
+      p = parts_of<MB>(a, prefix, s, head, blockIdx.x, group);
       if (p.first == p.last) return;
-      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) stat[r] = join_row<MB, D>(a, p, r);
-      __syncthreads();
     }
+    grid_dependency_wait();
     for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
       const int64_t row = s.row0 + rr / group;
@@ -642,19 +691,41 @@ __global__ void __launch_bounds__(FINISH_THREADS)
       float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float sum = 0.0f, top = 0.0f;
       if (s.len > 0) {
-        const float4 st = stat[r];
-        sum = st.z;
-        top = st.x;
-        for (int k = p.first; k <= p.last; ++k) {
-          const float *part = part_at<MB, D>(a, p, k);
-          const float f = exp2_fast(reinterpret_cast<const float4 *>(part + MB * D)[r].y - st.y);
-          const float4 z = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
-          y.x += z.x * f;
-          y.y += z.y * f;
-          y.z += z.z * f;
-          y.w += z.w * f;
+        // parts in the order of their CTAs, AHEAD of them loaded at a time
+        constexpr int AHEAD = 4;
+        float topv = NONE;
+        top = NONE;
+        for (int k0 = p.first; k0 <= p.last; k0 += AHEAD) {
+          float4 st[AHEAD], z[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const float *part = part_at<MB, D>(a, p, min(k0 + k, p.last));
+            st[k] = reinterpret_cast<const float4 *>(part + MB * D)[r];
+            z[k] = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
+          }
+          float m = top, mv = topv;
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            m = fmaxf(m, st[k].x);  // a part read twice does not raise it
+            mv = fmaxf(mv, st[k].y);
+          }
+          const float fl = exp2_fast(top - m), fo = exp2_fast(topv - mv);
+          sum *= fl;
+          y = make_float4(y.x * fo, y.y * fo, y.z * fo, y.w * fo);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (k0 + k <= p.last) {
+              const float f = exp2_fast(st[k].y - mv);
+              sum += st[k].z * exp2_fast(st[k].x - m);
+              y.x += z[k].x * f;
+              y.y += z[k].y * f;
+              y.z += z[k].z * f;
+              y.w += z[k].w * f;
+            }
+          top = m;
+          topv = mv;
         }
-        const float f = sum > 0.0f ? exp2_fast(st.y - st.x) / sum : 0.0f;
+        const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
         y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
       }
       *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
@@ -668,18 +739,21 @@ __global__ void __launch_bounds__(FINISH_THREADS)
   if constexpr (SCORES) {
     const int t = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
     if (((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS >= s.len) return;
-    float sum[4] = {};
-    float *lse2 = reinterpret_cast<float *>(stat);
+    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
+    float sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum[e] = a.q.d_weights_in && t + e < s.len ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f;
+    grid_dependency_wait();
     for (int r0 = 0; r0 < all; r0 += MB) {
       const int rows = min(MB, all - r0);
-      const Parts p = parts_of<MB>(a, b, s, head, r0 / MB, group);
+      const Parts p = parts_of<MB>(a, prefix, s, head, r0 / MB, group);
       __syncthreads();
-      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) {
+      for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
         const int rr = r0 + r;
-        const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
         float z;
         if (p.first == p.last) {
-          z = a.lse2[row];
+          z = a.lse2[(s.row0 + rr / group) * a.q.q_heads + head * group + rr % group];
         } else {
           const float4 st = join_row<MB, D>(a, p, r);
           z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
@@ -687,7 +761,8 @@ __global__ void __launch_bounds__(FINISH_THREADS)
         lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
       }
       __syncthreads();
-      if (t < s.len)
+      if (t < s.len) {
+#pragma unroll 4
         for (int r = 0; r < rows; ++r) {
           const int rr = r0 + r;
           const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
@@ -697,13 +772,11 @@ __global__ void __launch_bounds__(FINISH_THREADS)
           sum[2] += exp2_fast(z.z - lse2[r]);
           sum[3] += exp2_fast(z.w - lse2[r]);
         }
+      }
     }
-    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (t + e < s.len)
-        a.q.d_weights[at + e] =
-            (a.q.d_weights_in ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f) + sum[e];
+      if (t + e < s.len) a.q.d_weights[at + e] = sum[e];
   }
 }
 
@@ -721,13 +794,12 @@ int rows_of(int64_t max_rows) {
 constexpr int MAX_CTAS = 1024;
 
 struct Layout {
-  size_t prefix, part, lse2, scores, bytes;
+  size_t part, lse2, scores, bytes;
 };
 Layout layout_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, bool weights) {
   const int mb = rows_of(max_q * (q_heads / c.n_heads));
   Layout y;
-  y.prefix = 0;
-  y.part = ((MAX_BATCH + 1) * sizeof(int64_t) + 255) / 256 * 256;
+  y.part = 0;
   y.lse2 = y.part + (size_t)MAX_CTAS * 2 * mb * (c.head_dim + 4) * sizeof(float);
   y.scores = y.lse2 + (weights ? ((size_t)n_rows * q_heads * sizeof(float) + 255) / 256 * 256 : 0);
   y.bytes = y.scores + (weights ? (size_t)n_rows * q_heads * score_cols_of(c) * sizeof(float) : 0);
@@ -744,7 +816,7 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   const int group = a.q.q_heads / a.c.n_heads;
   const int64_t blocks = (a.q.max_q * group + S::MB - 1) / S::MB;
   const int64_t most = (int64_t)a.batch * a.c.n_heads * blocks * (a.score_cols / TILE);
-  a.ctas = (int)std::min<int64_t>(std::min(2 * dev.sm_count, MAX_CTAS), std::max<int64_t>(most, 1));
+  a.ctas = (int)std::min<int64_t>(std::min(S::per_sm * dev.sm_count, MAX_CTAS), std::max<int64_t>(most, 1));
   kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
   const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
@@ -802,7 +874,6 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
   a.status = d_status;
   a.wait_ns = gather_wait_limit_ns();
   a.score_cols = score_cols_of(c);
-  a.prefix = reinterpret_cast<int64_t *>(base + y.prefix);
   a.part = reinterpret_cast<float *>(base + y.part);
   a.lse2 = reinterpret_cast<float *>(base + y.lse2);
   a.scores = q.d_weights ? reinterpret_cast<float *>(base + y.scores) : nullptr;
