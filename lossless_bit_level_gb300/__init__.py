@@ -544,7 +544,9 @@ def _at(t):
 
 
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # the current stream's handle without building a Stream object around it
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None \
+        else stream.cuda_stream
 
 
 class KVCache:

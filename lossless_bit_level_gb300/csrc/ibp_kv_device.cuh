@@ -47,6 +47,18 @@ __device__ __forceinline__ int64_t kv_tile(const ibp_kv_cache &c, int page, int 
   return ((int64_t)page * c.n_heads + head) * c.page_tokens * c.head_dim;
 }
 
+// How a CTA goes over one (page, head) tile: every thread holds `per_thread` groups of 16
+// consecutive elements of a token. Four groups a thread where that leaves a warp: what a
+// thread works out once (its sequence, page, addresses) costs as much as converting 16
+// elements or two.
+template <int P, int D>
+struct Tile {
+  static constexpr int groups = P * D / 16;
+  static constexpr int threads = groups <= 128 ? 32 : groups <= 512 ? groups / 4 : 256;
+  static constexpr int per_thread = groups / threads;
+  static constexpr int step = threads / (D / 16);  // tokens between a thread's groups
+};
+
 template <int CODE>
 struct KvQmax {
   static constexpr float value = CODE == IBP_KV_INT8 ? 127.0f : 448.0f;
@@ -69,14 +81,11 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // Four values (already times the inverse scale) to four codes in one word. int8:
-// adding 1.5 * 2^23 leaves the value rounded to nearest even in the low byte.
+// adding 1.5 * 2^23 leaves the value rounded to nearest even in the low byte. Values a
+// rounding or two past +-qmax round to qmax; anything further, and NaN, needs
+// kv_encode4_any.
 template <int CODE>
 __device__ __forceinline__ uint32_t kv_encode4(float a, float b, float c, float d) {
-  constexpr float Q = KvQmax<CODE>::value;
-  a = a == a ? fminf(fmaxf(a, -Q), Q) : 0.0f;
-  b = b == b ? fminf(fmaxf(b, -Q), Q) : 0.0f;
-  c = c == c ? fminf(fmaxf(c, -Q), Q) : 0.0f;
-  d = d == d ? fminf(fmaxf(d, -Q), Q) : 0.0f;
   if constexpr (CODE == IBP_KV_INT8) {
     constexpr float R = 12582912.0f;
     const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a, R)),
@@ -89,6 +98,16 @@ __device__ __forceinline__ uint32_t kv_encode4(float a, float b, float c, float 
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
+}
+template <int CODE>
+__device__ __forceinline__ float kv_saturate(float a) {
+  constexpr float Q = KvQmax<CODE>::value;
+  return a == a ? fminf(fmaxf(a, -Q), Q) : 0.0f;
+}
+template <int CODE>
+__device__ __forceinline__ uint32_t kv_encode4_any(float a, float b, float c, float d) {
+  return kv_encode4<CODE>(kv_saturate<CODE>(a), kv_saturate<CODE>(b), kv_saturate<CODE>(c),
+                          kv_saturate<CODE>(d));
 }
 
 // Four codes to the numbers they stand for (before the scale).
@@ -111,38 +130,85 @@ __device__ __forceinline__ void kv_decode4(uint32_t w, float *x) {
   }
 }
 
-// 16 consecutive elements of a row (16-byte aligned) as floats.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("min.s16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+
+// 16 consecutive elements of a row (16-byte aligned) as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load16(const void *p, float *x) {
-  const uint4 *v = static_cast<const uint4 *>(p);
-  if constexpr (DT == IBP_FP32) {
+struct Raw16 {
+  static constexpr int vecs = DT == IBP_FP32 ? 4 : 2;
+  // magnitude bits of an infinity: everything finite lies below
+  static constexpr uint32_t inf = DT == IBP_FP32 ? 0x7F800000u : DT == IBP_BF16 ? 0x7F80u : 0x7C00u;
+  uint4 v[vecs];
+  __device__ __forceinline__ void load(const void *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 w = __ldg(v + i);
-      x[4 * i] = __uint_as_float(w.x);
-      x[4 * i + 1] = __uint_as_float(w.y);
-      x[4 * i + 2] = __uint_as_float(w.z);
-      x[4 * i + 3] = __uint_as_float(w.w);
-    }
-  } else {
+    for (int i = 0; i < vecs; ++i) v[i] = __ldg(static_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 w = __ldg(v + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < vecs; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    const uint4 w = v[i / 4];
+    return i % 4 == 0 ? w.x : i % 4 == 1 ? w.y : i % 4 == 2 ? w.z : w.w;
+  }
+  // Elements 4i .. 4i + 3 as floats.
+  __device__ __forceinline__ void four(int i, float *x) const {
+    if constexpr (DT == IBP_FP32) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(word(4 * i + k));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t u = word(2 * i + k);
         if constexpr (DT == IBP_BF16) {
-          x[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
-          x[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+          x[2 * k] = __uint_as_float(u << 16);
+          x[2 * k + 1] = __uint_as_float(u & 0xFFFF0000u);
         } else {
-          const __half2 h = *reinterpret_cast<const __half2 *>(&u[k]);
-          const float2 f = __half22float2(h);
-          x[8 * i + 2 * k] = f.x;
-          x[8 * i + 2 * k + 1] = f.y;
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+          x[2 * k] = f.x;
+          x[2 * k + 1] = f.y;
         }
       }
     }
   }
+  // The larger of m and the elements' magnitude bits (16-bit types: of both halves apart).
+  __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 4 * vecs; ++i)
+      m = DT == IBP_FP32 ? max(m, word(i) & 0x7FFFFFFFu) : max_u16x2(m, word(i) & 0x7FFF7FFFu);
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t fold(uint32_t m) {
+    return DT == IBP_FP32 ? m : max(m >> 16, m & 0xFFFFu);
+  }
+  __device__ __forceinline__ static float value(uint32_t bits) {
+    return DT == IBP_FP32   ? __uint_as_float(bits)
+           : DT == IBP_BF16 ? __uint_as_float(bits << 16)
+                            : __half2float(__ushort_as_half((unsigned short)bits));
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void load16(const void *p, float *x) {
+  Raw16<DT> r;
+  r.load(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.four(i, x + 4 * i);
 }
 
 // Two floats rounded once to a pair of 16-bit elements.
@@ -173,14 +239,13 @@ __device__ __forceinline__ void store16(void *p, const float *x) {
   }
 }
 
-// Largest of the block's values (every thread gets it); `sm`: 32 floats.
-__device__ __forceinline__ float block_max(float v, float *sm) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-  if (blockDim.x <= 32) return v;
+// Largest of the block's values (every thread gets it); `sm`: 32 words.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *sm) {
+  v = __reduce_max_sync(FULL, v);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
-  float m = sm[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) m = fmaxf(m, sm[w]);
+  uint32_t m = sm[0];
+  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) m = max(m, sm[w]);
   return m;
 }
 
