@@ -15,6 +15,10 @@ size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t
                                   int q_heads, bool with_weights);
 int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
                         int32_t *d_status, cudaStream_t s);
+// Many query rows a sequence (ibp_kv_prefill.cu); no weights.
+size_t kv_prefill_scratch_bytes(const ibp_kv_cache &c);
+int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
+                      int32_t *d_status, cudaStream_t s);
 size_t kv_evict_scratch_bytes(const ibp_kv_cache &c, int64_t budget);
 int launch_kv_evict(const ibp_kv_cache &c, const float *d_weights, int64_t weights_stride,
                     int64_t budget, int64_t recent, const ibp_kv_cache &dst, int32_t *d_new_lens,

@@ -10,27 +10,16 @@
 // of a maximum across lanes; fp16 and fp32 have the room).
 #include <algorithm>
 
-#include "ibp_kv_device.cuh"
+#include "ibp_kv_attention.cuh"
 
 namespace ibp {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float NONE = -1e30f;  // reference of a row that has seen no token yet
-
 constexpr int TILE = 64;      // tokens a stage holds
 constexpr int SLAB = 16;      // tokens a warp takes at a time; never more than one page
 constexpr int CONSUMERS = 4;  // warps that compute; one more fetches
 constexpr int THREADS = 32 * (CONSUMERS + 1);
-constexpr int MAX_BATCH = 256;  // sequences of one launch (their tile counts are in shared memory)
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -76,83 +65,13 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   }
 }
 
-// Orders this thread's shared-memory accesses before later bulk copies into the same place.
-__device__ __forceinline__ void fence_async_proxy() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory");
 }
 
-// How a launch is divided. A (sequence, K/V head, block of MB query rows) is a segment
-// of ceil(length / TILE) tiles; all tiles of all segments are laid end to end and every
-// CTA takes an equal stretch, so a batch of any mix of lengths fills the GPU and a
-// segment is joined from as many CTAs as it took.
-struct Split {
-  int64_t total;
-  int ctas;  // that have work: every one of them has a tile at least
-  __device__ __forceinline__ Split(int64_t tiles, int launched)
-      : total(tiles), ctas((int)min((int64_t)launched, tiles)) {}
-  __device__ __forceinline__ int64_t start(int cta) const { return total * cta / ctas; }
-  // the CTA whose stretch holds tile x
-  __device__ __forceinline__ int owner(int64_t x) const {
-    return (int)(((x + 1) * ctas - 1) / total);
-  }
-};
-
-struct AttentionArgs {
-  ibp_kv_cache c;
-  ibp_kv_query q;
-  int32_t *status;
-  uint64_t wait_ns;
-  int b0, batch, ctas, score_cols;
-  float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
-  float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
-  float *scores;    // [n_rows][q_heads][score_cols], or null
-};
-
-struct Sequence {
-  int64_t row0;  // its first query row
-  int n, len;    // query rows, tokens
-};
-
-__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, int32_t *status) {
-  Sequence s;
-  int64_t lo, hi;
-  kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + b, status, &lo, &hi);
-  if (hi - lo > a.q.max_q) {
-    report(status, IBP_ERR_INDEX);
-    hi = lo + a.q.max_q;
-  }
-  s.row0 = lo;
-  s.n = (int)(hi - lo);
-  s.len = kv_len(a.c, a.b0 + b, status);
-  return s;
-}
-
-__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
-
-// A tile's place: segment (b, head, block) and tile number.
-struct Place {
-  int b, seg, tile;
-};
-template <int MB>
-__device__ __forceinline__ int blocks_of(int n, int group) {
-  return (n * group + MB - 1) / MB;
-}
-
-__device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, int64_t x) {
-  int lo = 0, hi = batch;  // the last b with prefix[b] <= x (empty ones come before it)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (prefix[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 template <int D, int NT, int WQ>
 struct Shape {
+  using Plan = EvenPlan<8 * NT * WQ, TILE>;
   static constexpr int MB = 8 * NT * WQ;  // query rows of a segment
   // NT = 1 runs three CTAs on an SM (12 computing warps), NT = 2 two for its registers
   static constexpr int per_sm = NT == 1 ? 3 : 2;
@@ -176,6 +95,7 @@ template <int D, int CODE, int DT, int NT, int WQ, bool SCORES>
 __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
     kv_attend_kernel(const __grid_constant__ AttentionArgs a) {
   using S = Shape<D, NT, WQ>;
+  using Plan = typename S::Plan;
   constexpr int MB = S::MB, ST = S::STAGES, NS = S::slabs, J = D / 64, MT = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char *stages = smem;
@@ -205,7 +125,8 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
       int64_t tiles = 0;
       if (b < a.batch) {
         const Sequence s = sequence_of(a, b, cta == 0 ? a.status : nullptr);
-        tiles = (int64_t)c.n_heads * blocks_of<MB>(s.n, group) * tiles_of(s.len);
+        const Plan plan(s, group);
+        tiles = c.n_heads * plan.before(plan.blocks);
       }
       int64_t sum = tiles;
       for (int o = 1; o < 32; o <<= 1) {
@@ -239,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
       if (e >= pieces) return p;
       const int64_t x = lo + e / NP;
       const int b = find_sequence(prefix, a.batch, x);
-      const int len = kv_len(c, a.b0 + b, nullptr), nt = tiles_of(len);
+      const int len = kv_len(c, a.b0 + b, nullptr), nt = (len + TILE - 1) / TILE;
       const int64_t local = x - prefix[b], per_head = (prefix[b + 1] - prefix[b]) / c.n_heads;
       const int head = (int)(local / per_head), tile = (int)(local % nt);
       const int t = tile * TILE + (int)(e % NP) * PP;
@@ -307,7 +228,8 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   while (x < hi) {
     while (x >= prefix[b + 1]) ++b;
     const Sequence sq = sequence_of(a, b, nullptr);
-    const int nt = tiles_of(sq.len), blocks = blocks_of<MB>(sq.n, group);
+    const Plan plan(sq, group);
+    const int nt = plan.tiles_each, blocks = plan.blocks;
     const int64_t local = x - prefix[b];
     const int seg = (int)(local / nt), tile0 = (int)(local % nt);
     const int count = (int)min((int64_t)(nt - tile0), hi - x);
@@ -596,190 +518,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   }
 }
 
-// Where the parts of a segment lie.
-struct Parts {
-  Split split;
-  int64_t start;    // the segment's first tile
-  int first, last;  // CTAs
-};
-template <int MB>
-__device__ __forceinline__ Parts parts_of(const AttentionArgs &a, const int64_t *prefix,
-                                          const Sequence &s, int head, int block, int group) {
-  Parts p = {Split(prefix[1], a.ctas), 0, 0, 0};
-  const int nt = tiles_of(s.len);
-  p.start = prefix[0] + ((int64_t)head * blocks_of<MB>(s.n, group) + block) * nt;
-  p.first = p.split.owner(p.start);
-  p.last = p.split.owner(p.start + nt - 1);
-  return p;
-}
-// Only a segment's first CTA can have held another segment before it.
-template <int MB, int D>
-__device__ __forceinline__ const float *part_at(const AttentionArgs &a, const Parts &p, int cta) {
-  const int second = cta == p.first ? p.split.start(cta) < p.start : 0;
-  return a.part + ((int64_t)cta * 2 + second) * ((int64_t)MB * (D + 4));
-}
-
-// (m, mv, l) of one row over all parts: a warp's lanes take every 32nd part, then a
-// fixed tree.
-template <int MB, int D>
-__device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &p, int r) {
-  float4 y = make_float4(NONE, NONE, 0.0f, 0.0f);
-  for (int k = p.first + (int)(threadIdx.x & 31); k <= p.last; k += 32) {
-    const float4 z = reinterpret_cast<const float4 *>(part_at<MB, D>(a, p, k) + MB * D)[r];
-    const float m = fmaxf(y.x, z.x);
-    y.z = y.z * exp2_fast(y.x - m) + z.z * exp2_fast(z.x - m);
-    y.x = m;
-    y.y = fmaxf(y.y, z.y);
-  }
-  for (int o = 16; o > 0; o >>= 1) {
-    const float zx = __shfl_xor_sync(FULL, y.x, o), zl = __shfl_xor_sync(FULL, y.z, o);
-    const float m = fmaxf(y.x, zx);
-    y.y = fmaxf(y.y, __shfl_xor_sync(FULL, y.y, o));
-    y.z = y.z * exp2_fast(y.x - m) + zl * exp2_fast(zx - m);
-    y.x = m;
-  }
-  return y;
-}
-
-constexpr int FINISH_THREADS = 128;
-constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
-
-// Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
-// sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
-template <int D, int DT, int MB, bool SCORES>
-__global__ void __launch_bounds__(FINISH_THREADS, 8)
-    kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
-  __shared__ float lse2[MB];
-  __shared__ int64_t prefix[2];  // tiles before sequence b and in all
-  const int b = blockIdx.z, head = blockIdx.y;
-  const int group = a.q.q_heads / a.c.n_heads;
-  // what follows from the lengths alone is worked out before the attending kernel ends
-  // (whatever wrote the lengths ended before that one began)
-  const Sequence s = sequence_of(a, b, nullptr);
-  const int all = s.n * group;
-  if (threadIdx.x < 32) {
-    int64_t before = 0, total = 0;
-    for (int k = threadIdx.x; k < a.batch; k += 32) {
-      const Sequence other = sequence_of(a, k, nullptr);
-      const int64_t tiles = (int64_t)a.c.n_heads * blocks_of<MB>(other.n, group) * tiles_of(other.len);
-      total += tiles;
-      if (k < b) before += tiles;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(FULL, before, o);
-      total += __shfl_xor_sync(FULL, total, o);
-    }
-    if (threadIdx.x == 0) {
-      prefix[0] = before;
-      prefix[1] = total;
-    }
-  }
-  __syncthreads();
-  if ((int)blockIdx.x < row_blocks) {
-    const int r0 = blockIdx.x * MB, rows = min(MB, all - r0);
-    if (rows <= 0) return;
-    Parts p = {Split(1, 1), 0, 0, 0};
-    if (s.len > 0) {
-      p = parts_of<MB>(a, prefix, s, head, blockIdx.x, group);
-      if (p.first == p.last) return;
-    }
-    grid_dependency_wait();
-    for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
-      const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
-      const int64_t row = s.row0 + rr / group;
-      const int qh = head * group + rr % group;
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f, top = 0.0f;
-      if (s.len > 0) {
-        // parts in the order of their CTAs, AHEAD of them loaded at a time
-        constexpr int AHEAD = 4;
-        float topv = NONE;
-        top = NONE;
-        for (int k0 = p.first; k0 <= p.last; k0 += AHEAD) {
-          float4 st[AHEAD], z[AHEAD];
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k) {
-            const float *part = part_at<MB, D>(a, p, min(k0 + k, p.last));
-            st[k] = reinterpret_cast<const float4 *>(part + MB * D)[r];
-            z[k] = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
-          }
-          float m = top, mv = topv;
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k) {
-            m = fmaxf(m, st[k].x);  // a part read twice does not raise it
-            mv = fmaxf(mv, st[k].y);
-          }
-          const float fl = exp2_fast(top - m), fo = exp2_fast(topv - mv);
-          sum *= fl;
-          y = make_float4(y.x * fo, y.y * fo, y.z * fo, y.w * fo);
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k)
-            if (k0 + k <= p.last) {
-              const float f = exp2_fast(st[k].y - mv);
-              sum += st[k].z * exp2_fast(st[k].x - m);
-              y.x += z[k].x * f;
-              y.y += z[k].y * f;
-              y.z += z[k].z * f;
-              y.w += z[k].w * f;
-            }
-          top = m;
-          topv = mv;
-        }
-        const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
-        y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-      }
-      *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
-                                 2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
-          make_uint2(pack2<DT>(y.x, y.y), pack2<DT>(y.z, y.w));
-      if (piece == 0 && a.q.d_lse)
-        a.q.d_lse[row * a.q.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
-    }
-    return;
-  }
-  if constexpr (SCORES) {
-    const int t = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
-    if (((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS >= s.len) return;
-    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
-    float sum[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      sum[e] = a.q.d_weights_in && t + e < s.len ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f;
-    grid_dependency_wait();
-    for (int r0 = 0; r0 < all; r0 += MB) {
-      const int rows = min(MB, all - r0);
-      const Parts p = parts_of<MB>(a, prefix, s, head, r0 / MB, group);
-      __syncthreads();
-      for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
-        const int rr = r0 + r;
-        float z;
-        if (p.first == p.last) {
-          z = a.lse2[(s.row0 + rr / group) * a.q.q_heads + head * group + rr % group];
-        } else {
-          const float4 st = join_row<MB, D>(a, p, r);
-          z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
-        }
-        lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
-      }
-      __syncthreads();
-      if (t < s.len) {
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-          const int rr = r0 + r;
-          const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
-          const float4 z = *reinterpret_cast<const float4 *>(a.scores + row * a.score_cols + t);
-          sum[0] += exp2_fast(z.x - lse2[r]);
-          sum[1] += exp2_fast(z.y - lse2[r]);
-          sum[2] += exp2_fast(z.z - lse2[r]);
-          sum[3] += exp2_fast(z.w - lse2[r]);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (t + e < s.len) a.q.d_weights[at + e] = sum[e];
-  }
-}
-
 // ---- host side -------------------------------------------------------------------
 
 int score_cols_of(const ibp_kv_cache &c) {
@@ -790,8 +528,6 @@ int score_cols_of(const ibp_kv_cache &c) {
 int rows_of(int64_t max_rows) {
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
 }
-
-constexpr int MAX_CTAS = 1024;
 
 struct Layout {
   size_t part, lse2, scores, bytes;
@@ -820,7 +556,7 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
   const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
-  if (launch_dependent(kv_finish_kernel<D, DT, S::MB, SCORES>,
+  if (launch_dependent(kv_finish_kernel<D, DT, typename S::Plan, SCORES>,
                        dim3((unsigned)(blocks + chunks), (unsigned)a.c.n_heads, (unsigned)a.batch),
                        dim3(FINISH_THREADS), 0, s, a, (int)blocks) != cudaSuccess)
     return IBP_ERR_CUDA;
@@ -857,13 +593,21 @@ int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) 
 
 }  // namespace
 
+// More rows than a segment holds go to the kernel for many of them.
+static bool many_rows(const ibp_kv_cache &c, int64_t max_q, int q_heads, bool weights) {
+  return !weights && max_q * (q_heads / c.n_heads) > 64;
+}
+
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,
                                   int q_heads, bool with_weights) {
+  if (many_rows(c, max_q, q_heads, with_weights)) return kv_prefill_scratch_bytes(c);
   return layout_of(c, n_rows, max_q, q_heads, with_weights).bytes;
 }
 
 int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
                         int32_t *d_status, cudaStream_t s) {
+  if (many_rows(c, q.max_q, q.q_heads, q.d_weights != nullptr))
+    return launch_kv_prefill(c, q, d_scratch, d_status, s);
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
   const Layout y = layout_of(c, q.n_rows, q.max_q, q.q_heads, q.d_weights != nullptr);

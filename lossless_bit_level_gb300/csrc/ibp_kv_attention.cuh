@@ -1,0 +1,335 @@
+// Shared by the attention kernels of the 8-bit paged key/value cache: how a launch is
+// divided over the GPU, and the kernel that joins what was divided.
+#pragma once
+
+#include "ibp_kv_device.cuh"
+
+namespace ibp {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float NONE = -1e30f;  // reference of a row that has seen no token yet
+
+constexpr int MAX_BATCH = 256;  // sequences of one launch (their tile counts are in shared memory)
+constexpr int MAX_CTAS = 512;          // three to each of 152 SMs, and some
+constexpr int MAX_PREFILL_CTAS = 160;  // one to an SM
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Orders this thread's shared-memory accesses before later bulk copies into the same place.
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+struct AttentionArgs {
+  ibp_kv_cache c;
+  ibp_kv_query q;
+  int32_t *status;
+  uint64_t wait_ns;
+  int b0, batch, ctas, score_cols;
+  float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
+  float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
+  float *scores;    // [n_rows][q_heads][score_cols], or null
+};
+
+struct Sequence {
+  int64_t row0;  // its first query row
+  int n, len;    // query rows, tokens
+};
+
+__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, int32_t *status) {
+  Sequence s;
+  int64_t lo, hi;
+  kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + b, status, &lo, &hi);
+  if (hi - lo > a.q.max_q) {
+    report(status, IBP_ERR_INDEX);
+    hi = lo + a.q.max_q;
+  }
+  s.row0 = lo;
+  s.n = (int)(hi - lo);
+  s.len = kv_len(a.c, a.b0 + b, status);
+  return s;
+}
+
+// How a launch is divided. A (sequence, K/V head, block of MB query rows) is a segment of
+// tiles of TILE tokens; all tiles of all segments are laid end to end (sequence, head,
+// block, token) and every CTA takes an equal stretch, so a batch of any mix of lengths
+// fills the GPU and a segment is joined from as many CTAs as it took.
+struct Split {
+  int64_t total;
+  int ctas;  // that have work: every one of them has a tile at least
+  __device__ __forceinline__ Split(int64_t tiles, int launched)
+      : total(tiles), ctas((int)min((int64_t)launched, tiles)) {}
+  __device__ __forceinline__ int64_t start(int cta) const { return total * cta / ctas; }
+  // the CTA whose stretch holds tile x
+  __device__ __forceinline__ int owner(int64_t x) const {
+    return (int)(((x + 1) * ctas - 1) / total);
+  }
+};
+
+// Tiles of a sequence's blocks. EvenPlan: every block goes over all tokens (few query
+// rows: the last ones, so at most a tile is spared by their order).
+template <int MB_, int TILE_>
+struct EvenPlan {
+  static constexpr int MB = MB_, TILE = TILE_;
+  int blocks, tiles_each;
+  __device__ __forceinline__ EvenPlan(const Sequence &s, int group)
+      : blocks((s.n * group + MB - 1) / MB), tiles_each((s.len + TILE - 1) / TILE) {}
+  __device__ __forceinline__ int tiles(int) const { return tiles_each; }
+  __device__ __forceinline__ int64_t before(int block) const { return (int64_t)block * tiles_each; }
+  // the block that holds tile x of a head
+  __device__ __forceinline__ int find(int64_t x) const { return (int)(x / tiles_each); }
+};
+
+// CausalPlan: a block stops at the last token its last row sees. Block j's last query is
+// q_j = (MB (j + 1) - 1) / group (the sequence's last for the last block), so it has
+// floor((MB j + (len - n + TILE) group + MB - 1) / (TILE group)) tiles; their sum over j
+// is a sum of floors of an arithmetic progression, taken as in Euclid's algorithm.
+template <int MB_, int TILE_>
+struct CausalPlan {
+  static constexpr int MB = MB_, TILE = TILE_;
+  int blocks, group, n, len;
+  __device__ __forceinline__ CausalPlan(const Sequence &s, int g)
+      : blocks((s.n * g + MB - 1) / MB), group(g), n(s.n), len(s.len) {}
+  __device__ __forceinline__ int tiles(int block) const {
+    const int last = block == blocks - 1 ? n - 1 : (MB * (block + 1) - 1) / group;
+    return (max(len - n + last + 1, 0) + TILE - 1) / TILE;
+  }
+  __device__ __forceinline__ int64_t before(int block) const {
+    // blocks whose last query sees nothing have no tiles
+    const int64_t hidden = max((int64_t)(n - len) * group, (int64_t)0) / MB;
+    const bool all = block == blocks;
+    int64_t count = (all ? block - 1 : block) - hidden, sum = 0;
+    if (count > 0) {
+      int64_t m = (int64_t)TILE * group, a = MB;
+      int64_t b = MB * hidden + (int64_t)(len - n + TILE) * group + MB - 1, k = count;
+      for (;;) {
+        sum += (k - 1) * k / 2 * (a / m) + k * (b / m);
+        a %= m;
+        b %= m;
+        const int64_t y = a * k + b;
+        if (y < m) break;
+        k = y / m;
+        b = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+      }
+    }
+    return all && blocks > 0 ? sum + tiles(blocks - 1) : sum;
+  }
+  __device__ __forceinline__ int find(int64_t x) const {
+    int lo = 0, hi = blocks;  // the last block with before(block) <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+};
+
+__device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, int64_t x) {
+  int lo = 0, hi = batch;  // the last b with prefix[b] <= x (empty ones come before it)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Where the parts of a segment lie.
+struct Parts {
+  Split split;
+  int64_t start;    // the segment's first tile
+  int first, last;  // CTAs
+};
+__device__ __forceinline__ Parts parts_of(int64_t total, int64_t start, int tiles, int ctas) {
+  Parts p = {Split(total, ctas), start, 0, 0};
+  p.first = p.split.owner(start);
+  p.last = p.split.owner(start + tiles - 1);
+  return p;
+}
+// Only a segment's first CTA can have held another segment before it.
+template <int MB, int D>
+__device__ __forceinline__ const float *part_at(const AttentionArgs &a, const Parts &p, int cta) {
+  const int second = cta == p.first ? p.split.start(cta) < p.start : 0;
+  return a.part + ((int64_t)cta * 2 + second) * ((int64_t)MB * (D + 4));
+}
+
+// (m, mv, l) of one row over all parts: a warp's lanes take every 32nd part, then a
+// fixed tree.
+template <int MB, int D>
+__device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &p, int r) {
+  float4 y = make_float4(NONE, NONE, 0.0f, 0.0f);
+  for (int k = p.first + (int)(threadIdx.x & 31); k <= p.last; k += 32) {
+    const float4 z = reinterpret_cast<const float4 *>(part_at<MB, D>(a, p, k) + MB * D)[r];
+    const float m = fmaxf(y.x, z.x);
+    y.z = y.z * exp2_fast(y.x - m) + z.z * exp2_fast(z.x - m);
+    y.x = m;
+    y.y = fmaxf(y.y, z.y);
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    const float zx = __shfl_xor_sync(FULL, y.x, o), zl = __shfl_xor_sync(FULL, y.z, o);
+    const float m = fmaxf(y.x, zx);
+    y.y = fmaxf(y.y, __shfl_xor_sync(FULL, y.y, o));
+    y.z = y.z * exp2_fast(y.x - m) + zl * exp2_fast(zx - m);
+    y.x = m;
+  }
+  return y;
+}
+
+constexpr int FINISH_THREADS = 128;
+constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
+
+// Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
+// sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
+template <int D, int DT, typename Plan, bool SCORES>
+__global__ void __launch_bounds__(FINISH_THREADS, 8)
+    kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
+  constexpr int MB = Plan::MB;
+  __shared__ float lse2[MB];
+  __shared__ int64_t prefix[2];  // tiles before sequence b and in all
+  const int b = blockIdx.z, head = blockIdx.y;
+  const int group = a.q.q_heads / a.c.n_heads;
+  // what follows from the lengths alone is worked out before the attending kernel ends
+  // (whatever wrote the lengths ended before that one began)
+  const Sequence s = sequence_of(a, b, nullptr);
+  const Plan plan(s, group);
+  const int all = s.n * group;
+  if (threadIdx.x < 32) {
+    int64_t before = 0, total = 0;
+    for (int k = threadIdx.x; k < a.batch; k += 32) {
+      const Sequence other = sequence_of(a, k, nullptr);
+      const Plan theirs(other, group);
+      const int64_t tiles = a.c.n_heads * theirs.before(theirs.blocks);
+      total += tiles;
+      if (k < b) before += tiles;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(FULL, before, o);
+      total += __shfl_xor_sync(FULL, total, o);
+    }
+    if (threadIdx.x == 0) {
+      prefix[0] = before;
+      prefix[1] = total;
+    }
+  }
+  __syncthreads();
+  if ((int)blockIdx.x < row_blocks) {
+    const int r0 = blockIdx.x * MB, rows = min(MB, all - r0);
+    if (rows <= 0) return;
+    const int tiles = plan.tiles(blockIdx.x);
+    Parts p = {Split(1, 1), 0, 0, 0};
+    if (tiles > 0) {
+      p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(blockIdx.x),
+                   tiles, a.ctas);
+      if (p.first == p.last) return;
+    }
+    grid_dependency_wait();
+    for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
+      const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
+      const int64_t row = s.row0 + rr / group;
+      const int qh = head * group + rr % group;
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f, top = 0.0f;
+      if (tiles > 0) {
+        // parts in the order of their CTAs, AHEAD of them loaded at a time
+        constexpr int AHEAD = 4;
+        float topv = NONE;
+        top = NONE;
+        for (int k0 = p.first; k0 <= p.last; k0 += AHEAD) {
+          float4 st[AHEAD], z[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const float *part = part_at<MB, D>(a, p, min(k0 + k, p.last));
+            st[k] = reinterpret_cast<const float4 *>(part + MB * D)[r];
+            z[k] = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
+          }
+          float m = top, mv = topv;
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            m = fmaxf(m, st[k].x);  // a part read twice does not raise it
+            mv = fmaxf(mv, st[k].y);
+          }
+          const float fl = exp2_fast(top - m), fo = exp2_fast(topv - mv);
+          sum *= fl;
+          y = make_float4(y.x * fo, y.y * fo, y.z * fo, y.w * fo);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (k0 + k <= p.last) {
+              const float f = exp2_fast(st[k].y - mv);
+              sum += st[k].z * exp2_fast(st[k].x - m);
+              y.x += z[k].x * f;
+              y.y += z[k].y * f;
+              y.z += z[k].z * f;
+              y.w += z[k].w * f;
+            }
+          top = m;
+          topv = mv;
+        }
+        const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
+        y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+      }
+      *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
+                                 2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
+          make_uint2(pack2<DT>(y.x, y.y), pack2<DT>(y.z, y.w));
+      if (piece == 0 && a.q.d_lse)
+        a.q.d_lse[row * a.q.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
+    }
+    return;
+  }
+  if constexpr (SCORES) {
+    const int t = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
+    if (((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS >= s.len) return;
+    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
+    float sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum[e] = a.q.d_weights_in && t + e < s.len ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f;
+    grid_dependency_wait();
+    for (int r0 = 0; r0 < all; r0 += MB) {
+      const int rows = min(MB, all - r0);
+      const int block = r0 / MB;
+      const Parts p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
+                               plan.tiles(block), a.ctas);
+      __syncthreads();
+      for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
+        const int rr = r0 + r;
+        float z;
+        if (p.first == p.last) {
+          z = a.lse2[(s.row0 + rr / group) * a.q.q_heads + head * group + rr % group];
+        } else {
+          const float4 st = join_row<MB, D>(a, p, r);
+          z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
+        }
+        lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
+      }
+      __syncthreads();
+      if (t < s.len) {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+          const int rr = r0 + r;
+          const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
+          const float4 z = *reinterpret_cast<const float4 *>(a.scores + row * a.score_cols + t);
+          sum[0] += exp2_fast(z.x - lse2[r]);
+          sum[1] += exp2_fast(z.y - lse2[r]);
+          sum[2] += exp2_fast(z.z - lse2[r]);
+          sum[3] += exp2_fast(z.w - lse2[r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < s.len) a.q.d_weights[at + e] = sum[e];
+  }
+}
+
+}  // namespace
+
+}  // namespace ibp

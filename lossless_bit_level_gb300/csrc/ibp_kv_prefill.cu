@@ -1,0 +1,683 @@
+// Attention of many query rows over the 8-bit paged key/value cache, on the fifth
+// generation's matrix unit (declared in include/ibp.h; the formulas stand at the head of
+// ibp_kv_attention.cu).
+//
+// A CTA takes 256 query rows of one K/V head (the rows of all query heads that share it,
+// so shared heads fill the matrix unit) over tiles of 128 tokens. Codes become fp16 in
+// shared memory, exactly, once for both halves of 128 rows; S = Q K^T and O += P V
+// accumulate in tensor memory, P returns there as fp16. While the matrix unit works on
+// one half, the other half's 128 threads (one to a row) turn scores into probabilities:
+//   warps 0-3, 4-7  rows 0-127 and 128-255: references, exponentials, the final scaling
+//   warps 8-11      fetch codes a tile ahead into registers, convert, store swizzled
+//   warp 12         issues the matrix instructions
+// A page's key scale is a factor of its scores, its value scale one of its probabilities.
+#include <algorithm>
+
+#include "ibp_kv_attention.cuh"
+
+namespace ibp {
+
+namespace {
+
+constexpr int MB = 256;      // query rows of a segment
+constexpr int TILE = 128;    // tokens of a tile
+constexpr int GROUPS = TILE / 16;
+constexpr int STAGES = 2;    // of K and of V
+constexpr int INFOS = 4;     // tiles whose scales are kept
+constexpr int THREADS = 13 * 32;
+constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12;
+constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S (and P over it) at 128 w, O at 256 + 128 w
+using Plan = CausalPlan<MB, TILE>;
+
+// ---- tensor memory and the matrix instruction
+__device__ __forceinline__ void tmem_alloc(uint32_t *at) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)),
+               "r"(TMEM_COLS)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(TMEM_COLS));
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// The barrier is arrived at once every matrix instruction issued so far has finished.
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+
+#define R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), \
+                 "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), \
+                  "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+#define I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), \
+                 "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+
+// 32 columns of this warp's 32 lanes, a lane to a thread. The values may be used after
+// tmem_wait_load of the same registers.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&x)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : RW8(x, 0), RW8(x, 8), RW8(x, 16), RW8(x, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t *x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16};" ::"r"(at),
+      I8(x, 0), I8(x, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand in 128-byte rows of 64 fp16, swizzled in groups of 8 rows.
+// K-major (the summed index along the row): groups of 8 rows 1024 bytes apart. MN-major
+// (the summed index down the rows): the same 1024 bytes between groups of 8 of the summed
+// index, `block` bytes between blocks of 64 of the other.
+__device__ __forceinline__ uint64_t operand(const void *p, uint32_t block) {
+  return (uint64_t)((smem_u32(p) & 0x3FFFF) >> 4) | ((uint64_t)(block >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// fp16 operands, fp32 accumulators, 128 rows, n columns; vt: the second operand MN-major.
+__host__ __device__ constexpr uint32_t instruction(int n, bool vt) {
+  return (1u << 4) | ((vt ? 1u : 0u) << 16) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(128 / 16) << 24);
+}
+
+// Pairs of floats in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+
+// Scales of a tile's groups of 16 tokens (a group never spans two pages); bad: a bit for
+// each group whose page is not there.
+struct TileInfo {
+  float2 scale[GROUPS];  // key scale, log2 of the value scale
+  uint32_t bad;
+  uint32_t unused;
+};
+
+template <int D>
+struct Memory {
+  static constexpr int q_bytes = 128 * D * 2, kv_bytes = TILE * D * 2;
+  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, info = v + STAGES * kv_bytes;
+  static constexpr int bars = info + INFOS * (int)sizeof(TileInfo);
+  static constexpr int prefix = bars + 24 * 8;
+  static constexpr int words = prefix + (MAX_BATCH + 1) * 8;
+  static constexpr int bytes = words + 16 + 1024;  // the operands start on 1024 bytes
+};
+
+// Where a stretch stands: the segment of tile x and the tile within it.
+struct Cursor {
+  int b, head, block, tile, tiles;
+  Sequence seq;
+};
+__device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_t *prefix, int group,
+                                            int64_t x) {
+  Cursor c;
+  c.b = find_sequence(prefix, a.batch, x);
+  c.seq = sequence_of(a, c.b, nullptr);
+  const Plan plan(c.seq, group);
+  const int64_t local = x - prefix[c.b], per_head = (prefix[c.b + 1] - prefix[c.b]) / a.c.n_heads;
+  c.head = (int)(local / per_head);
+  const int64_t in = local - c.head * per_head;
+  c.block = plan.find(in);
+  c.tile = (int)(in - plan.before(c.block));
+  c.tiles = plan.tiles(c.block);
+  return c;
+}
+// The first tile of the next segment that has one (there is one: the caller's x < total).
+__device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64_t *prefix, int group,
+                                             Cursor &c) {
+  c.tile = 0;
+  for (;;) {
+    const Plan plan(c.seq, group);
+    if (++c.block == plan.blocks) {
+      c.block = 0;
+      if (++c.head == a.c.n_heads) {
+        c.head = 0;
+        do {
+          ++c.b;
+        } while (prefix[c.b] == prefix[c.b + 1]);
+        c.seq = sequence_of(a, c.b, nullptr);
+      }
+    }
+    c.tiles = Plan(c.seq, group).tiles(c.block);
+    if (c.tiles > 0) return;
+  }
+}
+
+// Codes to fp16, exactly (as in ibp_kv_attention.cu).
+template <int CODE, int HIGH>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  if constexpr (CODE == IBP_KV_INT8) {
+    const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, HIGH ? 0x4342 : 0x4140);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    uint32_t y;
+    const uint16_t x = HIGH ? (uint16_t)(w >> 16) : (uint16_t)w;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return y;
+  }
+}
+
+template <int D, int CODE, int DT>
+__global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ AttentionArgs a) {
+  using M = Memory<D>;
+  constexpr int BLOCKS = D / 64;  // of 64 elements
+  extern __shared__ unsigned char raw_smem[];
+  unsigned char *smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
+  uint64_t *k_full = bars, *k_free = bars + 2, *v_full = bars + 4, *v_free = bars + 6, *s_full = bars + 8,
+           *p_full = bars + 10, *o_done = bars + 12, *q_full = bars + 14, *info_full = bars + 16,
+           *last_bar = bars + 20;
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
+  uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const ibp_kv_cache &c = a.c;
+  const int group = a.q.q_heads / c.n_heads;
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_free[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&q_full[i], 4);
+    }
+    for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
+    mbar_init(last_bar, 1);
+    *abort = 0;
+    mbar_init_fence();
+  }
+  if (warp == ISSUE_WARP) {
+    tmem_alloc(tmem_at);
+    int64_t base = 0;
+    for (int k0 = 0; k0 < a.batch; k0 += 32) {
+      const int b = k0 + lane;
+      int64_t tiles = 0;
+      if (b < a.batch) {
+        const Plan plan(sequence_of(a, b, cta == 0 ? a.status : nullptr), group);
+        tiles = c.n_heads * plan.before(plan.blocks);
+      }
+      int64_t sum = tiles;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, sum, o);
+        if (lane >= o) sum += y;
+      }
+      if (b < a.batch) prefix[b] = base + sum - tiles;
+      base += __shfl_sync(FULL, sum, 31);
+    }
+    if (lane == 0) prefix[a.batch] = base;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  const Split split(prefix[a.batch], a.ctas);
+  const bool work = cta < split.ctas;
+  const int64_t lo = work ? split.start(cta) : 0, hi = work ? split.start(cta + 1) : 0;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, abort, a.wait_ns)) return true;
+    report(a.status, IBP_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
+  };
+
+  if (work && warp >= CONVERT_WARP && warp < ISSUE_WARP) {
+    // ---- codes to fp16: thread i of 128 takes the 16 elements PER * i of every STEP-th token
+    constexpr int PER = D / 16, STEP = 128 / PER, N = TILE / STEP;  // 8, 16, 8 or 4, 32, 4
+    const int tid = threadIdx.x - CONVERT_WARP * 32, key0 = tid / PER, piece = tid % PER;
+    const char *kc = static_cast<const char *>(c.k_codes), *vc = static_cast<const char *>(c.v_codes);
+    struct Place {
+      int b, head, t0, len;
+    };
+    Cursor cur = cursor_at(a, prefix, group, lo);
+    int64_t ahead = lo;  // the tile `cur` stands at
+    auto take = [&] {
+      const Place p = {cur.b, cur.head, cur.tile * TILE, cur.seq.len};
+      ++ahead;
+      if (++cur.tile == cur.tiles && ahead < hi) next_segment(a, prefix, group, cur);
+      return p;
+    };
+    // lane g < 8 looks up the page of tokens 16 g ..
+    struct Pages {
+      int page;
+      float ks, lv;
+    };
+    auto look_up = [&](const Place &p) {
+      Pages y = {-1, 0.0f, 0.0f};
+      const int t = p.t0 + (lane & 7) * 16;
+      if (t < p.len) {
+        y.page = kv_page(c, a.b0 + p.b, t / c.page_tokens, a.status);
+        if (y.page >= 0) {
+          const int64_t at = (int64_t)y.page * c.n_heads + p.head;
+          y.ks = __ldg(c.k_scales + at);
+          y.lv = __ldg(c.v_scales + at);
+        }
+      }
+      return y;
+    };
+    auto load = [&](const char *codes, const Place &p, const Pages &y, uint4 (&w)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int key = key0 + i * STEP, t = p.t0 + key;
+        const int page = __shfl_sync(FULL, y.page, key / 16);
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (page >= 0 && t < p.len)
+          w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + kv_tile(c, page, p.head) +
+                                                       (t & (c.page_tokens - 1)) * D + piece * 16));
+      }
+    };
+    // rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a row exclusive-
+    // or'ed with its number
+    auto convert = [&](unsigned char *to, const uint4 (&w)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int key = key0 + i * STEP;
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = 2 * piece + h;
+          const uint4 y = make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
+                                     code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+          *reinterpret_cast<uint4 *>(to + (at / 8) * (TILE * 128) + key * 128 + ((at ^ key) & 7) * 16) = y;
+        }
+      }
+      fence_async_proxy();
+      __syncwarp();
+    };
+    uint4 rk[N], rv[N];
+    const Place now = take();
+    Place next = now;
+    Pages py = look_up(now), ny = py;
+    load(kc, now, py, rk);
+    load(vc, now, py, rv);
+    if (lo + 1 < hi) {
+      next = take();
+      ny = look_up(next);
+    }
+    const int64_t n = hi - lo;
+    for (int64_t g = 0; g < n; ++g) {
+      const int s = (int)(g & 1);
+      const uint32_t again = (uint32_t)((g >> 1) & 1) ^ 1u;
+      if (g >= STAGES && !__all_sync(FULL, wait(&k_free[s], again))) break;
+      if (warp == CONVERT_WARP) {
+        TileInfo &t = info[g & (INFOS - 1)];
+        const unsigned bad = __ballot_sync(FULL, lane < GROUPS && py.page < 0);
+        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.lv));
+        if (lane == 0) t.bad = bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&info_full[g & (INFOS - 1)]);
+      }
+      convert(smem + M::k + s * M::kv_bytes, rk);
+      if (lane == 0) mbar_arrive(&k_full[s]);
+      if (g + 1 < n) load(kc, next, ny, rk);
+      if (g >= STAGES && !__all_sync(FULL, wait(&v_free[s], again))) break;
+      convert(smem + M::v + s * M::kv_bytes, rv);
+      if (lane == 0) mbar_arrive(&v_full[s]);
+      if (g + 1 < n) load(vc, next, ny, rv);
+      py = ny;
+      if (g + 2 < n) {
+        next = take();
+        ny = look_up(next);
+      }
+    }
+  } else if (work && warp == ISSUE_WARP) {
+    if (lane == 0) {
+      constexpr uint32_t is = instruction(TILE, false), io = instruction(D, true);
+      auto scores = [&](int w, int s) {
+        const unsigned char *q = smem + M::q + w * M::q_bytes, *k = smem + M::k + s * M::kv_bytes;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          mma_ss(tmem + 128 * w, operand(q + (i / 4) * (128 * 128) + (i % 4) * 32, 16),
+                 operand(k + (i / 4) * (TILE * 128) + (i % 4) * 32, 16), is, i > 0);
+        tc_commit(&s_full[w]);
+      };
+      Cursor cur = cursor_at(a, prefix, group, lo);
+      int64_t g = 0;  // tiles of the stretch begun
+      int segment = 0;
+      bool ok = true;
+      while (ok && lo + g < hi) {
+        const int count = (int)min((int64_t)(cur.tiles - cur.tile), hi - lo - g);
+        ok = wait(&k_full[g & 1], (uint32_t)((g >> 1) & 1));
+        for (int w = 0; w < 2 && ok; ++w) {
+          ok = wait(&q_full[w], (uint32_t)(segment & 1));
+          tc_fence_after();
+          if (ok) scores(w, (int)(g & 1));
+        }
+        if (ok) tc_commit(&k_free[g & 1]);
+        for (int j = 0; j < count && ok; ++j, ++g) {
+          const int s = (int)(g & 1);
+          const bool more = j + 1 < count;
+          for (int w = 0; w < 2 && ok; ++w) {
+            ok = wait(&p_full[w], (uint32_t)(g & 1)) && wait(&v_full[s], (uint32_t)((g >> 1) & 1));
+            if (ok && more) ok = wait(&k_full[(g + 1) & 1], (uint32_t)(((g + 1) >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < TILE / 16; ++i)
+              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i,
+                     operand(smem + M::v + s * M::kv_bytes + i * 2048, TILE * 128), io, j > 0 || i > 0);
+            tc_commit(&o_done[w]);
+            if (w == 1) tc_commit(&v_free[s]);
+            if (more) {
+              scores(w, (int)((g + 1) & 1));
+              if (w == 1) tc_commit(&k_free[(g + 1) & 1]);
+            }
+          }
+        }
+        ++segment;
+        if (ok && lo + g < hi) next_segment(a, prefix, group, cur);
+      }
+      // nothing may be left running when this CTA gives its memory back
+      tc_commit(last_bar);
+      mbar_wait(last_bar, 0, nullptr, a.wait_ns);
+    }
+    __syncwarp();
+  } else if (work && warp < CONVERT_WARP) {
+    // ---- one thread to a row
+    const int w = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+    const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
+    unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
+    Cursor cur = cursor_at(a, prefix, group, lo);
+    int64_t x = lo;
+    bool ok = true;
+    while (ok && x < hi) {
+      const int tile0 = cur.tile, count = (int)min((int64_t)(cur.tiles - tile0), hi - x);
+      const Sequence sq = cur.seq;
+      const int r0 = cur.block * MB, r = w * 128 + row, rr = r0 + r;
+      const int rows = min(MB, sq.n * group - r0);
+      const bool live = r < rows;
+      const int64_t q_row = sq.row0 + rr / group;
+      const int q_head = cur.head * group + rr % group;
+      // the row in fp16, brought to a largest magnitude in [1, 2) by a power of two (bf16);
+      // the sign of the scale goes with it, so that factors of scores are never negative
+      float rowc = 0.0f;
+      {
+        const char *src = static_cast<const char *>(a.q.q) + 2 * (q_row * a.q.q_row_stride +
+                                                                  q_head * a.q.q_head_stride);
+        Raw16<DT> y[D / 16];
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          y[i].clear();
+          if (live) y[i].load(src + 32 * i);
+        }
+        float up = a.q.scale < 0.0f ? -1.0f : 1.0f, down = 1.0f;
+        if constexpr (DT == IBP_BF16) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) most = y[i].largest(most);
+          const int e = min(max((int)(Raw16<DT>::fold(most) >> 7) - 127, -120), 120);
+          up *= __uint_as_float((uint32_t)(127 - e) << 23);
+          down = __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+        rowc = down * (fabsf(a.q.scale) * LOG2E);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float f[4];
+            y[i].four(k, f);
+            v[2 * k] = pack2<IBP_FP16>(f[0] * up, f[1] * up);
+            v[2 * k + 1] = pack2<IBP_FP16>(f[2] * up, f[3] * up);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = 2 * i + h;
+            *reinterpret_cast<uint4 *>(q_to + (at / 8) * (128 * 128) + ((at ^ row) & 7) * 16) =
+                make_uint4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+          }
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[w]);
+      }
+      const int limit = live ? max(sq.len - sq.n + rr / group + 1, 0) : 0x7FFFFFFF;
+      float m = NONE, mv = NONE;
+      uint64_t l = 0;  // two halves of the sum
+      for (int j = 0; j < count; ++j) {
+        const int64_t g = x - lo + j;
+        ok = __all_sync(FULL, wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1)) &&
+                                  wait(&s_full[w], (uint32_t)(g & 1)));
+        if (!ok) break;
+        tc_fence_after();
+        const TileInfo &t = info[g & (INFOS - 1)];
+        const int seen = limit - (tile0 + j) * TILE;  // columns this row sees
+        const bool whole = __all_sync(FULL, seen >= TILE && t.bad == 0);
+        uint32_t s[32];
+        // the largest score, and the largest with its value scale
+        float mn = m, mvn = mv;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          tmem_load(sp + 32 * q4, s);
+          tmem_wait_load(s);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int gi = 2 * q4 + h;
+            const float2 sc = t.scale[gi];
+            float top = -INFINITY;
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(s[16 * h + e]));
+            } else {
+              const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                top = e < n ? fmaxf(top, __uint_as_float(s[16 * h + e])) : top;
+              if (n <= 0) continue;
+            }
+            top *= rowc * sc.x;
+            mn = fmaxf(mn, top);
+            mvn = fmaxf(mvn, top + sc.y);
+          }
+        }
+        if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
+          const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
+          m = mn;
+          mv = mvn;
+          l = mul2(l, pair(fl, fl));
+          if (j > 0) {
+            ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)((g - 1) & 1)));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              tmem_load(op + 32 * q4, s);
+              tmem_wait_load(s);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * fo);
+              tmem_store16(op + 32 * q4, s);
+              tmem_store16(op + 32 * q4 + 16, s + 16);
+            }
+            tmem_wait_store();
+          }
+        }
+        const uint64_t minus = pair(-m, -m);
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          tmem_load(sp + 32 * q4, s);
+          tmem_wait_load(s);
+          uint32_t p[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int gi = 2 * q4 + h;
+            const float2 sc = t.scale[gi];
+            const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
+            const uint64_t ff = pair(f, f), gg = pair(gv, gv);
+            const int n = whole ? 16 : (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint64_t y = fma2(pair(__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1])),
+                                      ff, minus);
+              float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+              if (!whole) {
+                p0 = e < n ? p0 : 0.0f;
+                p1 = e + 1 < n ? p1 : 0.0f;
+              }
+              const uint64_t pp = pair(p0, p1);
+              l = add2(l, pp);
+              const uint64_t pw = mul2(pp, gg);
+              p[8 * h + e / 2] = pack2<IBP_FP16>(low(pw), high(pw));
+            }
+          }
+          tmem_store16(sp + 16 * q4, p);  // over columns that have been read
+        }
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      if (!ok) break;
+      // ---- finish the segment, or leave a part
+      const int64_t g = x - lo + count - 1;
+      ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)(g & 1)));
+      if (!ok) break;
+      tc_fence_after();
+      const float sum = low(l) + high(l);
+      const bool done = tile0 == 0 && count == cur.tiles;
+      float *part = a.part + ((int64_t)cta * 2 + (x == lo ? 0 : 1)) * ((int64_t)MB * (D + 4));
+      const float f = !done ? 1.0f : sum > 0.0f ? exp2_fast(mv - m) / sum : 0.0f;
+      char *out = static_cast<char *>(a.q.out) + 2 * (q_row * a.q.out_row_stride + q_head * a.q.out_head_stride);
+#pragma unroll
+      for (int q4 = 0; q4 < D / 32; ++q4) {
+        uint32_t s[32];
+        tmem_load(op + 32 * q4, s);
+        tmem_wait_load(s);
+        if (!live) continue;
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(s[e]) * f;
+        if (done) {
+          store16<DT>(out + 64 * q4, y);
+          store16<DT>(out + 64 * q4 + 32, y + 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(part + r * D + 32 * q4 + e) =
+                make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        }
+      }
+      tc_fence_before();
+      if (live) {
+        if (done) {
+          if (a.q.d_lse)
+            a.q.d_lse[q_row * a.q.q_heads + q_head] = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
+        } else {
+          reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(m, mv, sum, 0.0f);
+        }
+      }
+      x += count;
+      if (x < hi) next_segment(a, prefix, group, cur);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == ISSUE_WARP) tmem_free(tmem);
+}
+
+template <int D, int CODE, int DT>
+int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
+  const auto kernel = kv_prefill_kernel<D, CODE, DT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Memory<D>::bytes) !=
+      cudaSuccess)
+    return IBP_ERR_CUDA;
+  const int group = a.q.q_heads / a.c.n_heads;
+  const int64_t blocks = (a.q.max_q * group + MB - 1) / MB;
+  a.ctas = std::min(dev.sm_count, MAX_PREFILL_CTAS);
+  kernel<<<a.ctas, THREADS, Memory<D>::bytes, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+  return launch_dependent(kv_finish_kernel<D, DT, Plan, false>,
+                          dim3((unsigned)blocks, (unsigned)a.c.n_heads, (unsigned)a.batch),
+                          dim3(FINISH_THREADS), 0, s, a, (int)blocks) == cudaSuccess
+             ? IBP_OK
+             : IBP_ERR_CUDA;
+}
+
+template <int D>
+int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (a.c.code == IBP_KV_INT8)
+    return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_INT8, IBP_BF16>(a, dev, s)
+                                 : launch_for<D, IBP_KV_INT8, IBP_FP16>(a, dev, s);
+  return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_E4M3, IBP_BF16>(a, dev, s)
+                               : launch_for<D, IBP_KV_E4M3, IBP_FP16>(a, dev, s);
+}
+
+}  // namespace
+
+size_t kv_prefill_scratch_bytes(const ibp_kv_cache &c) {
+  return (size_t)MAX_PREFILL_CTAS * 2 * MB * (c.head_dim + 4) * sizeof(float);
+}
+
+int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
+                      int32_t *d_status, cudaStream_t s) {
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  AttentionArgs a = {};
+  a.c = c;
+  a.q = q;
+  a.status = d_status;
+  a.wait_ns = gather_wait_limit_ns();
+  a.part = static_cast<float *>(d_scratch);
+  for (a.b0 = 0; a.b0 < c.batch; a.b0 += MAX_BATCH) {
+    a.batch = std::min(c.batch - a.b0, MAX_BATCH);
+    if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
+      return rc;
+  }
+  return IBP_OK;
+}
+
+}  // namespace ibp
