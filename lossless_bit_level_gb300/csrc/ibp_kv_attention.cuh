@@ -186,6 +186,9 @@ __device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &
 
 constexpr int FINISH_THREADS = 128;
 constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
+// CTAs that share a segment's rows, 64 at most to one.
+template <typename Plan>
+constexpr int FINISH_SHARE = Plan::MB <= 64 ? 1 : Plan::MB / 64;
 
 // Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
 // sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
@@ -222,17 +225,19 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
   }
   __syncthreads();
   if ((int)blockIdx.x < row_blocks) {
-    const int r0 = blockIdx.x * MB, rows = min(MB, all - r0);
-    if (rows <= 0) return;
-    const int tiles = plan.tiles(blockIdx.x);
+    constexpr int SHARE = FINISH_SHARE<Plan>;
+    const int block = blockIdx.x / SHARE, r0 = block * MB;
+    const int from = blockIdx.x % SHARE * (MB / SHARE), rows = min(from + MB / SHARE, all - r0);
+    if (rows <= from) return;
+    const int tiles = plan.tiles(block);
     Parts p = {Split(1, 1), 0, 0, 0};
     if (tiles > 0) {
-      p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(blockIdx.x),
+      p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
                    tiles, a.ctas);
       if (p.first == p.last) return;
     }
     grid_dependency_wait();
-    for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
+    for (int u = threadIdx.x + from * (D / 4); u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
       const int64_t row = s.row0 + rr / group;
       const int qh = head * group + rr % group;

@@ -129,6 +129,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
 __device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
 
@@ -498,9 +503,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const int seen = limit - (tile0 + j) * TILE;  // columns this row sees
         const bool whole = __all_sync(FULL, seen >= TILE && t.bad == 0);
         uint32_t s[32];
-        // the largest score, and the largest with its value scale
-        float mn = m, mvn = mv;
-#pragma unroll
+        // the largest score, the largest with its value scale, the least value scale
+        float mn = m, mvn = mv, lv_least = INFINITY;
+#pragma unroll 1
         for (int q4 = 0; q4 < 4; ++q4) {
           tmem_load(sp + 32 * q4, s);
           tmem_wait_load(s);
@@ -508,20 +513,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           for (int h = 0; h < 2; ++h) {
             const int gi = 2 * q4 + h;
             const float2 sc = t.scale[gi];
-            float top = -INFINITY;
-            if (whole) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(s[16 * h + e]));
-            } else {
+            if (!whole) {
               const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                top = e < n ? fmaxf(top, __uint_as_float(s[16 * h + e])) : top;
+                if (e >= n) s[16 * h + e] = 0xFF800000u;
               if (n <= 0) continue;
             }
+            float top = fmaxf(__uint_as_float(s[16 * h]), __uint_as_float(s[16 * h + 1]));
+#pragma unroll
+            for (int e = 2; e < 16; e += 2)
+              top = max3(top, __uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1]));
             top *= rowc * sc.x;
             mn = fmaxf(mn, top);
             mvn = fmaxf(mvn, top + sc.y);
+            lv_least = fminf(lv_least, sc.y);
           }
         }
         if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)((g - 1) & 1)));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int q4 = 0; q4 < D / 32; ++q4) {
               tmem_load(op + 32 * q4, s);
               tmem_wait_load(s);
@@ -545,35 +551,60 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             tmem_wait_store();
           }
         }
-        const uint64_t minus = pair(-m, -m);
+        // A probability with its value scale is 2^(x + lv - mv), and the probability itself
+        // that times 2^(mv - m - lv): one exponential a score, and one a group for the sum.
+        // Where the value scales differ so much that the first could vanish with the second
+        // still counting, or a score is masked, the two are taken the other way round.
+        if (__all_sync(FULL, whole && lv_least + (m - mv) > -60.0f)) {
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            tmem_load(sp + 32 * q4, s);
+            tmem_wait_load(s);
+            uint32_t p[16];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          tmem_load(sp + 32 * q4, s);
-          tmem_wait_load(s);
-          uint32_t p[16];
+            for (int h = 0; h < 2; ++h) {
+              const float2 sc = t.scale[2 * q4 + h];
+              const float f = rowc * sc.x, up = sc.y - mv, back = exp2_fast(-(sc.y + (m - mv)));
+              const uint64_t ff = pair(f, f), uu = pair(up, up);
+              uint64_t sum = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int gi = 2 * q4 + h;
-            const float2 sc = t.scale[gi];
-            const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
-            const uint64_t ff = pair(f, f), gg = pair(gv, gv);
-            const int n = whole ? 16 : (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const uint64_t y = fma2(pair(__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1])),
-                                      ff, minus);
-              float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-              if (!whole) {
-                p0 = e < n ? p0 : 0.0f;
-                p1 = e + 1 < n ? p1 : 0.0f;
+              for (int e = 0; e < 16; e += 2) {
+                const uint64_t y = fma2(
+                    pair(__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1])), ff, uu);
+                const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+                sum = add2(sum, pair(p0, p1));
+                p[8 * h + e / 2] = pack2<IBP_FP16>(p0, p1);
               }
-              const uint64_t pp = pair(p0, p1);
-              l = add2(l, pp);
-              const uint64_t pw = mul2(pp, gg);
-              p[8 * h + e / 2] = pack2<IBP_FP16>(low(pw), high(pw));
+              l = fma2(sum, pair(back, back), l);
             }
+            tmem_store16(sp + 16 * q4, p);  // over columns that have been read
           }
-          tmem_store16(sp + 16 * q4, p);  // over columns that have been read
+        } else {
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            tmem_load(sp + 32 * q4, s);
+            tmem_wait_load(s);
+            uint32_t p[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int gi = 2 * q4 + h;
+              const float2 sc = t.scale[gi];
+              const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
+              const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+              float pw[16], sum = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float y = exp2_fast(fmaf(__uint_as_float(s[16 * h + e]), f, -m));
+                pw[e] = e < n ? y : 0.0f;
+                sum += pw[e];
+              }
+              l = add2(l, pair(sum, 0.0f));
+#pragma unroll
+              for (int e = 0; e < 16; e += 2)
+                p[8 * h + e / 2] = pack2<IBP_FP16>(pw[e] * gv, pw[e + 1] * gv);
+            }
+            tmem_store16(sp + 16 * q4, p);
+          }
         }
         tmem_wait_store();
         tc_fence_before();
@@ -591,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       float *part = a.part + ((int64_t)cta * 2 + (x == lo ? 0 : 1)) * ((int64_t)MB * (D + 4));
       const float f = !done ? 1.0f : sum > 0.0f ? exp2_fast(mv - m) / sum : 0.0f;
       char *out = static_cast<char *>(a.q.out) + 2 * (q_row * a.q.out_row_stride + q_head * a.q.out_head_stride);
-#pragma unroll
+#pragma unroll 1
       for (int q4 = 0; q4 < D / 32; ++q4) {
         uint32_t s[32];
         tmem_load(op + 32 * q4, s);
@@ -641,8 +672,9 @@ int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   kernel<<<a.ctas, THREADS, Memory<D>::bytes, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
   return launch_dependent(kv_finish_kernel<D, DT, Plan, false>,
-                          dim3((unsigned)blocks, (unsigned)a.c.n_heads, (unsigned)a.batch),
-                          dim3(FINISH_THREADS), 0, s, a, (int)blocks) == cudaSuccess
+                          dim3((unsigned)(blocks * FINISH_SHARE<Plan>), (unsigned)a.c.n_heads,
+                               (unsigned)a.batch),
+                          dim3(FINISH_THREADS), 0, s, a, (int)(blocks * FINISH_SHARE<Plan>)) == cudaSuccess
              ? IBP_OK
              : IBP_ERR_CUDA;
 }
