@@ -9,7 +9,8 @@
 // one half, the other half's 128 threads (one to a row) turn scores into probabilities:
 //   warps 0-3, 4-7  rows 0-127 and 128-255: references, exponentials, the final scaling
 //   warps 8-11      fetch codes a tile ahead into registers, convert, store swizzled
-//   warp 12         issues the matrix instructions
+//   warp 12         issues the matrix instructions (13-15 only complete its warpgroup)
+// Registers are handed out to match: a row's 128 scores stay in its thread's.
 // A page's key scale is a factor of its scores, its value scale one of its probabilities.
 #include <algorithm>
 
@@ -24,7 +25,9 @@ constexpr int TILE = 128;    // tokens of a tile
 constexpr int GROUPS = TILE / 16;
 constexpr int STAGES = 2;    // of K and of V
 constexpr int INFOS = 4;     // tiles whose scales are kept
-constexpr int THREADS = 13 * 32;
+constexpr int THREADS = 16 * 32;
+// registers a thread, out of 128 each at launch: 8 * 168 + 4 * 112 + 4 * 64 = 16 * 128 a lane
+constexpr int ROW_REGS = 168, CONVERT_REGS = 112, ISSUE_REGS = 64;
 constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S (and P over it) at 128 w, O at 256 + 128 w
 using Plan = CausalPlan<MB, TILE>;
@@ -93,8 +96,30 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t *x) {
       I8(x, 0), I8(x, 8)
       : "memory");
 }
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t *x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+               I8(x, 0)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
+      : R8(x, 0), R8(x, 8)
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : RW8(x, 0), RW8(x, 8)::"memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Shared-memory operand in 128-byte rows of 64 fp16, swizzled in groups of 8 rows.
@@ -151,12 +176,14 @@ struct Memory {
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, info = v + STAGES * kv_bytes;
   static constexpr int bars = info + INFOS * (int)sizeof(TileInfo);
   static constexpr int prefix = bars + 24 * 8;
-  static constexpr int words = prefix + (MAX_BATCH + 1) * 8;
+  static constexpr int cursors = (prefix + (MAX_BATCH + 1) * 8 + 15) / 16 * 16;
+  static constexpr int words = cursors + 12 * 48;
   static constexpr int bytes = words + 16 + 1024;  // the operands start on 1024 bytes
 };
 
-// Where a stretch stands: the segment of tile x and the tile within it.
-struct Cursor {
+// Where a stretch stands: the segment of tile x and the tile within it. Each warp keeps
+// its own in shared memory, out of the registers of its inner loop.
+struct __align__(16) Cursor {
   int b, head, block, tile, tiles;
   Sequence seq;
 };
@@ -174,6 +201,7 @@ __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_
   c.tiles = plan.tiles(c.block);
   return c;
 }
+static_assert(sizeof(Cursor) <= 48, "the place kept for it");
 // The first tile of the next segment that has one (there is one: the caller's x < total).
 __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64_t *prefix, int group,
                                              Cursor &c) {
@@ -213,7 +241,10 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
 template <int D, int CODE, int DT>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ AttentionArgs a) {
   using M = Memory<D>;
-  constexpr int BLOCKS = D / 64;  // of 64 elements
+  static_assert(M::info % alignof(TileInfo) == 0 && M::bars % 8 == 0 && M::prefix % 8 == 0 &&
+                    M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0,
+                "what lies in shared memory is aligned");
+
   extern __shared__ unsigned char raw_smem[];
   unsigned char *smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
@@ -279,7 +310,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     return false;
   };
 
-  if (work && warp >= CONVERT_WARP && warp < ISSUE_WARP) {
+  if (warp >= CONVERT_WARP && warp < ISSUE_WARP) {
+    fewer_registers<CONVERT_REGS>();
+    if (work) {
     // ---- codes to fp16: thread i of 128 takes the 16 elements PER * i of every STEP-th token
     constexpr int PER = D / 16, STEP = 128 / PER, N = TILE / STEP;  // 8, 16, 8 or 4, 32, 4
     const int tid = threadIdx.x - CONVERT_WARP * 32, key0 = tid / PER, piece = tid % PER;
@@ -287,28 +320,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     struct Place {
       int b, head, t0, len;
     };
-    Cursor cur = cursor_at(a, prefix, group, lo);
-    int64_t ahead = lo;  // the tile `cur` stands at
+    Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;  // one for all lanes
+    if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+    __syncwarp();
+    const int n = (int)(hi - lo);
+    int ahead = 0;  // tiles of the stretch taken
     auto take = [&] {
-      const Place p = {cur.b, cur.head, cur.tile * TILE, cur.seq.len};
+      const Place p = {cur->b, cur->head, cur->tile * TILE, cur->seq.len};
       ++ahead;
-      if (++cur.tile == cur.tiles && ahead < hi) next_segment(a, prefix, group, cur);
+      __syncwarp();
+      if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment(a, prefix, group, *cur);
+      __syncwarp();
       return p;
     };
-    // lane g < 8 looks up the page of tokens 16 g ..
+    // Lane g < 8 looks up the page of tokens 16 g .. : its id is asked for two tiles before
+    // its codes, its scales one tile before.
     struct Pages {
       int page;
-      float ks, lv;
+      float ks, vs;
     };
-    auto look_up = [&](const Place &p) {
-      Pages y = {-1, 0.0f, 0.0f};
+    auto ask = [&](const Place &p) {
       const int t = p.t0 + (lane & 7) * 16;
-      if (t < p.len) {
-        y.page = kv_page(c, a.b0 + p.b, t / c.page_tokens, a.status);
-        if (y.page >= 0) {
-          const int64_t at = (int64_t)y.page * c.n_heads + p.head;
+      return t < p.len ? __ldg(c.d_table + (int64_t)(a.b0 + p.b) * c.table_stride + t / c.page_tokens) : -1;
+    };
+    auto look_up = [&](const Place &p, int page) {
+      Pages y = {-1, 0.0f, 0.0f};
+      if (p.t0 + (lane & 7) * 16 < p.len) {
+        if (page >= 0 && page < c.n_pages) {
+          const int64_t at = (int64_t)page * c.n_heads + p.head;
+          y.page = page;
           y.ks = __ldg(c.k_scales + at);
-          y.lv = __ldg(c.v_scales + at);
+          y.vs = __ldg(c.v_scales + at);
+        } else {
+          report(a.status, IBP_ERR_INDEX);
         }
       }
       return y;
@@ -344,23 +388,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     };
     uint4 rk[N], rv[N];
     const Place now = take();
-    Place next = now;
-    Pages py = look_up(now), ny = py;
+    Place next = now, after = now;  // of tiles g + 1 and g + 2
+    Pages py = look_up(now, ask(now)), ny = py;
     load(kc, now, py, rk);
     load(vc, now, py, rv);
-    if (lo + 1 < hi) {
+    int asked = -1;
+    if (n > 1) {
       next = take();
-      ny = look_up(next);
+      ny = look_up(next, ask(next));
     }
-    const int64_t n = hi - lo;
-    for (int64_t g = 0; g < n; ++g) {
-      const int s = (int)(g & 1);
+    if (n > 2) {
+      after = take();
+      asked = ask(after);
+    }
+    for (int g = 0; g < n; ++g) {
+      const int s = g & 1;
       const uint32_t again = (uint32_t)((g >> 1) & 1) ^ 1u;
       if (g >= STAGES && !__all_sync(FULL, wait(&k_free[s], again))) break;
       if (warp == CONVERT_WARP) {
         TileInfo &t = info[g & (INFOS - 1)];
         const unsigned bad = __ballot_sync(FULL, lane < GROUPS && py.page < 0);
-        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.lv));
+        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.vs));
         if (lane == 0) t.bad = bad;
         __syncwarp();
         if (lane == 0) mbar_arrive(&info_full[g & (INFOS - 1)]);
@@ -373,13 +421,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       if (lane == 0) mbar_arrive(&v_full[s]);
       if (g + 1 < n) load(vc, next, ny, rv);
       py = ny;
-      if (g + 2 < n) {
-        next = take();
-        ny = look_up(next);
+      next = after;
+      if (g + 2 < n) ny = look_up(next, asked);
+      if (g + 3 < n) {
+        after = take();
+        asked = ask(after);
       }
     }
-  } else if (work && warp == ISSUE_WARP) {
-    if (lane == 0) {
+    }
+  } else if (warp >= ISSUE_WARP) {
+    fewer_registers<ISSUE_REGS>();
+    if (work && warp == ISSUE_WARP && lane == 0) {
       constexpr uint32_t is = instruction(TILE, false), io = instruction(D, true);
       auto scores = [&](int w, int s) {
         const unsigned char *q = smem + M::q + w * M::q_bytes, *k = smem + M::k + s * M::kv_bytes;
@@ -430,29 +482,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_wait(last_bar, 0, nullptr, a.wait_ns);
     }
     __syncwarp();
-  } else if (work && warp < CONVERT_WARP) {
+  } else {
+    more_registers<ROW_REGS>();
+    if (work) {
     // ---- one thread to a row
     const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
     unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
-    Cursor cur = cursor_at(a, prefix, group, lo);
-    int64_t x = lo;
+    Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
+    if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+    __syncwarp();
+    const int n_tiles = (int)(hi - lo), r = w * 128 + row;
+    int x = 0;  // tiles of the stretch done
     bool ok = true;
-    while (ok && x < hi) {
-      const int tile0 = cur.tile, count = (int)min((int64_t)(cur.tiles - tile0), hi - x);
-      const Sequence sq = cur.seq;
-      const int r0 = cur.block * MB, r = w * 128 + row, rr = r0 + r;
-      const int rows = min(MB, sq.n * group - r0);
-      const bool live = r < rows;
-      const int64_t q_row = sq.row0 + rr / group;
-      const int q_head = cur.head * group + rr % group;
+    while (ok && x < n_tiles) {
+      const int tile0 = cur->tile, count = min(cur->tiles - tile0, n_tiles - x);
+      const bool live = cur->block * MB + r < cur->seq.n * group;
+      const int rr = cur->block * MB + r;
       // the row in fp16, brought to a largest magnitude in [1, 2) by a power of two (bf16);
       // the sign of the scale goes with it, so that factors of scores are never negative
       float rowc = 0.0f;
       {
-        const char *src = static_cast<const char *>(a.q.q) + 2 * (q_row * a.q.q_row_stride +
-                                                                  q_head * a.q.q_head_stride);
+        const char *src = static_cast<const char *>(a.q.q) +
+                          2 * ((cur->seq.row0 + rr / group) * a.q.q_row_stride +
+                               (cur->head * group + rr % group) * a.q.q_head_stride);
         Raw16<DT> y[D / 16];
         uint32_t most = 0;
 #pragma unroll
@@ -490,11 +544,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[w]);
       }
-      const int limit = live ? max(sq.len - sq.n + rr / group + 1, 0) : 0x7FFFFFFF;
+      const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
       float m = NONE, mv = NONE;
       uint64_t l = 0;  // two halves of the sum
       for (int j = 0; j < count; ++j) {
-        const int64_t g = x - lo + j;
+        const int g = x + j;
         ok = __all_sync(FULL, wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1)) &&
                                   wait(&s_full[w], (uint32_t)(g & 1)));
         if (!ok) break;
@@ -502,33 +556,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const TileInfo &t = info[g & (INFOS - 1)];
         const int seen = limit - (tile0 + j) * TILE;  // columns this row sees
         const bool whole = __all_sync(FULL, seen >= TILE && t.bad == 0);
-        uint32_t s[32];
+        uint32_t s[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_load(sp + 32 * k, s[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_wait_load(s[k]);
         // the largest score, the largest with its value scale, the least value scale
         float mn = m, mvn = mv, lv_least = INFINITY;
-#pragma unroll 1
-        for (int q4 = 0; q4 < 4; ++q4) {
-          tmem_load(sp + 32 * q4, s);
-          tmem_wait_load(s);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int gi = 2 * q4 + h;
-            const float2 sc = t.scale[gi];
-            if (!whole) {
-              const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+        for (int gi = 0; gi < GROUPS; ++gi) {
+          const float2 sc = t.scale[gi];
+          uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
+          if (!whole) {
+            const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e >= n) s[16 * h + e] = 0xFF800000u;
-              if (n <= 0) continue;
-            }
-            float top = fmaxf(__uint_as_float(s[16 * h]), __uint_as_float(s[16 * h + 1]));
-#pragma unroll
-            for (int e = 2; e < 16; e += 2)
-              top = max3(top, __uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1]));
-            top *= rowc * sc.x;
-            mn = fmaxf(mn, top);
-            mvn = fmaxf(mvn, top + sc.y);
-            lv_least = fminf(lv_least, sc.y);
+            for (int e = 0; e < 16; ++e) sg[e] = e < n ? sg[e] : 0xFF800000u;
           }
+          float top = fmaxf(__uint_as_float(sg[0]), __uint_as_float(sg[1]));
+#pragma unroll
+          for (int e = 2; e < 16; e += 2)
+            top = max3(top, __uint_as_float(sg[e]), __uint_as_float(sg[e + 1]));
+          // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
+          top *= rowc * sc.x;
+          mn = fmaxf(mn, top);
+          mvn = fmaxf(mvn, top + sc.y);
+          lv_least = fminf(lv_least, sc.y);
         }
         if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
           const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
@@ -540,13 +592,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int q4 = 0; q4 < D / 32; ++q4) {
-              tmem_load(op + 32 * q4, s);
-              tmem_wait_load(s);
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t y[16];
+              tmem_load16(op + 16 * k, y);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * fo);
-              tmem_store16(op + 32 * q4, s);
-              tmem_store16(op + 32 * q4 + 16, s + 16);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
+              tmem_store16(op + 16 * k, y);
             }
             tmem_wait_store();
           }
@@ -556,54 +607,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         // Where the value scales differ so much that the first could vanish with the second
         // still counting, or a score is masked, the two are taken the other way round.
         if (__all_sync(FULL, whole && lv_least + (m - mv) > -60.0f)) {
-#pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
-            tmem_load(sp + 32 * q4, s);
-            tmem_wait_load(s);
-            uint32_t p[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 sc = t.scale[2 * q4 + h];
-              const float f = rowc * sc.x, up = sc.y - mv, back = exp2_fast(-(sc.y + (m - mv)));
-              const uint64_t ff = pair(f, f), uu = pair(up, up);
-              uint64_t sum = 0;
+          for (int gi = 0; gi < GROUPS; ++gi) {
+            const uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
+            const float2 sc = t.scale[gi];
+            const float f = rowc * sc.x, up = sc.y - mv;
+            const uint64_t ff = pair(f, f), uu = pair(up, up);
+            uint64_t sum = 0;
+            uint32_t p[8];
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint64_t y = fma2(
-                    pair(__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1])), ff, uu);
-                const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-                sum = add2(sum, pair(p0, p1));
-                p[8 * h + e / 2] = pack2<IBP_FP16>(p0, p1);
-              }
-              l = fma2(sum, pair(back, back), l);
+            for (int e = 0; e < 16; e += 2) {
+              const uint64_t y = fma2(pair(__uint_as_float(sg[e]), __uint_as_float(sg[e + 1])), ff, uu);
+              const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+              sum = add2(sum, pair(p0, p1));
+              p[e / 2] = pack2<IBP_FP16>(p0, p1);
             }
-            tmem_store16(sp + 16 * q4, p);  // over columns that have been read
+            const float back = exp2_fast(-(sc.y + (m - mv)));
+            l = fma2(sum, pair(back, back), l);
+            tmem_store8(sp + 8 * gi, p);  // over columns that have been read
           }
         } else {
-#pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
-            tmem_load(sp + 32 * q4, s);
-            tmem_wait_load(s);
-            uint32_t p[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int gi = 2 * q4 + h;
-              const float2 sc = t.scale[gi];
-              const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
-              const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
-              float pw[16], sum = 0.0f;
+          for (int gi = 0; gi < GROUPS; ++gi) {
+            const uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
+            const float2 sc = t.scale[gi];
+            const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
+            const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+            float sum = 0.0f;
+            uint32_t p[8];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y = exp2_fast(fmaf(__uint_as_float(s[16 * h + e]), f, -m));
-                pw[e] = e < n ? y : 0.0f;
-                sum += pw[e];
-              }
-              l = add2(l, pair(sum, 0.0f));
-#pragma unroll
-              for (int e = 0; e < 16; e += 2)
-                p[8 * h + e / 2] = pack2<IBP_FP16>(pw[e] * gv, pw[e + 1] * gv);
+            for (int e = 0; e < 16; e += 2) {
+              float p0 = exp2_fast(fmaf(__uint_as_float(sg[e]), f, -m));
+              float p1 = exp2_fast(fmaf(__uint_as_float(sg[e + 1]), f, -m));
+              p0 = e < n ? p0 : 0.0f;
+              p1 = e + 1 < n ? p1 : 0.0f;
+              sum += p0 + p1;
+              p[e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
             }
-            tmem_store16(sp + 16 * q4, p);
+            l = add2(l, pair(sum, 0.0f));
+            tmem_store8(sp + 8 * gi, p);
           }
         }
         tmem_wait_store();
@@ -613,13 +655,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
       if (!ok) break;
       // ---- finish the segment, or leave a part
-      const int64_t g = x - lo + count - 1;
+      const int g = x + count - 1;
       ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)(g & 1)));
       if (!ok) break;
       tc_fence_after();
       const float sum = low(l) + high(l);
-      const bool done = tile0 == 0 && count == cur.tiles;
-      float *part = a.part + ((int64_t)cta * 2 + (x == lo ? 0 : 1)) * ((int64_t)MB * (D + 4));
+      const bool done = tile0 == 0 && count == cur->tiles;
+      const int64_t q_row = cur->seq.row0 + rr / group;
+      const int q_head = cur->head * group + rr % group;
+      float *part = a.part + ((int64_t)cta * 2 + (x == 0 ? 0 : 1)) * ((int64_t)MB * (D + 4));
       const float f = !done ? 1.0f : sum > 0.0f ? exp2_fast(mv - m) / sum : 0.0f;
       char *out = static_cast<char *>(a.q.out) + 2 * (q_row * a.q.out_row_stride + q_head * a.q.out_head_stride);
 #pragma unroll 1
@@ -651,7 +695,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
       }
       x += count;
-      if (x < hi) next_segment(a, prefix, group, cur);
+      __syncwarp();
+      if (lane == 0 && x < n_tiles) next_segment(a, prefix, group, *cur);
+      __syncwarp();
+    }
     }
   }
   tc_fence_before();
@@ -665,6 +712,12 @@ int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   const auto kernel = kv_prefill_kernel<D, CODE, DT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Memory<D>::bytes) !=
       cudaSuccess)
+    return IBP_ERR_CUDA;
+  // a warp that asks for more registers waits until others have given them up: they must
+  // be there
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+      16 * attr.numRegs < 8 * ROW_REGS + 4 * CONVERT_REGS + 4 * ISSUE_REGS)
     return IBP_ERR_CUDA;
   const int group = a.q.q_heads / a.c.n_heads;
   const int64_t blocks = (a.q.max_q * group + MB - 1) / MB;
