@@ -8,7 +8,7 @@
 // accumulate in tensor memory, P returns there as fp16. While the matrix unit works on
 // one half, the other half's 128 threads (one to a row) turn scores into probabilities:
 //   warps 0-3, 4-7  rows 0-127 and 128-255: references, exponentials, the final scaling
-//   warps 8-11      fetch codes a tile ahead into registers, convert, store swizzled
+//   warps 8-11      fetch codes a tile ahead, convert, store swizzled
 //   warp 12         issues the matrix instructions (13-15 only complete its warpgroup)
 // Registers are handed out to match: a row's 128 scores stay in its thread's.
 // A page's key scale is a factor of its scores, its value scale one of its probabilities.
@@ -25,9 +25,10 @@ constexpr int TILE = 128;    // tokens of a tile
 constexpr int GROUPS = TILE / 16;
 constexpr int STAGES = 2;    // of K and of V
 constexpr int INFOS = 4;     // tiles whose scales are kept
+constexpr int BATCH = 128;   // sequences of one launch
 constexpr int THREADS = 16 * 32;
-// registers a thread, out of 128 each at launch: 8 * 168 + 4 * 112 + 4 * 64 = 16 * 128 a lane
-constexpr int ROW_REGS = 168, CONVERT_REGS = 112, ISSUE_REGS = 64;
+// registers a thread, out of 128 each at launch: 8 * 168 + 4 * 88 + 4 * 88 = 16 * 128 a lane
+constexpr int ROW_REGS = 168, CONVERT_REGS = 88, ISSUE_REGS = 88;
 constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S (and P over it) at 128 w, O at 256 + 128 w
 using Plan = CausalPlan<MB, TILE>;
@@ -126,9 +127,13 @@ __device__ __forceinline__ void fewer_registers() {
 // K-major (the summed index along the row): groups of 8 rows 1024 bytes apart. MN-major
 // (the summed index down the rows): the same 1024 bytes between groups of 8 of the summed
 // index, `block` bytes between blocks of 64 of the other.
-__device__ __forceinline__ uint64_t operand(const void *p, uint32_t block) {
-  return (uint64_t)((smem_u32(p) & 0x3FFFF) >> 4) | ((uint64_t)(block >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// (The descriptor's upper half is the same for all; `offset` bytes are added to the start.)
+__device__ __forceinline__ uint32_t operand(const void *p, uint32_t block) {
+  return (smem_u32(p) >> 4) | ((block >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t operand_at(uint32_t base, uint32_t offset) {
+  constexpr uint32_t upper = (1024 >> 4) | (1u << 14) | (2u << 29);
+  return ((uint64_t)upper << 32) | (base + (offset >> 4));
 }
 // fp16 operands, fp32 accumulators, 128 rows, n columns; vt: the second operand MN-major.
 __host__ __device__ constexpr uint32_t instruction(int n, bool vt) {
@@ -173,12 +178,13 @@ struct TileInfo {
 template <int D>
 struct Memory {
   static constexpr int q_bytes = 128 * D * 2, kv_bytes = TILE * D * 2;
-  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, info = v + STAGES * kv_bytes;
-  static constexpr int bars = info + INFOS * (int)sizeof(TileInfo);
+  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + STAGES * kv_bytes,
+                       raw_v = raw_k + TILE * D;
+  static constexpr int info = raw_v + TILE * D, bars = info + INFOS * (int)sizeof(TileInfo);
   static constexpr int prefix = bars + 24 * 8;
-  static constexpr int cursors = (prefix + (MAX_BATCH + 1) * 8 + 15) / 16 * 16;
+  static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 12 * 48;
-  static constexpr int bytes = words + 16 + 1024;  // the operands start on 1024 bytes
+  static constexpr int bytes = words + 16;
 };
 
 // Where a stretch stands: the segment of tile x and the tile within it. Each warp keeps
@@ -244,9 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   static_assert(M::info % alignof(TileInfo) == 0 && M::bars % 8 == 0 && M::prefix % 8 == 0 &&
                     M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0,
                 "what lies in shared memory is aligned");
-
-  extern __shared__ unsigned char raw_smem[];
-  unsigned char *smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem[];
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
   uint64_t *k_full = bars, *k_free = bars + 2, *v_full = bars + 4, *v_free = bars + 6, *s_full = bars + 8,
@@ -260,6 +264,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads;
   grid_launch_dependents();
+  if (smem_u32(smem) & 1023) {  // the operands' rows would be swizzled otherwise than written
+    report(a.status, IBP_ERR_CUDA);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
@@ -357,24 +365,30 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
       return y;
     };
-    auto load = [&](const char *codes, const Place &p, const Pages &y, uint4 (&w)[N]) {
-#pragma unroll
+    // Codes go through a place of the thread's own in shared memory, so that no other
+    // thread is waited for and the loops stay short.
+    auto fetch = [&](unsigned char *raw, const char *codes, const Place &p, const Pages &y) {
+#pragma unroll 2
       for (int i = 0; i < N; ++i) {
         const int key = key0 + i * STEP, t = p.t0 + key;
         const int page = __shfl_sync(FULL, y.page, key / 16);
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (page >= 0 && t < p.len)
-          w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + kv_tile(c, page, p.head) +
-                                                       (t & (c.page_tokens - 1)) * D + piece * 16));
+        const bool there = page >= 0 && t < p.len;
+        const char *from = codes;
+        if (there) from += kv_tile(c, page, p.head) + (t & (c.page_tokens - 1)) * D + piece * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(raw + (i * 128 + tid) * 16)),
+                     "l"(from), "r"(there ? 16 : 0)  // zeros where nothing is held
+                     : "memory");
       }
+      cp_async_commit();
     };
     // rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a row exclusive-
     // or'ed with its number
-    auto convert = [&](unsigned char *to, const uint4 (&w)[N]) {
-#pragma unroll
+    auto convert = [&](unsigned char *to, const unsigned char *raw) {
+#pragma unroll 2
       for (int i = 0; i < N; ++i) {
         const int key = key0 + i * STEP;
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const uint4 w = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int at = 2 * piece + h;
@@ -386,12 +400,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       fence_async_proxy();
       __syncwarp();
     };
-    uint4 rk[N], rv[N];
     const Place now = take();
     Place next = now, after = now;  // of tiles g + 1 and g + 2
     Pages py = look_up(now, ask(now)), ny = py;
-    load(kc, now, py, rk);
-    load(vc, now, py, rv);
+    fetch(smem + M::raw_k, kc, now, py);
+    fetch(smem + M::raw_v, vc, now, py);
     int asked = -1;
     if (n > 1) {
       next = take();
@@ -413,13 +426,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(&info_full[g & (INFOS - 1)]);
       }
-      convert(smem + M::k + s * M::kv_bytes, rk);
+      cp_async_wait<1>();  // this tile's K
+      convert(smem + M::k + s * M::kv_bytes, smem + M::raw_k);
       if (lane == 0) mbar_arrive(&k_full[s]);
-      if (g + 1 < n) load(kc, next, ny, rk);
+      if (g + 1 < n) fetch(smem + M::raw_k, kc, next, ny); else cp_async_commit();
       if (g >= STAGES && !__all_sync(FULL, wait(&v_free[s], again))) break;
-      convert(smem + M::v + s * M::kv_bytes, rv);
+      cp_async_wait<1>();  // this tile's V
+      convert(smem + M::v + s * M::kv_bytes, smem + M::raw_v);
       if (lane == 0) mbar_arrive(&v_full[s]);
-      if (g + 1 < n) load(vc, next, ny, rv);
+      if (g + 1 < n) fetch(smem + M::raw_v, vc, next, ny); else cp_async_commit();
       py = ny;
       next = after;
       if (g + 2 < n) ny = look_up(next, asked);
@@ -428,17 +443,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         asked = ask(after);
       }
     }
+    cp_async_wait<0>();
     }
   } else if (warp >= ISSUE_WARP) {
     fewer_registers<ISSUE_REGS>();
     if (work && warp == ISSUE_WARP && lane == 0) {
       constexpr uint32_t is = instruction(TILE, false), io = instruction(D, true);
+      const uint32_t q_at = operand(smem + M::q, 16), k_at = operand(smem + M::k, 16),
+                     v_at = operand(smem + M::v, TILE * 128);
       auto scores = [&](int w, int s) {
-        const unsigned char *q = smem + M::q + w * M::q_bytes, *k = smem + M::k + s * M::kv_bytes;
+        const uint32_t q = q_at + w * (M::q_bytes >> 4), k = k_at + s * (M::kv_bytes >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + 128 * w, operand(q + (i / 4) * (128 * 128) + (i % 4) * 32, 16),
-                 operand(k + (i / 4) * (TILE * 128) + (i % 4) * 32, 16), is, i > 0);
+          mma_ss(tmem + 128 * w, operand_at(q, (i / 4) * (128 * 128) + (i % 4) * 32),
+                 operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0);
         tc_commit(&s_full[w]);
       };
       Cursor cur = cursor_at(a, prefix, group, lo);
@@ -458,14 +476,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           const int s = (int)(g & 1);
           const bool more = j + 1 < count;
           for (int w = 0; w < 2 && ok; ++w) {
-            ok = wait(&p_full[w], (uint32_t)(g & 1)) && wait(&v_full[s], (uint32_t)((g >> 1) & 1));
-            if (ok && more) ok = wait(&k_full[(g + 1) & 1], (uint32_t)(((g + 1) >> 1) & 1));
+            // what is there earliest first: a wait on a full barrier takes its time too
+            if (w == 0) {
+              ok = wait(&v_full[s], (uint32_t)((g >> 1) & 1));
+              if (ok && more) ok = wait(&k_full[(g + 1) & 1], (uint32_t)(((g + 1) >> 1) & 1));
+            }
+            ok = ok && wait(&p_full[w], (uint32_t)(g & 1));
             if (!ok) break;
             tc_fence_after();
+            const uint32_t v = v_at + s * (M::kv_bytes >> 4);
 #pragma unroll
             for (int i = 0; i < TILE / 16; ++i)
-              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i,
-                     operand(smem + M::v + s * M::kv_bytes + i * 2048, TILE * 128), io, j > 0 || i > 0);
+              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i, operand_at(v, i * 2048), io,
+                     j > 0 || i > 0);
             tc_commit(&o_done[w]);
             if (w == 1) tc_commit(&v_free[s]);
             if (more) {
@@ -757,8 +780,8 @@ int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scra
   a.status = d_status;
   a.wait_ns = gather_wait_limit_ns();
   a.part = static_cast<float *>(d_scratch);
-  for (a.b0 = 0; a.b0 < c.batch; a.b0 += MAX_BATCH) {
-    a.batch = std::min(c.batch - a.b0, MAX_BATCH);
+  for (a.b0 = 0; a.b0 < c.batch; a.b0 += BATCH) {
+    a.batch = std::min(c.batch - a.b0, BATCH);
     if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
       return rc;
   }
