@@ -8,8 +8,10 @@
 // accumulate in tensor memory, P returns there as fp16. While the matrix unit works on
 // one half, the other half's 128 threads (one to a row) turn scores into probabilities:
 //   warps 0-3, 4-7  rows 0-127 and 128-255: references, exponentials, the final scaling
-//   warps 8-11      fetch codes a tile ahead, convert, store swizzled
-//   warp 12         issues the matrix instructions (13-15 only complete its warpgroup)
+//   warps 8-11      convert codes, store them swizzled
+//   warp 12         issues the matrix instructions
+//   warp 13         looks up pages and scales, fetches codes with bulk copies two tiles ahead
+//                   (14 and 15 only complete the warpgroup)
 // Registers are handed out to match: a row's 128 scores stay in its thread's.
 // A page's key scale is a factor of its scores, its value scale one of its probabilities.
 #include <algorithm>
@@ -23,13 +25,14 @@ namespace {
 constexpr int MB = 256;      // query rows of a segment
 constexpr int TILE = 128;    // tokens of a tile
 constexpr int GROUPS = TILE / 16;
-constexpr int STAGES = 2;    // of K and of V
+constexpr int STAGES = 2;    // of K in fp16, and of codes; V in fp16 has one: it is converted while
+                             // the first half of the rows takes its exponentials
 constexpr int INFOS = 4;     // tiles whose scales are kept
 constexpr int BATCH = 128;   // sequences of one launch
 constexpr int THREADS = 16 * 32;
 // registers a thread, out of 128 each at launch: 8 * 168 + 4 * 88 + 4 * 88 = 16 * 128 a lane
 constexpr int ROW_REGS = 168, CONVERT_REGS = 88, ISSUE_REGS = 88;
-constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12;
+constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12, FETCH_WARP = 13;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S (and P over it) at 128 w, O at 256 + 128 w
 using Plan = CausalPlan<MB, TILE>;
 
@@ -168,22 +171,22 @@ __device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint3
 __device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
 
 // Scales of a tile's groups of 16 tokens (a group never spans two pages); bad: a bit for
-// each group whose page is not there.
+// each group whose page is not there; held: tokens of the tile that the sequence has.
 struct TileInfo {
   float2 scale[GROUPS];  // key scale, log2 of the value scale
   uint32_t bad;
-  uint32_t unused;
+  int held;
 };
 
 template <int D>
 struct Memory {
   static constexpr int q_bytes = 128 * D * 2, kv_bytes = TILE * D * 2;
-  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + STAGES * kv_bytes,
-                       raw_v = raw_k + TILE * D;
-  static constexpr int info = raw_v + TILE * D, bars = info + INFOS * (int)sizeof(TileInfo);
+  static constexpr int raw_bytes = 2 * TILE * D;  // K, then V
+  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw = v + kv_bytes;
+  static constexpr int info = raw + STAGES * raw_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
   static constexpr int prefix = bars + 24 * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
-  static constexpr int words = cursors + 12 * 48;
+  static constexpr int words = cursors + 9 * 48;
   static constexpr int bytes = words + 16;
 };
 
@@ -253,9 +256,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   extern __shared__ __align__(1024) unsigned char smem[];
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
-  uint64_t *k_full = bars, *k_free = bars + 2, *v_full = bars + 4, *v_free = bars + 6, *s_full = bars + 8,
-           *p_full = bars + 10, *o_done = bars + 12, *q_full = bars + 14, *info_full = bars + 16,
-           *last_bar = bars + 20;
+  uint64_t *k_full = bars, *k_free = bars + 2, *raw_full = bars + 4, *raw_free = bars + 6,
+           *s_full = bars + 8, *p_full = bars + 10, *o_done = bars + 12, *q_full = bars + 14,
+           *info_full = bars + 16, *last_bar = bars + 20, *v_full = bars + 21, *v_free = bars + 22;
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
@@ -272,8 +275,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
       mbar_init(&k_free[i], 1);
-      mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 1);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_free[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
@@ -281,6 +284,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
     mbar_init(last_bar, 1);
+    mbar_init(v_full, 4);
+    mbar_init(v_free, 1);
     *abort = 0;
     mbar_init_fence();
   }
@@ -321,129 +326,57 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   if (warp >= CONVERT_WARP && warp < ISSUE_WARP) {
     fewer_registers<CONVERT_REGS>();
     if (work) {
-    // ---- codes to fp16: thread i of 128 takes the 16 elements PER * i of every STEP-th token
+    // ---- codes to fp16: thread i of 128 takes the 16 elements from 16 (i % PER) of every
+    // STEP-th token. Rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a
+    // row exclusive-or'ed with its number (which is the same for all of a thread's tokens).
     constexpr int PER = D / 16, STEP = 128 / PER, N = TILE / STEP;  // 8, 16, 8 or 4, 32, 4
     const int tid = threadIdx.x - CONVERT_WARP * 32, key0 = tid / PER, piece = tid % PER;
-    const char *kc = static_cast<const char *>(c.k_codes), *vc = static_cast<const char *>(c.v_codes);
-    struct Place {
-      int b, head, t0, len;
-    };
-    Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;  // one for all lanes
-    if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
-    __syncwarp();
     const int n = (int)(hi - lo);
-    int ahead = 0;  // tiles of the stretch taken
-    auto take = [&] {
-      const Place p = {cur->b, cur->head, cur->tile * TILE, cur->seq.len};
-      ++ahead;
-      __syncwarp();
-      if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment(a, prefix, group, *cur);
-      __syncwarp();
-      return p;
-    };
-    // Lane g < 8 looks up the page of tokens 16 g .. : its id is asked for two tiles before
-    // its codes, its scales one tile before.
-    struct Pages {
-      int page;
-      float ks, vs;
-    };
-    auto ask = [&](const Place &p) {
-      const int t = p.t0 + (lane & 7) * 16;
-      return t < p.len ? __ldg(c.d_table + (int64_t)(a.b0 + p.b) * c.table_stride + t / c.page_tokens) : -1;
-    };
-    auto look_up = [&](const Place &p, int page) {
-      Pages y = {-1, 0.0f, 0.0f};
-      if (p.t0 + (lane & 7) * 16 < p.len) {
-        if (page >= 0 && page < c.n_pages) {
-          const int64_t at = (int64_t)page * c.n_heads + p.head;
-          y.page = page;
-          y.ks = __ldg(c.k_scales + at);
-          y.vs = __ldg(c.v_scales + at);
-        } else {
-          report(a.status, IBP_ERR_INDEX);
-        }
-      }
-      return y;
-    };
-    // Codes go through a place of the thread's own in shared memory, so that no other
-    // thread is waited for and the loops stay short.
-    auto fetch = [&](unsigned char *raw, const char *codes, const Place &p, const Pages &y) {
-#pragma unroll 2
-      for (int i = 0; i < N; ++i) {
-        const int key = key0 + i * STEP, t = p.t0 + key;
-        const int page = __shfl_sync(FULL, y.page, key / 16);
-        const bool there = page >= 0 && t < p.len;
-        const char *from = codes;
-        if (there) from += kv_tile(c, page, p.head) + (t & (c.page_tokens - 1)) * D + piece * 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(raw + (i * 128 + tid) * 16)),
-                     "l"(from), "r"(there ? 16 : 0)  // zeros where nothing is held
-                     : "memory");
-      }
-      cp_async_commit();
-    };
-    // rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a row exclusive-
-    // or'ed with its number
-    auto convert = [&](unsigned char *to, const unsigned char *raw) {
-#pragma unroll 2
-      for (int i = 0; i < N; ++i) {
-        const int key = key0 + i * STEP;
-        const uint4 w = *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    int to[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int at = 2 * piece + h;
-          const uint4 y = make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
-                                     code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
-          *reinterpret_cast<uint4 *>(to + (at / 8) * (TILE * 128) + key * 128 + ((at ^ key) & 7) * 16) = y;
+    for (int h = 0; h < 2; ++h) {
+      const int at = 2 * piece + h;
+      to[h] = (at / 8) * (TILE * 128) + key0 * 128 + ((at ^ key0) & 7) * 16;
+    }
+    bool ok = true;
+    for (int g = 0; g < n && ok; ++g) {
+      const int s = g & 1;
+      ok = __all_sync(FULL, wait(&raw_full[s], (uint32_t)((g >> 1) & 1)));
+      if (!ok) break;
+      const TileInfo &t = info[g & (INFOS - 1)];
+      const int held = t.held;
+      const uint32_t bad = t.bad;
+#pragma unroll 1
+      for (int is_v = 0; is_v < 2; ++is_v) {
+        if (is_v ? g >= 1 : g >= STAGES) {
+          ok = __all_sync(FULL, is_v ? wait(v_free, (uint32_t)((g - 1) & 1))
+                                     : wait(&k_free[s], (uint32_t)((g >> 1) & 1) ^ 1u));
+          if (!ok) break;
+        }
+        const unsigned char *raw = smem + M::raw + s * M::raw_bytes + is_v * (TILE * D) + tid * 16;
+        unsigned char *out = smem + (is_v ? M::v : M::k + s * M::kv_bytes);
+#pragma unroll 4
+        for (int i = 0; i < N; ++i) {
+          uint4 w = *reinterpret_cast<const uint4 *>(raw + i * 2048);
+          if (held < TILE || bad) {  // what no page gave is not a number of ours
+            const int key = key0 + i * STEP;
+            if (key >= held || ((bad >> (key / 16)) & 1)) w = make_uint4(0u, 0u, 0u, 0u);
+          }
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
+                make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
+                           code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(is_v ? v_full : &k_full[s]);
+          if (is_v) mbar_arrive(&raw_free[s]);
         }
       }
-      fence_async_proxy();
-      __syncwarp();
-    };
-    const Place now = take();
-    Place next = now, after = now;  // of tiles g + 1 and g + 2
-    Pages py = look_up(now, ask(now)), ny = py;
-    fetch(smem + M::raw_k, kc, now, py);
-    fetch(smem + M::raw_v, vc, now, py);
-    int asked = -1;
-    if (n > 1) {
-      next = take();
-      ny = look_up(next, ask(next));
     }
-    if (n > 2) {
-      after = take();
-      asked = ask(after);
-    }
-    for (int g = 0; g < n; ++g) {
-      const int s = g & 1;
-      const uint32_t again = (uint32_t)((g >> 1) & 1) ^ 1u;
-      if (g >= STAGES && !__all_sync(FULL, wait(&k_free[s], again))) break;
-      if (warp == CONVERT_WARP) {
-        TileInfo &t = info[g & (INFOS - 1)];
-        const unsigned bad = __ballot_sync(FULL, lane < GROUPS && py.page < 0);
-        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.vs));
-        if (lane == 0) t.bad = bad;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&info_full[g & (INFOS - 1)]);
-      }
-      cp_async_wait<1>();  // this tile's K
-      convert(smem + M::k + s * M::kv_bytes, smem + M::raw_k);
-      if (lane == 0) mbar_arrive(&k_full[s]);
-      if (g + 1 < n) fetch(smem + M::raw_k, kc, next, ny); else cp_async_commit();
-      if (g >= STAGES && !__all_sync(FULL, wait(&v_free[s], again))) break;
-      cp_async_wait<1>();  // this tile's V
-      convert(smem + M::v + s * M::kv_bytes, smem + M::raw_v);
-      if (lane == 0) mbar_arrive(&v_full[s]);
-      if (g + 1 < n) fetch(smem + M::raw_v, vc, next, ny); else cp_async_commit();
-      py = ny;
-      next = after;
-      if (g + 2 < n) ny = look_up(next, asked);
-      if (g + 3 < n) {
-        after = take();
-        asked = ask(after);
-      }
-    }
-    cp_async_wait<0>();
     }
   } else if (warp >= ISSUE_WARP) {
     fewer_registers<ISSUE_REGS>();
@@ -473,24 +406,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         if (ok) tc_commit(&k_free[g & 1]);
         for (int j = 0; j < count && ok; ++j, ++g) {
-          const int s = (int)(g & 1);
           const bool more = j + 1 < count;
           for (int w = 0; w < 2 && ok; ++w) {
             // what is there earliest first: a wait on a full barrier takes its time too
             if (w == 0) {
-              ok = wait(&v_full[s], (uint32_t)((g >> 1) & 1));
+              ok = wait(v_full, (uint32_t)(g & 1));
               if (ok && more) ok = wait(&k_full[(g + 1) & 1], (uint32_t)(((g + 1) >> 1) & 1));
             }
             ok = ok && wait(&p_full[w], (uint32_t)(g & 1));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v = v_at + s * (M::kv_bytes >> 4);
 #pragma unroll
             for (int i = 0; i < TILE / 16; ++i)
-              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i, operand_at(v, i * 2048), io,
+              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i, operand_at(v_at, i * 2048), io,
                      j > 0 || i > 0);
             tc_commit(&o_done[w]);
-            if (w == 1) tc_commit(&v_free[s]);
+            if (w == 1) tc_commit(v_free);
             if (more) {
               scores(w, (int)((g + 1) & 1));
               if (w == 1) tc_commit(&k_free[(g + 1) & 1]);
@@ -503,6 +434,100 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       // nothing may be left running when this CTA gives its memory back
       tc_commit(last_bar);
       mbar_wait(last_bar, 0, nullptr, a.wait_ns);
+    }
+    if (work && warp == FETCH_WARP) {
+      // ---- a bulk copy for each part of a page that lies in the tile
+      const int PP = min(c.page_tokens, TILE), n = (int)(hi - lo);
+      const char *kc = static_cast<const char *>(c.k_codes), *vc = static_cast<const char *>(c.v_codes);
+      struct Place {
+        int b, head, t0, len;
+      };
+      Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + 8;  // one for all lanes
+      if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+      __syncwarp();
+      int ahead = 0;  // tiles of the stretch taken
+      auto take = [&] {
+        const Place p = {cur->b, cur->head, cur->tile * TILE, cur->seq.len};
+        ++ahead;
+        __syncwarp();
+        if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment(a, prefix, group, *cur);
+        __syncwarp();
+        return p;
+      };
+      // Lane g < 8 looks up the page of tokens 16 g .. : its id is asked for two tiles before
+      // its codes, its scales one tile before.
+      struct Pages {
+        int page;
+        float ks, vs;
+      };
+      auto ask = [&](const Place &p) {
+        const int t = p.t0 + (lane & 7) * 16;
+        return t < p.len ? __ldg(c.d_table + (int64_t)(a.b0 + p.b) * c.table_stride + t / c.page_tokens) : -1;
+      };
+      auto look_up = [&](const Place &p, int page) {
+        Pages y = {-1, 0.0f, 0.0f};
+        if (p.t0 + (lane & 7) * 16 < p.len) {
+          if (page >= 0 && page < c.n_pages) {
+            const int64_t at = (int64_t)page * c.n_heads + p.head;
+            y.page = page;
+            y.ks = __ldg(c.k_scales + at);
+            y.vs = __ldg(c.v_scales + at);
+          } else {
+            report(a.status, IBP_ERR_INDEX);
+          }
+        }
+        return y;
+      };
+      Place now = take(), next = now, after = now;  // tiles g, g + 1 and g + 2
+      Pages py = look_up(now, ask(now)), ny = py;
+      int asked = -1;
+      if (n > 1) {
+        next = take();
+        ny = look_up(next, ask(next));
+      }
+      if (n > 2) {
+        after = take();
+        asked = ask(after);
+      }
+      int g = 0;
+      for (; g < n; ++g) {
+        const int s = g & 1;
+        if (g >= STAGES && !__all_sync(FULL, wait(&raw_free[s], (uint32_t)((g >> 1) & 1) ^ 1u))) break;
+        TileInfo &t = info[g & (INFOS - 1)];
+        const unsigned bad = __ballot_sync(FULL, lane < GROUPS && py.page < 0);
+        const bool starts = lane < GROUPS && (lane * 16) % PP == 0 && py.page >= 0;
+        const unsigned copies = __ballot_sync(FULL, starts);
+        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.vs));
+        if (lane == 0) {
+          t.bad = bad;
+          t.held = min(now.len - now.t0, TILE);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&info_full[g & (INFOS - 1)]);
+          mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(__popc(copies) * 2 * PP * D));
+        }
+        __syncwarp();
+        if (starts) {
+          unsigned char *to = smem + M::raw + s * M::raw_bytes + lane * 16 * D;
+          const int64_t at = kv_tile(c, py.page, now.head) +
+                             (int64_t)((now.t0 + lane * 16) & (c.page_tokens - 1)) * D;
+          bulk_load(to, kc + at, PP * D, &raw_full[s]);
+          bulk_load(to + TILE * D, vc + at, PP * D, &raw_full[s]);
+        }
+        now = next;
+        next = after;
+        py = ny;
+        if (g + 2 < n) ny = look_up(next, asked);
+        if (g + 3 < n) {
+          after = take();
+          asked = ask(after);
+        }
+      }
+      // no copy may land after this CTA is gone
+      if (g < n)
+        for (int k = max(g - STAGES, 0); k < g; ++k)
+          mbar_wait(&raw_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
     }
     __syncwarp();
   } else {
