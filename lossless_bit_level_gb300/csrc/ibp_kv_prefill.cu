@@ -12,7 +12,6 @@
 //   warp 12         issues the matrix instructions
 //   warp 13         looks up pages and scales, fetches codes with bulk copies two tiles ahead
 //                   (14 and 15 only complete the warpgroup)
-// Registers are handed out to match: a row's 128 scores stay in its thread's.
 // A page's key scale is a factor of its scores, its value scale one of its probabilities.
 #include <algorithm>
 
@@ -52,24 +51,36 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The barrier is arrived at once every matrix instruction issued so far has finished.
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+// One lane of the warp, the same every time; the matrix instructions are issued by it while
+// the whole warp computes their operands (uniform over the warp, so in uniform registers).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// The barrier is arrived at once every matrix instruction issued so far has finished.
+__device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t mine) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(mine)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                       uint32_t mine) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(mine)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                       uint32_t mine) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(mine)
       : "memory");
 }
 
@@ -115,6 +126,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
       "[%16];"
       : R8(x, 0), R8(x, 8)
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&x)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : RW8(x, 0), RW8(x, 8)::"memory");
 }
 template <int N>
@@ -338,102 +351,109 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int at = 2 * piece + h;
       to[h] = (at / 8) * (TILE * 128) + key0 * 128 + ((at ^ key0) & 7) * 16;
     }
-    bool ok = true;
-    for (int g = 0; g < n && ok; ++g) {
-      const int s = g & 1;
-      ok = __all_sync(FULL, wait(&raw_full[s], (uint32_t)((g >> 1) & 1)));
-      if (!ok) break;
+    // K of tile 0, then K of tile g + 1 before V of tile g: the scores of a tile are wanted
+    // a tile before its values
+#pragma unroll 1
+    for (int step = 0; step < 2 * n; ++step) {
+      const bool is_v = step > 0 && (step % 2 == 0 || step == 2 * n - 1);
+      const int g = is_v ? (step == 2 * n - 1 ? n - 1 : step / 2 - 1) : (step + 1) / 2, s = g & 1;
+      const uint32_t turn = (uint32_t)(g >> 1) & 1;
+      bool ok = is_v ? g == 0 || wait(v_free, (uint32_t)(g - 1) & 1)
+                     : wait(&raw_full[s], turn) && (g < STAGES || wait(&k_free[s], turn ^ 1u));
+      if (!__all_sync(FULL, ok)) break;
       const TileInfo &t = info[g & (INFOS - 1)];
       const int held = t.held;
       const uint32_t bad = t.bad;
-#pragma unroll 1
-      for (int is_v = 0; is_v < 2; ++is_v) {
-        if (is_v ? g >= 1 : g >= STAGES) {
-          ok = __all_sync(FULL, is_v ? wait(v_free, (uint32_t)((g - 1) & 1))
-                                     : wait(&k_free[s], (uint32_t)((g >> 1) & 1) ^ 1u));
-          if (!ok) break;
-        }
-        const unsigned char *raw = smem + M::raw + s * M::raw_bytes + is_v * (TILE * D) + tid * 16;
-        unsigned char *out = smem + (is_v ? M::v : M::k + s * M::kv_bytes);
-#pragma unroll 4
-        for (int i = 0; i < N; ++i) {
-          uint4 w = *reinterpret_cast<const uint4 *>(raw + i * 2048);
-          if (held < TILE || bad) {  // what no page gave is not a number of ours
-            const int key = key0 + i * STEP;
-            if (key >= held || ((bad >> (key / 16)) & 1)) w = make_uint4(0u, 0u, 0u, 0u);
-          }
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      const unsigned char *raw = smem + M::raw + s * M::raw_bytes + (is_v ? TILE * D : 0) + tid * 16;
+      unsigned char *out = smem + (is_v ? M::v : M::k + s * M::kv_bytes);
+      uint4 w[N];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
-                make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
-                           code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+      for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + i * 2048);
+      if (held < TILE || bad) {  // what no page gave is not a number of ours
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int key = key0 + i * STEP;
+          if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(is_v ? v_full : &k_full[s]);
-          if (is_v) mbar_arrive(&raw_free[s]);
-        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
+              make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
+                         code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+      }
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(is_v ? v_full : &k_full[s]);
+        if (is_v) mbar_arrive(&raw_free[s]);
       }
     }
     }
   } else if (warp >= ISSUE_WARP) {
     fewer_registers<ISSUE_REGS>();
-    if (work && warp == ISSUE_WARP && lane == 0) {
+    if (work && warp == ISSUE_WARP) {
       constexpr uint32_t is = instruction(TILE, false), io = instruction(D, true);
+      const uint32_t mine = elect_one();
       const uint32_t q_at = operand(smem + M::q, 16), k_at = operand(smem + M::k, 16),
                      v_at = operand(smem + M::v, TILE * 128);
-      auto scores = [&](int w, int s) {
+      auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, wait(bar, parity)); };
+      auto scores = [&](int w, uint32_t s) {
         const uint32_t q = q_at + w * (M::q_bytes >> 4), k = k_at + s * (M::kv_bytes >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           mma_ss(tmem + 128 * w, operand_at(q, (i / 4) * (128 * 128) + (i % 4) * 32),
-                 operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0);
-        tc_commit(&s_full[w]);
+                 operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0, mine);
+        tc_commit(&s_full[w], mine);
       };
       Cursor cur = cursor_at(a, prefix, group, lo);
-      int64_t g = 0;  // tiles of the stretch begun
-      int segment = 0;
+      const int n = (int)(hi - lo);
+      int g = 0;  // tiles of the stretch begun
+      uint32_t segment = 0;
       bool ok = true;
-      while (ok && lo + g < hi) {
-        const int count = (int)min((int64_t)(cur.tiles - cur.tile), hi - lo - g);
-        ok = wait(&k_full[g & 1], (uint32_t)((g >> 1) & 1));
+      while (ok && g < n) {
+        const int count = min(cur.tiles - cur.tile, n - g);
+        ok = ready(&k_full[g & 1], (g >> 1) & 1);
         for (int w = 0; w < 2 && ok; ++w) {
-          ok = wait(&q_full[w], (uint32_t)(segment & 1));
+          ok = ready(&q_full[w], segment & 1);
           tc_fence_after();
-          if (ok) scores(w, (int)(g & 1));
+          if (ok) scores(w, g & 1);
         }
-        if (ok) tc_commit(&k_free[g & 1]);
+        if (ok) tc_commit(&k_free[g & 1], mine);
         for (int j = 0; j < count && ok; ++j, ++g) {
           const bool more = j + 1 < count;
+#pragma unroll 1
           for (int w = 0; w < 2 && ok; ++w) {
             // what is there earliest first: a wait on a full barrier takes its time too
-            if (w == 0) {
-              ok = wait(v_full, (uint32_t)(g & 1));
-              if (ok && more) ok = wait(&k_full[(g + 1) & 1], (uint32_t)(((g + 1) >> 1) & 1));
-            }
-            ok = ok && wait(&p_full[w], (uint32_t)(g & 1));
+            if (w == 0) ok = ready(v_full, g & 1);
+            ok = ok && ready(&p_full[w], g & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < TILE / 16; ++i)
               mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i, operand_at(v_at, i * 2048), io,
-                     j > 0 || i > 0);
-            tc_commit(&o_done[w]);
-            if (w == 1) tc_commit(v_free);
+                     j > 0 || i > 0, mine);
+            tc_commit(&o_done[w], mine);
+            if (w == 1) tc_commit(v_free, mine);
             if (more) {
-              scores(w, (int)((g + 1) & 1));
-              if (w == 1) tc_commit(&k_free[(g + 1) & 1]);
+              if (w == 0) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(w, (g + 1) & 1);
+              if (w == 1) tc_commit(&k_free[(g + 1) & 1], mine);
             }
           }
         }
         ++segment;
-        if (ok && lo + g < hi) next_segment(a, prefix, group, cur);
+        if (ok && g < n) next_segment(a, prefix, group, cur);
       }
       // nothing may be left running when this CTA gives its memory back
-      tc_commit(last_bar);
+      tc_commit(last_bar, mine);
       mbar_wait(last_bar, 0, nullptr, a.wait_ns);
+      __syncwarp();
     }
     if (work && warp == FETCH_WARP) {
       // ---- a bulk copy for each part of a page that lies in the tile
@@ -604,31 +624,37 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const TileInfo &t = info[g & (INFOS - 1)];
         const int seen = limit - (tile0 + j) * TILE;  // columns this row sees
         const bool whole = __all_sync(FULL, seen >= TILE && t.bad == 0);
-        uint32_t s[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_load(sp + 32 * k, s[k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_wait_load(s[k]);
-        // the largest score, the largest with its value scale, the least value scale
+        // the largest score, the largest with its value scale, the least value scale; groups
+        // of 16 columns in turn, the next one on its way (short loops: long straight code
+        // waits for instructions)
         float mn = m, mvn = mv, lv_least = INFINITY;
-#pragma unroll
-        for (int gi = 0; gi < GROUPS; ++gi) {
+        uint32_t s0[16], s1[16];
+        auto raise = [&](uint32_t (&x)[16], int gi) {
           const float2 sc = t.scale[gi];
-          uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
           if (!whole) {
             const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sg[e] = e < n ? sg[e] : 0xFF800000u;
+            for (int e = 0; e < 16; ++e) x[e] = e < n ? x[e] : 0xFF800000u;
           }
-          float top = fmaxf(__uint_as_float(sg[0]), __uint_as_float(sg[1]));
+          float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
           for (int e = 2; e < 16; e += 2)
-            top = max3(top, __uint_as_float(sg[e]), __uint_as_float(sg[e + 1]));
+            top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
           top *= rowc * sc.x;
           mn = fmaxf(mn, top);
           mvn = fmaxf(mvn, top + sc.y);
           lv_least = fminf(lv_least, sc.y);
+        };
+        tmem_load16(sp, s0);
+#pragma unroll 1
+        for (int gi = 0; gi < GROUPS; gi += 2) {
+          tmem_wait16(s0);
+          tmem_load16(sp + 16 * gi + 16, s1);
+          raise(s0, gi);
+          tmem_wait16(s1);
+          if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
+          raise(s1, gi + 1);
         }
         if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
           const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
@@ -643,6 +669,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             for (int k = 0; k < D / 16; ++k) {
               uint32_t y[16];
               tmem_load16(op + 16 * k, y);
+              tmem_wait16(y);
 #pragma unroll
               for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
               tmem_store16(op + 16 * k, y);
@@ -654,46 +681,62 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         // that times 2^(mv - m - lv): one exponential a score, and one a group for the sum.
         // Where the value scales differ so much that the first could vanish with the second
         // still counting, or a score is masked, the two are taken the other way round.
-        if (__all_sync(FULL, whole && lv_least + (m - mv) > -60.0f)) {
+        const bool near = __all_sync(FULL, whole && lv_least + (m - mv) > -60.0f);
+        auto weigh = [&](const uint32_t (&x)[16], int gi) {
+          const float2 sc = t.scale[gi];
+          const float f = rowc * sc.x, up = sc.y - mv;
+          const uint64_t ff = pair(f, f), uu = pair(up, up);
+          uint64_t sum = 0;
+          uint32_t p[8];
 #pragma unroll
-          for (int gi = 0; gi < GROUPS; ++gi) {
-            const uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
-            const float2 sc = t.scale[gi];
-            const float f = rowc * sc.x, up = sc.y - mv;
-            const uint64_t ff = pair(f, f), uu = pair(up, up);
-            uint64_t sum = 0;
-            uint32_t p[8];
+          for (int e = 0; e < 16; e += 2) {
+            const uint64_t y = fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, uu);
+            const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+            sum = add2(sum, pair(p0, p1));
+            p[e / 2] = pack2<IBP_FP16>(p0, p1);
+          }
+          const float back = exp2_fast(-(sc.y + (m - mv)));
+          l = fma2(sum, pair(back, back), l);
+          tmem_store8(sp + 8 * gi, p);  // over columns that have been read
+        };
+        auto weigh_masked = [&](const uint32_t (&x)[16], int gi) {
+          const float2 sc = t.scale[gi];
+          const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
+          const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
+          float sum = 0.0f;
+          uint32_t p[8];
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const uint64_t y = fma2(pair(__uint_as_float(sg[e]), __uint_as_float(sg[e + 1])), ff, uu);
-              const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-              sum = add2(sum, pair(p0, p1));
-              p[e / 2] = pack2<IBP_FP16>(p0, p1);
-            }
-            const float back = exp2_fast(-(sc.y + (m - mv)));
-            l = fma2(sum, pair(back, back), l);
-            tmem_store8(sp + 8 * gi, p);  // over columns that have been read
+          for (int e = 0; e < 16; e += 2) {
+            float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), f, -m));
+            float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), f, -m));
+            p0 = e < n ? p0 : 0.0f;
+            p1 = e + 1 < n ? p1 : 0.0f;
+            sum += p0 + p1;
+            p[e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
+          }
+          l = add2(l, pair(sum, 0.0f));
+          tmem_store8(sp + 8 * gi, p);
+        };
+        tmem_load16(sp, s0);
+        if (near) {
+#pragma unroll 1
+          for (int gi = 0; gi < GROUPS; gi += 2) {
+            tmem_wait16(s0);
+            tmem_load16(sp + 16 * gi + 16, s1);
+            weigh(s0, gi);
+            tmem_wait16(s1);
+            if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
+            weigh(s1, gi + 1);
           }
         } else {
-#pragma unroll
-          for (int gi = 0; gi < GROUPS; ++gi) {
-            const uint32_t *sg = s[gi / 2] + 16 * (gi & 1);
-            const float2 sc = t.scale[gi];
-            const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
-            const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
-            float sum = 0.0f;
-            uint32_t p[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float p0 = exp2_fast(fmaf(__uint_as_float(sg[e]), f, -m));
-              float p1 = exp2_fast(fmaf(__uint_as_float(sg[e + 1]), f, -m));
-              p0 = e < n ? p0 : 0.0f;
-              p1 = e + 1 < n ? p1 : 0.0f;
-              sum += p0 + p1;
-              p[e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
-            }
-            l = add2(l, pair(sum, 0.0f));
-            tmem_store8(sp + 8 * gi, p);
+#pragma unroll 1
+          for (int gi = 0; gi < GROUPS; gi += 2) {
+            tmem_wait16(s0);
+            tmem_load16(sp + 16 * gi + 16, s1);
+            weigh_masked(s0, gi);
+            tmem_wait16(s1);
+            if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
+            weigh_masked(s1, gi + 1);
           }
         }
         tmem_wait_store();
