@@ -32,7 +32,11 @@ constexpr int THREADS = 16 * 32;
 // registers a thread, out of 128 each at launch: 8 * 168 + 4 * 88 + 4 * 88 = 16 * 128 a lane
 constexpr int ROW_REGS = 168, CONVERT_REGS = 88, ISSUE_REGS = 88;
 constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12, FETCH_WARP = 13;
-constexpr uint32_t TMEM_COLS = 512, O_COL = 256;  // S (and P over it) at 128 w, O at 256 + 128 w
+// Scores come 64 tokens (half a tile) at a time, in turn in two places for each half of the
+// rows, so that the next ones are there when a thread is done with the last: S (and P over
+// it) at 128 w + 64 (half), O at 256 + 128 w.
+constexpr int HALF = 64;
+constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 using Plan = CausalPlan<MB, TILE>;
 
 // ---- tensor memory and the matrix instruction
@@ -91,16 +95,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 #define I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), \
                  "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
 
-// 32 columns of this warp's 32 lanes, a lane to a thread. The values may be used after
-// tmem_wait_load of the same registers.
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&x)[32]) {
+// Columns of this warp's 32 lanes, a lane to a thread. The values may be used after
+// tmem_wait of the same registers.
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t *x) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[32]) {
+__device__ __forceinline__ void tmem_wait32(uint32_t *x) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : RW8(x, 0), RW8(x, 8), RW8(x, 16), RW8(x, 24)::"memory");
 }
@@ -110,11 +114,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t *x) {
       "%15,%16};" ::"r"(at),
       I8(x, 0), I8(x, 8)
       : "memory");
-}
-__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t *x) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
-               I8(x, 0)
-               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -197,7 +196,7 @@ struct Memory {
   static constexpr int raw_bytes = 2 * TILE * D;  // K, then V
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw = v + kv_bytes;
   static constexpr int info = raw + STAGES * raw_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
-  static constexpr int prefix = bars + 24 * 8;
+  static constexpr int prefix = bars + 28 * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 9 * 48;
   static constexpr int bytes = words + 16;
@@ -270,8 +269,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
   uint64_t *k_full = bars, *k_free = bars + 2, *raw_full = bars + 4, *raw_free = bars + 6,
-           *s_full = bars + 8, *p_full = bars + 10, *o_done = bars + 12, *q_full = bars + 14,
-           *info_full = bars + 16, *last_bar = bars + 20, *v_full = bars + 21, *v_free = bars + 22;
+           *o_done = bars + 8, *q_full = bars + 10, *info_full = bars + 12, *last_bar = bars + 16,
+           *v_full = bars + 17, *v_free = bars + 18;
+  uint64_t *s_full = bars + 20, *p_full = bars + 24;  // [2 w + half]
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
@@ -290,12 +290,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_init(&k_free[i], 1);
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_free[i], 4);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
       mbar_init(&q_full[i], 4);
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
     mbar_init(last_bar, 1);
     mbar_init(v_full, 4);
     mbar_init(v_free, 1);
@@ -396,18 +398,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   } else if (warp >= ISSUE_WARP) {
     fewer_registers<ISSUE_REGS>();
     if (work && warp == ISSUE_WARP) {
-      constexpr uint32_t is = instruction(TILE, false), io = instruction(D, true);
+      constexpr uint32_t is = instruction(HALF, false), io = instruction(D, true);
       const uint32_t mine = elect_one();
       const uint32_t q_at = operand(smem + M::q, 16), k_at = operand(smem + M::k, 16),
                      v_at = operand(smem + M::v, TILE * 128);
       auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, wait(bar, parity)); };
-      auto scores = [&](int w, uint32_t s) {
-        const uint32_t q = q_at + w * (M::q_bytes >> 4), k = k_at + s * (M::kv_bytes >> 4);
+      // half h of the tile whose K is in stage s
+      auto scores = [&](int w, uint32_t s, int h) {
+        const uint32_t q = q_at + w * (M::q_bytes >> 4),
+                       k = k_at + s * (M::kv_bytes >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + 128 * w, operand_at(q, (i / 4) * (128 * 128) + (i % 4) * 32),
+          mma_ss(tmem + 128 * w + HALF * h, operand_at(q, (i / 4) * (128 * 128) + (i % 4) * 32),
                  operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0, mine);
-        tc_commit(&s_full[w], mine);
+        tc_commit(&s_full[2 * w + h], mine);
       };
       Cursor cur = cursor_at(a, prefix, group, lo);
       const int n = (int)(hi - lo);
@@ -417,33 +421,35 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       while (ok && g < n) {
         const int count = min(cur.tiles - cur.tile, n - g);
         ok = ready(&k_full[g & 1], (g >> 1) & 1);
-        for (int w = 0; w < 2 && ok; ++w) {
-          ok = ready(&q_full[w], segment & 1);
+#pragma unroll 1
+        for (int i = 0; i < 4 && ok; ++i) {
+          if (i < 2) ok = ready(&q_full[i & 1], segment & 1);
           tc_fence_after();
-          if (ok) scores(w, g & 1);
+          if (ok) scores(i & 1, g & 1, i >> 1);
         }
         if (ok) tc_commit(&k_free[g & 1], mine);
         for (int j = 0; j < count && ok; ++j, ++g) {
           const bool more = j + 1 < count;
 #pragma unroll 1
-          for (int w = 0; w < 2 && ok; ++w) {
+          for (int i = 0; i < 4 && ok; ++i) {  // both halves of the tile, of the rows each
+            const int w = i & 1, h = i >> 1;
             // what is there earliest first: a wait on a full barrier takes its time too
-            if (w == 0) ok = ready(v_full, g & 1);
-            ok = ok && ready(&p_full[w], g & 1);
+            if (i == 0) {
+              ok = ready(v_full, g & 1);
+              if (ok && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+            }
+            ok = ok && ready(&p_full[2 * w + h], g & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < TILE / 16; ++i)
-              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + 8 * i, operand_at(v_at, i * 2048), io,
-                     j > 0 || i > 0, mine);
+            for (int e = 0; e < HALF / 16; ++e)
+              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + HALF * h + 8 * e,
+                     operand_at(v_at + h * (HALF * 128 >> 4), e * 2048), io, j > 0 || h > 0 || e > 0, mine);
             tc_commit(&o_done[w], mine);
-            if (w == 1) tc_commit(v_free, mine);
+            if (i == 3) tc_commit(v_free, mine);
             if (more) {
-              if (w == 0) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              scores(w, (g + 1) & 1);
-              if (w == 1) tc_commit(&k_free[(g + 1) & 1], mine);
+              scores(w, (g + 1) & 1, h);
+              if (i == 3) tc_commit(&k_free[(g + 1) & 1], mine);
             }
           }
         }
@@ -613,141 +619,132 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&q_full[w]);
       }
       const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
-      float m = NONE, mv = NONE;
-      uint64_t l = 0;  // two halves of the sum
-      for (int j = 0; j < count; ++j) {
-        const int g = x + j;
-        ok = __all_sync(FULL, wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1)) &&
-                                  wait(&s_full[w], (uint32_t)(g & 1)));
+      float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by
+      uint64_t l = 0;                           // two halves of the sum
+      auto rescale = [&](float by, int before) {  // the output so far, once instruction `before` is done
+        ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)(before & 1)));
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t y[16];
+          tmem_load16(op + 16 * k, y);
+          tmem_wait16(y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * by);
+          tmem_store16(op + 16 * k, y);
+        }
+        tmem_wait_store();
+      };
+#pragma unroll 1
+      for (int j = 0; j < 2 * count; ++j) {
+        const int u = 2 * x + j, g = u >> 1, h = u & 1;  // halves of tiles done, the tile, its half
+        ok = __all_sync(FULL, (h || wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1))) &&
+                                  wait(&s_full[2 * w + h], (uint32_t)(g & 1)));
         if (!ok) break;
         tc_fence_after();
-        const TileInfo &t = info[g & (INFOS - 1)];
-        const int seen = limit - (tile0 + j) * TILE;  // columns this row sees
-        const bool whole = __all_sync(FULL, seen >= TILE && t.bad == 0);
-        // the largest score, the largest with its value scale, the least value scale; groups
-        // of 16 columns in turn, the next one on its way (short loops: long straight code
-        // waits for instructions)
-        float mn = m, mvn = mv, lv_least = INFINITY;
-        uint32_t s0[16], s1[16];
-        auto raise = [&](uint32_t (&x)[16], int gi) {
-          const float2 sc = t.scale[gi];
-          if (!whole) {
-            const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = e < n ? x[e] : 0xFF800000u;
-          }
-          float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-#pragma unroll
-          for (int e = 2; e < 16; e += 2)
-            top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
-          top *= rowc * sc.x;
-          mn = fmaxf(mn, top);
-          mvn = fmaxf(mvn, top + sc.y);
-          lv_least = fminf(lv_least, sc.y);
-        };
-        tmem_load16(sp, s0);
-#pragma unroll 1
-        for (int gi = 0; gi < GROUPS; gi += 2) {
-          tmem_wait16(s0);
-          tmem_load16(sp + 16 * gi + 16, s1);
-          raise(s0, gi);
-          tmem_wait16(s1);
-          if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
-          raise(s1, gi + 1);
+        const float2 *scale = info[g & (INFOS - 1)].scale + 4 * h;
+        const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
+        const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
+        const uint32_t at = sp + HALF * h;
+        uint32_t s[HALF], p[HALF / 2];
+        if (__any_sync(FULL, over > 0.0f)) {
+          const float by = exp2_fast(-over);
+          rescale(by, u - 1);
+          if (!ok) break;
+          m += over;
+          mv += over;
+          l = mul2(l, pair(by, by));
+          over = 0.0f;
         }
-        if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
-          const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
-          m = mn;
-          mv = mvn;
-          l = mul2(l, pair(fl, fl));
-          if (j > 0) {
-            ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)((g - 1) & 1)));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t y[16];
-              tmem_load16(op + 16 * k, y);
-              tmem_wait16(y);
+        tmem_load32(at, s);
+        tmem_load32(at + 32, s + 32);
+        tmem_wait32(s);
+        tmem_wait32(s + 32);
+        // With the references as they are: a probability with its value scale is
+        // 2^(x + lv - mv), and the probability itself that times 2^(mv - m - lv), so one
+        // exponential a score and one a group for the sum. It stands if every row has a
+        // reference, sees all 64 tokens, has no value scale so small that the first could
+        // vanish with the second still counting, and nothing passed fp16's range.
+        const float least = fminf(fminf(scale[0].y, scale[1].y), fminf(scale[2].y, scale[3].y));
+        bool stands = __all_sync(FULL, seen >= HALF && bad == 0 && m > 0.5f * NONE &&
+                                           least + (m - mv) > -60.0f);
+        if (stands) {
+          uint64_t sum_l = l;
+          float top = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
-              tmem_store16(op + 16 * k, y);
+          for (int k = 0; k < 4; ++k) {
+            const float2 sc = scale[k];
+            const float f = rowc * sc.x, up = sc.y - mv;
+            const uint64_t ff = pair(f, f), uu = pair(up, up);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 16 * k; e < 16 * k + 16; e += 2) {
+              const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
+              top = max3(top, low(y), high(y));
+              const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+              sum = add2(sum, pair(p0, p1));
+              p[e / 2] = pack2<IBP_FP16>(p0, p1);
             }
-            tmem_wait_store();
+            const float back = exp2_fast(-(sc.y + (m - mv)));
+            sum_l = fma2(sum, pair(back, back), sum_l);
+          }
+          stands = __all_sync(FULL, top <= 15.0f);
+          if (stands) {
+            l = sum_l;
+            if (top > 8.0f) over = top;
           }
         }
-        // A probability with its value scale is 2^(x + lv - mv), and the probability itself
-        // that times 2^(mv - m - lv): one exponential a score, and one a group for the sum.
-        // Where the value scales differ so much that the first could vanish with the second
-        // still counting, or a score is masked, the two are taken the other way round.
-        const bool near = __all_sync(FULL, whole && lv_least + (m - mv) > -60.0f);
-        auto weigh = [&](const uint32_t (&x)[16], int gi) {
-          const float2 sc = t.scale[gi];
-          const float f = rowc * sc.x, up = sc.y - mv;
-          const uint64_t ff = pair(f, f), uu = pair(up, up);
-          uint64_t sum = 0;
-          uint32_t p[8];
+        if (!stands) {  // masks, new references, then both exponents apart
+          float mn = m, mvn = mv;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const uint64_t y = fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ff, uu);
-            const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-            sum = add2(sum, pair(p0, p1));
-            p[e / 2] = pack2<IBP_FP16>(p0, p1);
-          }
-          const float back = exp2_fast(-(sc.y + (m - mv)));
-          l = fma2(sum, pair(back, back), l);
-          tmem_store8(sp + 8 * gi, p);  // over columns that have been read
-        };
-        auto weigh_masked = [&](const uint32_t (&x)[16], int gi) {
-          const float2 sc = t.scale[gi];
-          const float f = rowc * sc.x, gv = exp2_fast(fminf(sc.y + (m - mv), 120.0f));
-          const int n = (t.bad >> gi) & 1 ? 0 : seen - 16 * gi;
-          float sum = 0.0f;
-          uint32_t p[8];
+          for (int k = 0; k < 4; ++k) {
+            const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
+            float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), f, -m));
-            float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), f, -m));
-            p0 = e < n ? p0 : 0.0f;
-            p1 = e + 1 < n ? p1 : 0.0f;
-            sum += p0 + p1;
-            p[e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
+            for (int e = 0; e < 16; ++e) top = e < n ? fmaxf(top, __uint_as_float(s[16 * k + e])) : top;
+            // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
+            top *= rowc * scale[k].x;
+            mn = fmaxf(mn, top);
+            mvn = fmaxf(mvn, top + scale[k].y);
           }
-          l = add2(l, pair(sum, 0.0f));
-          tmem_store8(sp + 8 * gi, p);
-        };
-        tmem_load16(sp, s0);
-        if (near) {
-#pragma unroll 1
-          for (int gi = 0; gi < GROUPS; gi += 2) {
-            tmem_wait16(s0);
-            tmem_load16(sp + 16 * gi + 16, s1);
-            weigh(s0, gi);
-            tmem_wait16(s1);
-            if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
-            weigh(s1, gi + 1);
+          if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
+            const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
+            m = mn;
+            mv = mvn;
+            l = mul2(l, pair(fl, fl));
+            if (j > 0) {
+              rescale(fo, u - 1);
+              if (!ok) break;
+            }
           }
-        } else {
-#pragma unroll 1
-          for (int gi = 0; gi < GROUPS; gi += 2) {
-            tmem_wait16(s0);
-            tmem_load16(sp + 16 * gi + 16, s1);
-            weigh_masked(s0, gi);
-            tmem_wait16(s1);
-            if (gi + 2 < GROUPS) tmem_load16(sp + 16 * gi + 32, s0);
-            weigh_masked(s1, gi + 1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = rowc * scale[k].x, gv = exp2_fast(fminf(scale[k].y + (m - mv), 120.0f));
+            const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float p0 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e]), f, -m));
+              float p1 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e + 1]), f, -m));
+              p0 = e < n ? p0 : 0.0f;
+              p1 = e + 1 < n ? p1 : 0.0f;
+              sum += p0 + p1;
+              p[8 * k + e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
+            }
+            l = add2(l, pair(sum, 0.0f));
           }
         }
+        tmem_store16(at, p);  // over columns that have been read
+        tmem_store16(at + 16, p + 16);
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        if (lane == 0) mbar_arrive(&p_full[2 * w + h]);
       }
       if (!ok) break;
       // ---- finish the segment, or leave a part
-      const int g = x + count - 1;
-      ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)(g & 1)));
+      ok = __all_sync(FULL, wait(&o_done[w], 1u));  // a tile's second half is an odd one
       if (!ok) break;
       tc_fence_after();
       const float sum = low(l) + high(l);
@@ -760,8 +757,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll 1
       for (int q4 = 0; q4 < D / 32; ++q4) {
         uint32_t s[32];
-        tmem_load(op + 32 * q4, s);
-        tmem_wait_load(s);
+        tmem_load32(op + 32 * q4, s);
+        tmem_wait32(s);
         if (!live) continue;
         float y[32];
 #pragma unroll
