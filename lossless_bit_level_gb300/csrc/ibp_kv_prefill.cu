@@ -24,9 +24,9 @@ namespace {
 constexpr int MB = 256;      // query rows of a segment
 constexpr int TILE = 128;    // tokens of a tile
 constexpr int GROUPS = TILE / 16;
-constexpr int STAGES = 2;    // of K in fp16, and of codes; V in fp16 has one: it is converted while
-                             // the first half of the rows takes its exponentials
-constexpr int INFOS = 4;     // tiles whose scales are kept
+constexpr int STAGES = 2;    // tiles of K in fp16, and of its codes; of V's codes there is one
+constexpr int V_HALVES = 3;  // half tiles of V in fp16
+constexpr int INFOS = 8;     // tiles whose scales are kept
 constexpr int BATCH = 128;   // sequences of one launch
 constexpr int THREADS = 16 * 32;
 // registers a thread, out of 128 each at launch: 8 * 168 + 4 * 88 + 4 * 88 = 16 * 128 a lane
@@ -192,11 +192,13 @@ struct TileInfo {
 
 template <int D>
 struct Memory {
-  static constexpr int q_bytes = 128 * D * 2, kv_bytes = TILE * D * 2;
-  static constexpr int raw_bytes = 2 * TILE * D;  // K, then V
-  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw = v + kv_bytes;
-  static constexpr int info = raw + STAGES * raw_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
-  static constexpr int prefix = bars + 28 * 8;
+  static constexpr int q_bytes = 128 * D * 2, kv_bytes = TILE * D * 2, half_bytes = HALF * D * 2;
+  static constexpr int code_bytes = TILE * D;
+  static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + V_HALVES * half_bytes,
+                       raw_v = raw_k + STAGES * code_bytes;
+  static constexpr int info = raw_v + code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
+  static constexpr int barriers = 31 + INFOS;  // see the kernel's list of them
+  static constexpr int prefix = bars + barriers * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 9 * 48;
   static constexpr int bytes = words + 16;
@@ -263,15 +265,16 @@ template <int D, int CODE, int DT>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ AttentionArgs a) {
   using M = Memory<D>;
   static_assert(M::info % alignof(TileInfo) == 0 && M::bars % 8 == 0 && M::prefix % 8 == 0 &&
-                    M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0,
-                "what lies in shared memory is aligned");
+                    M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0 && M::bytes <= 227 * 1024,
+                "what lies in shared memory is aligned and fits");
   extern __shared__ __align__(1024) unsigned char smem[];
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
-  uint64_t *k_full = bars, *k_free = bars + 2, *raw_full = bars + 4, *raw_free = bars + 6,
-           *o_done = bars + 8, *q_full = bars + 10, *info_full = bars + 12, *last_bar = bars + 16,
-           *v_full = bars + 17, *v_free = bars + 18;
-  uint64_t *s_full = bars + 20, *p_full = bars + 24;  // [2 w + half]
+  uint64_t *k_full = bars, *k_free = bars + 2, *raw_k_full = bars + 4, *raw_k_free = bars + 6,
+           *q_full = bars + 8, *last_bar = bars + 10, *raw_v_full = bars + 11, *raw_v_free = bars + 12,
+           *v_full = bars + 13, *v_free = bars + 16;
+  // [2 w + half]: a row's thread may be two instructions ahead of the last one done
+  uint64_t *s_full = bars + 19, *p_full = bars + 23, *o_done = bars + 27, *info_full = bars + 31;
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
@@ -288,19 +291,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
       mbar_init(&k_free[i], 1);
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_free[i], 4);
-      mbar_init(&o_done[i], 1);
+      mbar_init(&raw_k_full[i], 1);
+      mbar_init(&raw_k_free[i], 4);
       mbar_init(&q_full[i], 4);
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
     }
     mbar_init(last_bar, 1);
-    mbar_init(v_full, 4);
-    mbar_init(v_free, 1);
+    mbar_init(raw_v_full, 1);
+    mbar_init(raw_v_free, 4);
+    for (int i = 0; i < V_HALVES; ++i) {
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_free[i], 1);
+    }
     *abort = 0;
     mbar_init_fence();
   }
@@ -341,57 +348,68 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   if (warp >= CONVERT_WARP && warp < ISSUE_WARP) {
     fewer_registers<CONVERT_REGS>();
     if (work) {
-    // ---- codes to fp16: thread i of 128 takes the 16 elements from 16 (i % PER) of every
-    // STEP-th token. Rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a
-    // row exclusive-or'ed with its number (which is the same for all of a thread's tokens).
-    constexpr int PER = D / 16, STEP = 128 / PER, N = TILE / STEP;  // 8, 16, 8 or 4, 32, 4
-    const int tid = threadIdx.x - CONVERT_WARP * 32, key0 = tid / PER, piece = tid % PER;
+    // ---- codes to fp16, half a tile at a time: a thread takes 16 elements of every STEP-th
+    // token. Rows of tokens, 64 elements to a 128-byte row, the 16-byte pieces of a row
+    // exclusive-or'ed with its number (which is the same for all of a thread's tokens). At
+    // 128 elements, 16 threads take two tokens, the second four of each eight those of the
+    // other token: then neither the loads nor the stores of eight threads share a bank.
+    constexpr int PER = D / 16, STEP = 128 / PER, N = HALF / STEP;  // 8, 16, 4 or 4, 32, 2
+    const int tid = threadIdx.x - CONVERT_WARP * 32;
+    const int piece = D == 128 ? tid & 7 : tid & 3;
+    const int key0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 3) ^ (tid >> 2)) & 1) : tid >> 2;
     const int n = (int)(hi - lo);
+    const int from = key0 * D + piece * 16, block = (2 * piece) / 8;
     int to[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = 2 * piece + h;
-      to[h] = (at / 8) * (TILE * 128) + key0 * 128 + ((at ^ key0) & 7) * 16;
-    }
+    for (int h = 0; h < 2; ++h) to[h] = key0 * 128 + (((2 * piece + h) ^ key0) & 7) * 16;
     // K of tile 0, then K of tile g + 1 before V of tile g: the scores of a tile are wanted
     // a tile before its values
+    bool ok = true;
 #pragma unroll 1
-    for (int step = 0; step < 2 * n; ++step) {
+    for (int step = 0; step < 2 * n && ok; ++step) {
       const bool is_v = step > 0 && (step % 2 == 0 || step == 2 * n - 1);
       const int g = is_v ? (step == 2 * n - 1 ? n - 1 : step / 2 - 1) : (step + 1) / 2, s = g & 1;
       const uint32_t turn = (uint32_t)(g >> 1) & 1;
-      bool ok = is_v ? g == 0 || wait(v_free, (uint32_t)(g - 1) & 1)
-                     : wait(&raw_full[s], turn) && (g < STAGES || wait(&k_free[s], turn ^ 1u));
-      if (!__all_sync(FULL, ok)) break;
-      const TileInfo &t = info[g & (INFOS - 1)];
-      const int held = t.held;
-      const uint32_t bad = t.bad;
-      const unsigned char *raw = smem + M::raw + s * M::raw_bytes + (is_v ? TILE * D : 0) + tid * 16;
-      unsigned char *out = smem + (is_v ? M::v : M::k + s * M::kv_bytes);
-      uint4 w[N];
+      ok = is_v ? wait(raw_v_full, (uint32_t)g & 1)
+                : wait(&raw_k_full[s], turn) && (g < STAGES || wait(&k_free[s], turn ^ 1u));
+      const int held = info[g & (INFOS - 1)].held;
+      const uint32_t bad = info[g & (INFOS - 1)].bad;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int nth = 2 * g + half, slot = nth % V_HALVES;
+        if (is_v && nth >= V_HALVES) ok = ok && wait(&v_free[slot], (uint32_t)(nth / V_HALVES - 1) & 1);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        const unsigned char *raw = smem + (is_v ? M::raw_v : M::raw_k + s * M::code_bytes) +
+                                   half * (HALF * D) + from;
+        unsigned char *out = smem + (is_v ? M::v + slot * M::half_bytes + block * (HALF * 128)
+                                          : M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128));
+        uint4 w[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + i * 2048);
-      if (held < TILE || bad) {  // what no page gave is not a number of ours
+        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + i * (STEP * D));
+        if (held < TILE || bad) {  // what no page gave is not a number of ours
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int key = half * HALF + key0 + i * STEP;
+            if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int key = key0 + i * STEP;
-          if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
+                make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
+                           code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
         }
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
-              make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
-                         code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
-      }
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(is_v ? v_full : &k_full[s]);
-        if (is_v) mbar_arrive(&raw_free[s]);
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          if (is_v) mbar_arrive(&v_full[slot]);
+          else if (half) mbar_arrive(&k_full[s]);
+          if (half) mbar_arrive(is_v ? raw_v_free : &raw_k_free[s]);
+        }
       }
     }
     }
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       constexpr uint32_t is = instruction(HALF, false), io = instruction(D, true);
       const uint32_t mine = elect_one();
       const uint32_t q_at = operand(smem + M::q, 16), k_at = operand(smem + M::k, 16),
-                     v_at = operand(smem + M::v, TILE * 128);
+                     v_at = operand(smem + M::v, HALF * 128);
       auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, wait(bar, parity)); };
       // half h of the tile whose K is in stage s
       auto scores = [&](int w, uint32_t s, int h) {
@@ -416,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       Cursor cur = cursor_at(a, prefix, group, lo);
       const int n = (int)(hi - lo);
       int g = 0;  // tiles of the stretch begun
-      uint32_t segment = 0;
+      uint32_t segment = 0, slot = 0, slot_turn = 0;  // of V's halves
       bool ok = true;
       while (ok && g < n) {
         const int count = min(cur.tiles - cur.tile, n - g);
@@ -434,19 +452,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           for (int i = 0; i < 4 && ok; ++i) {  // both halves of the tile, of the rows each
             const int w = i & 1, h = i >> 1;
             // what is there earliest first: a wait on a full barrier takes its time too
-            if (i == 0) {
-              ok = ready(v_full, g & 1);
-              if (ok && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-            }
+            if (i == 0 && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+            if (w == 0) ok = ok && ready(&v_full[slot], slot_turn);
             ok = ok && ready(&p_full[2 * w + h], g & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < HALF / 16; ++e)
               mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + HALF * h + 8 * e,
-                     operand_at(v_at + h * (HALF * 128 >> 4), e * 2048), io, j > 0 || h > 0 || e > 0, mine);
-            tc_commit(&o_done[w], mine);
-            if (i == 3) tc_commit(v_free, mine);
+                     operand_at(v_at + slot * (M::half_bytes >> 4), e * 2048), io, j > 0 || h > 0 || e > 0, mine);
+            tc_commit(&o_done[2 * w + h], mine);
+            if (w == 1) {
+              tc_commit(&v_free[slot], mine);
+              if (++slot == V_HALVES) {
+                slot = 0;
+                slot_turn ^= 1u;
+              }
+            }
             if (more) {
               scores(w, (g + 1) & 1, h);
               if (i == 3) tc_commit(&k_free[(g + 1) & 1], mine);
@@ -515,32 +537,47 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         after = take();
         asked = ask(after);
       }
-      int g = 0;
-      for (; g < n; ++g) {
-        const int s = g & 1;
-        if (g >= STAGES && !__all_sync(FULL, wait(&raw_free[s], (uint32_t)((g >> 1) & 1) ^ 1u))) break;
-        TileInfo &t = info[g & (INFOS - 1)];
-        const unsigned bad = __ballot_sync(FULL, lane < GROUPS && py.page < 0);
-        const bool starts = lane < GROUPS && (lane * 16) % PP == 0 && py.page >= 0;
+      auto copy = [&](const char *codes, const Place &p, const Pages &y, unsigned char *to, uint64_t *bar) {
+        const bool starts = lane < GROUPS && (lane * 16) % PP == 0 && y.page >= 0;
         const unsigned copies = __ballot_sync(FULL, starts);
-        if (lane < GROUPS) t.scale[lane] = make_float2(py.ks, log2f(py.vs));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(copies) * PP * D));
+        __syncwarp();
+        if (starts)
+          bulk_load(to + lane * 16 * D,
+                    codes + kv_tile(c, y.page, p.head) +
+                        (int64_t)((p.t0 + lane * 16) & (c.page_tokens - 1)) * D,
+                    PP * D, bar);
+      };
+      auto fetch_k = [&](int g, const Place &p, const Pages &y) {
+        const int s = g & 1;
+        if (g >= STAGES &&
+            !__all_sync(FULL, wait(&raw_k_free[s], (uint32_t)((g >> 1) & 1) ^ 1u)))
+          return false;
+        TileInfo &t = info[g & (INFOS - 1)];
+        const unsigned bad = __ballot_sync(FULL, lane < GROUPS && y.page < 0);
+        if (lane < GROUPS) t.scale[lane] = make_float2(y.ks, log2f(y.vs));
         if (lane == 0) {
           t.bad = bad;
-          t.held = min(now.len - now.t0, TILE);
+          t.held = min(p.len - p.t0, TILE);
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&info_full[g & (INFOS - 1)]);
-          mbar_arrive_expect_tx(&raw_full[s], (uint32_t)(__popc(copies) * 2 * PP * D));
+        if (lane == 0) mbar_arrive(&info_full[g & (INFOS - 1)]);
+        copy(kc, p, y, smem + M::raw_k + s * M::code_bytes, &raw_k_full[s]);
+        return true;
+      };
+      int k_sent = 0, v_sent = 0;
+      bool ok = fetch_k(0, now, py);
+      k_sent = ok;
+      for (int g = 0; g < n && ok; ++g) {
+        if (g + 1 < n) {
+          ok = fetch_k(g + 1, next, ny);
+          if (!ok) break;
+          k_sent = g + 2;
         }
-        __syncwarp();
-        if (starts) {
-          unsigned char *to = smem + M::raw + s * M::raw_bytes + lane * 16 * D;
-          const int64_t at = kv_tile(c, py.page, now.head) +
-                             (int64_t)((now.t0 + lane * 16) & (c.page_tokens - 1)) * D;
-          bulk_load(to, kc + at, PP * D, &raw_full[s]);
-          bulk_load(to + TILE * D, vc + at, PP * D, &raw_full[s]);
-        }
+        if (g >= 1) ok = __all_sync(FULL, wait(raw_v_free, (uint32_t)(g - 1) & 1));
+        if (!ok) break;
+        copy(vc, now, py, smem + M::raw_v, raw_v_full);
+        v_sent = g + 1;
         now = next;
         next = after;
         py = ny;
@@ -551,9 +588,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
       }
       // no copy may land after this CTA is gone
-      if (g < n)
-        for (int k = max(g - STAGES, 0); k < g; ++k)
-          mbar_wait(&raw_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
+      if (!ok) {
+        for (int k = max(k_sent - STAGES, 0); k < k_sent; ++k)
+          mbar_wait(&raw_k_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
+        if (v_sent) mbar_wait(raw_v_full, (uint32_t)(v_sent - 1) & 1, nullptr, a.wait_ns);
+      }
     }
     __syncwarp();
   } else {
@@ -622,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by
       uint64_t l = 0;                           // two halves of the sum
       auto rescale = [&](float by, int before) {  // the output so far, once instruction `before` is done
-        ok = __all_sync(FULL, wait(&o_done[w], (uint32_t)(before & 1)));
+        ok = __all_sync(FULL, wait(&o_done[2 * w + (before & 1)], (uint32_t)(before >> 1) & 1));
         if (!ok) return;
         tc_fence_after();
 #pragma unroll 1
@@ -744,7 +783,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
       if (!ok) break;
       // ---- finish the segment, or leave a part
-      ok = __all_sync(FULL, wait(&o_done[w], 1u));  // a tile's second half is an odd one
+      ok = __all_sync(FULL, wait(&o_done[2 * w + 1], (uint32_t)(x + count - 1) & 1));
       if (!ok) break;
       tc_fence_after();
       const float sum = low(l) + high(l);
