@@ -9,9 +9,10 @@
 // one half, the other half's 128 threads (one to a row) turn scores into probabilities:
 //   warps 0-3, 4-7  rows 0-127 and 128-255: references, exponentials, the final scaling
 //   warps 8-11      convert codes, store them swizzled
-//   warp 12         issues the matrix instructions
+//   warps 12, 14    issue the matrix instructions of a half each (one warp alone took 75
+//                   cycles an instruction)
 //   warp 13         looks up pages and scales, fetches codes with bulk copies two tiles ahead
-//                   (14 and 15 only complete the warpgroup)
+//                   (15 only completes the warpgroup)
 // A page's key scale is a factor of its scores, its value scale one of its probabilities.
 #include <algorithm>
 
@@ -197,7 +198,7 @@ struct Memory {
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + V_HALVES * half_bytes,
                        raw_v = raw_k + STAGES * code_bytes;
   static constexpr int info = raw_v + code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
-  static constexpr int barriers = 31 + INFOS;  // see the kernel's list of them
+  static constexpr int barriers = 32 + INFOS;  // see the kernel's list of them
   static constexpr int prefix = bars + barriers * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 9 * 48;
@@ -271,10 +272,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
   uint64_t *k_full = bars, *k_free = bars + 2, *raw_k_full = bars + 4, *raw_k_free = bars + 6,
-           *q_full = bars + 8, *last_bar = bars + 10, *raw_v_full = bars + 11, *raw_v_free = bars + 12,
-           *v_full = bars + 13, *v_free = bars + 16;
+           *q_full = bars + 8, *last = bars + 10, *raw_v_full = bars + 12, *raw_v_free = bars + 13,
+           *v_full = bars + 14, *v_free = bars + 17;
   // [2 w + half]: a row's thread may be two instructions ahead of the last one done
-  uint64_t *s_full = bars + 19, *p_full = bars + 23, *o_done = bars + 27, *info_full = bars + 31;
+  uint64_t *s_full = bars + 20, *p_full = bars + 24, *o_done = bars + 28, *info_full = bars + 32;
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
@@ -290,10 +291,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_free[i], 1);
+      mbar_init(&k_free[i], 2);
       mbar_init(&raw_k_full[i], 1);
       mbar_init(&raw_k_free[i], 4);
       mbar_init(&q_full[i], 4);
+      mbar_init(&last[i], 1);
     }
     for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
     for (int i = 0; i < 4; ++i) {
@@ -301,12 +303,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(last_bar, 1);
     mbar_init(raw_v_full, 1);
     mbar_init(raw_v_free, 4);
     for (int i = 0; i < V_HALVES; ++i) {
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 1);
+      mbar_init(&v_free[i], 2);
     }
     *abort = 0;
     mbar_init_fence();
@@ -415,21 +416,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     }
   } else if (warp >= ISSUE_WARP) {
     fewer_registers<ISSUE_REGS>();
-    if (work && warp == ISSUE_WARP) {
+    if (work && (warp == ISSUE_WARP || warp == ISSUE_WARP + 2)) {
       constexpr uint32_t is = instruction(HALF, false), io = instruction(D, true);
-      const uint32_t mine = elect_one();
-      const uint32_t q_at = operand(smem + M::q, 16), k_at = operand(smem + M::k, 16),
+      const int w = (warp - ISSUE_WARP) / 2;
+      const uint32_t mine = elect_one(), s_at = tmem + 128 * w, o_at = tmem + O_COL + 128 * w;
+      const uint32_t q_at = operand(smem + M::q + w * M::q_bytes, 16), k_at = operand(smem + M::k, 16),
                      v_at = operand(smem + M::v, HALF * 128);
       auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, wait(bar, parity)); };
       // half h of the tile whose K is in stage s
-      auto scores = [&](int w, uint32_t s, int h) {
-        const uint32_t q = q_at + w * (M::q_bytes >> 4),
-                       k = k_at + s * (M::kv_bytes >> 4) + h * (HALF * 128 >> 4);
+      auto scores = [&](uint32_t s, int h) {
+        const uint32_t k = k_at + s * (M::kv_bytes >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + 128 * w + HALF * h, operand_at(q, (i / 4) * (128 * 128) + (i % 4) * 32),
+          mma_ss(s_at + HALF * h, operand_at(q_at, (i / 4) * (128 * 128) + (i % 4) * 32),
                  operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0, mine);
         tc_commit(&s_full[2 * w + h], mine);
+        if (h) tc_commit(&k_free[s], mine);
       };
       Cursor cur = cursor_at(a, prefix, group, lo);
       const int n = (int)(hi - lo);
@@ -438,49 +440,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       bool ok = true;
       while (ok && g < n) {
         const int count = min(cur.tiles - cur.tile, n - g);
-        ok = ready(&k_full[g & 1], (g >> 1) & 1);
-#pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i) {
-          if (i < 2) ok = ready(&q_full[i & 1], segment & 1);
-          tc_fence_after();
-          if (ok) scores(i & 1, g & 1, i >> 1);
-        }
-        if (ok) tc_commit(&k_free[g & 1], mine);
+        ok = ready(&k_full[g & 1], (g >> 1) & 1) && ready(&q_full[w], segment & 1);
+        if (!ok) break;
+        tc_fence_after();
+        scores(g & 1, 0);
+        scores(g & 1, 1);
         for (int j = 0; j < count && ok; ++j, ++g) {
           const bool more = j + 1 < count;
 #pragma unroll 1
-          for (int i = 0; i < 4 && ok; ++i) {  // both halves of the tile, of the rows each
-            const int w = i & 1, h = i >> 1;
+          for (int h = 0; h < 2; ++h) {
             // what is there earliest first: a wait on a full barrier takes its time too
-            if (i == 0 && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-            if (w == 0) ok = ok && ready(&v_full[slot], slot_turn);
-            ok = ok && ready(&p_full[2 * w + h], g & 1);
+            if (h == 0 && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+            ok = ok && ready(&v_full[slot], slot_turn) && ready(&p_full[2 * w + h], g & 1);
             if (!ok) break;
             tc_fence_after();
+            const uint32_t v = v_at + slot * (M::half_bytes >> 4), first = j > 0 || h > 0;
 #pragma unroll
             for (int e = 0; e < HALF / 16; ++e)
-              mma_ts(tmem + O_COL + 128 * w, tmem + 128 * w + HALF * h + 8 * e,
-                     operand_at(v_at + slot * (M::half_bytes >> 4), e * 2048), io, j > 0 || h > 0 || e > 0, mine);
+              mma_ts(o_at, s_at + HALF * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first, mine);
             tc_commit(&o_done[2 * w + h], mine);
-            if (w == 1) {
-              tc_commit(&v_free[slot], mine);
-              if (++slot == V_HALVES) {
-                slot = 0;
-                slot_turn ^= 1u;
-              }
+            tc_commit(&v_free[slot], mine);
+            if (++slot == V_HALVES) {
+              slot = 0;
+              slot_turn ^= 1u;
             }
-            if (more) {
-              scores(w, (g + 1) & 1, h);
-              if (i == 3) tc_commit(&k_free[(g + 1) & 1], mine);
-            }
+            if (more) scores((g + 1) & 1, h);
           }
         }
         ++segment;
         if (ok && g < n) next_segment(a, prefix, group, cur);
       }
       // nothing may be left running when this CTA gives its memory back
-      tc_commit(last_bar, mine);
-      mbar_wait(last_bar, 0, nullptr, a.wait_ns);
+      tc_commit(&last[w], mine);
+      mbar_wait(&last[w], 0, nullptr, a.wait_ns);
       __syncwarp();
     }
     if (work && warp == FETCH_WARP) {
