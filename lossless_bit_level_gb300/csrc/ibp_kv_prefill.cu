@@ -25,8 +25,8 @@ namespace {
 constexpr int MB = 256;      // query rows of a segment
 constexpr int TILE = 128;    // tokens of a tile
 constexpr int GROUPS = TILE / 16;
-constexpr int STAGES = 2;    // tiles of K in fp16, and of its codes; of V's codes there is one
-constexpr int V_HALVES = 3;  // half tiles of V in fp16
+constexpr int STAGES = 2;    // tiles of K in fp16, of K's codes and of V's codes
+constexpr int V_HALVES = 2;  // half tiles of V in fp16
 constexpr int INFOS = 8;     // tiles whose scales are kept
 constexpr int BATCH = 128;   // sequences of one launch
 constexpr int THREADS = 16 * 32;
@@ -197,7 +197,7 @@ struct Memory {
   static constexpr int code_bytes = TILE * D;
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + V_HALVES * half_bytes,
                        raw_v = raw_k + STAGES * code_bytes;
-  static constexpr int info = raw_v + code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
+  static constexpr int info = raw_v + STAGES * code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
   static constexpr int barriers = 32 + INFOS;  // see the kernel's list of them
   static constexpr int prefix = bars + barriers * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   TileInfo *info = reinterpret_cast<TileInfo *>(smem + M::info);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::bars);
   uint64_t *k_full = bars, *k_free = bars + 2, *raw_k_full = bars + 4, *raw_k_free = bars + 6,
-           *q_full = bars + 8, *last = bars + 10, *raw_v_full = bars + 12, *raw_v_free = bars + 13,
-           *v_full = bars + 14, *v_free = bars + 17;
+           *q_full = bars + 8, *last = bars + 10, *raw_v_full = bars + 12, *raw_v_free = bars + 14,
+           *v_full = bars + 16, *v_free = bars + 18;
   // [2 w + half]: a row's thread may be two instructions ahead of the last one done
   uint64_t *s_full = bars + 20, *p_full = bars + 24, *o_done = bars + 28, *info_full = bars + 32;
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
@@ -294,6 +294,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_init(&k_free[i], 2);
       mbar_init(&raw_k_full[i], 1);
       mbar_init(&raw_k_free[i], 4);
+      mbar_init(&raw_v_full[i], 1);
+      mbar_init(&raw_v_free[i], 4);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_free[i], 2);
       mbar_init(&q_full[i], 4);
       mbar_init(&last[i], 1);
     }
@@ -302,12 +306,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
-    }
-    mbar_init(raw_v_full, 1);
-    mbar_init(raw_v_free, 4);
-    for (int i = 0; i < V_HALVES; ++i) {
-      mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 2);
     }
     *abort = 0;
     mbar_init_fence();
@@ -371,19 +369,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const bool is_v = step > 0 && (step % 2 == 0 || step == 2 * n - 1);
       const int g = is_v ? (step == 2 * n - 1 ? n - 1 : step / 2 - 1) : (step + 1) / 2, s = g & 1;
       const uint32_t turn = (uint32_t)(g >> 1) & 1;
-      ok = is_v ? wait(raw_v_full, (uint32_t)g & 1)
+      ok = is_v ? wait(&raw_v_full[s], turn)
                 : wait(&raw_k_full[s], turn) && (g < STAGES || wait(&k_free[s], turn ^ 1u));
       const int held = info[g & (INFOS - 1)].held;
       const uint32_t bad = info[g & (INFOS - 1)].bad;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const int nth = 2 * g + half, slot = nth % V_HALVES;
-        if (is_v && nth >= V_HALVES) ok = ok && wait(&v_free[slot], (uint32_t)(nth / V_HALVES - 1) & 1);
+        if (is_v && g >= 1) ok = ok && wait(&v_free[half], (uint32_t)(g - 1) & 1);
         ok = __all_sync(FULL, ok);
         if (!ok) break;
-        const unsigned char *raw = smem + (is_v ? M::raw_v : M::raw_k + s * M::code_bytes) +
+        const unsigned char *raw = smem + (is_v ? M::raw_v : M::raw_k) + s * M::code_bytes +
                                    half * (HALF * D) + from;
-        unsigned char *out = smem + (is_v ? M::v + slot * M::half_bytes + block * (HALF * 128)
+        unsigned char *out = smem + (is_v ? M::v + half * M::half_bytes + block * (HALF * 128)
                                           : M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128));
         uint4 w[N];
 #pragma unroll
@@ -407,9 +404,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) {
-          if (is_v) mbar_arrive(&v_full[slot]);
+          if (is_v) mbar_arrive(&v_full[half]);
           else if (half) mbar_arrive(&k_full[s]);
-          if (half) mbar_arrive(is_v ? raw_v_free : &raw_k_free[s]);
+          if (half) mbar_arrive(is_v ? &raw_v_free[s] : &raw_k_free[s]);
         }
       }
     }
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       Cursor cur = cursor_at(a, prefix, group, lo);
       const int n = (int)(hi - lo);
       int g = 0;  // tiles of the stretch begun
-      uint32_t segment = 0, slot = 0, slot_turn = 0;  // of V's halves
+      uint32_t segment = 0;
       bool ok = true;
       while (ok && g < n) {
         const int count = min(cur.tiles - cur.tile, n - g);
@@ -451,19 +448,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           for (int h = 0; h < 2; ++h) {
             // what is there earliest first: a wait on a full barrier takes its time too
             if (h == 0 && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-            ok = ok && ready(&v_full[slot], slot_turn) && ready(&p_full[2 * w + h], g & 1);
+            ok = ok && ready(&v_full[h], g & 1) && ready(&p_full[2 * w + h], g & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v = v_at + slot * (M::half_bytes >> 4), first = j > 0 || h > 0;
+            const uint32_t v = v_at + h * (M::half_bytes >> 4), first = j > 0 || h > 0;
 #pragma unroll
             for (int e = 0; e < HALF / 16; ++e)
               mma_ts(o_at, s_at + HALF * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first, mine);
             tc_commit(&o_done[2 * w + h], mine);
-            tc_commit(&v_free[slot], mine);
-            if (++slot == V_HALVES) {
-              slot = 0;
-              slot_turn ^= 1u;
-            }
+            tc_commit(&v_free[h], mine);
             if (more) scores((g + 1) & 1, h);
           }
         }
@@ -566,9 +559,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           if (!ok) break;
           k_sent = g + 2;
         }
-        if (g >= 1) ok = __all_sync(FULL, wait(raw_v_free, (uint32_t)(g - 1) & 1));
+        const int s = g & 1;
+        if (g >= STAGES) ok = __all_sync(FULL, wait(&raw_v_free[s], (uint32_t)((g >> 1) & 1) ^ 1u));
         if (!ok) break;
-        copy(vc, now, py, smem + M::raw_v, raw_v_full);
+        copy(vc, now, py, smem + M::raw_v + s * M::code_bytes, &raw_v_full[s]);
         v_sent = g + 1;
         now = next;
         next = after;
@@ -583,7 +577,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       if (!ok) {
         for (int k = max(k_sent - STAGES, 0); k < k_sent; ++k)
           mbar_wait(&raw_k_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
-        if (v_sent) mbar_wait(raw_v_full, (uint32_t)(v_sent - 1) & 1, nullptr, a.wait_ns);
+        for (int k = max(v_sent - STAGES, 0); k < v_sent; ++k)
+          mbar_wait(&raw_v_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
       }
     }
     __syncwarp();
