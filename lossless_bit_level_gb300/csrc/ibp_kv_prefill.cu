@@ -175,11 +175,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
 __device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
 
@@ -361,53 +356,68 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     int to[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) to[h] = key0 * 128 + (((2 * piece + h) ^ key0) & 7) * 16;
-    // K of tile 0, then K of tile g + 1 before V of tile g: the scores of a tile are wanted
-    // a tile before its values
-    bool ok = true;
-#pragma unroll 1
-    for (int step = 0; step < 2 * n && ok; ++step) {
-      const bool is_v = step > 0 && (step % 2 == 0 || step == 2 * n - 1);
-      const int g = is_v ? (step == 2 * n - 1 ? n - 1 : step / 2 - 1) : (step + 1) / 2, s = g & 1;
-      const uint32_t turn = (uint32_t)(g >> 1) & 1;
-      ok = is_v ? wait(&raw_v_full[s], turn)
-                : wait(&raw_k_full[s], turn) && (g < STAGES || wait(&k_free[s], turn ^ 1u));
-      const int held = info[g & (INFOS - 1)].held;
-      const uint32_t bad = info[g & (INFOS - 1)].bad;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (is_v && g >= 1) ok = ok && wait(&v_free[half], (uint32_t)(g - 1) & 1);
-        ok = __all_sync(FULL, ok);
-        if (!ok) break;
-        const unsigned char *raw = smem + (is_v ? M::raw_v : M::raw_k) + s * M::code_bytes +
-                                   half * (HALF * D) + from;
-        unsigned char *out = smem + (is_v ? M::v + half * M::half_bytes + block * (HALF * 128)
-                                          : M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128));
-        uint4 w[N];
+    int held = 0;
+    uint32_t bad = 0;
+    auto convert = [&](const unsigned char *raw, unsigned char *out, int half) {
+      uint4 w[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + i * (STEP * D));
-        if (held < TILE || bad) {  // what no page gave is not a number of ours
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int key = half * HALF + key0 + i * STEP;
-            if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
+      for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + from + i * (STEP * D));
+      if (held < TILE || bad) {  // what no page gave is not a number of ours
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const int key = half * HALF + key0 + i * STEP;
+          if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
-                make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
-                           code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+      for (int i = 0; i < N; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint4 *>(out + to[h] + i * (STEP * 128)) =
+              make_uint4(code_pair<CODE, 0>(u[2 * h]), code_pair<CODE, 1>(u[2 * h]),
+                         code_pair<CODE, 0>(u[2 * h + 1]), code_pair<CODE, 1>(u[2 * h + 1]));
+      }
+    };
+    auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, wait(bar, parity)); };
+    auto done = [&](uint64_t *bar, uint64_t *raw_bar) {
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar);
+        if (raw_bar) mbar_arrive(raw_bar);
+      }
+    };
+    // K of tile 0, then K of tile g + 1 before V of tile g: the scores of a tile are wanted
+    // a tile before its values
+#pragma unroll 1
+    for (int g = -1; g < n; ++g) {
+      if (g + 1 < n) {
+        const int s = (g + 1) & 1;
+        const uint32_t turn = (uint32_t)((g + 1) >> 1) & 1;
+        if (!ready(&raw_k_full[s], turn) || (g + 1 >= STAGES && !ready(&k_free[s], turn ^ 1u))) break;
+        held = info[(g + 1) & (INFOS - 1)].held;
+        bad = info[(g + 1) & (INFOS - 1)].bad;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+          convert(smem + M::raw_k + s * M::code_bytes + half * (HALF * D),
+                  smem + M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128), half);
+        done(&k_full[s], &raw_k_free[s]);
+      }
+      if (g >= 0) {
+        const int s = g & 1;
+        held = info[g & (INFOS - 1)].held;
+        bad = info[g & (INFOS - 1)].bad;
+        bool ok = ready(&raw_v_full[s], (uint32_t)(g >> 1) & 1);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (g >= 1) ok = ok && ready(&v_free[half], (uint32_t)(g - 1) & 1);
+          if (!ok) break;
+          convert(smem + M::raw_v + s * M::code_bytes + half * (HALF * D),
+                  smem + M::v + half * M::half_bytes + block * (HALF * 128), half);
+          done(&v_full[half], half ? &raw_v_free[s] : nullptr);
         }
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) {
-          if (is_v) mbar_arrive(&v_full[half]);
-          else if (half) mbar_arrive(&k_full[s]);
-          if (half) mbar_arrive(is_v ? &raw_v_free[s] : &raw_k_free[s]);
-        }
+        if (!ok) break;
       }
     }
     }
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
                                            least + (m - mv) > -60.0f);
         if (stands) {
           uint64_t sum_l = l;
-          float top = -INFINITY;
+          float most = 0.0f;  // the largest sum of a group: no probability in it is larger
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 sc = scale[k];
@@ -707,18 +717,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll
             for (int e = 16 * k; e < 16 * k + 16; e += 2) {
               const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
-              top = max3(top, low(y), high(y));
               const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
               sum = add2(sum, pair(p0, p1));
               p[e / 2] = pack2<IBP_FP16>(p0, p1);
             }
             const float back = exp2_fast(-(sc.y + (m - mv)));
             sum_l = fma2(sum, pair(back, back), sum_l);
+            most = fmaxf(most, low(sum) + high(sum));
           }
-          stands = __all_sync(FULL, top <= 15.0f);
+          stands = __all_sync(FULL, most <= 32768.0f);
           if (stands) {
             l = sum_l;
-            if (top > 8.0f) over = top;
+            if (most > 1024.0f) over = log2f(most);
           }
         }
         if (!stands) {  // masks, new references, then both exponents apart
