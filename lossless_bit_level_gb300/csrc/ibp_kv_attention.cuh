@@ -151,23 +151,23 @@ __device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, i
   return lo;
 }
 
-// Where the parts of a segment lie.
+// Where the parts of a segment lie. Only a segment's first CTA can have held another
+// segment before it.
 struct Parts {
-  Split split;
-  int64_t start;    // the segment's first tile
   int first, last;  // CTAs
+  int second;       // the first one's part is its second
 };
 __device__ __forceinline__ Parts parts_of(int64_t total, int64_t start, int tiles, int ctas) {
-  Parts p = {Split(total, ctas), start, 0, 0};
-  p.first = p.split.owner(start);
-  p.last = p.split.owner(start + tiles - 1);
+  const Split split(total, ctas);
+  Parts p;
+  p.first = split.owner(start);
+  p.last = split.owner(start + tiles - 1);
+  p.second = split.start(p.first) < start;
   return p;
 }
-// Only a segment's first CTA can have held another segment before it.
 template <int MB, int D>
 __device__ __forceinline__ const float *part_at(const AttentionArgs &a, const Parts &p, int cta) {
-  const int second = cta == p.first ? p.split.start(cta) < p.start : 0;
-  return a.part + ((int64_t)cta * 2 + second) * ((int64_t)MB * (D + 4));
+  return a.part + ((int64_t)cta * 2 + (cta == p.first ? p.second : 0)) * ((int64_t)MB * (D + 4));
 }
 
 // (m, mv, l) of one row over all parts: a warp's lanes take every 32nd part, then a
@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
   __shared__ float lse2[MB];
+  __shared__ Parts where;
   __shared__ int64_t prefix[2];  // tiles before sequence b and in all
   const int b = blockIdx.z, head = blockIdx.y;
   const int group = a.q.q_heads / a.c.n_heads;
@@ -238,12 +239,12 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
     const int from = blockIdx.x % SHARE * (MB / SHARE), rows = min(from + MB / SHARE, all - r0);
     if (rows <= from) return;
     const int tiles = plan.tiles(block);
-    Parts p = {Split(1, 1), 0, 0, 0};
-    if (tiles > 0) {
-      p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
-                   tiles, a.ctas);
-      if (p.first == p.last) return;
-    }
+    if (threadIdx.x == 0 && tiles > 0)
+      where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
+                       tiles, a.ctas);
+    __syncthreads();
+    const Parts p = where;
+    if (tiles > 0 && p.first == p.last) return;
     grid_dependency_wait();
     for (int u = threadIdx.x + from * (D / 4); u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
       float sum = 0.0f, top = 0.0f;
       if (tiles > 0) {
         // parts in the order of their CTAs, AHEAD of them loaded at a time
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = MB > 64 ? 2 : 4;  // many rows are cut in two, few in many
         float topv = NONE;
         top = NONE;
         for (int k0 = p.first; k0 <= p.last; k0 += AHEAD) {
@@ -309,9 +310,12 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
     for (int r0 = 0; r0 < all; r0 += MB) {
       const int rows = min(MB, all - r0);
       const int block = r0 / MB;
-      const Parts p = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
-                               plan.tiles(block), a.ctas);
       __syncthreads();
+      if (threadIdx.x == 0)
+        where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
+                         plan.tiles(block), a.ctas);
+      __syncthreads();
+      const Parts p = where;
       for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
         const int rr = r0 + r;
         float z;

@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&q_full[w]);
       }
       const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
-      float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by
+      float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by,
+      bool pending = false;                     // if any row's are
       uint64_t l = 0;                           // two halves of the sum
       auto rescale = [&](float by, int before) {  // the output so far, once instruction `before` is done
         ok = __all_sync(FULL, wait(&o_done[2 * w + (before & 1)], (uint32_t)(before >> 1) & 1));
@@ -684,14 +685,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
         const uint32_t at = sp + HALF * h;
         uint32_t s[HALF], p[HALF / 2];
-        if (__any_sync(FULL, over > 0.0f)) {
+        if (pending) {
           const float by = exp2_fast(-over);
           rescale(by, u - 1);
           if (!ok) break;
           m += over;
           mv += over;
           l = mul2(l, pair(by, by));
-          over = 0.0f;
         }
         tmem_load32(at, s);
         tmem_load32(at + 32, s + 32);
@@ -702,35 +702,32 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         // exponential a score and one a group for the sum. It stands if every row has a
         // reference, sees all 64 tokens, has no value scale so small that the first could
         // vanish with the second still counting, and nothing passed fp16's range.
-        const float least = fminf(fminf(scale[0].y, scale[1].y), fminf(scale[2].y, scale[3].y));
-        bool stands = __all_sync(FULL, seen >= HALF && bad == 0 && m > 0.5f * NONE &&
-                                           least + (m - mv) > -60.0f);
-        if (stands) {
-          uint64_t sum_l = l;
-          float most = 0.0f;  // the largest sum of a group: no probability in it is larger
+        uint64_t sum_l = l;
+        // the largest sum of a group: no probability in it is larger
+        float most = seen >= HALF && bad == 0 ? 0.0f : INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 sc = scale[k];
-            const float f = rowc * sc.x, up = sc.y - mv;
-            const uint64_t ff = pair(f, f), uu = pair(up, up);
-            uint64_t sum = 0;
+        for (int k = 0; k < 4; ++k) {
+          const float2 sc = scale[k];
+          const float f = rowc * sc.x, up = sc.y - mv;
+          const uint64_t ff = pair(f, f), uu = pair(up, up);
+          uint64_t sum = 0;
 #pragma unroll
-            for (int e = 16 * k; e < 16 * k + 16; e += 2) {
-              const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
-              const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-              sum = add2(sum, pair(p0, p1));
-              p[e / 2] = pack2<IBP_FP16>(p0, p1);
-            }
-            const float back = exp2_fast(-(sc.y + (m - mv)));
-            sum_l = fma2(sum, pair(back, back), sum_l);
-            most = fmaxf(most, low(sum) + high(sum));
+          for (int e = 16 * k; e < 16 * k + 16; e += 2) {
+            const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
+            const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+            sum = add2(sum, pair(p0, p1));
+            p[e / 2] = pack2<IBP_FP16>(p0, p1);
           }
-          stands = __all_sync(FULL, most <= 32768.0f);
-          if (stands) {
-            l = sum_l;
-            if (most > 1024.0f) over = log2f(most);
-          }
+          const float back = exp2_fast(-(sc.y + (m - mv)));
+          sum_l = fma2(sum, pair(back, back), sum_l);
+          most = fmaxf(most, fmaxf(low(sum) + high(sum), back <= 0x1p60f ? 0.0f : INFINITY));
         }
+        // (a row of NaN has no largest sum and stands; its output is NaN either way)
+        const uint32_t top = __reduce_max_sync(FULL, __float_as_uint(most));
+        const bool stands = top <= __float_as_uint(32768.0f);
+        pending = stands && top > __float_as_uint(1024.0f);
+        if (stands) l = sum_l;
+        if (pending) over = most > 1024.0f ? log2f(most) : 0.0f;
         if (!stands) {  // masks, new references, then both exponents apart
           float mn = m, mvn = mv;
 #pragma unroll
