@@ -193,7 +193,8 @@ __device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &
 }
 
 constexpr int FINISH_THREADS = 128;
-constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS;
+constexpr int WEIGHT_CHUNKS = 2;  // of 4 tokens a thread
+constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS * WEIGHT_CHUNKS;
 // CTAs that share a segment's rows, 64 at most to one.
 template <typename Plan>
 constexpr int FINISH_SHARE = Plan::MB <= 64 ? 1 : Plan::MB / 64;
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
   __shared__ float lse2[MB];
+  __shared__ int64_t score_at[SCORES ? MB : 1];  // first score of each row
   __shared__ Parts where;
   __shared__ int64_t prefix[2];  // tiles before sequence b and in all
   const int b = blockIdx.z, head = blockIdx.y;
@@ -299,13 +301,18 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
     return;
   }
   if constexpr (SCORES) {
-    const int t = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
-    if (((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS >= s.len) return;
-    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t;
-    float sum[4];
+    const int t0 = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
+    constexpr int STEP = 4 * FINISH_THREADS;
+    if (t0 - 4 * (int)threadIdx.x >= s.len) return;
+    const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t0;
+    float sum[WEIGHT_CHUNKS][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      sum[e] = a.q.d_weights_in && t + e < s.len ? a.q.decay * a.q.d_weights_in[at + e] : 0.0f;
+    for (int k = 0; k < WEIGHT_CHUNKS; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[k][e] = a.q.d_weights_in && t0 + k * STEP + e < s.len
+                        ? a.q.decay * a.q.d_weights_in[at + k * STEP + e]
+                        : 0.0f;
     grid_dependency_wait();
     for (int r0 = 0; r0 < all; r0 += MB) {
       const int rows = min(MB, all - r0);
@@ -314,36 +321,45 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
       if (threadIdx.x == 0)
         where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
                          plan.tiles(block), a.ctas);
+      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) {
+        const int rr = r0 + r;
+        score_at[r] = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
+      }
       __syncthreads();
       const Parts p = where;
       for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
-        const int rr = r0 + r;
         float z;
         if (p.first == p.last) {
-          z = a.lse2[(s.row0 + rr / group) * a.q.q_heads + head * group + rr % group];
+          z = a.lse2[score_at[r]];
         } else {
           const float4 st = join_row<MB, D>(a, p, r);
           z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
         }
         lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) score_at[r] *= a.score_cols;
       }
       __syncthreads();
-      if (t < s.len) {
 #pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-          const int rr = r0 + r;
-          const int64_t row = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
-          const float4 z = *reinterpret_cast<const float4 *>(a.scores + row * a.score_cols + t);
-          sum[0] += exp2_fast(z.x - lse2[r]);
-          sum[1] += exp2_fast(z.y - lse2[r]);
-          sum[2] += exp2_fast(z.z - lse2[r]);
-          sum[3] += exp2_fast(z.w - lse2[r]);
-        }
+      for (int r = 0; r < rows; ++r) {
+        const float *from = a.scores + score_at[r] + t0;
+        const float z = lse2[r];
+#pragma unroll
+        for (int k = 0; k < WEIGHT_CHUNKS; ++k)
+          if (t0 + k * STEP < s.len) {
+            const float4 x = *reinterpret_cast<const float4 *>(from + k * STEP);
+            sum[k][0] += exp2_fast(x.x - z);
+            sum[k][1] += exp2_fast(x.y - z);
+            sum[k][2] += exp2_fast(x.z - z);
+            sum[k][3] += exp2_fast(x.w - z);
+          }
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (t + e < s.len) a.q.d_weights[at + e] = sum[e];
+    for (int k = 0; k < WEIGHT_CHUNKS; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t0 + k * STEP + e < s.len) a.q.d_weights[at + k * STEP + e] = sum[k][e];
   }
 }
 
