@@ -6,8 +6,8 @@
 // both are multiplied by 2^(old - new) whenever a reference rises, and the output is
 // o 2^(mv - m) / l. The value scale enters the exponent, with a reference mv of its own,
 // so that the second product's factors stay within fp16 whatever the scales of the
-// pages are; a reference only rises once a score passes it by 2^8 (a vote a slab instead
-// of a maximum across lanes; fp16 and fp32 have the room).
+// pages are; a reference only rises once the largest score has grown by 2^8 (a vote a slab
+// instead of a maximum across lanes; fp16 and fp32 have the room).
 #include <algorithm>
 
 #include "ibp_kv_attention.cuh"
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
             }
             acc[k][w] = y0;
             acc[k][w + 2] = y1;
-            rise |= fmaxf(y0, y1) > fminf(m[k][w], mv[k][w] - info.lv) + 8.0f;
+            rise |= fmaxf(y0, y1) > fminf(m[k][w], mv[k][w] + SHIFT - info.lv) + 8.0f;
             if constexpr (SCORES) {
               if (wq * 8 * NT + 8 * k + 2 * t4 + w < rows) {
                 score[k][w][t0 + g] = y0;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
             for (int w = 0; w < 2; ++w) {
               float top = fmaxf(acc[k][w], acc[k][w + 2]);
               for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, sh));
-              const float mn = fmaxf(m[k][w], top), mvn = fmaxf(mv[k][w], top + info.lv);
+              const float mn = fmaxf(m[k][w], top), mvn = fmaxf(mv[k][w], top + info.lv - SHIFT);
               const float fl = exp2_fast(m[k][w] - mn), fo = exp2_fast(mv[k][w] - mvn);
               m[k][w] = mn;
               mv[k][w] = mvn;

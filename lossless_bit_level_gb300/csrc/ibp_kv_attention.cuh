@@ -11,6 +11,9 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NONE = -1e30f;  // reference of a row that has seen no token yet
+// A reference of the second product is set so that the largest factor is 2^SHIFT: fp16
+// then holds factors 2^-31 of the largest, and there is room for it to grow by 2^8.
+constexpr float SHIFT = 7.0f;
 
 constexpr int MAX_BATCH = 256;  // sequences of one launch (their tile counts are in shared memory)
 constexpr int MAX_CTAS = 512;          // three to each of 152 SMs, and some

@@ -38,6 +38,10 @@ constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12, FETCH_WARP = 13;
 // it) at 128 w + 64 (half), O at 256 + 128 w.
 constexpr int HALF = 64;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
+// The largest factor of a row when its reference is set is 2^ROW_SHIFT (from a sum of 16
+// factors: between that and 2^4 times it). Lower than SHIFT: here a row that outgrows its
+// reference costs the whole warp (2048 rows over 8192 tokens: 306 us with 7, 277 with 4).
+constexpr float ROW_SHIFT = 2.0f;
 using Plan = CausalPlan<MB, TILE>;
 
 // ---- tensor memory and the matrix instruction
@@ -725,9 +729,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         // (a row of NaN has no largest sum and stands; its output is NaN either way)
         const uint32_t top = __reduce_max_sync(FULL, __float_as_uint(most));
         const bool stands = top <= __float_as_uint(32768.0f);
-        pending = stands && top > __float_as_uint(1024.0f);
+        pending = stands && top > __float_as_uint(16384.0f);
         if (stands) l = sum_l;
-        if (pending) over = most > 1024.0f ? log2f(most) : 0.0f;
+        if (pending) over = most > 16384.0f ? log2f(most) - (4.0f + ROW_SHIFT) : 0.0f;
         if (!stands) {  // masks, new references, then both exponents apart
           float mn = m, mvn = mv;
 #pragma unroll
@@ -739,7 +743,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
             top *= rowc * scale[k].x;
             mn = fmaxf(mn, top);
-            mvn = fmaxf(mvn, top + scale[k].y);
+            mvn = fmaxf(mvn, top + scale[k].y - ROW_SHIFT);
           }
           if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
             const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
