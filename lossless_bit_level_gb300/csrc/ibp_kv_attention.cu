@@ -37,6 +37,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// Within a rare branch: keeps it from being turned into selects that every pass goes through.
+__device__ __forceinline__ void stay_a_branch() { asm volatile("" ::: "memory"); }
+
 // Codes to fp16, exactly. int8: the byte of code + 128 below 0x64 is 1024 + 128 + code.
 template <int CODE>
 __device__ __forceinline__ uint32_t code_bias(uint32_t w) {
@@ -312,11 +315,41 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
         const int t0 = tile * TILE + slab * SLAB;
         if (t0 >= sq.len) break;
         const SlabInfo info = slabs[s * NS + slab];
-        float acc[NT][4];
+        const bool whole = info.n == SLAB && t0 + SLAB <= least;
+        // values: lane (g, t) holds D/8 consecutive elements of tokens 2t, 2t+1, 2t+8, 2t+9;
+        // asked for before the scores where registers allow (82 -> 78 us for 48 ragged
+        // sequences of 64 elements a head; at 128 they spill: 61 -> 65 us for a layer)
+        constexpr bool EARLY = D == 64;
+        uint32_t v[4][D / 32];
+        auto load_values = [&] {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 2 * t4 + (e & 1) + 8 * (e >> 1);
+            const unsigned char *p = vt + (slab * SLAB + row) * D + g * (D / 8);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(p);
+              v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2 *>(p);
+              v[e][0] = w.x; v[e][1] = w.y;
+            }
+          }
+          if (!whole) {  // what lies past the length is not a number of ours
+            stay_a_branch();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (2 * t4 + (e & 1) + 8 * (e >> 1) >= info.n)
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) v[e][w] = 0u;
+          }
+        };
+        if constexpr (EARLY) load_values();
+        // two chains of products, added at the end: a chain waits for each of its own
+        float acc[NT][4], odd[NT][4];
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) acc[k][e] = odd[k][e] = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const unsigned char *at = kt + (slab * SLAB + g) * D + 16 * (t4 + 4 * j);
@@ -330,30 +363,43 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
                            a2 = code_pair<CODE, 1>(ua), a3 = code_pair<CODE, 1>(ub);
 #pragma unroll
             for (int k = 0; k < NT; ++k)
-              mma16816(acc[k], a0, a1, a2, a3, qb[k][4 * j + e][0], qb[k][4 * j + e][1]);
+              mma16816(e & 1 ? odd[k] : acc[k], a0, a1, a2, a3, qb[k][4 * j + e][0], qb[k][4 * j + e][1]);
           }
         }
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[k][e] += odd[k][e];
         // scores of tokens g, g + 8 and rows 2t, 2t + 1
-        const bool whole = info.n == SLAB && t0 + SLAB <= least;
-        bool rise = false;
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const float f = rowc[k][w] * info.ks;
-            float y0 = acc[k][w] * f, y1 = acc[k][w + 2] * f;
-            if (!whole) {
+            acc[k][w] *= f;
+            acc[k][w + 2] *= f;
+          }
+        if (!whole) {
+          stay_a_branch();
+#pragma unroll
+          for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
               const int seen = min(limit[k][w] - t0, info.n);
-              if (g >= seen) y0 = -INFINITY;
-              if (g + 8 >= seen) y1 = -INFINITY;
+              if (g >= seen) acc[k][w] = -INFINITY;
+              if (g + 8 >= seen) acc[k][w + 2] = -INFINITY;
             }
-            acc[k][w] = y0;
-            acc[k][w + 2] = y1;
-            rise |= fmaxf(y0, y1) > fminf(m[k][w], mv[k][w] + SHIFT - info.lv) + 8.0f;
+        }
+        bool rise = false;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            rise |= fmaxf(acc[k][w], acc[k][w + 2]) > fminf(m[k][w], mv[k][w] + SHIFT - info.lv) + 8.0f;
             if constexpr (SCORES) {
               if (wq * 8 * NT + 8 * k + 2 * t4 + w < rows) {
-                score[k][w][t0 + g] = y0;
-                score[k][w][t0 + g + 8] = y1;
+                score[k][w][t0 + g] = acc[k][w];
+                score[k][w][t0 + g + 8] = acc[k][w + 2];
               }
             }
           }
@@ -388,23 +434,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
           pb[k][0] = transpose8(pack2<IBP_FP16>(p[0], p[1]));
           pb[k][1] = transpose8(pack2<IBP_FP16>(p[2], p[3]));
         }
-        // values: lane (g, t) holds D/8 consecutive elements of tokens 2t, 2t+1, 2t+8, 2t+9
-        uint32_t v[4][D / 32];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 2 * t4 + (e & 1) + 8 * (e >> 1);
-          const unsigned char *p = vt + (slab * SLAB + row) * D + g * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(p);
-            v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p);
-            v[e][0] = w.x; v[e][1] = w.y;
-          }
-          if (!whole && row >= info.n)  // what lies past the length is not a number of ours
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) v[e][w] = 0u;
-        }
+        if constexpr (!EARLY) load_values();
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           const uint32_t u0 = code_bias<CODE>(v[0][w]), u1 = code_bias<CODE>(v[1][w]);
