@@ -204,8 +204,12 @@ constexpr int FINISH_SHARE = Plan::MB <= 64 ? 1 : Plan::MB / 64;
 
 // Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
 // sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
+// Parts loaded at a time: a long sequence with few rows is cut into dozens and waits for
+// them in turn, many rows are cut in two. (The CTAs that add up weights need the registers.)
+template <typename Plan, bool SCORES>
+constexpr int JOIN_AHEAD = Plan::MB > 64 ? 2 : SCORES || Plan::MB > 16 ? 4 : 16;
 template <int D, int DT, typename Plan, bool SCORES>
-__global__ void __launch_bounds__(FINISH_THREADS, 8)
+__global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
   __shared__ float lse2[MB];
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, 8)
       float sum = 0.0f, top = 0.0f;
       if (tiles > 0) {
         // parts in the order of their CTAs, AHEAD of them loaded at a time
-        constexpr int AHEAD = MB > 64 ? 2 : 4;  // many rows are cut in two, few in many
+        constexpr int AHEAD = JOIN_AHEAD<Plan, SCORES>;
         float topv = NONE;
         top = NONE;
         for (int k0 = p.first; k0 <= p.last; k0 += AHEAD) {
