@@ -38,6 +38,13 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// What the joining kernel for many rows needs of a CTA's place: the segment its stretch
+// begins in (tile: how many of the segment's tiles lie before it; 0: none).
+struct Cut {
+  int64_t total;  // tiles of the launch
+  int b, head, block, tile, tiles, unused;
+};
+
 struct AttentionArgs {
   ibp_kv_cache c;
   ibp_kv_query q;
@@ -47,6 +54,7 @@ struct AttentionArgs {
   float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
   float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
   float *scores;    // [n_rows][q_heads][score_cols], or null
+  Cut *cuts;        // [ctas] (many rows)
 };
 
 struct Sequence {
@@ -198,16 +206,12 @@ __device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &
 constexpr int FINISH_THREADS = 128;
 constexpr int WEIGHT_CHUNKS = 2;  // of 4 tokens a thread
 constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS * WEIGHT_CHUNKS;
-// CTAs that share a segment's rows, 64 at most to one.
-template <typename Plan>
-constexpr int FINISH_SHARE = Plan::MB <= 64 ? 1 : Plan::MB / 64;
-
 // Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
 // sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
 // Parts loaded at a time: a long sequence with few rows is cut into dozens and waits for
-// them in turn, many rows are cut in two. (The CTAs that add up weights need the registers.)
+// them in turn. (The CTAs that add up weights need the registers.)
 template <typename Plan, bool SCORES>
-constexpr int JOIN_AHEAD = Plan::MB > 64 ? 2 : SCORES || Plan::MB > 16 ? 4 : 16;
+constexpr int JOIN_AHEAD = SCORES || Plan::MB > 16 ? 4 : 16;
 template <int D, int DT, typename Plan, bool SCORES>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
@@ -243,10 +247,8 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   }
   __syncthreads();
   if ((int)blockIdx.x < row_blocks) {
-    constexpr int SHARE = FINISH_SHARE<Plan>;
-    const int block = blockIdx.x / SHARE, r0 = block * MB;
-    const int from = blockIdx.x % SHARE * (MB / SHARE), rows = min(from + MB / SHARE, all - r0);
-    if (rows <= from) return;
+    const int block = blockIdx.x, r0 = block * MB, rows = min(MB, all - r0);
+    if (rows <= 0) return;
     const int tiles = plan.tiles(block);
     if (threadIdx.x == 0 && tiles > 0)
       where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
     const Parts p = where;
     if (tiles > 0 && p.first == p.last) return;
     grid_dependency_wait();
-    for (int u = threadIdx.x + from * (D / 4); u < rows * (D / 4); u += FINISH_THREADS) {
+    for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
       const int64_t row = s.row0 + rr / group;
       const int qh = head * group + rr % group;

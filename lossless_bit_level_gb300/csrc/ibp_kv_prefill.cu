@@ -599,237 +599,309 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   } else {
     more_registers<ROW_REGS>();
     if (work) {
-    // ---- one thread to a row
-    const int w = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-    const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
-    unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
-    Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
-    if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
-    __syncwarp();
-    const int n_tiles = (int)(hi - lo), r = w * 128 + row;
-    int x = 0;  // tiles of the stretch done
-    bool ok = true;
-    while (ok && x < n_tiles) {
-      const int tile0 = cur->tile, count = min(cur->tiles - tile0, n_tiles - x);
-      const bool live = cur->block * MB + r < cur->seq.n * group;
-      const int rr = cur->block * MB + r;
-      // the row in fp16, brought to a largest magnitude in [1, 2) by a power of two (bf16);
-      // the sign of the scale goes with it, so that factors of scores are never negative
-      float rowc = 0.0f;
-      {
-        const char *src = static_cast<const char *>(a.q.q) +
-                          2 * ((cur->seq.row0 + rr / group) * a.q.q_row_stride +
-                               (cur->head * group + rr % group) * a.q.q_head_stride);
-        Raw16<DT> y[D / 16];
-        uint32_t most = 0;
+      // ---- one thread to a row
+      const int w = warp >> 2, row = threadIdx.x & 127;
+      const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+      const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
+      unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
+      Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
+      if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+      __syncwarp();
+      if (threadIdx.x == 0) {
+        const Cut cut = {prefix[a.batch], cur->b, cur->head, cur->block, cur->tile, cur->tiles, 0};
+        a.cuts[cta] = cut;
+      }
+      const int n_tiles = (int)(hi - lo), r = w * 128 + row;
+      int x = 0;  // tiles of the stretch done
+      bool ok = true;
+      while (ok && x < n_tiles) {
+        const int tile0 = cur->tile, count = min(cur->tiles - tile0, n_tiles - x);
+        const bool live = cur->block * MB + r < cur->seq.n * group;
+        const int rr = cur->block * MB + r;
+        // the row in fp16, brought to a largest magnitude in [1, 2) by a power of two (bf16);
+        // the sign of the scale goes with it, so that factors of scores are never negative
+        float rowc = 0.0f;
+        {
+          const char *src = static_cast<const char *>(a.q.q) +
+                            2 * ((cur->seq.row0 + rr / group) * a.q.q_row_stride +
+                                 (cur->head * group + rr % group) * a.q.q_head_stride);
+          Raw16<DT> y[D / 16];
+          uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          y[i].clear();
-          if (live) y[i].load(src + 32 * i);
+          for (int i = 0; i < D / 16; ++i) {
+            y[i].clear();
+            if (live) y[i].load(src + 32 * i);
+          }
+          float up = a.q.scale < 0.0f ? -1.0f : 1.0f, down = 1.0f;
+          if constexpr (DT == IBP_BF16) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) most = y[i].largest(most);
+            const int e = min(max((int)(Raw16<DT>::fold(most) >> 7) - 127, -120), 120);
+            up *= __uint_as_float((uint32_t)(127 - e) << 23);
+            down = __uint_as_float((uint32_t)(127 + e) << 23);
+          }
+          rowc = down * (fabsf(a.q.scale) * LOG2E);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float f[4];
+              y[i].four(k, f);
+              v[2 * k] = pack2<IBP_FP16>(f[0] * up, f[1] * up);
+              v[2 * k + 1] = pack2<IBP_FP16>(f[2] * up, f[3] * up);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int at = 2 * i + h;
+              *reinterpret_cast<uint4 *>(q_to + (at / 8) * (128 * 128) + ((at ^ row) & 7) * 16) =
+                  make_uint4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            }
+          }
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[w]);
         }
-        float up = a.q.scale < 0.0f ? -1.0f : 1.0f, down = 1.0f;
-        if constexpr (DT == IBP_BF16) {
+        const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
+        float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by,
+        bool pending = false;                     // if any row's are
+        uint64_t l = 0;                           // two halves of the sum
+        auto rescale = [&](float by, int before) {  // the output so far, once instruction `before` is done
+          ok = __all_sync(FULL, wait(&o_done[2 * w + (before & 1)], (uint32_t)(before >> 1) & 1));
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t y[16];
+            tmem_load16(op + 16 * k, y);
+            tmem_wait16(y);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) most = y[i].largest(most);
-          const int e = min(max((int)(Raw16<DT>::fold(most) >> 7) - 127, -120), 120);
-          up *= __uint_as_float((uint32_t)(127 - e) << 23);
-          down = __uint_as_float((uint32_t)(127 + e) << 23);
-        }
-        rowc = down * (fabsf(a.q.scale) * LOG2E);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t v[8];
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * by);
+            tmem_store16(op + 16 * k, y);
+          }
+          tmem_wait_store();
+        };
+#pragma unroll 1
+        for (int j = 0; j < 2 * count; ++j) {
+          const int u = 2 * x + j, g = u >> 1, h = u & 1;  // halves of tiles done, the tile, its half
+          ok = __all_sync(FULL, (h || wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1))) &&
+                                    wait(&s_full[2 * w + h], (uint32_t)(g & 1)));
+          if (!ok) break;
+          tc_fence_after();
+          const float2 *scale = info[g & (INFOS - 1)].scale + 4 * h;
+          const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
+          const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
+          const uint32_t at = sp + HALF * h;
+          uint32_t s[HALF], p[HALF / 2];
+          if (pending) {
+            const float by = exp2_fast(-over);
+            rescale(by, u - 1);
+            if (!ok) break;
+            m += over;
+            mv += over;
+            l = mul2(l, pair(by, by));
+          }
+          tmem_load32(at, s);
+          tmem_load32(at + 32, s + 32);
+          tmem_wait32(s);
+          tmem_wait32(s + 32);
+          // With the references as they are: a probability with its value scale is
+          // 2^(x + lv - mv), and the probability itself that times 2^(mv - m - lv), so one
+          // exponential a score and one a group for the sum. It stands if every row has a
+          // reference, sees all 64 tokens, has no value scale so small that the first could
+          // vanish with the second still counting, and nothing passed fp16's range.
+          uint64_t sum_l = l;
+          // the largest sum of a group: no probability in it is larger
+          float most = seen >= HALF && bad == 0 ? 0.0f : INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float f[4];
-            y[i].four(k, f);
-            v[2 * k] = pack2<IBP_FP16>(f[0] * up, f[1] * up);
-            v[2 * k + 1] = pack2<IBP_FP16>(f[2] * up, f[3] * up);
-          }
+            const float2 sc = scale[k];
+            const float f = rowc * sc.x, up = sc.y - mv;
+            const uint64_t ff = pair(f, f), uu = pair(up, up);
+            uint64_t sum = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int at = 2 * i + h;
-            *reinterpret_cast<uint4 *>(q_to + (at / 8) * (128 * 128) + ((at ^ row) & 7) * 16) =
-                make_uint4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            for (int e = 16 * k; e < 16 * k + 16; e += 2) {
+              const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
+              const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
+              sum = add2(sum, pair(p0, p1));
+              p[e / 2] = pack2<IBP_FP16>(p0, p1);
+            }
+            const float back = exp2_fast(-(sc.y + (m - mv)));
+            sum_l = fma2(sum, pair(back, back), sum_l);
+            most = fmaxf(most, fmaxf(low(sum) + high(sum), back <= 0x1p60f ? 0.0f : INFINITY));
           }
-        }
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[w]);
-      }
-      const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
-      float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by,
-      bool pending = false;                     // if any row's are
-      uint64_t l = 0;                           // two halves of the sum
-      auto rescale = [&](float by, int before) {  // the output so far, once instruction `before` is done
-        ok = __all_sync(FULL, wait(&o_done[2 * w + (before & 1)], (uint32_t)(before >> 1) & 1));
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t y[16];
-          tmem_load16(op + 16 * k, y);
-          tmem_wait16(y);
+          // (a row of NaN has no largest sum and stands; its output is NaN either way)
+          const uint32_t top = __reduce_max_sync(FULL, __float_as_uint(most));
+          const bool stands = top <= __float_as_uint(32768.0f);
+          pending = stands && top > __float_as_uint(16384.0f);
+          if (stands) l = sum_l;
+          if (pending) over = most > 16384.0f ? log2f(most) - (4.0f + ROW_SHIFT) : 0.0f;
+          if (!stands) {  // masks, new references, then both exponents apart
+            float mn = m, mvn = mv;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * by);
-          tmem_store16(op + 16 * k, y);
+            for (int k = 0; k < 4; ++k) {
+              const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
+              float top = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = e < n ? fmaxf(top, __uint_as_float(s[16 * k + e])) : top;
+              // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
+              top *= rowc * scale[k].x;
+              mn = fmaxf(mn, top);
+              mvn = fmaxf(mvn, top + scale[k].y - ROW_SHIFT);
+            }
+            if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
+              const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
+              m = mn;
+              mv = mvn;
+              l = mul2(l, pair(fl, fl));
+              if (j > 0) {
+                rescale(fo, u - 1);
+                if (!ok) break;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float f = rowc * scale[k].x, gv = exp2_fast(fminf(scale[k].y + (m - mv), 120.0f));
+              const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
+              float sum = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float p0 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e]), f, -m));
+                float p1 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e + 1]), f, -m));
+                p0 = e < n ? p0 : 0.0f;
+                p1 = e + 1 < n ? p1 : 0.0f;
+                sum += p0 + p1;
+                p[8 * k + e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
+              }
+              l = add2(l, pair(sum, 0.0f));
+            }
+          }
+          tmem_store16(at, p);  // over columns that have been read
+          tmem_store16(at + 16, p + 16);
+          tmem_wait_store();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * w + h]);
         }
-        tmem_wait_store();
-      };
-#pragma unroll 1
-      for (int j = 0; j < 2 * count; ++j) {
-        const int u = 2 * x + j, g = u >> 1, h = u & 1;  // halves of tiles done, the tile, its half
-        ok = __all_sync(FULL, (h || wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1))) &&
-                                  wait(&s_full[2 * w + h], (uint32_t)(g & 1)));
+        if (!ok) break;
+        // ---- finish the segment, or leave a part
+        ok = __all_sync(FULL, wait(&o_done[2 * w + 1], (uint32_t)(x + count - 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        const float2 *scale = info[g & (INFOS - 1)].scale + 4 * h;
-        const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
-        const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
-        const uint32_t at = sp + HALF * h;
-        uint32_t s[HALF], p[HALF / 2];
-        if (pending) {
-          const float by = exp2_fast(-over);
-          rescale(by, u - 1);
-          if (!ok) break;
-          m += over;
-          mv += over;
-          l = mul2(l, pair(by, by));
-        }
-        tmem_load32(at, s);
-        tmem_load32(at + 32, s + 32);
-        tmem_wait32(s);
-        tmem_wait32(s + 32);
-        // With the references as they are: a probability with its value scale is
-        // 2^(x + lv - mv), and the probability itself that times 2^(mv - m - lv), so one
-        // exponential a score and one a group for the sum. It stands if every row has a
-        // reference, sees all 64 tokens, has no value scale so small that the first could
-        // vanish with the second still counting, and nothing passed fp16's range.
-        uint64_t sum_l = l;
-        // the largest sum of a group: no probability in it is larger
-        float most = seen >= HALF && bad == 0 ? 0.0f : INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 sc = scale[k];
-          const float f = rowc * sc.x, up = sc.y - mv;
-          const uint64_t ff = pair(f, f), uu = pair(up, up);
-          uint64_t sum = 0;
-#pragma unroll
-          for (int e = 16 * k; e < 16 * k + 16; e += 2) {
-            const uint64_t y = fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ff, uu);
-            const float p0 = exp2_fast(low(y)), p1 = exp2_fast(high(y));
-            sum = add2(sum, pair(p0, p1));
-            p[e / 2] = pack2<IBP_FP16>(p0, p1);
-          }
-          const float back = exp2_fast(-(sc.y + (m - mv)));
-          sum_l = fma2(sum, pair(back, back), sum_l);
-          most = fmaxf(most, fmaxf(low(sum) + high(sum), back <= 0x1p60f ? 0.0f : INFINITY));
-        }
-        // (a row of NaN has no largest sum and stands; its output is NaN either way)
-        const uint32_t top = __reduce_max_sync(FULL, __float_as_uint(most));
-        const bool stands = top <= __float_as_uint(32768.0f);
-        pending = stands && top > __float_as_uint(16384.0f);
-        if (stands) l = sum_l;
-        if (pending) over = most > 16384.0f ? log2f(most) - (4.0f + ROW_SHIFT) : 0.0f;
-        if (!stands) {  // masks, new references, then both exponents apart
-          float mn = m, mvn = mv;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
-            float top = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = e < n ? fmaxf(top, __uint_as_float(s[16 * k + e])) : top;
-            // (a masked group's -inf times a scale of zero is not a number: not a maximum either)
-            top *= rowc * scale[k].x;
-            mn = fmaxf(mn, top);
-            mvn = fmaxf(mvn, top + scale[k].y - ROW_SHIFT);
-          }
-          if (__any_sync(FULL, mn > m + 8.0f || mvn > mv + 8.0f)) {
-            const float fl = exp2_fast(m - mn), fo = exp2_fast(mv - mvn);
-            m = mn;
-            mv = mvn;
-            l = mul2(l, pair(fl, fl));
-            if (j > 0) {
-              rescale(fo, u - 1);
-              if (!ok) break;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float f = rowc * scale[k].x, gv = exp2_fast(fminf(scale[k].y + (m - mv), 120.0f));
-            const int n = (bad >> k) & 1 ? 0 : seen - 16 * k;
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float p0 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e]), f, -m));
-              float p1 = exp2_fast(fmaf(__uint_as_float(s[16 * k + e + 1]), f, -m));
-              p0 = e < n ? p0 : 0.0f;
-              p1 = e + 1 < n ? p1 : 0.0f;
-              sum += p0 + p1;
-              p[8 * k + e / 2] = pack2<IBP_FP16>(p0 * gv, p1 * gv);
-            }
-            l = add2(l, pair(sum, 0.0f));
-          }
-        }
-        tmem_store16(at, p);  // over columns that have been read
-        tmem_store16(at + 16, p + 16);
-        tmem_wait_store();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * w + h]);
-      }
-      if (!ok) break;
-      // ---- finish the segment, or leave a part
-      ok = __all_sync(FULL, wait(&o_done[2 * w + 1], (uint32_t)(x + count - 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const float sum = low(l) + high(l);
-      const bool done = tile0 == 0 && count == cur->tiles;
-      const int64_t q_row = cur->seq.row0 + rr / group;
-      const int q_head = cur->head * group + rr % group;
-      float *part = a.part + ((int64_t)cta * 2 + (x == 0 ? 0 : 1)) * ((int64_t)MB * (D + 4));
-      const float f = !done ? 1.0f : sum > 0.0f ? exp2_fast(mv - m) / sum : 0.0f;
-      char *out = static_cast<char *>(a.q.out) + 2 * (q_row * a.q.out_row_stride + q_head * a.q.out_head_stride);
+        const float sum = low(l) + high(l);
+        const bool done = tile0 == 0 && count == cur->tiles;
+        const int64_t q_row = cur->seq.row0 + rr / group;
+        const int q_head = cur->head * group + rr % group;
+        float *part = a.part + ((int64_t)cta * 2 + (x == 0 ? 0 : 1)) * ((int64_t)MB * (D + 4));
+        const float f = !done ? 1.0f : sum > 0.0f ? exp2_fast(mv - m) / sum : 0.0f;
+        char *out = static_cast<char *>(a.q.out) +
+                    2 * (q_row * a.q.out_row_stride + q_head * a.q.out_head_stride);
 #pragma unroll 1
-      for (int q4 = 0; q4 < D / 32; ++q4) {
-        uint32_t s[32];
-        tmem_load32(op + 32 * q4, s);
-        tmem_wait32(s);
-        if (!live) continue;
-        float y[32];
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t s[32];
+          tmem_load32(op + 32 * q4, s);
+          tmem_wait32(s);
+          if (!live) continue;
+          float y[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(s[e]) * f;
-        if (done) {
-          store16<DT>(out + 64 * q4, y);
-          store16<DT>(out + 64 * q4 + 32, y + 16);
-        } else {
+          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(s[e]) * f;
+          if (done) {
+            store16<DT>(out + 64 * q4, y);
+            store16<DT>(out + 64 * q4 + 32, y + 16);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(part + r * D + 32 * q4 + e) =
-                make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(part + r * D + 32 * q4 + e) =
+                  make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          }
         }
-      }
-      tc_fence_before();
-      if (live) {
-        if (done) {
-          if (a.q.d_lse)
-            a.q.d_lse[q_row * a.q.q_heads + q_head] = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
-        } else {
-          reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(m, mv, sum, 0.0f);
+        tc_fence_before();
+        if (live) {
+          if (done) {
+            if (a.q.d_lse)
+              a.q.d_lse[q_row * a.q.q_heads + q_head] = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
+          } else {
+            reinterpret_cast<float4 *>(part + MB * D)[r] = make_float4(m, mv, sum, 0.0f);
+          }
         }
+        x += count;
+        __syncwarp();
+        if (lane == 0 && x < n_tiles) next_segment(a, prefix, group, *cur);
+        __syncwarp();
       }
-      x += count;
-      __syncwarp();
-      if (lane == 0 && x < n_tiles) next_segment(a, prefix, group, *cur);
-      __syncwarp();
+    } else if (threadIdx.x == 0) {
+      const Cut none = {prefix[a.batch], 0, 0, 0, 0, 0, 0};
+      a.cuts[cta] = none;
     }
+    // blocks of rows that see nothing have no tiles: the CTAs share them out by heads
+    for (int i = cta; i < a.batch * c.n_heads; i += gridDim.x) {
+      const int b = i / c.n_heads, head = i % c.n_heads;
+      const Sequence sq = sequence_of(a, b, nullptr);
+      if (sq.n <= sq.len) continue;
+      const Plan plan(sq, group);
+      for (int block = 0; block < plan.blocks && plan.tiles(block) == 0; ++block) {
+        const int rr = block * MB + (int)threadIdx.x;
+        if (rr >= sq.n * group) continue;
+        const int64_t row = sq.row0 + rr / group;
+        const int qh = head * group + rr % group;
+        char *out = static_cast<char *>(a.q.out) + 2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride);
+#pragma unroll 1
+        for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4 *>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = -INFINITY;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == ISSUE_WARP) tmem_free(tmem);
+}
+
+constexpr int JOIN_SHARE = 8, JOIN_THREADS = 128;  // CTAs to a cut segment's rows
+
+// Joins the segment that CTA blockIdx.y's stretch begins in, if the one before holds its
+// first part: what it needs of the plan the attending kernel has left beside the parts.
+template <int D, int DT>
+__global__ void __launch_bounds__(JOIN_THREADS, 8) kv_join_kernel(const __grid_constant__ AttentionArgs a) {
+  const int c = blockIdx.y + 1, group = a.q.q_heads / a.c.n_heads;
+  grid_dependency_wait();
+  const Cut cut = a.cuts[c];
+  if (cut.tile == 0) return;
+  const Split split(a.cuts[0].total, a.ctas);
+  const int64_t lo = split.start(c), begin = lo - cut.tile, end = begin + cut.tiles;
+  const int64_t before = split.start(c - 1);
+  if (before > begin) return;  // an earlier CTA begins in this segment too
+  int last = c;
+  while (last + 1 < split.ctas && split.start(last + 1) < end) ++last;
+  const Sequence s = sequence_of(a, cut.b, nullptr);
+  const int r0 = cut.block * MB, share = MB / JOIN_SHARE;
+  const int from = blockIdx.x * share, to = min(from + share, s.n * group - r0);
+  constexpr int64_t PART = (int64_t)MB * (D + 4);
+  for (int u = from * (D / 4) + (int)threadIdx.x; u < to * (D / 4); u += JOIN_THREADS) {
+    const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = NONE, topv = NONE, sum = 0.0f;
+    for (int k = c - 1; k <= last; ++k) {  // in the order of the tokens
+      const float *part = a.part + ((int64_t)k * 2 + (k < c && before < begin ? 1 : 0)) * PART;
+      const float4 st = reinterpret_cast<const float4 *>(part + MB * D)[r];
+      const float4 z = reinterpret_cast<const float4 *>(part)[r * (D / 4) + piece];
+      const float m = fmaxf(top, st.x), mv = fmaxf(topv, st.y);
+      const float keep = exp2_fast(topv - mv), f = exp2_fast(st.y - mv);
+      sum = sum * exp2_fast(top - m) + st.z * exp2_fast(st.x - m);
+      y = make_float4(y.x * keep + z.x * f, y.y * keep + z.y * f, y.z * keep + z.z * f,
+                      y.w * keep + z.w * f);
+      top = m;
+      topv = mv;
+    }
+    const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
+    const int64_t row = s.row0 + rr / group;
+    const int qh = cut.head * group + rr % group;
+    *reinterpret_cast<uint2 *>(static_cast<char *>(a.q.out) +
+                               2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + 4 * piece)) =
+        make_uint2(pack2<DT>(y.x * f, y.y * f), pack2<DT>(y.z * f, y.w * f));
+    if (piece == 0 && a.q.d_lse)
+      a.q.d_lse[row * a.q.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
+  }
 }
 
 template <int D, int CODE, int DT>
@@ -844,17 +916,14 @@ int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
       16 * attr.numRegs < 8 * ROW_REGS + 4 * CONVERT_REGS + 4 * ISSUE_REGS)
     return IBP_ERR_CUDA;
-  const int group = a.q.q_heads / a.c.n_heads;
-  const int64_t blocks = (a.q.max_q * group + MB - 1) / MB;
   a.ctas = std::min(dev.sm_count, MAX_PREFILL_CTAS);
   kernel<<<a.ctas, THREADS, Memory<D>::bytes, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
-  return launch_dependent(kv_finish_kernel<D, DT, Plan, false>,
-                          dim3((unsigned)(blocks * FINISH_SHARE<Plan>), (unsigned)a.c.n_heads,
-                               (unsigned)a.batch),
-                          dim3(FINISH_THREADS), 0, s, a, (int)(blocks * FINISH_SHARE<Plan>)) == cudaSuccess
-             ? IBP_OK
-             : IBP_ERR_CUDA;
+  if (a.ctas > 1 &&
+      launch_dependent(kv_join_kernel<D, DT>, dim3(JOIN_SHARE, (unsigned)(a.ctas - 1)), dim3(JOIN_THREADS),
+                       0, s, a) != cudaSuccess)
+    return IBP_ERR_CUDA;
+  return IBP_OK;
 }
 
 template <int D>
@@ -869,7 +938,7 @@ int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) 
 }  // namespace
 
 size_t kv_prefill_scratch_bytes(const ibp_kv_cache &c) {
-  return (size_t)MAX_PREFILL_CTAS * 2 * MB * (c.head_dim + 4) * sizeof(float);
+  return MAX_PREFILL_CTAS * (sizeof(Cut) + (size_t)2 * MB * (c.head_dim + 4) * sizeof(float));
 }
 
 int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
@@ -881,7 +950,8 @@ int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scra
   a.q = q;
   a.status = d_status;
   a.wait_ns = gather_wait_limit_ns();
-  a.part = static_cast<float *>(d_scratch);
+  a.cuts = static_cast<Cut *>(d_scratch);
+  a.part = reinterpret_cast<float *>(a.cuts + MAX_PREFILL_CTAS);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += BATCH) {
     a.batch = std::min(c.batch - a.b0, BATCH);
     if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
