@@ -239,7 +239,19 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
     uint32_t qb[NT][MT][2];
     float rowc[NT][2];
     int limit[NT][2], least = 0x7FFFFFFF;
-    float *score[NT][2];
+    // Where a lane's scores go: a K/V head's rows of a sequence lie one after another, so that
+    // at 128 elements a head one address serves them all (one a row spills: 91 -> 74 us for 16
+    // rows of 128 heads over 4,096 tokens; at 64 elements
+    // one a row is faster: 85 -> 80 us for 48 ragged sequences).
+    constexpr bool ONE = D == 128;
+    float *score[ONE ? 1 : NT][ONE ? 1 : 2] = {};
+    if constexpr (SCORES)
+#pragma unroll
+      for (int k = 0; k < (ONE ? 1 : NT); ++k)
+#pragma unroll
+        for (int w = 0; w < (ONE ? 1 : 2); ++w)
+          score[k][w] = a.scores +
+                        (first_row(a, sq, head) + r0 + wq * 8 * NT + 8 * k + 2 * t4 + w) * a.score_cols + g;
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       const int r = wq * 8 * NT + 8 * k + g;
@@ -281,9 +293,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
         rowc[k][w] = __shfl_sync(FULL, factor, (2 * t4 + w) * 4);
         limit[k][w] = col < rows ? max(sq.len - sq.n + cc / group + 1, 0) : 0x7FFFFFFF;
         least = min(least, limit[k][w]);
-        if constexpr (SCORES)
-          score[k][w] = a.scores + ((sq.row0 + cc / group) * a.q.q_heads + head * group +
-                                    cc % group) * a.score_cols;
       }
     }
     for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(FULL, least, o));
@@ -398,8 +407,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
             rise |= fmaxf(acc[k][w], acc[k][w + 2]) > fminf(m[k][w], mv[k][w] + SHIFT - info.lv) + 8.0f;
             if constexpr (SCORES) {
               if (wq * 8 * NT + 8 * k + 2 * t4 + w < rows) {
-                score[k][w][t0 + g] = acc[k][w];
-                score[k][w][t0 + g + 8] = acc[k][w + 2];
+                float *to = (ONE ? score[0][0] + (int64_t)(8 * k + w) * a.score_cols
+                                 : score[ONE ? 0 : k][ONE ? 0 : w]) + t0;
+                to[0] = acc[k][w];
+                to[8] = acc[k][w + 2];
               }
             }
           }
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
           if (piece == 0) {
             const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
             if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
-            if constexpr (SCORES) a.lse2[row * a.q.q_heads + qh] = z;
+            if constexpr (SCORES) a.lse2[first_row(a, sq, head) + rr] = z;
           }
         } else {
           reinterpret_cast<float4 *>(part)[r * (D / 4) + piece] = y;
@@ -547,7 +558,10 @@ int score_cols_of(const ibp_kv_cache &c) {
   return (c.table_cols * c.page_tokens + TILE - 1) / TILE * TILE;
 }
 
-// Query rows of a segment: the fewest that hold a sequence's rows of one K/V head.
+// Query rows of a segment: the fewest that hold a sequence's rows of one K/V head, so that
+// its codes are read and converted for all of them at once (no more than 32 rows come here
+// without weights). 64 sequences of 16,384 tokens, 8 heads of 128 elements: 16 rows 494 us,
+// in segments of 8 662; 32 rows 840 us, in segments of 16 961.
 int rows_of(int64_t max_rows) {
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
 }
@@ -599,9 +613,7 @@ int launch_rows(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     case 32:
       return w ? launch_shape<D, CODE, DT, 2, 2, true>(a, dev, s)
                : launch_shape<D, CODE, DT, 2, 2, false>(a, dev, s);
-    default:
-      return w ? launch_shape<D, CODE, DT, 2, 4, true>(a, dev, s)
-               : launch_shape<D, CODE, DT, 2, 4, false>(a, dev, s);
+    default: return launch_shape<D, CODE, DT, 2, 4, true>(a, dev, s);  // weights: see many_rows
   }
 }
 
@@ -616,9 +628,11 @@ int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) 
 
 }  // namespace
 
-// More rows than a segment holds go to the kernel for many of them.
+// More rows go to the kernel for many of them, which keeps no scores to add weights up from.
+// (128 K/V heads over 4,096 tokens, 128 elements a head, this kernel against that one:
+// 24 rows 84 us | 88, 32 rows 87 | 91, 64 rows 142 | 94, 128 rows 236 | 97.)
 static bool many_rows(const ibp_kv_cache &c, int64_t max_q, int q_heads, bool weights) {
-  return !weights && max_q * (q_heads / c.n_heads) > 64;
+  return !weights && max_q * (q_heads / c.n_heads) > 32;
 }
 
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,

@@ -52,8 +52,8 @@ struct AttentionArgs {
   uint64_t wait_ns;
   int b0, batch, ctas, score_cols;
   float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
-  float *lse2;      // [n_rows][q_heads]: of segments that one CTA finished
-  float *scores;    // [n_rows][q_heads][score_cols], or null
+  float *lse2;      // of segments that one CTA finished, in the order of first_row
+  float *scores;    // [n_rows * q_heads][score_cols] in that order, or null
   Cut *cuts;        // [ctas] (many rows)
 };
 
@@ -74,6 +74,11 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, i
   s.n = (int)(hi - lo);
   s.len = kv_len(a.c, a.b0 + b, status);
   return s;
+}
+
+// A sequence's query rows of one K/V head, row by row: where they begin among all.
+__device__ __forceinline__ int64_t first_row(const AttentionArgs &a, const Sequence &s, int head) {
+  return s.row0 * a.q.q_heads + (int64_t)head * s.n * (a.q.q_heads / a.c.n_heads);
 }
 
 // How a launch is divided. A (sequence, K/V head, block of MB query rows) is a segment of
@@ -217,7 +222,6 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
   __shared__ float lse2[MB];
-  __shared__ int64_t score_at[SCORES ? MB : 1];  // first score of each row
   __shared__ Parts where;
   __shared__ int64_t prefix[2];  // tiles before sequence b and in all
   const int b = blockIdx.z, head = blockIdx.y;
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
     const int t0 = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
     constexpr int STEP = 4 * FINISH_THREADS;
     if (t0 - 4 * (int)threadIdx.x >= s.len) return;
+    const int64_t row0 = first_row(a, s, head);
     const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t0;
     float sum[WEIGHT_CHUNKS][4];
 #pragma unroll
@@ -330,28 +335,22 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
       if (threadIdx.x == 0)
         where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
                          plan.tiles(block), a.ctas);
-      for (int r = threadIdx.x; r < rows; r += FINISH_THREADS) {
-        const int rr = r0 + r;
-        score_at[r] = (s.row0 + rr / group) * a.q.q_heads + head * group + rr % group;
-      }
       __syncthreads();
       const Parts p = where;
       for (int r = threadIdx.x >> 5; r < rows; r += FINISH_THREADS / 32) {
         float z;
         if (p.first == p.last) {
-          z = a.lse2[score_at[r]];
+          z = a.lse2[row0 + r0 + r];
         } else {
           const float4 st = join_row<MB, D>(a, p, r);
           z = st.z > 0.0f ? st.x + log2f(st.z) : -INFINITY;
         }
         lse2[r] = z == -INFINITY ? INFINITY : z;  // a row that saw nothing adds nothing
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) score_at[r] *= a.score_cols;
       }
       __syncthreads();
+      const float *from = a.scores + (row0 + r0) * a.score_cols + t0;
 #pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const float *from = a.scores + score_at[r] + t0;
+      for (int r = 0; r < rows; ++r, from += a.score_cols) {
         const float z = lse2[r];
 #pragma unroll
         for (int k = 0; k < WEIGHT_CHUNKS; ++k)
