@@ -433,8 +433,8 @@ int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, i
  * library's, the paper has no counterpart): the rows of the tokens attention reads on
  * the GPU are held in 8 bits an element with one scale for each page and head.
  *
- * Layout. At most 65535 sequences and 4096 heads. K codes, V codes: [n_pages][n_heads][page_tokens][head_dim] bytes, each
- * (page, head) one contiguous tile; scales: [n_pages][n_heads] floats. Token t of
+ * Layout. At most 65535 sequences and 4096 heads. K codes, V codes:
+ * [n_pages][n_heads][page_tokens][head_dim] bytes, each (page, head) one contiguous tile; scales: [n_pages][n_heads] floats. Token t of
  * sequence b lies in slot t % page_tokens of page d_table[b*table_stride +
  * t / page_tokens]; its value is code * scale. page_tokens is 16, 32, 64 or 128,
  * head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
@@ -515,8 +515,8 @@ typedef struct {
 
 /* Attention over the cache: out = sum_t p_t v_t with p = softmax over the tokens a row
  * sees of scale * q . k_t, sums and statistics in single precision; a row that sees
- * nothing gives zeros and lse = -inf. d_weights (weights_stride >= the capacity): for t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is
- * null) + the sum of p_t over the rows and query heads of (b, h), in a fixed order;
+ * nothing gives zeros and lse = -inf. d_weights (weights_stride >= the capacity): for
+ * t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is null) + the sum of p_t over the rows and query heads of (b, h), in a fixed order;
  * entries at or past the length are left alone. d_scratch: the size
  * ibp_kv_attention_scratch_bytes gives for the same cache and query shapes (16-byte
  * aligned; smaller: IBP_ERR_ARG), overwritten. Asynchronous on s, capturable. */

@@ -211,12 +211,19 @@ __device__ __forceinline__ float4 join_row(const AttentionArgs &a, const Parts &
 constexpr int FINISH_THREADS = 128;
 constexpr int WEIGHT_CHUNKS = 2;  // of 4 tokens a thread
 constexpr int WEIGHT_TOKENS = 4 * FINISH_THREADS * WEIGHT_CHUNKS;
-// Blocks x < row_blocks join the parts of one segment (and clear the rows of empty
-// sequences); the others add up the weights of WEIGHT_TOKENS tokens from the scores.
 // Parts loaded at a time: a long sequence with few rows is cut into dozens and waits for
-// them in turn. (The CTAs that add up weights need the registers.)
+// them in turn (120,001 and 70,000 tokens: 77 us with 4 at a time, 73 with 16). The CTAs
+// that add up weights need the registers.
 template <typename Plan, bool SCORES>
 constexpr int JOIN_AHEAD = SCORES || Plan::MB > 16 ? 4 : 16;
+
+// After few rows. Blocks x < row_blocks join the parts of one segment (and clear the rows
+// of empty sequences): o = sum_k o_k 2^(mv_k - mv), l = sum_k l_k 2^(m_k - m) in the order of
+// the parts, so that results do not depend on timing. The others add up the weights of
+// WEIGHT_TOKENS tokens from the scores, p_t = 2^(score - log2 of the row's sum), rows in
+// their order: once the sums are known, without atomics, and for what no row sees the
+// score -inf gives 0. 48 ragged sequences of 28 rows, 4 heads (43 MB of scores, in L2 or
+// HBM): 23 us alone, waiting for loads; it starts while the attending kernel ends.
 template <int D, int DT, typename Plan, bool SCORES>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {

@@ -5,10 +5,13 @@ namespace ibp {
 
 namespace {
 
-// One CTA quantises what one (page, head) tile of K or V receives: its source comes in
-// 16-byte loads and its codes leave in 16-byte stores, and the values stay in registers
-// as they came between the maximum (of the magnitude bits, two 16-bit elements at a time)
-// and the rounding, so rows are read once and codes written once.
+// scale = max |x| / qmax over a page's tile, code = rn(x / scale): bound by HBM, 3 bytes
+// moved an element (bf16) for about two operations. One CTA quantises what one (page, head)
+// tile of K or V receives: its source comes in 16-byte loads and its codes leave in 16-byte
+// stores, and the values stay in registers as they came between the maximum (of the
+// magnitude bits, two 16-bit elements at a time) and the rounding, so rows are read once
+// and codes written once. A tile a CTA needs no exchange between CTAs for the scale.
+// 8 prompts of 4,096 tokens, 32 heads of 128 bf16 (805 MB moved): 149 us, 5.4 TB/s.
 
 // Work item -> (sequence, page): sequence b's items start at cu[b]/P + 2b (its rows
 // touch at most (rows - 1)/P + 2 pages, so items of two sequences never overlap).
@@ -173,7 +176,8 @@ __global__ void __launch_bounds__(Tile<P, D>::threads)
 
 // The same for a few rows a sequence: one warp to a tile, which reads its rows twice
 // (the second time from L1) and touches the codes that are there only when the scale
-// grows.
+// grows. Bound by the chain of loads (offsets, length, table, scale and rows) and the
+// launch: one token for each of 64 sequences, 8 heads of 128, takes 6.6 us.
 constexpr int FEW_WARPS = 4;
 
 template <int P, int D, int DT, int CODE>
@@ -240,8 +244,11 @@ __global__ void __launch_bounds__(32 * FEW_WARPS)
   }
 }
 
-// One CTA turns READ_TOKENS tokens of one head back into values; a thread moves 16
-// elements at a time.
+// value = rn(code * scale): bound by HBM (3 bytes an element in bf16). One CTA turns
+// READ_TOKENS tokens of one head back into values; a thread moves 16 elements at a time,
+// and the tokens need no exchange, so the split follows the output alone. 8 sequences of
+// 4,096 tokens, 32 heads of 128 (805 MB moved): 124 us, 6.5 TB/s. (All loads of a thread
+// ahead of its stores measured slower.)
 constexpr int READ_TOKENS = 64;
 constexpr int READ_THREADS = 128;
 
@@ -293,8 +300,11 @@ int append_code(const ibp_kv_cache &c, const ibp_kv_rows &r, int32_t *new_lens, 
   const int64_t items_each = each > 0 ? (each - 1) / P + 2 : 1;
   const int64_t items = r.d_cu ? r.n_rows / P + 2 * (int64_t)c.batch : items_each * c.batch;
   if (items > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
-  // a warp to a tile while a sequence brings less than a quarter of a page (64 sequences
-  // of one token, 8 heads: 9.3 us with a CTA to a tile, see the figures above)
+  // A warp to a tile while a sequence brings less than a quarter of a page: no barrier, and
+  // a quarter as many CTAs, but a warp takes more rows in turn. One token for each of 64
+  // sequences, 8 heads of 128: 6.6 us, with a CTA to a tile 9.3 (alone, cold). In pages of 64,
+  // calls of 64 sequences: 8 rows each 8.9 us | 10.9 with a CTA, 24 rows 10.9 | 10.9; of 8
+  // sequences: 15 rows 8.9 | 8.9, 24 rows 10.9 | 8.9, 64 rows 13.0 | 8.9.
   if (r.n_rows < (int64_t)c.batch * (P / 4)) {
     const int64_t ctas = (items * 2 * c.n_heads + FEW_WARPS - 1) / FEW_WARPS;
     if (ctas > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;

@@ -1,4 +1,4 @@
-"""Attention of many query rows over the 8-bit cache (the matrix-unit path: more than 64
+"""Attention of many query rows over the 8-bit cache (the matrix-unit path: more than 32
 rows of a K/V head, no weights), where its own arithmetic can go wrong (needs a GPU). The
 tolerances are those of test_gpu_kv.py."""
 from __future__ import annotations
@@ -16,6 +16,7 @@ pytestmark = pytest.mark.gpu
 
 ROWS = [
     # (lengths, query rows, q heads, kv heads, dim, page, code, dtype)
+    ([50], [33], 1, 1, 128, 16, "int8", "fp16"),
     ([128], [65], 1, 1, 128, 128, "int8", "bf16"),
     ([129], [129], 1, 1, 64, 16, "e4m3", "fp16"),
     ([255, 257, 0, 1, 640], [255, 100, 90, 1, 3], 4, 2, 128, 64, "int8", "bf16"),
@@ -23,6 +24,7 @@ ROWS = [
     ([1000, 77], [10, 77], 24, 2, 128, 16, "e4m3", "bf16"),      # twelve heads to a key head
     ([1500], [1100], 3, 3, 128, 64, "int8", "fp16"),
     ([2000, 3, 500], [70, 3, 500], 2, 2, 64, 128, "e4m3", "bf16"),
+    ([30, 0, 700, 2], [600, 300, 40, 530], 3, 3, 64, 16, "int8", "bf16"),  # blocks that see nothing
 ]
 
 
