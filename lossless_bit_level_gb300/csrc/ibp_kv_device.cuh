@@ -80,6 +80,37 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= FLT_MAX ? a : 0.0f;
 }
 
+// Pairs of floats in one instruction, to spare issue slots. A packed product that goes into
+// a packed sum may become one operation with one rounding: kept apart where codes depend
+// on it (kv_encode4 adds one by one).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ void mul4(float *x, float f) {
+  const uint64_t ff = pair(f, f), a = mul2(pair(x[0], x[1]), ff), b = mul2(pair(x[2], x[3]), ff);
+  x[0] = low(a);
+  x[1] = high(a);
+  x[2] = low(b);
+  x[3] = high(b);
+}
+
 // Four values (already times the inverse scale) to four codes in one word. int8:
 // adding 1.5 * 2^23 leaves the value rounded to nearest even in the low byte. Values a
 // rounding or two past +-qmax round to qmax; anything further, and NaN, needs
@@ -117,8 +148,13 @@ __device__ __forceinline__ void kv_decode4(uint32_t w, float *x) {
     // offset binary u = code + 128 in the low byte of 2^23's bit pattern
     const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.0f;
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t y = add2(pair(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)),
+                                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + i))),
+                              pair(-8388736.0f, -8388736.0f));
+      x[i] = low(y);
+      x[i + 1] = high(y);
+    }
   } else {
     const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
     const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);

@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 1024 / Tile<P, D>::thread
       for (int i = 0; i < 4; ++i) {
         float x[4];
         kv_decode4<CODE>(u[i], x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], scale[g]), inverse);
+        mul4(x, scale[g]);
+        mul4(x, inverse);
         v[i] = decltype(saturate)::value ? kv_encode4_any<CODE>(x[0], x[1], x[2], x[3])
                                          : kv_encode4<CODE>(x[0], x[1], x[2], x[3]);
       }

@@ -57,8 +57,7 @@ __device__ __forceinline__ uint4 encode16(const Raw16<DT> &x, float inverse) {
   for (int i = 0; i < 4; ++i) {
     float y[4];
     x.four(i, y);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __fmul_rn(y[k], inverse);
+    mul4(y, inverse);
     w[i] = ANY ? kv_encode4_any<CODE>(y[0], y[1], y[2], y[3])
                : kv_encode4<CODE>(y[0], y[1], y[2], y[3]);
   }
@@ -74,8 +73,8 @@ __device__ __forceinline__ uint4 rescale16(uint4 old, float ratio) {
   for (int i = 0; i < 4; ++i) {
     float y[4];
     kv_decode4<CODE>(o[i], y);
-    w[i] = kv_encode4<CODE>(__fmul_rn(y[0], ratio), __fmul_rn(y[1], ratio),
-                            __fmul_rn(y[2], ratio), __fmul_rn(y[3], ratio));
+    mul4(y, ratio);
+    w[i] = kv_encode4<CODE>(y[0], y[1], y[2], y[3]);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(READ_THREADS)
         kv_decode4<CODE>(w.z, x + 8);
         kv_decode4<CODE>(w.w, x + 12);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(x[e], scale);
+        for (int e = 0; e < 16; e += 4) mul4(x + e, scale);
       }
     }
     store16<DT>(out, x);

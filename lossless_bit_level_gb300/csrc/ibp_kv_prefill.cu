@@ -169,28 +169,6 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool vt) {
   return (1u << 4) | ((vt ? 1u : 0u) << 16) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(128 / 16) << 24);
 }
 
-// Pairs of floats in one instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-
 // Scales of a tile's groups of 16 tokens (a group never spans two pages); bad: a bit for
 // each group whose page is not there; held: tokens of the tile that the sequence has.
 struct TileInfo {
