@@ -276,12 +276,11 @@ __device__ __forceinline__ float largest_code(uint4 w) {
 // its largest code times that scale (rounding keeps the order): the maximum is taken over
 // codes, and the values are formed once. The scattered rows are read once and stay in
 // registers; a row of a head is whole 32-byte sectors (64 or 128 bytes), so scattering costs
-// little, and what bounds it is instruction issue (70 % of the slots at 8 sequences cut
-// from at most 4,096 to 2,048 tokens, 32 heads of 128: 57 us, 4.7 TB/s). At most 64
-// registers, so that an SM holds 1024 threads: a thread waits for its list entries and
-// then for rows.
+// little, and what bounds it is instruction issue (64 % of the slots at 8 sequences cut
+// from at most 4,096 to 2,048 tokens, 32 heads of 128: 52 us, 5.2 TB/s) beside the wait for
+// list entries and then for rows. At most 80 registers, so that an SM holds 704 threads.
 template <int P, int D, int CODE>
-__global__ void __launch_bounds__(Tile<P, D>::threads, 1024 / Tile<P, D>::threads)
+__global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads)
     kv_move_kernel(ibp_kv_cache c, ibp_kv_cache dst, int budget, const int64_t *list,
                    int32_t *status) {
   constexpr int T = Tile<P, D>::threads, G = Tile<P, D>::per_thread, GD = D / 16,
