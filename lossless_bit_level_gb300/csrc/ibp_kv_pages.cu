@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS)
 // value = rn(code * scale): bound by HBM (3 bytes an element in bf16). One CTA turns
 // READ_TOKENS tokens of one head back into values; a thread moves 16 elements at a time,
 // and the tokens need no exchange, so the split follows the output alone. 8 sequences of
-// 4,096 tokens, 32 heads of 128 (805 MB moved): 124 us, 6.5 TB/s. (All loads of a thread
+// 4,096 tokens, 32 heads of 128 (805 MB moved): 122 us, 6.6 TB/s. (All loads of a thread
 // ahead of its stores measured slower.)
 constexpr int READ_TOKENS = 64;
 constexpr int READ_THREADS = 128;
