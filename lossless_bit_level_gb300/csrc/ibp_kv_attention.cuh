@@ -223,7 +223,9 @@ constexpr int JOIN_AHEAD = SCORES || Plan::MB > 16 ? 4 : 16;
 // WEIGHT_TOKENS tokens from the scores, p_t = 2^(score - log2 of the row's sum), rows in
 // their order: once the sums are known, without atomics, and for what no row sees the
 // score -inf gives 0. 48 ragged sequences of 28 rows, 4 heads (43 MB of scores, in L2 or
-// HBM): 23 us alone, waiting for loads; it starts while the attending kernel ends.
+// HBM): 23 us alone, waiting for loads; it starts while the attending kernel ends. Every
+// block waits for that kernel before it returns, with work or without: what comes next in
+// the stream or a graph may be ordered behind this grid alone.
 template <int D, int DT, typename Plan, bool SCORES>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
@@ -259,15 +261,14 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   __syncthreads();
   if ((int)blockIdx.x < row_blocks) {
     const int block = blockIdx.x, r0 = block * MB, rows = min(MB, all - r0);
-    if (rows <= 0) return;
-    const int tiles = plan.tiles(block);
+    const int tiles = rows > 0 ? plan.tiles(block) : 0;
     if (threadIdx.x == 0 && tiles > 0)
       where = parts_of(prefix[1], prefix[0] + head * plan.before(plan.blocks) + plan.before(block),
                        tiles, a.ctas);
     __syncthreads();
     const Parts p = where;
-    if (tiles > 0 && p.first == p.last) return;
     grid_dependency_wait();
+    if (rows <= 0 || (tiles > 0 && p.first == p.last)) return;
     for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;
       const int64_t row = s.row0 + rr / group;
@@ -323,7 +324,6 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   if constexpr (SCORES) {
     const int t0 = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
     constexpr int STEP = 4 * FINISH_THREADS;
-    if (t0 - 4 * (int)threadIdx.x >= s.len) return;
     const int64_t row0 = first_row(a, s, head);
     const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t0;
     float sum[WEIGHT_CHUNKS][4];
@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
                         ? a.q.decay * a.q.d_weights_in[at + k * STEP + e]
                         : 0.0f;
     grid_dependency_wait();
+    if (t0 - 4 * (int)threadIdx.x >= s.len) return;
     for (int r0 = 0; r0 < all; r0 += MB) {
       const int rows = min(MB, all - r0);
       const int block = r0 / MB;

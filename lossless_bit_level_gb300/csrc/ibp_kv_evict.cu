@@ -290,13 +290,12 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads
   const bool is_v = (int)blockIdx.y >= c.n_heads;
   const int b = blockIdx.z, t0 = blockIdx.x * P + threadIdx.x / GD;
   const int out = min(kv_len(c, b, nullptr), budget);
-  if ((int)blockIdx.x * P >= out) return;
-  const int to = kv_page(dst, b, blockIdx.x, status);
-  if (to < 0) return;
+  const int to = (int)blockIdx.x * P < out ? kv_page(dst, b, blockIdx.x, status) : -1;
   const int64_t *row = list + ((int64_t)b * c.n_heads + head) * budget + t0;
   const char *codes = static_cast<const char *>(is_v ? c.v_codes : c.k_codes) + (threadIdx.x % GD) * 16;
   const float *scales = is_v ? c.v_scales : c.k_scales;
-  grid_dependency_wait();  // the list
+  grid_dependency_wait();  // for the list; also before a return: what comes next may be
+  if (to < 0) return;      // ordered behind this grid alone
   int64_t from[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) from[g] = t0 + g * STEP < out ? row[g * STEP] : -1;
