@@ -726,11 +726,12 @@ def probe_read(src: torch.Tensor, sink: torch.Tensor, nbytes: int | None = None,
 
 def testing_set_wait_limit_ns(ns: int) -> int:
     """ibp_testing_set_wait_limit_ns (include/ibp_testing.h): the limit of the gather
-    kernels' bounded waits, in ns (0: the default 2 s); returns the previous one."""
+    and attention kernels' bounded waits, in ns (0: the default 2 s); returns the previous one."""
     return int(load().ibp_testing_set_wait_limit_ns(int(ns)))
 
 
 def testing_withhold_plans(on: bool) -> bool:
     """ibp_testing_withhold_plans (include/ibp_testing.h): the warp-specialised
-    gather's planners keep their plans from the decoders; returns the previous setting."""
+    gather's planners keep their plans from the decoders, the attention kernels' fetching
+    warps stop early; returns the previous setting."""
     return bool(load().ibp_testing_withhold_plans(1 if on else 0))

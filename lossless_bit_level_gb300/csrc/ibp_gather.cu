@@ -971,6 +971,8 @@ uint64_t gather_wait_limit_ns() {
   return v ? v : WAIT_TIMEOUT_NS;
 }
 
+int withhold_plans() { return g_withhold_plans.load(std::memory_order_relaxed) ? 1 : 0; }
+
 int gather_units_per_row(const RowGeom &g) {
   const int block_bytes = g.lwb * 4;
   const int seg_blocks = std::max(1, std::min({g.nb, 32, SEG_TARGET_BYTES / block_bytes}));
@@ -999,7 +1001,7 @@ int launch_gather(const void *slots, int64_t slot_bytes, const uint64_t *d_offse
   a.pos_in_index = pos_in_index ? 1u : 0u;
   a.idx_count = d_idx_count;
   a.wait_ns = gather_wait_limit_ns();
-  a.withhold_plans = g_withhold_plans.load(std::memory_order_relaxed) ? 1u : 0u;
+  a.withhold_plans = (uint32_t)withhold_plans();
   a.claim_table = claim ? claim->table : nullptr;
   a.claim_mask = claim ? claim->mask : 0u;
   a.claim_owner = claim ? claim->owner : nullptr;

@@ -194,13 +194,16 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
     Piece next = look_up(lane), now = next;
     bool ok = true;
     int64_t i = 0;
-    for (; i < hi - lo && ok; ++i) {
+    const int64_t upto = a.withhold ? 1 : hi - lo;
+    for (; i < upto && ok; ++i) {
       const int s = (int)(i % ST), e = (int)((i * NP) & 31);
       if (e == 0) {
         now = next;
         next = look_up(i * NP + 32 + lane);
       }
-      if (i >= ST) ok = mbar_wait(&freed[s], (uint32_t)((i / ST) & 1) ^ 1u, abort, a.wait_ns);
+      // (a warp whose wait ran out goes on freeing stages without having seen their tiles: after
+      // that nothing is fetched into them, as its copies may be in flight still)
+      if (i >= ST) ok = mbar_wait(&freed[s], (uint32_t)((i / ST) & 1) ^ 1u, abort, a.wait_ns) && !*abort;
       ok = __all_sync(FULL, ok);
       if (!ok) break;
       const int64_t at = __shfl_sync(FULL, now.at, e + lane % NP);
@@ -223,15 +226,14 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
         bulk_load(to + TILE * D, vc + at, PP * D, &full[s]);
       }
     }
-    if (!ok) {
-      if (lane == 0) {
-        report(a.status, IBP_ERR_TIMEOUT);
-        *abort = 1;
-      }
-      // no copy may land after this CTA is gone
-      for (int64_t k = i > ST ? i - ST : 0; k < i; ++k)
-        mbar_wait(&full[k % ST], (uint32_t)((k / ST) & 1), nullptr, a.wait_ns);
+    if (!ok && lane == 0) {
+      report(a.status, IBP_ERR_TIMEOUT);
+      *abort = 1;
     }
+    // no copy may land after this CTA is gone, and the others may have stopped waiting for them
+#pragma unroll 1
+    for (int64_t k = i > ST ? i - ST : 0; k < i; ++k)
+      drain(&full[k % ST], (uint32_t)((k / ST) & 1), a.status);
     return;
   }
 
@@ -675,6 +677,7 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
   a.q = q;
   a.status = d_status;
   a.wait_ns = gather_wait_limit_ns();
+  a.withhold = withhold_plans();
   a.score_cols = score_cols_of(c);
   a.part = reinterpret_cast<float *>(base + y.part);
   a.lse2 = reinterpret_cast<float *>(base + y.lse2);

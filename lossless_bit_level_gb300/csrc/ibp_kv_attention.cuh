@@ -33,6 +33,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       : "memory");
 }
 
+// Before a CTA ends: waits for a barrier that copies or matrix instructions in flight complete
+// by themselves. They do so within microseconds; the limit is its own, far above that of the
+// waits that may have run out before, and what it leaves undone is recorded.
+constexpr uint64_t DRAIN_NS = 5 * WAIT_TIMEOUT_NS;
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (!mbar_wait(bar, parity, nullptr, DRAIN_NS)) report(status, IBP_ERR_TIMEOUT);
+}
+
 // Orders this thread's shared-memory accesses before later bulk copies into the same place.
 __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -50,6 +58,7 @@ struct AttentionArgs {
   ibp_kv_query q;
   int32_t *status;
   uint64_t wait_ns;
+  int withhold;     // testing: fetch the first tile of a stretch only
   int b0, batch, ctas, score_cols;
   float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
   float *lse2;      // of segments that one CTA finished, in the order of first_row

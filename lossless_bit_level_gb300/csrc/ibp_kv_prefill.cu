@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       }
       // nothing may be left running when this CTA gives its memory back
       tc_commit(&last[w], mine);
-      mbar_wait(&last[w], 0, nullptr, a.wait_ns);
+      drain(&last[w], 0, a.status);
       __syncwarp();
     }
     if (work && warp == FETCH_WARP) {
@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       int k_sent = 0, v_sent = 0;
       bool ok = fetch_k(0, now, py);
       k_sent = ok;
-      for (int g = 0; g < n && ok; ++g) {
+      const int upto = a.withhold ? 1 : n;
+      for (int g = 0; g < upto && ok; ++g) {
         if (g + 1 < n) {
           ok = fetch_k(g + 1, next, ny);
           if (!ok) break;
@@ -575,12 +576,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           asked = ask(after);
         }
       }
-      // no copy may land after this CTA is gone
-      if (!ok) {
-        for (int k = max(k_sent - STAGES, 0); k < k_sent; ++k)
-          mbar_wait(&raw_k_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
-        for (int k = max(v_sent - STAGES, 0); k < v_sent; ++k)
-          mbar_wait(&raw_v_full[k & 1], (uint32_t)((k >> 1) & 1), nullptr, a.wait_ns);
+      // no copy may land after this CTA is gone, and the others may have stopped waiting for them
+#pragma unroll 1
+      for (int i = 0; i < 2 * STAGES; ++i) {
+        const int k = (i < STAGES ? k_sent : v_sent) - 1 - i % STAGES;
+        if (k >= 0)
+          drain((i < STAGES ? raw_k_full : raw_v_full) + (k & 1), (uint32_t)((k >> 1) & 1), a.status);
       }
     }
     __syncwarp();
@@ -940,6 +941,7 @@ int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scra
   a.q = q;
   a.status = d_status;
   a.wait_ns = gather_wait_limit_ns();
+  a.withhold = withhold_plans();
   a.cuts = static_cast<Cut *>(d_scratch);
   a.part = reinterpret_cast<float *>(a.cuts + MAX_PREFILL_CTAS);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += BATCH) {
