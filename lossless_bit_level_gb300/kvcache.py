@@ -19,6 +19,8 @@ and buffers and orders launches on the current stream.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import KVCache, kv_append, kv_attention, kv_attention_scratch_bytes, kv_evict, \
@@ -98,6 +100,17 @@ class DecodeCache:
             raise RuntimeError(f"{sum(need)} pages are needed and {len(self._free)} are free")
         return [[self._free.pop() for _ in range(n)] for n in need]
 
+    @contextlib.contextmanager
+    def _pages_for(self, need: list[int]):
+        """Pages of the pool, need[b] for each sequence, which go back to it if what is done
+        with them raises (a call that refuses its arguments, no memory)."""
+        taken = self._take([max(n, 0) for n in need])
+        try:
+            yield taken
+        except BaseException:
+            self._free.extend(reversed([p for pages in taken for p in pages]))
+            raise
+
     def _write_table(self, handle: KVCache, rows: list[list[int]]) -> None:
         cols = handle.table.shape[1]
         host = torch.tensor([r + [-1] * (cols - len(r)) for r in rows], dtype=torch.int32)
@@ -111,14 +124,14 @@ class DecodeCache:
         if max(after, default=0) > self.max_tokens:
             raise ValueError(f"a sequence would hold {max(after)} of {self.max_tokens} tokens")
         need = [-(-n // self.page_tokens) - len(p) for n, p in zip(after, self._pages)]
-        for p, new in zip(self._pages, self._take(need)):
-            p.extend(new)
         now, later = self._handles
-        if any(need):
-            self._write_table(now, self._pages)
-        kv_append(now, k, v, cu=self._offsets(counts), new_lens=later.lens, status=self.status)
-        now.lens.copy_(later.lens)
-        self.lengths = after
+        with self._pages_for(need) as new:
+            pages = [p + q for p, q in zip(self._pages, new)]
+            if any(need):
+                self._write_table(now, pages)
+            kv_append(now, k, v, cu=self._offsets(counts), new_lens=later.lens, status=self.status)
+            now.lens.copy_(later.lens)
+        self.lengths, self._pages = after, pages
 
     def load(self, k_store, v_store, counts=None) -> None:
         """Append the rows of two compressed tensors (``offload.CompressedTensor``, a row a
@@ -156,12 +169,12 @@ class DecodeCache:
             raise RuntimeError("evict goes by the weights, which this cache does not track")
         now, later = self._handles
         kept = [min(n, budget) for n in self.lengths]
-        pages = self._take([-(-n // self.page_tokens) for n in kept])
-        self._write_table(later, pages)
-        scratch = self._workspace(kv_evict_scratch_bytes(now, budget))
-        into = self._weights_after if budget <= self.max_tokens else None
-        kv_evict(now, self.weights, budget, recent, later, scratch, new_weights=into,
-                 status=self.status)
+        with self._pages_for([-(-n // self.page_tokens) for n in kept]) as pages:
+            self._write_table(later, pages)
+            scratch = self._workspace(kv_evict_scratch_bytes(now, budget))
+            into = self._weights_after if budget <= self.max_tokens else None
+            kv_evict(now, self.weights, budget, recent, later, scratch, new_weights=into,
+                     status=self.status)
         for p in self._pages:
             self._free.extend(p)
         if into is not None:
