@@ -519,7 +519,10 @@ typedef struct {
  * t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is null) + the sum of p_t over the rows and query heads of (b, h), in a fixed order;
  * entries at or past the length are left alone. d_scratch: the size
  * ibp_kv_attention_scratch_bytes gives for the same cache and query shapes (16-byte
- * aligned; smaller: IBP_ERR_ARG), overwritten. Asynchronous on s, capturable. */
+ * aligned; smaller: IBP_ERR_ARG), overwritten. With weights it holds n_rows * q_heads *
+ * capacity floats of scores, but at most 1 GiB of them (or one row of one sequence): a
+ * call that needs more goes over its rows in slices, a pair of launches each, in a fixed
+ * order. Asynchronous on s, capturable. */
 int ibp_kv_attention_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
                                    int32_t q_heads, int with_weights, size_t *bytes);
 int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void *d_scratch,

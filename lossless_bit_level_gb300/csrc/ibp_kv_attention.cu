@@ -14,6 +14,7 @@
 // factors are rounded to fp16 (2^-11 of each), where the sum l adds the unrounded ones.
 // Scores, references, sums and outputs are fp32 until the output is stored.
 #include <algorithm>
+#include <numeric>
 
 #include "ibp_kv_attention.cuh"
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
       const int b = k0 + lane;
       int64_t tiles = 0;
       if (b < a.batch) {
-        const Sequence s = sequence_of(a, b, cta == 0 ? a.status : nullptr);
+        const Slice s = slice_of<SCORES>(a, b, cta == 0 ? a.status : nullptr);
         const Plan plan(s, group);
         tiles = c.n_heads * plan.before(plan.blocks);
       }
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   uint32_t phase = 0;
   while (x < hi) {
     while (x >= prefix[b + 1]) ++b;
-    const Sequence sq = sequence_of(a, b, nullptr);
+    const Slice sq = slice_of<SCORES>(a, b, nullptr);
     const Plan plan(sq, group);
     const int nt = plan.tiles_each, blocks = plan.blocks;
     const int64_t local = x - prefix[b];
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
 #pragma unroll
         for (int w = 0; w < (ONE ? 1 : 2); ++w)
           score[k][w] = a.scores +
-                        (first_row(a, sq, head) + r0 + wq * 8 * NT + 8 * k + 2 * t4 + w) * a.score_cols + g;
+                        (score_row(a, sq, b, head) + r0 + wq * 8 * NT + 8 * k + 2 * t4 + w) * a.score_cols + g;
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       const int r = wq * 8 * NT + 8 * k + g;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
       for (int w = 0; w < 2; ++w) {
         const int col = wq * 8 * NT + 8 * k + 2 * t4 + w, cc = r0 + col;
         rowc[k][w] = __shfl_sync(FULL, factor, (2 * t4 + w) * 4);
-        limit[k][w] = col < rows ? max(sq.len - sq.n + cc / group + 1, 0) : 0x7FFFFFFF;
+        limit[k][w] = col < rows ? max(sq.at + cc / group + 1, 0) : 0x7FFFFFFF;
         least = min(least, limit[k][w]);
       }
     }
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
           if (piece == 0) {
             const float z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
             if (a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
-            if constexpr (SCORES) a.lse2[first_row(a, sq, head) + rr] = z;
+            if constexpr (SCORES) a.lse2[score_row(a, sq, b, head) + rr] = z;
           }
         } else {
           reinterpret_cast<float4 *>(part)[r * (D / 4) + piece] = y;
@@ -589,18 +590,47 @@ int rows_of(int64_t max_rows) {
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
 }
 
+// How many sequences and how many rows of each a launch is for. The scores that weights are
+// added up from are held for those alone: at most SCORE_BYTES of them, or one row of one
+// sequence. Where all rows of a call need more, it goes over them in slices, one after another,
+// and adds each slice's probabilities to the weights that the one before left; sequences are
+// divided before a slice gets fewer rows than a segment takes.
+constexpr int64_t SCORE_BYTES = int64_t(1) << 30;
+struct Portion {
+  int batch, rows;     // rows 0: all of them
+  int64_t score_rows;  // rows whose scores are held
+};
+Portion portion_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, bool weights) {
+  if (!weights) return {MAX_BATCH, 0, 0};
+  const int64_t row_bytes = std::max<int64_t>((int64_t)q_heads * score_cols_of(c) * sizeof(float), 1);
+  const int64_t fit = std::max<int64_t>(SCORE_BYTES / row_bytes, 1);
+  if (n_rows <= fit) return {MAX_BATCH, 0, n_rows};
+  const int64_t group = q_heads / c.n_heads, whole = 64 / std::gcd<int64_t>(64, group);
+  const int64_t most = std::min(max_q, n_rows), least = std::min((64 + group - 1) / group, most);
+  Portion y;
+  y.batch = (int)std::min<int64_t>({std::max<int64_t>(fit / least, 1), c.batch, MAX_BATCH});
+  int64_t rows = std::max<int64_t>(fit / y.batch, 1);
+  if (rows > whole) rows -= rows % whole;  // whole segments of 64 rows
+  y.rows = (int)std::min(rows, most);
+  y.score_rows = (int64_t)y.batch * y.rows;
+  return y;
+}
+
 struct Layout {
   size_t part, lse2, scores, bytes;
 };
-Layout layout_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, bool weights) {
-  const int mb = rows_of(max_q * (q_heads / c.n_heads));
+Layout layout_of(const ibp_kv_cache &c, const Portion &p, int64_t max_q, int q_heads) {
+  const int mb = rows_of((p.rows ? p.rows : max_q) * (q_heads / c.n_heads));
   Layout y;
   y.part = 0;
   y.lse2 = y.part + (size_t)MAX_CTAS * 2 * mb * (c.head_dim + 4) * sizeof(float);
-  y.scores = y.lse2 + (weights ? ((size_t)n_rows * q_heads * sizeof(float) + 255) / 256 * 256 : 0);
-  y.bytes = y.scores + (weights ? (size_t)n_rows * q_heads * score_cols_of(c) * sizeof(float) : 0);
+  y.scores = y.lse2 + ((size_t)p.score_rows * q_heads * sizeof(float) + 255) / 256 * 256;
+  y.bytes = y.scores + (size_t)p.score_rows * q_heads * score_cols_of(c) * sizeof(float);
   return y;
 }
+
+// Query rows of a sequence that one launch is for, at most.
+int64_t launch_rows_of(const AttentionArgs &a) { return a.slice_rows ? a.slice_rows : a.q.max_q; }
 
 template <int D, int CODE, int DT, int NT, int WQ, bool SCORES>
 int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
@@ -610,7 +640,7 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
       cudaSuccess)
     return IBP_ERR_CUDA;
   const int group = a.q.q_heads / a.c.n_heads;
-  const int64_t blocks = (a.q.max_q * group + S::MB - 1) / S::MB;
+  const int64_t blocks = (launch_rows_of(a) * group + S::MB - 1) / S::MB;
   const int64_t most = (int64_t)a.batch * a.c.n_heads * blocks * (a.score_cols / TILE);
   a.ctas = (int)std::min<int64_t>(std::min(S::per_sm * dev.sm_count, MAX_CTAS), std::max<int64_t>(most, 1));
   kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
@@ -626,7 +656,7 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
 template <int D, int CODE, int DT>
 int launch_rows(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const bool w = a.q.d_weights != nullptr;
-  switch (rows_of(a.q.max_q * (a.q.q_heads / a.c.n_heads))) {
+  switch (rows_of(launch_rows_of(a) * (a.q.q_heads / a.c.n_heads))) {
     case 8:
       return w ? launch_shape<D, CODE, DT, 1, 1, true>(a, dev, s)
                : launch_shape<D, CODE, DT, 1, 1, false>(a, dev, s);
@@ -661,7 +691,7 @@ static bool many_rows(const ibp_kv_cache &c, int64_t max_q, int q_heads, bool we
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,
                                   int q_heads, bool with_weights) {
   if (many_rows(c, max_q, q_heads, with_weights)) return kv_prefill_scratch_bytes(c);
-  return layout_of(c, n_rows, max_q, q_heads, with_weights).bytes;
+  return layout_of(c, portion_of(c, n_rows, max_q, q_heads, with_weights), max_q, q_heads).bytes;
 }
 
 int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
@@ -670,7 +700,8 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
     return launch_kv_prefill(c, q, d_scratch, d_status, s);
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
-  const Layout y = layout_of(c, q.n_rows, q.max_q, q.q_heads, q.d_weights != nullptr);
+  const Portion p = portion_of(c, q.n_rows, q.max_q, q.q_heads, q.d_weights != nullptr);
+  const Layout y = layout_of(c, p, q.max_q, q.q_heads);
   char *base = static_cast<char *>(d_scratch);
   AttentionArgs a;
   a.c = c;
@@ -682,10 +713,18 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
   a.part = reinterpret_cast<float *>(base + y.part);
   a.lse2 = reinterpret_cast<float *>(base + y.lse2);
   a.scores = q.d_weights ? reinterpret_cast<float *>(base + y.scores) : nullptr;
-  for (a.b0 = 0; a.b0 < c.batch; a.b0 += MAX_BATCH) {
-    a.batch = std::min(c.batch - a.b0, MAX_BATCH);
-    if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
-      return rc;
+  a.slice_rows = p.rows;
+  const int64_t most = std::min(q.max_q, q.n_rows);  // rows that a sequence can have
+  for (a.b0 = 0; a.b0 < c.batch; a.b0 += p.batch) {
+    a.batch = std::min(c.batch - a.b0, p.batch);
+    a.slice0 = 0;
+    do {
+      a.q.d_weights_in = a.slice0 ? q.d_weights : q.d_weights_in;
+      a.q.decay = a.slice0 ? 1.0f : q.decay;
+      if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
+        return rc;
+      a.slice0 += p.rows;
+    } while (p.rows && a.slice0 < most);
   }
   return IBP_OK;
 }

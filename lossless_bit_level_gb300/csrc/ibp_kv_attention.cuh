@@ -60,9 +60,10 @@ struct AttentionArgs {
   uint64_t wait_ns;
   int withhold;     // testing: fetch the first tile of a stretch only
   int b0, batch, ctas, score_cols;
+  int slice0, slice_rows;  // rows of a sequence that this launch is for (slice_rows 0: all)
   float *part;      // [ctas][2] partial results: MB rows of D values, then MB of (m, mv, l, 0)
-  float *lse2;      // of segments that one CTA finished, in the order of first_row
-  float *scores;    // [n_rows * q_heads][score_cols] in that order, or null
+  float *lse2;      // of segments that one CTA finished, in the order of score_row
+  float *scores;    // [rows * q_heads][score_cols] in that order, or null
   Cut *cuts;        // [ctas] (many rows)
 };
 
@@ -85,9 +86,29 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, i
   return s;
 }
 
-// A sequence's query rows of one K/V head, row by row: where they begin among all.
-__device__ __forceinline__ int64_t first_row(const AttentionArgs &a, const Sequence &s, int head) {
-  return s.row0 * a.q.q_heads + (int64_t)head * s.n * (a.q.q_heads / a.c.n_heads);
+// The rows of a sequence that the launch is for: all but where scores are kept for the weights
+// and those of all rows would take too much room.
+struct Slice : Sequence {
+  int at;  // position of the first of them: row i sees the tokens up to at + i
+};
+template <bool SCORES>
+__device__ __forceinline__ Slice slice_of(const AttentionArgs &a, int b, int32_t *status) {
+  Slice s;
+  static_cast<Sequence &>(s) = sequence_of(a, b, status);
+  s.at = s.len - s.n;
+  if (SCORES && a.slice_rows) {
+    const int skip = min(a.slice0, s.n);
+    s.row0 += skip;
+    s.at += skip;
+    s.n = min(s.n - skip, a.slice_rows);
+  }
+  return s;
+}
+
+// The rows of one K/V head of sequence b, row by row: where their scores begin.
+__device__ __forceinline__ int64_t score_row(const AttentionArgs &a, const Slice &s, int b, int head) {
+  const int64_t row = a.slice_rows ? (int64_t)b * a.slice_rows : s.row0;
+  return row * a.q.q_heads + (int64_t)head * s.n * (a.q.q_heads / a.c.n_heads);
 }
 
 // How a launch is divided. A (sequence, K/V head, block of MB query rows) is a segment of
@@ -246,13 +267,13 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   const int group = a.q.q_heads / a.c.n_heads;
   // what follows from the lengths alone is worked out before the attending kernel ends
   // (whatever wrote the lengths ended before that one began)
-  const Sequence s = sequence_of(a, b, nullptr);
+  const Slice s = slice_of<SCORES>(a, b, nullptr);
   const Plan plan(s, group);
   const int all = s.n * group;
   if (threadIdx.x < 32) {
     int64_t before = 0, total = 0;
     for (int k = threadIdx.x; k < a.batch; k += 32) {
-      const Sequence other = sequence_of(a, k, nullptr);
+      const Slice other = slice_of<SCORES>(a, k, nullptr);
       const Plan theirs(other, group);
       const int64_t tiles = a.c.n_heads * theirs.before(theirs.blocks);
       total += tiles;
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   if constexpr (SCORES) {
     const int t0 = ((int)blockIdx.x - row_blocks) * WEIGHT_TOKENS + 4 * (int)threadIdx.x;
     constexpr int STEP = 4 * FINISH_THREADS;
-    const int64_t row0 = first_row(a, s, head);
+    const int64_t row0 = score_row(a, s, b, head);
     const int64_t at = ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.q.weights_stride + t0;
     float sum[WEIGHT_CHUNKS][4];
 #pragma unroll
