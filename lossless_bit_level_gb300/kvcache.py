@@ -62,7 +62,6 @@ class DecodeCache:
             self.weights = zeros(batch, n_heads, self.max_tokens, dtype=torch.float32)
             self._weights_after = torch.zeros_like(self.weights)
         self.status = zeros(1, dtype=torch.int32)
-        self._scratch = torch.empty(0, dtype=torch.uint8, device=self.device)
 
     @property
     def cache(self) -> KVCache:
@@ -74,9 +73,9 @@ class DecodeCache:
         return len(self._free)
 
     def _workspace(self, n: int) -> torch.Tensor:
-        if self._scratch.numel() < n:
-            self._scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return self._scratch
+        """Scratch of one call: PyTorch's allocator takes it back when the call is in the stream,
+        so that the layers of a model share what the largest of their calls needs."""
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
 
     def _counts(self, counts, n: int) -> list[int]:
         batch = len(self.lengths)
@@ -154,8 +153,8 @@ class DecodeCache:
         counts = self._counts(counts, q.shape[0])
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         most, track = max(counts, default=0), self.weights is not None
-        scratch = self._workspace(max(16, kv_attention_scratch_bytes(
-            self.cache, q.shape[0], most, q.shape[1], track)))
+        scratch = self._workspace(kv_attention_scratch_bytes(
+            self.cache, q.shape[0], most, q.shape[1], track))
         kv_attention(self.cache, q, out, scale, scratch, cu_q=self._offsets(counts), max_q=most,
                      lse=lse, weights=self.weights, weights_in=self.weights, decay=self.decay,
                      status=self.status)

@@ -1,6 +1,9 @@
 """Bookkeeping of kvcache.DecodeCache on the host (no GPU needed): the pages, tables and
 lengths that it hands out, with the cache's tensors in host memory and the library's calls
 replaced by ones that only move lengths. Refusals come from the library itself."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -120,3 +123,23 @@ def test_what_one_sequence_has_too_many_is_not_anothers(monkeypatch):
     cache.append(rows[:64], rows[:64], counts=[0, 64])
     assert cache.lengths == [16, 80] and cache.pages_free == 0
     consistent(cache)
+
+
+def test_scratch_is_not_kept(monkeypatch):
+    """A cache (one for each layer) holds no workspace between calls."""
+    cache, seen = held(monkeypatch), []
+
+    def attention(cache, q, out, scale, scratch, **kw):
+        seen.append((weakref.ref(scratch), scratch.numel()))
+
+    def evict(cache, weights, budget, recent, dst, scratch, **kw):
+        seen.append((weakref.ref(scratch), scratch.numel()))
+        fake_evict(cache, weights, budget, recent, dst, scratch, **kw)
+
+    monkeypatch.setattr(kvcache, "kv_attention", attention)
+    monkeypatch.setattr(kvcache, "kv_evict", evict)
+    cache.attend(torch.zeros((80, 4, 64), dtype=torch.bfloat16), 0.1)
+    cache.evict(32, 16)
+    gc.collect()
+    assert len(seen) == 2 and all(n >= 16 for _, n in seen)
+    assert all(ref() is None for ref, _ in seen)
