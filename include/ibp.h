@@ -445,8 +445,11 @@ int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, i
  * Quantisation of a page's tile whose largest finite magnitude is a: scale = a * (1 /
  * qmax) (qmax 127 for IBP_KV_INT8, 448 for IBP_KV_E4M3) held in [2^-100, 2^120], or 0
  * when a is 0; code = value * (1 / scale), rounded to nearest even and saturated to +-qmax. A
- * NaN becomes code 0, an infinity the largest code of its sign. All of it is IEEE
- * single precision, so equal inputs give equal codes.
+ * NaN becomes code 0, an infinity the largest code of its sign (0 where the scale is 0).
+ * All of it is IEEE single precision, so equal inputs give equal codes. Append and evict write
+ * finite codes and scales only; in a pool that a caller fills, held tokens have scales that are
+ * finite and not negative, and no NaN codes (eviction follows the rule above for others too; in
+ * attention a value that is NaN may reach rows that do not see its token).
  *
  * Device-detected errors of these calls: a page id outside [0, n_pages), a length
  * outside [0, capacity] (it is clamped) or offsets that do not rise within [0, n_rows]

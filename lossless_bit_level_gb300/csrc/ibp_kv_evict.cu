@@ -271,10 +271,32 @@ __device__ __forceinline__ float largest_code(uint4 w) {
   }
 }
 
+// The larger of two numbers, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// The largest finite magnitude of a token's 16 values, one by one.
+template <int CODE>
+__device__ __noinline__ float largest_finite(uint4 w, float scale) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  float most = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    float x[4];
+    kv_decode4<CODE>(u[i], x);
+    for (int k = 0; k < 4; ++k) most = fmaxf(most, finite_abs(__fmul_rn(x[k], scale)));
+  }
+  return most;
+}
+
 // One CTA per (sequence, head, destination page, K or V): the kept tokens' values,
 // their maximum, their codes. A token's codes share one scale, so its largest value is
 // its largest code times that scale (rounding keeps the order): the maximum is taken over
-// codes, and the values are formed once. The scattered rows are read once and stay in
+// codes, and the values are formed once. (A product that is not finite comes from a NaN code or
+// from a scale that no append writes, in a pool that a caller filled: the thread's values are
+// then gone over one by one.) The scattered rows are read once and stay in
 // registers; a row of a head is whole 32-byte sectors (64 or 128 bytes), so scattering costs
 // little, and what bounds it is instruction issue (64 % of the slots at 8 sequences cut
 // from at most 4,096 to 2,048 tokens, 32 heads of 128: 52 us, 5.2 TB/s) beside the wait for
@@ -312,8 +334,15 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads
     }
   }
 #pragma unroll
-  for (int g = 0; g < G; ++g) largest = fmaxf(largest, __fmul_rn(largest_code<CODE>(w[g]), scale[g]));
-  largest = __uint_as_float(block_max(__float_as_uint(finite_abs(largest)), sm));
+  for (int g = 0; g < G; ++g)
+    largest = max_nan(largest, __fmul_rn(largest_code<CODE>(w[g]), fabsf(scale[g])));
+  const bool odd = !(largest <= FLT_MAX);
+  if (odd) {
+    largest = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) largest = fmaxf(largest, largest_finite<CODE>(w[g], scale[g]));
+  }
+  largest = __uint_as_float(block_max(__float_as_uint(largest), sm));
   const float new_scale = kv_scale<CODE>(largest), inverse = kv_inverse(new_scale);
   if (threadIdx.x == 0)
     (is_v ? dst.v_scales : dst.k_scales)[(int64_t)to * c.n_heads + head] = new_scale;
@@ -336,7 +365,7 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads
       if (t0 + g * STEP < out) put[g * T] = make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
-  if (new_scale < 0x1p120f)
+  if (new_scale < 0x1p120f && !odd)
     put_all(std::false_type());
   else
     put_all(std::true_type());
