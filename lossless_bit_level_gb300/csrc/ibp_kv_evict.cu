@@ -41,11 +41,12 @@ struct SelectArgs {
   const float *weights;
   int64_t stride, new_stride;
   int budget, recent, cached;  // cached: keys that the shared memory given holds
+  int most;                    // tokens that can be kept: the smaller of budget and capacity
   int page_shift;
   int32_t *new_lens;
   float *new_weights;
   int32_t *kept;
-  int64_t *list;  // [batch][n_heads][budget]: page * page_tokens + slot, or -1
+  int64_t *list;  // [batch][n_heads][most]: page * page_tokens + slot, or -1
   int32_t *status;
 };
 
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(SELECT_THREADS[CLUSTER], CLUSTER ? 1 : 4)
   grid_launch_dependents();
   const float *w = a.weights + bh * a.stride;
   const int len = kv_len(c, b, a.status), out = min(len, a.budget);
-  int64_t *row = a.list + bh * a.budget;
+  int64_t *row = a.list + bh * a.most;
   int32_t *kept = a.kept ? a.kept + bh * a.budget : nullptr;
   float *new_w = a.new_weights ? a.new_weights + bh * a.new_stride : nullptr;
   auto put = [&](int at, int t, float x, int page) {
@@ -303,7 +304,7 @@ __device__ __noinline__ float largest_finite(uint4 w, float scale) {
 // list entries and then for rows. At most 80 registers, so that an SM holds 704 threads.
 template <int P, int D, int CODE>
 __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads)
-    kv_move_kernel(ibp_kv_cache c, ibp_kv_cache dst, int budget, const int64_t *list,
+    kv_move_kernel(ibp_kv_cache c, ibp_kv_cache dst, int most, const int64_t *list,
                    int32_t *status) {
   constexpr int T = Tile<P, D>::threads, G = Tile<P, D>::per_thread, GD = D / 16,
                 STEP = Tile<P, D>::step;
@@ -311,9 +312,9 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads
   const int head = blockIdx.y % c.n_heads;
   const bool is_v = (int)blockIdx.y >= c.n_heads;
   const int b = blockIdx.z, t0 = blockIdx.x * P + threadIdx.x / GD;
-  const int out = min(kv_len(c, b, nullptr), budget);
+  const int out = min(kv_len(c, b, nullptr), most);
   const int to = (int)blockIdx.x * P < out ? kv_page(dst, b, blockIdx.x, status) : -1;
-  const int64_t *row = list + ((int64_t)b * c.n_heads + head) * budget + t0;
+  const int64_t *row = list + ((int64_t)b * c.n_heads + head) * most + t0;
   const char *codes = static_cast<const char *>(is_v ? c.v_codes : c.k_codes) + (threadIdx.x % GD) * 16;
   const float *scales = is_v ? c.v_scales : c.k_scales;
   grid_dependency_wait();  // for the list; also before a return: what comes next may be
@@ -372,31 +373,35 @@ __global__ void __launch_bounds__(Tile<P, D>::threads, 704 / Tile<P, D>::threads
 }
 
 template <int P, int D>
-int move_code(const ibp_kv_cache &c, const ibp_kv_cache &dst, int budget, const int64_t *list,
+int move_code(const ibp_kv_cache &c, const ibp_kv_cache &dst, int most, const int64_t *list,
               int32_t *status, cudaStream_t s) {
-  const int64_t cap = (int64_t)c.table_cols * P;
-  const dim3 grid((unsigned)((std::min<int64_t>(budget, cap) + P - 1) / P),
-                  (unsigned)(2 * c.n_heads), (unsigned)c.batch);
+  const dim3 grid((unsigned)((most + P - 1) / P), (unsigned)(2 * c.n_heads), (unsigned)c.batch);
   if (grid.x == 0) return IBP_OK;
   const auto kernel = c.code == IBP_KV_INT8 ? kv_move_kernel<P, D, IBP_KV_INT8>
                                             : kv_move_kernel<P, D, IBP_KV_E4M3>;
-  return launch_dependent(kernel, grid, dim3(Tile<P, D>::threads), 0, s, c, dst, budget, list,
+  return launch_dependent(kernel, grid, dim3(Tile<P, D>::threads), 0, s, c, dst, most, list,
                           status) == cudaSuccess
              ? IBP_OK
              : IBP_ERR_CUDA;
 }
 
 template <int P>
-int move_dim(const ibp_kv_cache &c, const ibp_kv_cache &dst, int budget, const int64_t *list,
+int move_dim(const ibp_kv_cache &c, const ibp_kv_cache &dst, int most, const int64_t *list,
              int32_t *status, cudaStream_t s) {
-  return c.head_dim == 64 ? move_code<P, 64>(c, dst, budget, list, status, s)
-                          : move_code<P, 128>(c, dst, budget, list, status, s);
+  return c.head_dim == 64 ? move_code<P, 64>(c, dst, most, list, status, s)
+                          : move_code<P, 128>(c, dst, most, list, status, s);
 }
 
 }  // namespace
 
+// Tokens of a list that can be kept.
+static int most_of(const ibp_kv_cache &c, int64_t budget) {
+  return (int)std::min(budget, (int64_t)c.table_cols * c.page_tokens);
+}
+
 size_t kv_evict_scratch_bytes(const ibp_kv_cache &c, int64_t budget) {
-  return ((size_t)c.batch * c.n_heads * budget * sizeof(int64_t) + 15) / 16 * 16;
+  const size_t bytes = (size_t)c.batch * c.n_heads * most_of(c, budget) * sizeof(int64_t);
+  return std::max<size_t>((bytes + 15) / 16 * 16, 16);
 }
 
 int launch_kv_evict(const ibp_kv_cache &c, const float *d_weights, int64_t weights_stride,
@@ -416,10 +421,12 @@ int launch_kv_evict(const ibp_kv_cache &c, const float *d_weights, int64_t weigh
          cap >= (int64_t)cluster * 2 * 4096)
     cluster *= 2;
   const int threads = SELECT_THREADS[cluster > 1];
+  const int most = most_of(c, budget);
   const int64_t stretch = (cap + cluster * threads - 1) / (cluster * threads) * threads;
   const int cached = stretch <= MAX_CACHED ? (int)stretch : 0;
   const SelectArgs a = {c,           d_weights,   weights_stride, new_weights_stride,
-                        (int)budget, (int)recent, cached, __builtin_ctz((unsigned)c.page_tokens), d_new_lens,
+                        (int)budget, (int)recent, cached, most,
+                        __builtin_ctz((unsigned)c.page_tokens), d_new_lens,
                         d_new_weights, d_kept, list, d_status};
   const auto select = cluster > 1 ? kv_select_kernel<true> : kv_select_kernel<false>;
   if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -438,10 +445,10 @@ int launch_kv_evict(const ibp_kv_cache &c, const float *d_weights, int64_t weigh
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, select, a) != cudaSuccess) return IBP_ERR_CUDA;
   switch (c.page_tokens) {
-    case 16: return move_dim<16>(c, dst, (int)budget, list, d_status, s);
-    case 32: return move_dim<32>(c, dst, (int)budget, list, d_status, s);
-    case 64: return move_dim<64>(c, dst, (int)budget, list, d_status, s);
-    default: return move_dim<128>(c, dst, (int)budget, list, d_status, s);
+    case 16: return move_dim<16>(c, dst, most, list, d_status, s);
+    case 32: return move_dim<32>(c, dst, most, list, d_status, s);
+    case 64: return move_dim<64>(c, dst, most, list, d_status, s);
+    default: return move_dim<128>(c, dst, most, list, d_status, s);
   }
 }
 

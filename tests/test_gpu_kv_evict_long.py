@@ -24,3 +24,8 @@ LISTS = [
 @pytest.mark.parametrize("kind", ["random", "ties", "equal", "odd"])
 def test_long_lists(lens, heads, page, code, budget, recent, kind):
     test_gpu_kv.test_evict_is_exact(lens, heads, page, 64, code, budget, recent, kind)
+
+
+@pytest.mark.parametrize("budget", [300, 320, 321, 100_000])
+def test_budgets_around_and_past_the_capacity(budget):
+    test_gpu_kv.test_evict_is_exact([300, 0, 17], 2, 64, 64, "int8", budget, 9, "random")

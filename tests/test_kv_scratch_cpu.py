@@ -40,3 +40,11 @@ def test_what_fits_is_held_for_all_rows(lib):
     n = attention_bytes(lib, cache, 128, 128, 128, 1)
     assert n >= 128 * 128 * 4096 * 4
     assert attention_bytes(lib, cache, 128, 128, 128, 0) < 64 << 20
+
+
+def test_evictions_scratch_goes_by_what_can_be_kept(lib):
+    size = ctypes.c_size_t(0)
+    cache = struct(batch=8, n_heads=32, table_cols=64, table_stride=64)
+    for budget, kept in ((1, 1), (4095, 4095), (4096, 4096), (10 ** 6, 4096), (1 << 30, 4096)):
+        assert lib.ibp_kv_evict_scratch_bytes(ctypes.byref(cache), budget, ctypes.byref(size)) == 0
+        assert size.value == 8 * 32 * kept * 8
