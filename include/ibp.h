@@ -502,7 +502,8 @@ int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out
  * own keys are in the cache already) and sees the tokens up to and including it.
  * q_heads is a multiple of n_heads; query heads g*q_heads/n_heads .. share K/V head g.
  * dtype IBP_FP16 or IBP_BF16 (of q and out). Strides in elements, whole multiples of
- * 16 bytes. */
+ * 16 bytes. max_q at most 2^30 (IBP_ERR_ARG), n_rows * q_heads / n_heads too
+ * (IBP_ERR_UNSUPPORTED). */
 typedef struct {
   const void *q;             /* device, 16-byte aligned */
   void *out;                 /* device, 16-byte aligned, rows and heads strided */

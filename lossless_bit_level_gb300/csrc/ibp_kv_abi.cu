@@ -84,9 +84,11 @@ int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out
 static int kv_query_sizes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
                           int32_t q_heads) {
   if (int rc = kv_geometry(cache)) return rc;
-  if (n_rows < 0 || max_q < 0 || n_rows > KV_MAX_CAPACITY || q_heads <= 0 ||
-      q_heads % cache->n_heads != 0 || q_heads > 65535)
+  if (n_rows < 0 || max_q < 0 || n_rows > KV_MAX_CAPACITY || max_q > KV_MAX_CAPACITY ||
+      q_heads <= 0 || q_heads % cache->n_heads != 0 || q_heads > 65535)
     return IBP_ERR_ARG;
+  // the rows of a K/V head of one sequence are counted in 32 bits
+  if (n_rows * (q_heads / cache->n_heads) > KV_MAX_CAPACITY) return IBP_ERR_UNSUPPORTED;
   return IBP_OK;
 }
 

@@ -606,12 +606,12 @@ Portion portion_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_h
   const int64_t fit = std::max<int64_t>(SCORE_BYTES / row_bytes, 1);
   if (n_rows <= fit) return {MAX_BATCH, 0, n_rows};
   const int64_t group = q_heads / c.n_heads, whole = 64 / std::gcd<int64_t>(64, group);
-  const int64_t most = std::min(max_q, n_rows), least = std::min((64 + group - 1) / group, most);
+  const int64_t least = std::min((64 + group - 1) / group, max_q);
   Portion y;
   y.batch = (int)std::min<int64_t>({std::max<int64_t>(fit / least, 1), c.batch, MAX_BATCH});
   int64_t rows = std::max<int64_t>(fit / y.batch, 1);
   if (rows > whole) rows -= rows % whole;  // whole segments of 64 rows
-  y.rows = (int)std::min(rows, most);
+  y.rows = (int)std::min(rows, max_q);
   y.score_rows = (int64_t)y.batch * y.rows;
   return y;
 }
@@ -690,12 +690,15 @@ static bool many_rows(const ibp_kv_cache &c, int64_t max_q, int q_heads, bool we
 
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,
                                   int q_heads, bool with_weights) {
+  max_q = std::min(max_q, n_rows);
   if (many_rows(c, max_q, q_heads, with_weights)) return kv_prefill_scratch_bytes(c);
   return layout_of(c, portion_of(c, n_rows, max_q, q_heads, with_weights), max_q, q_heads).bytes;
 }
 
-int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scratch,
+int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &query, void *d_scratch,
                         int32_t *d_status, cudaStream_t s) {
+  ibp_kv_query q = query;
+  q.max_q = std::min(q.max_q, q.n_rows);  // what a sequence can have, however high the bound given
   if (many_rows(c, q.max_q, q.q_heads, q.d_weights != nullptr))
     return launch_kv_prefill(c, q, d_scratch, d_status, s);
   DeviceInfo dev;
@@ -714,7 +717,6 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
   a.lse2 = reinterpret_cast<float *>(base + y.lse2);
   a.scores = q.d_weights ? reinterpret_cast<float *>(base + y.scores) : nullptr;
   a.slice_rows = p.rows;
-  const int64_t most = std::min(q.max_q, q.n_rows);  // rows that a sequence can have
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += p.batch) {
     a.batch = std::min(c.batch - a.b0, p.batch);
     a.slice0 = 0;
@@ -724,7 +726,7 @@ int launch_kv_attention(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_sc
       if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
         return rc;
       a.slice0 += p.rows;
-    } while (p.rows && a.slice0 < most);
+    } while (p.rows && a.slice0 < q.max_q);
   }
   return IBP_OK;
 }

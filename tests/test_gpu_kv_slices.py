@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import lossless_bit_level_gb300 as ibp
-from kv_harness import cache_of, pools, rounded
+from kv_harness import cache_of, offsets, pools, rounded
 from test_gpu_kv import check_attention, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +53,27 @@ def test_a_prompt_with_weights_in_a_large_table():
     ibp.kv_attention(cache, q, torch.empty_like(q), 0.125, scratch, max_q=n, weights=acc,
                      weights_in=acc, decay=0.5)
     assert torch.equal(acc[0, :, :n], w[0, :, :n]) and torch.equal(acc[0, :, n:], w_in[0, :, n:])
+
+
+@pytest.mark.parametrize("weights", [False, True])
+def test_a_bound_far_above_the_rows_there_are(weights):
+    """max_q as a program that captures graphs may set it: the same bits as with the exact one."""
+    rng = np.random.default_rng(9)
+    lens, counts = [300, 70, 5], [3, 1, 4]
+    want = cache_of(rng, lens, 2, 16, 64, "int8")
+    cache = pools(want, rng)
+    q = rounded(rng.standard_normal((8, 4, 64)), "bf16").cuda()
+    outs = []
+    for max_q in (8, 1 << 20, 1 << 30):
+        scratch = torch.empty(ibp.kv_attention_scratch_bytes(cache, 8, max_q, 4, weights),
+                              dtype=torch.uint8, device="cuda")
+        out, status = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+        w = torch.zeros((3, 2, cache.capacity), device="cuda") if weights else None
+        ibp.kv_attention(cache, q, out, 0.125, scratch, cu_q=offsets(counts), max_q=max_q, weights=w,
+                         status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        outs.append((out, w))
+    for out, w in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and (w is None or torch.equal(w, outs[0][1]))
+    check_attention(want, q, counts, 0.125, outs[0][0], None, None, None)

@@ -5,7 +5,7 @@ import pytest
 
 import lossless_bit_level_gb300 as ibp
 from lossless_bit_level_gb300 import build_lib
-from test_kv_cpu import struct
+from test_kv_cpu import query, struct
 
 
 @pytest.fixture(scope="module")
@@ -48,3 +48,26 @@ def test_evictions_scratch_goes_by_what_can_be_kept(lib):
     for budget, kept in ((1, 1), (4095, 4095), (4096, 4096), (10 ** 6, 4096), (1 << 30, 4096)):
         assert lib.ibp_kv_evict_scratch_bytes(ctypes.byref(cache), budget, ctypes.byref(size)) == 0
         assert size.value == 8 * 32 * kept * 8
+
+
+def test_rows_a_sequence_are_bounded_by_all_rows(lib):
+    """max_q is a bound that a caller may set high: it changes nothing past n_rows, and one
+    that cannot be meant is refused."""
+    size = ctypes.c_size_t(0)
+    cache = struct(batch=4, n_heads=2)
+    for weights in (0, 1):
+        few = attention_bytes(lib, cache, 6, 6, 4, weights)
+        assert attention_bytes(lib, cache, 6, 1 << 20, 4, weights) == few
+        for max_q in ((1 << 30) + 1, 1 << 33, 1 << 62, (1 << 63) - 1):
+            assert lib.ibp_kv_attention_scratch_bytes(ctypes.byref(cache), 6, max_q, 4, weights,
+                                                      ctypes.byref(size)) == ibp.ERR_ARG
+    # 2^32 (row, head) pairs of a K/V head: more than the kernels count
+    assert lib.ibp_kv_attention_scratch_bytes(ctypes.byref(struct(n_heads=1)), 1 << 20, 1 << 20, 4096,
+                                              0, ctypes.byref(size)) == ibp.ERR_UNSUPPORTED
+
+
+def test_a_bound_that_overflows_is_refused(lib):
+    """4 * 2^62 is 0 in 64 bits: no rows of no sequence."""
+    q = query(n_rows=0, max_q=1 << 62, d_cu=None, d_weights=16, weights_stride=256)
+    assert lib.ibp_kv_attention(ctypes.byref(struct(batch=4)), ctypes.byref(q), 16, 1 << 40, None,
+                                None) == ibp.ERR_ARG
