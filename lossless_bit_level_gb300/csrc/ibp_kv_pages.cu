@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(READ_THREADS)
   const float *scales = is_v ? c.v_scales : c.k_scales;
   const int len = kv_len(c, b, status);
   const int64_t i0 = (int64_t)blockIdx.x * READ_TOKENS + sub;
-  const int64_t first = (begin ? __ldg(begin + b) : 0) + i0;  // below 2^31
+  // (a sequence holds at most 2^30 tokens: what begins past that is zeros from anywhere there)
+  const int first = (int)min((begin ? __ldg(begin + b) : 0) + i0, KV_MAX_CAPACITY);
   char *out = static_cast<char *>(is_v ? v_out : k_out) +
               ((((int64_t)b * n_out + i0) * c.n_heads + head) * D + d0) * ES;
   const int left = (int)min(n_out - i0, (int64_t)READ_TOKENS);
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(READ_THREADS)
 #pragma unroll
   for (int k = 0; k < READ_TOKENS; k += STEP, out += out_step) {
     if (k >= left) break;
-    const int t = (int)first + k;
+    const int t = first + k;
     float x[16] = {};
     if (t >= 0 && t < len) {
       const int page = kv_page(c, b, t >> page_shift, status);
