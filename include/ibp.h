@@ -502,7 +502,7 @@ int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out
  * own keys are in the cache already) and sees the tokens up to and including it.
  * q_heads is a multiple of n_heads; query heads g*q_heads/n_heads .. share K/V head g.
  * dtype IBP_FP16 or IBP_BF16 (of q and out). Strides in elements, whole multiples of
- * 16 bytes. max_q at most 2^30 (IBP_ERR_ARG), n_rows * q_heads / n_heads too
+ * 16 bytes; those of out put no two heads over one another (IBP_ERR_ARG). max_q at most 2^30 (IBP_ERR_ARG), n_rows * q_heads / n_heads too
  * (IBP_ERR_UNSUPPORTED). */
 typedef struct {
   const void *q;             /* device, 16-byte aligned */
@@ -540,7 +540,8 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
  * from the source's; capacity >= the smaller of budget and the source's): values
  * code * scale requantised page by page. dst->d_lens is not read. d_new_lens [batch]
  * receives min(length, budget); d_new_weights (nullable, [batch][n_heads]
- * [new_weights_stride], new_weights_stride >= budget) the kept weights, then zeros;
+ * [new_weights_stride], new_weights_stride >= budget, apart from d_weights) the kept
+ * weights, then zeros;
  * d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old positions, then -1.
  * 0 <= recent <= budget, budget >= 1. Asynchronous on s, two launches. */
 int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes);

@@ -39,6 +39,25 @@ bool stride_ok(int64_t stride, int elem_bytes) {
   return stride >= 0 && stride <= (int64_t(1) << 40) && stride * elem_bytes % 16 == 0;
 }
 
+// Whether heads of `dim` elements, `heads` of them `head_stride` apart in each of n_rows rows
+// `row_stride` apart, share an element (they are written by different threads).
+bool heads_overlap(int64_t n_rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim) {
+  if ((n_rows > 1 && row_stride < dim) || (heads > 1 && head_stride < dim)) return true;
+  if (n_rows <= 1 || heads <= 1) return false;
+  if ((row_stride - dim) / head_stride >= heads - 1 || (head_stride - dim) / row_stride >= n_rows - 1)
+    return false;  // whole rows, or whole columns of heads, one after another
+  for (int64_t j = 1; j < heads; ++j) {  // head j against the rows around it
+    const int64_t i = j * head_stride / row_stride, past = j * head_stride - i * row_stride;
+    if ((i < n_rows && past < dim) || (i + 1 < n_rows && row_stride - past < dim)) return true;
+  }
+  return false;
+}
+
+bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 }  // namespace
 
 }  // namespace ibp
@@ -109,6 +128,8 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
   if (!stride_ok(q.q_row_stride, 2) || !stride_ok(q.q_head_stride, 2) ||
       !stride_ok(q.out_row_stride, 2) || !stride_ok(q.out_head_stride, 2))
     return IBP_ERR_ARG;
+  if (heads_overlap(q.n_rows, q.out_row_stride, q.q_heads, q.out_head_stride, cache->head_dim))
+    return IBP_ERR_ARG;
   if (!q.d_cu && q.n_rows != cache->batch * q.max_q) return IBP_ERR_ARG;
   if (q.n_rows > 0 && q.max_q == 0) return IBP_ERR_ARG;
   if (!(q.scale == q.scale) || (q.d_weights && !(q.decay == q.decay))) return IBP_ERR_ARG;
@@ -158,6 +179,10 @@ int ibp_kv_evict(const ibp_kv_cache *cache, const float *d_weights, int64_t weig
       !device_ptr(d_new_lens, 4) || !device_or_null(d_new_weights, 4) ||
       !device_or_null(d_kept, 4) || !device_ptr(d_scratch, 16) || !device_or_null(d_status, 4) ||
       d_new_lens == cache->d_lens)
+    return IBP_ERR_ARG;
+  const size_t lists = (size_t)cache->batch * cache->n_heads * sizeof(float);
+  if (d_new_weights &&
+      ranges_overlap(d_weights, lists * weights_stride, d_new_weights, lists * new_weights_stride))
     return IBP_ERR_ARG;
   return launch_kv_evict(*cache, d_weights, weights_stride, budget, recent, *dst, d_new_lens,
                          d_new_weights, new_weights_stride, d_kept, d_scratch, d_status,
