@@ -12,8 +12,9 @@ were attended least:
                                       |  attend (adds up each token's probabilities)
                                       +--evict--> fewer pages --read--> rows again
 
-The pages of all sequences come from one pool; the host knows every length, so no call
-waits for the GPU. All arithmetic is in the library's kernels (``ibp_kv_append``,
+The pages of all sequences come from one pool; the host knows every length, and what it
+sends goes through pinned memory, so no call waits for the GPU (``check`` does). The host's
+part of a call is Python that a graph cannot capture; the package's own calls can be. All arithmetic is in the library's kernels (``ibp_kv_append``,
 ``ibp_kv_read``, ``ibp_kv_attention``, ``ibp_kv_evict``); this module only hands out pages
 and buffers and orders launches on the current stream.
 """
@@ -88,11 +89,15 @@ class DecodeCache:
             raise ValueError(f"counts must be {batch} numbers that add up to {n}")
         return counts
 
+    def _pinned(self, numbers) -> torch.Tensor:
+        # a copy from pageable memory waits for the stream once it is larger than 64 KB
+        return torch.tensor(numbers, dtype=torch.int32, pin_memory=self.device.type == "cuda")
+
     def _offsets(self, counts: list[int]) -> torch.Tensor:
         cu = [0]
         for c in counts:
             cu.append(cu[-1] + c)
-        return torch.tensor(cu, dtype=torch.int32).to(self.device, non_blocking=True)
+        return self._pinned(cu).to(self.device, non_blocking=True)
 
     def _take(self, need: list[int]) -> list[list[int]]:
         if sum(need) > len(self._free):
@@ -111,14 +116,16 @@ class DecodeCache:
             raise
 
     def _write_table(self, handle: KVCache, rows: list[list[int]]) -> None:
-        cols = handle.table.shape[1]
-        host = torch.tensor([r + [-1] * (cols - len(r)) for r in rows], dtype=torch.int32)
-        handle.table.copy_(host, non_blocking=True)
+        # the columns in use; what a table holds past a sequence's pages is never read
+        cols = max((len(r) for r in rows), default=0)
+        if cols:
+            host = self._pinned([r + [-1] * (cols - len(r)) for r in rows])
+            handle.table[:, :cols].copy_(host, non_blocking=True)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, counts=None) -> None:
         """Rows [n, heads, head_dim] behind what the sequences hold: counts[b] of them to
         sequence b, one sequence after another (None: the same number each)."""
-        counts = self._counts(counts, k.shape[0])
+        each, counts = counts, self._counts(counts, k.shape[0])
         after = [n + c for n, c in zip(self.lengths, counts)]
         if max(after, default=0) > self.max_tokens:
             raise ValueError(f"a sequence would hold {max(after)} of {self.max_tokens} tokens")
@@ -128,7 +135,8 @@ class DecodeCache:
             pages = [p + q for p, q in zip(self._pages, new)]
             if any(need):
                 self._write_table(now, pages)
-            kv_append(now, k, v, cu=self._offsets(counts), new_lens=later.lens, status=self.status)
+            kv_append(now, k, v, cu=None if each is None else self._offsets(counts),
+                      new_lens=later.lens, status=self.status)
             now.lens.copy_(later.lens)
         self.lengths, self._pages = after, pages
 
@@ -150,13 +158,14 @@ class DecodeCache:
                lse: torch.Tensor | None = None) -> torch.Tensor:
         """softmax(scale * q k) v of query rows [n, q_heads, head_dim], counts[b] of them the
         last tokens of sequence b. Adds their probabilities to the tokens' weights."""
-        counts = self._counts(counts, q.shape[0])
+        each, counts = counts, self._counts(counts, q.shape[0])
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         most, track = max(counts, default=0), self.weights is not None
         scratch = self._workspace(kv_attention_scratch_bytes(
             self.cache, q.shape[0], most, q.shape[1], track))
-        kv_attention(self.cache, q, out, scale, scratch, cu_q=self._offsets(counts), max_q=most,
-                     lse=lse, weights=self.weights, weights_in=self.weights, decay=self.decay,
+        kv_attention(self.cache, q, out, scale, scratch,
+                     cu_q=None if each is None else self._offsets(counts), max_q=most, lse=lse,
+                     weights=self.weights, weights_in=self.weights, decay=self.decay,
                      status=self.status)
         return out
 
