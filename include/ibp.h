@@ -434,9 +434,9 @@ int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, i
  * the GPU are held in 8 bits an element with one scale for each page and head.
  *
  * Layout. At most 65535 sequences and 4096 heads. K codes, V codes:
- * [n_pages][n_heads][page_tokens][head_dim] bytes, each (page, head) one contiguous tile; scales: [n_pages][n_heads] floats. Token t of
- * sequence b lies in slot t % page_tokens of page d_table[b*table_stride +
- * t / page_tokens]; its value is code * scale. page_tokens is 16, 32, 64 or 128,
+ * [n_pages][n_heads][page_tokens][head_dim] bytes, each (page, head) one contiguous tile;
+ * scales: [n_pages][n_heads] floats. Token t of sequence b lies in slot t % page_tokens of
+ * page d_table[b*table_stride + t / page_tokens]; its value is code * scale. page_tokens is 16, 32, 64 or 128,
  * head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
  * page_tokens tokens (its capacity, at most 2^30). No two entries that name a page in
  * use may name the same one in a call that writes pages; entries past a sequence's last
@@ -484,7 +484,8 @@ typedef struct {
  * rows need a larger one s'; the codes there then become round(code * (s / s')). A page
  * whose first slot is written starts a new scale. d_new_lens (nullable, [batch], not
  * d_lens itself) receives the lengths after the call; d_lens is not changed. Rows past
- * the capacity are dropped with IBP_ERR_INDEX. Calling it again with the same lengths
+ * the capacity are dropped with IBP_ERR_INDEX (with offsets that do not rise, d_new_lens
+ * may be written in part only). Calling it again with the same lengths
  * and rows leaves the pages as they are. Asynchronous on s, one launch. */
 int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
                   int32_t *d_status, ibp_stream_t s);
@@ -518,10 +519,13 @@ typedef struct {
 } ibp_kv_query;
 
 /* Attention over the cache: out = sum_t p_t v_t with p = softmax over the tokens a row
- * sees of scale * q . k_t, sums and statistics in single precision; a row that sees
- * nothing gives zeros and lse = -inf. d_weights (weights_stride >= the capacity): for
- * t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is null) + the sum of p_t over the rows and query heads of (b, h), in a fixed order;
- * entries at or past the length are left alone. d_scratch: the size
+ * sees of scale * q . k_t, sums and statistics in single precision (the factors p_t of
+ * the sum are rounded to fp16, and bf16 queries to fp16 times a power of two); a row that
+ * sees nothing gives zeros and lse = -inf. d_weights (weights_stride >= the capacity): for
+ * t < d_lens[b], weights[b][h][t] = decay * weights_in[b][h][t] (0 when that is null) + the
+ * sum of p_t over the rows and query heads of (b, h), in a fixed order; entries at or past
+ * the length are left alone. The largest count chooses the kernel for all sequences of a
+ * call: one with hundreds of rows is better attended apart from decoding ones. d_scratch: the size
  * ibp_kv_attention_scratch_bytes gives for the same cache and query shapes (16-byte
  * aligned; smaller: IBP_ERR_ARG), overwritten. With weights it holds n_rows * q_heads *
  * capacity floats of scores, but at most 1 GiB of them (or one row of one sequence): a
@@ -541,8 +545,7 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
  * code * scale requantised page by page. dst->d_lens is not read. d_new_lens [batch]
  * receives min(length, budget); d_new_weights (nullable, [batch][n_heads]
  * [new_weights_stride], new_weights_stride >= budget, apart from d_weights) the kept
- * weights, then zeros;
- * d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old positions, then -1.
+ * weights, then zeros; d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old positions, then -1.
  * 0 <= recent <= budget, budget >= 1. Asynchronous on s, two launches. */
 int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes);
 int ibp_kv_evict(const ibp_kv_cache *cache, const float *d_weights, int64_t weights_stride,

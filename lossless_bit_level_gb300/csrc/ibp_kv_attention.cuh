@@ -144,7 +144,9 @@ struct EvenPlan {
 // CausalPlan: a block stops at the last token its last row sees. Block j's last query is
 // q_j = (MB (j + 1) - 1) / group (the sequence's last for the last block), so it has
 // floor((MB j + (len - n + TILE) group + MB - 1) / (TILE group)) tiles; their sum over j
-// is a sum of floors of an arithmetic progression, taken as in Euclid's algorithm.
+// is a sum of floors of an arithmetic progression. The steps are the published ones: whole
+// parts out, then slope and modulus change places as in Euclid's algorithm (Graham, Knuth and
+// Patashnik, Concrete Mathematics, 3.5, reciprocity of such sums).
 template <int MB_, int TILE_>
 struct CausalPlan {
   static constexpr int MB = MB_, TILE = TILE_;

@@ -113,7 +113,8 @@ __device__ __forceinline__ void mul4(float *x, float f) {
 }
 
 // Four values (already times the inverse scale) to four codes in one word. int8:
-// adding 1.5 * 2^23 leaves the value rounded to nearest even in the low byte. Values a
+// adding 1.5 * 2^23 leaves the value rounded to nearest even in the low byte (the magic-number
+// conversion: Warren, Hacker's Delight, chapter on floating point). Values a
 // rounding or two past +-qmax round to qmax; anything further, and NaN, needs
 // kv_encode4_any.
 template <int CODE>
