@@ -263,8 +263,9 @@ __global__ void __launch_bounds__(READ_THREADS)
   const float *scales = is_v ? c.v_scales : c.k_scales;
   const int len = kv_len(c, b, status);
   const int64_t i0 = (int64_t)blockIdx.x * READ_TOKENS + sub;
-  // (a sequence holds at most 2^30 tokens: what begins past that is zeros from anywhere there)
-  const int first = (int)min((begin ? __ldg(begin + b) : 0) + i0, KV_MAX_CAPACITY);
+  // without a sign: a token before the sequence wraps to one far past it, and none wraps back
+  // (the sums are above -2^31 and below 2^31 + 2^30)
+  const uint32_t first = (begin ? (uint32_t)__ldg(begin + b) : 0u) + (uint32_t)i0;
   char *out = static_cast<char *>(is_v ? v_out : k_out) +
               ((((int64_t)b * n_out + i0) * c.n_heads + head) * D + d0) * ES;
   const int left = (int)min(n_out - i0, (int64_t)READ_TOKENS);
@@ -272,10 +273,10 @@ __global__ void __launch_bounds__(READ_THREADS)
 #pragma unroll
   for (int k = 0; k < READ_TOKENS; k += STEP, out += out_step) {
     if (k >= left) break;
-    const int t = first + k;
+    const uint32_t t = first + k;
     float x[16] = {};
-    if (t >= 0 && t < len) {
-      const int page = kv_page(c, b, t >> page_shift, status);
+    if (t < (uint32_t)len) {
+      const int page = kv_page(c, b, (int)(t >> page_shift), status);
       if (page >= 0) {
         const int64_t tile = (int64_t)page * c.n_heads + head;
         const float scale = __ldg(scales + tile);
