@@ -436,8 +436,8 @@ int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, i
  * Layout. At most 65535 sequences and 4096 heads. K codes, V codes:
  * [n_pages][n_heads][page_tokens][head_dim] bytes, each (page, head) one contiguous tile;
  * scales: [n_pages][n_heads] floats. Token t of sequence b lies in slot t % page_tokens of
- * page d_table[b*table_stride + t / page_tokens]; its value is code * scale. page_tokens is 16, 32, 64 or 128,
- * head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
+ * page d_table[b*table_stride + t / page_tokens]; its value is code * scale. page_tokens
+ * is 16, 32, 64 or 128, head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
  * page_tokens tokens (its capacity, at most 2^30). No two entries that name a page in
  * use may name the same one in a call that writes pages; entries past a sequence's last
  * page are never read.
@@ -503,8 +503,8 @@ int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out
  * own keys are in the cache already) and sees the tokens up to and including it.
  * q_heads is a multiple of n_heads; query heads g*q_heads/n_heads .. share K/V head g.
  * dtype IBP_FP16 or IBP_BF16 (of q and out). Strides in elements, whole multiples of
- * 16 bytes; those of out put no two heads over one another (IBP_ERR_ARG). max_q at most 2^30 (IBP_ERR_ARG), n_rows * q_heads / n_heads too
- * (IBP_ERR_UNSUPPORTED). */
+ * 16 bytes; those of out put no two heads over one another (IBP_ERR_ARG). max_q at most
+ * 2^30 (IBP_ERR_ARG), n_rows * q_heads / n_heads too (IBP_ERR_UNSUPPORTED). */
 typedef struct {
   const void *q;             /* device, 16-byte aligned */
   void *out;                 /* device, 16-byte aligned, rows and heads strided */
@@ -545,7 +545,8 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
  * code * scale requantised page by page. dst->d_lens is not read. d_new_lens [batch]
  * receives min(length, budget); d_new_weights (nullable, [batch][n_heads]
  * [new_weights_stride], new_weights_stride >= budget, apart from d_weights) the kept
- * weights, then zeros; d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old positions, then -1.
+ * weights, then zeros; d_kept (nullable, [batch][n_heads][budget]) the kept tokens' old
+ * positions, then -1.
  * 0 <= recent <= budget, budget >= 1. Asynchronous on s, two launches. */
 int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes);
 int ibp_kv_evict(const ibp_kv_cache *cache, const float *d_weights, int64_t weights_stride,

@@ -14,7 +14,8 @@ were attended least:
 
 The pages of all sequences come from one pool; the host knows every length, and what it
 sends goes through pinned memory, so no call waits for the GPU (``check`` does). The host's
-part of a call is Python that a graph cannot capture; the package's own calls can be. All arithmetic is in the library's kernels (``ibp_kv_append``,
+part of a call is Python that a graph cannot capture; the package's own calls can be. All
+arithmetic is in the library's kernels (``ibp_kv_append``,
 ``ibp_kv_read``, ``ibp_kv_attention``, ``ibp_kv_evict``); this module only hands out pages
 and buffers and orders launches on the current stream.
 """
