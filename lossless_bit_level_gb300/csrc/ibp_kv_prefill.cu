@@ -42,9 +42,11 @@ constexpr int THREADS = 16 * 32;
 // registers a thread, out of 128 each at launch: 8 * 168 + 4 * 88 + 4 * 88 = 16 * 128 a lane
 constexpr int ROW_REGS = 168, CONVERT_REGS = 88, ISSUE_REGS = 88;
 constexpr int CONVERT_WARP = 8, ISSUE_WARP = 12, FETCH_WARP = 13;
-// Scores come 64 tokens (half a tile) at a time, in turn in two places for each half of the
-// rows, so that the next ones are there when a thread is done with the last: S (and P over
-// it) at 128 w + 64 (half), O at 256 + 128 w.
+// Scores come 64 tokens (half a tile) at a time. Once a thread has read them into its registers
+// the next ones may go over them, so that they are there when it is done; P goes to two places of
+// its own in turn. No instruction writes what an earlier one may still read: matrix instructions
+// of different accumulators need not run in the order of their issue. S at 128 w, P at
+// 128 w + 64 + 32 (half), O at 256 + 128 w.
 constexpr int HALF = 64;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 // The largest factor of a row when its reference is set is 2^ROW_SHIFT (from a sum of 16
@@ -184,7 +186,7 @@ struct Memory {
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + V_HALVES * half_bytes,
                        raw_v = raw_k + STAGES * code_bytes;
   static constexpr int info = raw_v + STAGES * code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
-  static constexpr int barriers = 32 + INFOS;  // see the kernel's list of them
+  static constexpr int barriers = 36 + INFOS;  // see the kernel's list of them
   static constexpr int prefix = bars + barriers * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 9 * 48;
@@ -261,7 +263,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
            *q_full = bars + 8, *last = bars + 10, *raw_v_full = bars + 12, *raw_v_free = bars + 14,
            *v_full = bars + 16, *v_free = bars + 18;
   // [2 w + half]: a row's thread may be two instructions ahead of the last one done
-  uint64_t *s_full = bars + 20, *p_full = bars + 24, *o_done = bars + 28, *info_full = bars + 32;
+  uint64_t *s_full = bars + 20, *p_full = bars + 24, *o_done = bars + 28, *s_free = bars + 32,
+           *info_full = bars + 36;
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int i = 0; i < INFOS; ++i) mbar_init(&info_full[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
     }
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         const uint32_t k = k_at + s * (M::kv_bytes >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(s_at + HALF * h, operand_at(q_at, (i / 4) * (128 * 128) + (i % 4) * 32),
+          mma_ss(s_at, operand_at(q_at, (i / 4) * (128 * 128) + (i % 4) * 32),
                  operand_at(k, (i / 4) * (TILE * 128) + (i % 4) * 32), is, i > 0, mine);
         tc_commit(&s_full[2 * w + h], mine);
         if (h) tc_commit(&k_free[s], mine);
@@ -443,23 +447,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (!ok) break;
         tc_fence_after();
         scores(g & 1, 0);
-        scores(g & 1, 1);
         for (int j = 0; j < count && ok; ++j, ++g) {
-          const bool more = j + 1 < count;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            // what is there earliest first: a wait on a full barrier takes its time too
-            if (h == 0 && more) ok = ready(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
-            ok = ok && ready(&v_full[h], g & 1) && ready(&p_full[2 * w + h], g & 1);
+            if (h == 0 || j + 1 < count) {  // the scores after these, once these have been read
+              const int next = g + h;
+              if (h) ok = ready(&k_full[next & 1], (next >> 1) & 1);
+              ok = ok && ready(&s_free[2 * w + h], g & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(next & 1, h ^ 1);
+            }
+            ok = ready(&v_full[h], g & 1) && ready(&p_full[2 * w + h], g & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t v = v_at + h * (M::half_bytes >> 4), first = j > 0 || h > 0;
 #pragma unroll
             for (int e = 0; e < HALF / 16; ++e)
-              mma_ts(o_at, s_at + HALF * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first, mine);
+              mma_ts(o_at, s_at + HALF + 32 * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first,
+                     mine);
             tc_commit(&o_done[2 * w + h], mine);
             tc_commit(&v_free[h], mine);
-            if (more) scores((g + 1) & 1, h);
           }
         }
         ++segment;
@@ -680,8 +688,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           const float2 *scale = info[g & (INFOS - 1)].scale + 4 * h;
           const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
           const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
-          const uint32_t at = sp + HALF * h;
           uint32_t s[HALF], p[HALF / 2];
+          tmem_load32(sp, s);
+          tmem_load32(sp + 32, s + 32);
+          tmem_wait32(s);
+          tmem_wait32(s + 32);
+          tc_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive(&s_free[2 * w + h]);
           if (pending) {
             const float by = exp2_fast(-over);
             rescale(by, u - 1);
@@ -690,10 +704,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
             mv += over;
             l = mul2(l, pair(by, by));
           }
-          tmem_load32(at, s);
-          tmem_load32(at + 32, s + 32);
-          tmem_wait32(s);
-          tmem_wait32(s + 32);
           // With the references as they are: a probability with its value scale is
           // 2^(x + lv - mv), and the probability itself that times 2^(mv - m - lv), so one
           // exponential a score and one a group for the sum. It stands if every row has a
@@ -765,7 +775,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
               l = add2(l, pair(sum, 0.0f));
             }
           }
-          tmem_store16(at, p);  // over columns that have been read
+          const uint32_t at = sp + HALF + 32 * h;  // (the product before the last has read it:
+          tmem_store16(at, p);                     // these scores were committed behind it)
           tmem_store16(at + 16, p + 16);
           tmem_wait_store();
           tc_fence_before();
