@@ -106,23 +106,41 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 
 #define R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), \
                  "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
-#define RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), \
-                  "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
 #define I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), \
                  "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
 
-// Columns of this warp's 32 lanes, a lane to a thread. The values may be used after
-// tmem_wait of the same registers.
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t *x) {
+// Columns of this warp's 32 lanes, a lane to a thread, loaded and waited for in one statement:
+// nothing may copy a register in between.
+__device__ __forceinline__ void tmem_read64(uint32_t at, uint32_t *x) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
-      : "r"(at));
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24), R8(x, 32), R8(x, 40), R8(x, 48), R8(x, 56)
+      : "r"(at)
+      : "memory");
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t *x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : RW8(x, 0), RW8(x, 8), RW8(x, 16), RW8(x, 24)::"memory");
+__device__ __forceinline__ void tmem_read32(uint32_t at, uint32_t *x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read16(uint32_t at, uint32_t *x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8)
+      : "r"(at)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t *x) {
   asm volatile(
@@ -135,16 +153,6 @@ __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-      "[%16];"
-      : R8(x, 0), R8(x, 8)
-      : "r"(at));
-}
-__device__ __forceinline__ void tmem_wait16(uint32_t (&x)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : RW8(x, 0), RW8(x, 8)::"memory");
-}
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -670,8 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
             uint32_t y[16];
-            tmem_load16(op + 16 * k, y);
-            tmem_wait16(y);
+            tmem_read16(op + 16 * k, y);
 #pragma unroll
             for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * by);
             tmem_store16(op + 16 * k, y);
@@ -689,10 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
           const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
           uint32_t s[HALF], p[HALF / 2];
-          tmem_load32(sp, s);
-          tmem_load32(sp + 32, s + 32);
-          tmem_wait32(s);
-          tmem_wait32(s + 32);
+          tmem_read64(sp, s);
           tc_fence_before();
           __syncwarp();
           if (elect_one()) mbar_arrive(&s_free[2 * w + h]);
@@ -799,8 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t s[32];
-          tmem_load32(op + 32 * q4, s);
-          tmem_wait32(s);
+          tmem_read32(op + 32 * q4, s);
           if (!live) continue;
           float y[32];
 #pragma unroll
