@@ -687,7 +687,7 @@ int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) 
 // 24 rows 84 us | 88, 32 rows 87 | 91, 64 rows 142 | 94, 128 rows 236 | 97.) Measured with equal
 // counts; the largest count decides for the whole launch, so a chunk of a prompt takes
 // decoding sequences along: 63 of 4,096 tokens with one row beside one with 512, 32 query heads
-// on 8, take 317 us in one call and 117 + 85 in two.
+// on 8, take 323 us in one call and 117 + 85 in two.
 static bool many_rows(const ibp_kv_cache &c, int64_t max_q, int q_heads, bool weights) {
   return !weights && max_q * (q_heads / c.n_heads) > 32;
 }

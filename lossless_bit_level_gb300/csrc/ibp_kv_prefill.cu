@@ -17,12 +17,13 @@
 //
 // Bound by arithmetic: 4 D operations a (row, token) pair, and one exponential. Up to 2,048
 // rows of 2 sequences of 5,001 to 8,192 tokens, 32 query heads on 8 of 128 elements (241
-// GFLOP): 253 us with the joining, 951 TFLOP/s, half of what plain products reach. The
-// matrix unit is busy 56 % of the time; what bounds it is the chain of a half tile (wait for
-// scores, 64 exponentials a thread, store P, hand over: about 2,000 cycles for the two halves
+// GFLOP): 259 us with the joining, 929 TFLOP/s, half of what plain products reach. The
+// matrix unit is busy 59 % of the time; what bounds it is the chain of a half tile (read scores,
+// 64 exponentials a thread, store P, hand over: about 2,000 cycles for the two halves
 // that take turns) and shared memory, which holds Q and both fp16 tiles. Places for scores
 // of 128 tokens would need all of tensor memory; starting one half late was slower (282 us
-// against 270).
+// against 270). Two places for scores with P over them took 272 us with a wait for the product
+// that reads P.
 #include <algorithm>
 
 #include "ibp_kv_attention.cuh"
