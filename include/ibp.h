@@ -490,6 +490,43 @@ typedef struct {
 int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
                   int32_t *d_status, ibp_stream_t s);
 
+/* Rotation of positions: d_table[p][i] holds the cosine and sine of pair i at position p. Pair
+ * i of a head's first dim elements is (i, i + dim/2), or (2i, 2i + 1) when interleaved is not
+ * 0; the rest of the head stays as it is. dim is a multiple of 16 from 16 to head_dim. A row
+ * has a position on each of `axes` (1 to 4) axes, d_positions [n_rows][axes]; null: its
+ * token's number in the sequence on every axis. Pair i goes by the position on axis[i]
+ * (axis[0 .. dim/2 - 1] < axes), so any layout of time, height and width is a matter of
+ * axis[]. A pair (x, y) becomes (x c - y s, y c + x s), every product and sum rounded to
+ * single precision. A position outside [0, n_positions) is held within it, with
+ * IBP_ERR_INDEX. */
+typedef struct {
+  const float *d_table;      /* device, 16-byte aligned, [n_positions][dim/2][2] */
+  const int32_t *d_positions; /* device, or null */
+  int64_t n_positions;       /* 1 to 2^30 */
+  int32_t dim, axes, interleaved;
+  uint8_t axis[64];
+} ibp_kv_rotation;
+
+/* Query rows that are rotated with the new rows: row r belongs to the token that row r of K
+ * becomes. Same type as K; strides as in ibp_kv_query; out is q itself (with its strides) or
+ * memory apart from it and from K and V. */
+typedef struct {
+  const void *q;             /* device, 16-byte aligned */
+  void *out;                 /* device, 16-byte aligned */
+  int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+  int32_t q_heads;           /* 1 to 65535 */
+} ibp_kv_turned;
+
+/* ibp_kv_append with the rotation applied to K on the way: keys are quantised from the
+ * rotated values in single precision (a NaN or infinity follows the quantisation's rule
+ * after the rotation), values as they are. queries (nullable): rotated too and rounded once
+ * to their type, whether or not there was room for their tokens; rows that belong to no
+ * sequence (before d_cu[0], at or past d_cu[batch]) are left as they are. Asynchronous on s,
+ * one launch. */
+int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_rows *rows,
+                          const ibp_kv_rotation *rotation, const ibp_kv_turned *queries,
+                          int32_t *d_new_lens, int32_t *d_status, ibp_stream_t s);
+
 /* Read back: token d_begin[b] + i (d_begin null: i) of every sequence b, i < n_out, as
  * values rounded once to dtype into k_out and v_out ([batch][n_out][n_heads][head_dim],
  * either may be null; 16-byte aligned device memory): rows the codec's calls take.

@@ -102,6 +102,21 @@ class KVQuery(ctypes.Structure):
                 ("scale", ctypes.c_float), ("decay", ctypes.c_float)]
 
 
+class KVRotationStruct(ctypes.Structure):
+    """ibp_kv_rotation"""
+    _fields_ = [("d_table", ctypes.c_void_p), ("d_positions", ctypes.c_void_p),
+                ("n_positions", ctypes.c_int64), ("dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
+
+
+class KVTurned(ctypes.Structure):
+    """ibp_kv_turned"""
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32)]
+
+
 SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp_build_meta",
            "ibp_compress", "ibp_decompress_gather", "ibp_query", "ibp_probe_read",
            "ibp_build_meta_noalloc", "ibp_meta_select_scratch_bytes", "ibp_build_meta_select",
@@ -112,7 +127,7 @@ SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp
            "ibp_meta_finalize", "ibp_build_meta_block_positions", "ibp_gather_dedup_scratch_bytes",
            "ibp_decompress_gather_dedup", "ibp_query_async", "ibp_kv_append", "ibp_kv_read",
            "ibp_kv_attention_scratch_bytes", "ibp_kv_attention", "ibp_kv_evict_scratch_bytes",
-           "ibp_kv_evict")
+           "ibp_kv_evict", "ibp_kv_append_rotated")
 
 # declared in include/ibp_testing.h (a testing hook, not part of the codec)
 TESTING_SYMBOLS = ("ibp_testing_set_wait_limit_ns", "ibp_testing_withhold_plans")
@@ -178,6 +193,7 @@ def load() -> ctypes.CDLL:
     lib.ibp_kv_evict_scratch_bytes.argtypes = [vp, i64, szp]
     lib.ibp_kv_evict.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, ctypes.c_size_t,
                                  vp, vp]
+    lib.ibp_kv_append_rotated.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     for name in SYMBOLS[1:]:
         getattr(lib, name).restype = i32
     lib.ibp_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -606,6 +622,41 @@ def _int32(t: torch.Tensor | None, n: int, what: str):
     return _at(t)
 
 
+def rotation_table(n_positions: int, dim: int, base: float = 10000.0,
+                   device: torch.device | str = "cuda") -> torch.Tensor:
+    """Cosines and sines [n_positions, dim/2, 2] of the angles p * base^(-2i/dim), which are
+    taken in 64 bits (in 32 those of far positions are off by whole fractions of a turn)."""
+    pairs = dim // 2
+    inverse = float(base) ** (-torch.arange(pairs, dtype=torch.float64, device=device) / pairs)
+    out = torch.empty((n_positions, pairs, 2), dtype=torch.float32, device=device)
+    for at in range(0, n_positions, 1 << 16):  # 64-bit angles of a part at a time
+        p = torch.arange(at, min(at + (1 << 16), n_positions), dtype=torch.float64, device=device)
+        angle = p[:, None] * inverse[None, :]
+        out[at:at + p.numel(), :, 0] = angle.cos()
+        out[at:at + p.numel(), :, 1] = angle.sin()
+    return out
+
+
+class KVRotation:
+    """Rotation of positions (``ibp_kv_rotation``): ``table`` [n_positions, dim/2, 2] float32,
+    the cosine and sine of each pair at each position (``rotation_table``, or a caller's own
+    scaling of the angles); ``axis``: the axis of positions that each pair goes by, numbers
+    from 0 to 3 (None: one axis); ``interleaved``: pairs are (2i, 2i + 1) instead of
+    (i, i + dim/2). The caller keeps the table where it is."""
+
+    def __init__(self, table: torch.Tensor, axis=None, interleaved: bool = False):
+        if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or \
+                not table.is_contiguous():
+            raise ValueError("table must be contiguous float32 [n_positions, dim/2, 2]")
+        pairs = table.shape[1]
+        axis = [0] * pairs if axis is None else [int(a) for a in axis]
+        if len(axis) != pairs or pairs > 64 or any(not 0 <= a < 4 for a in axis):
+            raise ValueError(f"axis must be {pairs} numbers from 0 to 3, of 64 pairs at most")
+        self.table, self.axes = table, max(axis, default=0) + 1
+        self.struct = KVRotationStruct(_at(table), None, table.shape[0], 2 * pairs, self.axes,
+                                       int(bool(interleaved)), (ctypes.c_uint8 * 64)(*axis))
+
+
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor | None = None,
               new_lens: torch.Tensor | None = None, status: torch.Tensor | None = None,
               stream=None) -> None:
@@ -621,6 +672,40 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor
     _check(load().ibp_kv_append(cache.address, ctypes.addressof(rows),
                                 _int32(new_lens, cache.batch, "new_lens"), _at(status),
                                 _raw_stream(stream)), "ibp_kv_append")
+
+
+def kv_append_rotated(cache: KVCache, k: torch.Tensor, v: torch.Tensor, rotation: KVRotation,
+                      positions: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None, cu: torch.Tensor | None = None,
+                      new_lens: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """ibp_kv_append_rotated: ``kv_append`` with ``rotation`` applied to ``k`` on the way, and
+    to the query rows ``q`` ([n_rows, q_heads, head_dim], k's type), which go to ``q_out``
+    (None: q itself). ``positions``: int32 [n_rows, axes] (None: each row's token number)."""
+    kr, kh = _head_rows(k, cache, cache.n_heads, "k")
+    vr, vh = _head_rows(v, cache, cache.n_heads, "v")
+    n = k.shape[0]
+    if v.dtype != k.dtype or v.shape[0] != n:
+        raise ValueError("k and v must have one dtype and row count")
+    rows = KVRows(_at(k), _at(v), _int32(cu, cache.batch + 1, "cu"), n, kr, kh, vr, vh,
+                  dtype_code(k))
+    turn = KVRotationStruct.from_buffer_copy(rotation.struct)
+    turn.d_positions = _int32(positions, n * rotation.axes, "positions")
+    queries = None
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        if q.dtype != k.dtype or q.shape[0] != n or q_out.dtype != q.dtype or q_out.shape != q.shape:
+            raise ValueError("q and q_out must have k's dtype and row count, and one shape")
+        qr, qh = _head_rows(q, cache, q.shape[1], "q")
+        orow, oh = _head_rows(q_out, cache, q.shape[1], "q_out")
+        queries = KVTurned(_at(q), _at(q_out), qr, qh, orow, oh, q.shape[1])
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _check(load().ibp_kv_append_rotated(
+        cache.address, ctypes.addressof(rows), ctypes.addressof(turn),
+        None if queries is None else ctypes.addressof(queries),
+        _int32(new_lens, cache.batch, "new_lens"), _at(status), _raw_stream(stream)),
+        "ibp_kv_append_rotated")
 
 
 def kv_read(cache: KVCache, k_out: torch.Tensor | None, v_out: torch.Tensor | None,

@@ -9,6 +9,9 @@ constexpr int64_t KV_MAX_CAPACITY = int64_t(1) << 30;
 
 int launch_kv_append(const ibp_kv_cache &c, const ibp_kv_rows &r, int32_t *d_new_lens,
                      int32_t *d_status, cudaStream_t s);
+int launch_kv_append_rotated(const ibp_kv_cache &c, const ibp_kv_rows &r, const ibp_kv_rotation &t,
+                             const ibp_kv_turned *q, int32_t *d_new_lens, int32_t *d_status,
+                             cudaStream_t s);
 int launch_kv_read(const ibp_kv_cache &c, const int32_t *d_begin, int64_t n_out, void *k_out,
                    void *v_out, int dtype, int32_t *d_status, cudaStream_t s);
 size_t kv_attention_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q,

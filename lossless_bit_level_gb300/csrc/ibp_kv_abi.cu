@@ -66,8 +66,9 @@ using namespace ibp;
 
 extern "C" {
 
-int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
-                  int32_t *d_status, ibp_stream_t s) {
+// What both appends ask of their rows; 1: there is nothing to do.
+static int kv_append_check(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
+                           int32_t *d_status) {
   if (int rc = kv_geometry(cache)) return rc;
   if (!rows) return IBP_ERR_ARG;
   if (!float_dtype(rows->dtype)) return IBP_ERR_DTYPE;
@@ -76,15 +77,65 @@ int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d
       !stride_ok(rows->k_head_stride, es) || !stride_ok(rows->v_row_stride, es) ||
       !stride_ok(rows->v_head_stride, es))
     return IBP_ERR_ARG;
-  if (cache->batch == 0) return rows->n_rows == 0 ? IBP_OK : IBP_ERR_ARG;
+  if (cache->batch == 0) return rows->n_rows == 0 ? 1 : IBP_ERR_ARG;
   if (!rows->d_cu && rows->n_rows % cache->batch != 0) return IBP_ERR_ARG;
-  if (rows->n_rows == 0 && !d_new_lens) return IBP_OK;
+  if (rows->n_rows == 0 && !d_new_lens) return 1;
   if (!kv_pointers(cache) || !device_or_null(rows->d_cu, 4) || !device_or_null(d_new_lens, 4) ||
       !device_or_null(d_status, 4) || d_new_lens == cache->d_lens)
     return IBP_ERR_ARG;
   if (rows->n_rows > 0 && (!device_ptr(rows->k, 16) || !device_ptr(rows->v, 16)))
     return IBP_ERR_ARG;
+  return IBP_OK;
+}
+
+int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d_new_lens,
+                  int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_append_check(cache, rows, d_new_lens, d_status)) return rc > 0 ? IBP_OK : rc;
   return launch_kv_append(*cache, *rows, d_new_lens, d_status, reinterpret_cast<cudaStream_t>(s));
+}
+
+// Bytes from the first element of n rows of heads to past the last one.
+static size_t rows_span(int64_t n, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim,
+                        int elem_bytes) {
+  return n > 0 ? (size_t)((n - 1) * row_stride + (heads - 1) * head_stride + dim) * elem_bytes : 0;
+}
+
+int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_rows *rows,
+                          const ibp_kv_rotation *rotation, const ibp_kv_turned *queries,
+                          int32_t *d_new_lens, int32_t *d_status, ibp_stream_t s) {
+  if (!rotation) return IBP_ERR_ARG;
+  if (int rc = kv_geometry(cache)) return rc;
+  const ibp_kv_rotation &t = *rotation;
+  if (t.dim < 16 || t.dim > cache->head_dim || t.dim % 16 != 0 || t.axes < 1 || t.axes > 4 ||
+      t.n_positions < 1 || t.n_positions > KV_MAX_CAPACITY)
+    return IBP_ERR_ARG;
+  for (int i = 0; i < t.dim / 2; ++i)
+    if (t.axis[i] >= t.axes) return IBP_ERR_ARG;
+  const int nothing = kv_append_check(cache, rows, d_new_lens, d_status);
+  if (nothing < 0) return nothing;
+  const int es = rows->dtype == IBP_FP32 ? 4 : 2;
+  if (queries) {
+    const ibp_kv_turned &q = *queries;
+    if (q.q_heads < 1 || q.q_heads > 65535 || !stride_ok(q.q_row_stride, es) ||
+        !stride_ok(q.q_head_stride, es) || !stride_ok(q.out_row_stride, es) ||
+        !stride_ok(q.out_head_stride, es) ||
+        heads_overlap(rows->n_rows, q.out_row_stride, q.q_heads, q.out_head_stride, cache->head_dim))
+      return IBP_ERR_ARG;
+  }
+  if (nothing) return IBP_OK;
+  if (!device_ptr(t.d_table, 16) || !device_or_null(t.d_positions, 4)) return IBP_ERR_ARG;
+  if (queries && rows->n_rows > 0) {
+    const ibp_kv_turned &q = *queries;
+    if (!device_ptr(q.q, 16) || !device_ptr(q.out, 16)) return IBP_ERR_ARG;
+    const bool same = q.q == q.out && q.q_row_stride == q.out_row_stride && q.q_head_stride == q.out_head_stride;
+    if (!same && ranges_overlap(q.q, rows_span(rows->n_rows, q.q_row_stride, q.q_heads, q.q_head_stride,
+                                               cache->head_dim, es),
+                                q.out, rows_span(rows->n_rows, q.out_row_stride, q.q_heads, q.out_head_stride,
+                                                 cache->head_dim, es)))
+      return IBP_ERR_ARG;
+  }
+  return launch_kv_append_rotated(*cache, *rows, t, queries, d_new_lens, d_status,
+                                  reinterpret_cast<cudaStream_t>(s));
 }
 
 int ibp_kv_read(const ibp_kv_cache *cache, const int32_t *d_begin, int64_t n_out, void *k_out,

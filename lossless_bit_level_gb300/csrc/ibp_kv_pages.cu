@@ -1,5 +1,5 @@
 // Append and read of the 8-bit paged key/value cache (declared in include/ibp.h).
-#include "ibp_kv_device.cuh"
+#include "ibp_kv_append.cuh"
 
 namespace ibp {
 
@@ -12,82 +12,6 @@ namespace {
 // magnitude bits, two 16-bit elements at a time) and the rounding, so rows are read once
 // and codes written once. A tile a CTA needs no exchange between CTAs for the scale.
 // 8 prompts of 4,096 tokens, 32 heads of 128 bf16 (805 MB moved): 149 us, 5.4 TB/s.
-
-// Work item -> (sequence, page): sequence b's items start at cu[b]/P + 2b (its rows
-// touch at most (rows - 1)/P + 2 pages, so items of two sequences never overlap).
-struct AppendPlace {
-  int64_t lo, t0, end;  // first row of the sequence; tokens t0 .. end - 1 of the page and past it
-  int b, len, page;     // page < 0: nothing to do
-};
-
-template <int P>
-__device__ __forceinline__ int64_t first_item(const ibp_kv_rows &r, int b) {
-  return max(__ldg(r.d_cu + b), 0) / P + 2 * (int64_t)b;
-}
-
-template <int P>
-__device__ __forceinline__ AppendPlace place_of(const ibp_kv_cache &c, const ibp_kv_rows &r,
-                                                int64_t each, int b, int64_t nth, bool reports,
-                                                int32_t *new_lens, int32_t *status) {
-  AppendPlace p;
-  p.b = b;
-  p.page = -1;
-  int64_t hi;
-  kv_row_range(r.d_cu, r.n_rows, each, b, status, &p.lo, &hi);
-  p.len = kv_len(c, b, status);
-  const int64_t cap = (int64_t)c.table_cols * P;
-  const int64_t all = p.len + (hi - p.lo);
-  p.end = all < cap ? all : cap;
-  if (nth < 0) return p;
-  if (nth == 0 && reports) {
-    if (p.end != all) report(status, IBP_ERR_INDEX);
-    if (new_lens) new_lens[b] = (int32_t)p.end;
-  }
-  p.t0 = (p.len / P + nth) * P;
-  if (p.t0 < p.end && hi > p.lo) p.page = kv_page(c, b, (int)(p.t0 / P), status);
-  return p;
-}
-
-// 16 values times the inverse scale to 16 codes; ANY: some may be infinite, NaN or past
-// what the scale covers.
-template <int DT, int CODE, bool ANY>
-__device__ __forceinline__ uint4 encode16(const Raw16<DT> &x, float inverse) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float y[4];
-    x.four(i, y);
-    mul4(y, inverse);
-    w[i] = ANY ? kv_encode4_any<CODE>(y[0], y[1], y[2], y[3])
-               : kv_encode4<CODE>(y[0], y[1], y[2], y[3]);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Codes of tokens that were there, moved to a larger scale.
-template <int CODE>
-__device__ __forceinline__ uint4 rescale16(uint4 old, float ratio) {
-  const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float y[4];
-    kv_decode4<CODE>(o[i], y);
-    mul4(y, ratio);
-    w[i] = kv_encode4<CODE>(y[0], y[1], y[2], y[3]);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <int DT>
-__device__ __noinline__ float largest_finite(const Raw16<DT> &x, float most) {
-  for (int i = 0; i < 4; ++i) {
-    float y[4];
-    x.four(i, y);
-    for (int k = 0; k < 4; ++k) most = fmaxf(most, finite_abs(y[k]));
-  }
-  return most;
-}
 
 template <int P, int D, int DT, int CODE>
 __global__ void __launch_bounds__(Tile<P, D>::threads)
@@ -105,15 +29,15 @@ __global__ void __launch_bounds__(Tile<P, D>::threads)
     int below = 0;
     for (int k0 = 0; k0 < c.batch; k0 += T) {
       const int k = k0 + (int)threadIdx.x;
-      below += __syncthreads_count(k < c.batch && first_item<P>(r, k) <= item);
+      below += __syncthreads_count(k < c.batch && first_item(r, k, page_shift(P)) <= item);
     }
     b = max(below - 1, 0);
-    nth = item - first_item<P>(r, b);
+    nth = item - first_item(r, b, page_shift(P));
   } else {
     b = (int)(item / items_each);
     nth = item - items_each * b;
   }
-  const AppendPlace p = place_of<P>(c, r, each, b, nth, head == 0 && !is_v && threadIdx.x == 0,
+  const AppendPlace p = place_of(c, r, each, b, nth, page_shift(P), head == 0 && !is_v && threadIdx.x == 0,
                                     new_lens, status);
   if (p.page < 0) return;
   const int64_t lo = p.lo, t0 = p.t0, end = p.end;
@@ -195,14 +119,14 @@ __global__ void __launch_bounds__(32 * FEW_WARPS)
   if (r.d_cu) {
     int below = 0;
     for (int k0 = 0; k0 < c.batch; k0 += 32)
-      below += __popc(__ballot_sync(FULL, k0 + lane < c.batch && first_item<P>(r, k0 + lane) <= item));
+      below += __popc(__ballot_sync(FULL, k0 + lane < c.batch && first_item(r, k0 + lane, page_shift(P)) <= item));
     b = max(below - 1, 0);
-    nth = item - first_item<P>(r, b);
+    nth = item - first_item(r, b, page_shift(P));
   } else {
     b = (int)(item / items_each);
     nth = item - items_each * b;
   }
-  const AppendPlace p = place_of<P>(c, r, each, b, nth, which == 0 && lane == 0, new_lens, status);
+  const AppendPlace p = place_of(c, r, each, b, nth, page_shift(P), which == 0 && lane == 0, new_lens, status);
   if (p.page < 0) return;
   const char *src = static_cast<const char *>(is_v ? r.v : r.k);
   const int64_t row_stride = is_v ? r.v_row_stride : r.k_row_stride;
@@ -345,7 +269,7 @@ int read_code(const ibp_kv_cache &c, const int32_t *begin, int64_t n_out, void *
   if (chunks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)chunks, (unsigned)(c.n_heads * ((k_out != nullptr) + (v_out != nullptr))),
                   (unsigned)c.batch);
-  const int shift = c.page_tokens == 16 ? 4 : c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
+  const int shift = page_shift(c.page_tokens);
   const auto kernel = c.code == IBP_KV_INT8 ? kv_read_kernel<D, DT, IBP_KV_INT8>
                                             : kv_read_kernel<D, DT, IBP_KV_E4M3>;
   kernel<<<grid, READ_THREADS, 0, s>>>(c, shift, begin, n_out, k_out, v_out, status);
