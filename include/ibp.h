@@ -573,6 +573,49 @@ int ibp_kv_attention_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, in
 int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void *d_scratch,
                      size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
 
+/* Bounds of pages, for selecting among them: d_bounds [n_pages][n_heads][2][head_dim] (16-byte
+ * aligned) receives the least and the largest K code of each element over the tokens that a
+ * page holds, in units of scale * qmax / 127: for IBP_KV_INT8 the codes (-127 for -128), for
+ * IBP_KV_E4M3 code * 127 / 448 rounded down (least) and up (largest); whole numbers in
+ * [-127, 127]. Written for the pages of the tokens from d_begin[b] (null or negative: 0) to
+ * the length of each sequence, after an append the pages that it touched when d_begin holds
+ * the lengths before it; other pages' bounds are left alone. Asynchronous on s, capturable. */
+int ibp_kv_bounds(const ibp_kv_cache *cache, int8_t *d_bounds, const int32_t *d_begin,
+                  int32_t *d_status, ibp_stream_t s);
+
+/* Selection of pages: for every sequence b and K/V head h, d_columns[b][h][0 .. pages - 1]
+ * receives columns of the page table in rising order, then -1: all that the sequence has
+ * where these are no more than `pages`, otherwise column 0, those where its query rows stand
+ * (positions d_lens[b] - n and on) and of the others those of the highest scores, among equal
+ * ones (a NaN is the lowest) the lowest column first. None for a sequence without rows.
+ * The score of a page for a query row whose largest magnitude is in [2^e, 2^(e+1)), e held in
+ * [-100, 100]: with n_d = q_d 2^(6-e) rounded to nearest even and held in [-127, 127] (0 for a
+ * NaN), the whole number s = sum_d max(n_d least_d, n_d largest_d) of the page's bounds, times
+ * 2^(e-6); the largest over the sequence's rows and the query heads that share h counts, times
+ * the page's K scale, rounded once to single precision. It is the same on every run. Since no
+ * token of a page has a product with the rounded query above it, the page that holds the
+ * best token is not passed over for one that cannot hold a better one.
+ * Of `query`, q, d_cu, n_rows, max_q, q_row_stride, q_head_stride, q_heads and dtype count.
+ * pages holds column 0 and the rows' own: at least (max_q - 1 + page_tokens - 1) /
+ * page_tokens + 2 (IBP_ERR_ARG). d_scratch: what ibp_kv_select_scratch_bytes gives (16-byte
+ * aligned), overwritten. Asynchronous on s, capturable, two launches. */
+int ibp_kv_select_scratch_bytes(const ibp_kv_cache *cache, size_t *bytes);
+int ibp_kv_select(const ibp_kv_cache *cache, const int8_t *d_bounds, const ibp_kv_query *query,
+                  int64_t pages, int32_t *d_columns, void *d_scratch, size_t scratch_bytes,
+                  int32_t *d_status, ibp_stream_t s);
+
+/* Attention over the pages that d_columns ([batch][n_heads][pages], as ibp_kv_select writes it)
+ * names, as ibp_kv_attention over the whole cache (without weights: IBP_ERR_ARG). A sequence
+ * has the smaller of `pages` and its number of pages as entries; the last of them must be the
+ * columns where its rows stand, in order, the others distinct columns before those in any
+ * order. A different entry is an IBP_ERR_INDEX and its page is left out. d_scratch: the size
+ * ibp_kv_attention_selected_scratch_bytes gives. Asynchronous on s, capturable. */
+int ibp_kv_attention_selected_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
+                                            int32_t q_heads, int64_t pages, size_t *bytes);
+int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *query,
+                              const int32_t *d_columns, int64_t pages, void *d_scratch,
+                              size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
+
 /* Eviction by accumulated weight: of every sequence b and head h longer than budget,
  * keeps the last `recent` tokens and, of the others, the budget - recent with the
  * largest d_weights[b][h][t] (equal weights: the lowest t first; a NaN counts as the

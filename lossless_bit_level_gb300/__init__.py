@@ -127,7 +127,9 @@ SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp
            "ibp_meta_finalize", "ibp_build_meta_block_positions", "ibp_gather_dedup_scratch_bytes",
            "ibp_decompress_gather_dedup", "ibp_query_async", "ibp_kv_append", "ibp_kv_read",
            "ibp_kv_attention_scratch_bytes", "ibp_kv_attention", "ibp_kv_evict_scratch_bytes",
-           "ibp_kv_evict", "ibp_kv_append_rotated")
+           "ibp_kv_evict", "ibp_kv_append_rotated", "ibp_kv_bounds",
+           "ibp_kv_select_scratch_bytes", "ibp_kv_select",
+           "ibp_kv_attention_selected_scratch_bytes", "ibp_kv_attention_selected")
 
 # declared in include/ibp_testing.h (a testing hook, not part of the codec)
 TESTING_SYMBOLS = ("ibp_testing_set_wait_limit_ns", "ibp_testing_withhold_plans")
@@ -194,6 +196,11 @@ def load() -> ctypes.CDLL:
     lib.ibp_kv_evict.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, ctypes.c_size_t,
                                  vp, vp]
     lib.ibp_kv_append_rotated.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.ibp_kv_bounds.argtypes = [vp, vp, vp, vp, vp]
+    lib.ibp_kv_select_scratch_bytes.argtypes = [vp, szp]
+    lib.ibp_kv_select.argtypes = [vp, vp, vp, i64, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.ibp_kv_attention_selected_scratch_bytes.argtypes = [vp, i64, i64, i32, i64, szp]
+    lib.ibp_kv_attention_selected.argtypes = [vp, vp, vp, i64, vp, ctypes.c_size_t, vp, vp]
     for name in SYMBOLS[1:]:
         getattr(lib, name).restype = i32
     lib.ibp_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -727,6 +734,42 @@ def kv_read(cache: KVCache, k_out: torch.Tensor | None, v_out: torch.Tensor | No
                               _at(status), _raw_stream(stream)), "ibp_kv_read")
 
 
+def _query(cache: KVCache, q: torch.Tensor, out: torch.Tensor | None, scale: float, cu_q, max_q,
+           lse) -> KVQuery:
+    """ibp_kv_query of query rows, without weights."""
+    n, heads = q.shape[0], q.shape[1]
+    qr, qh = _head_rows(q, cache, heads, "q")
+    orow = oh = 0
+    if out is not None:
+        orow, oh = _head_rows(out, cache, heads, "out")
+        if out.dtype != q.dtype or out.shape[0] != n:
+            raise ValueError("out must have q's dtype and shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * heads or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [n_rows, q_heads]")
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("cu_q needs max_q, the most rows that a sequence has")
+        max_q = n // max(cache.batch, 1)
+    return KVQuery(_at(q), _at(out), _at(lse), _int32(cu_q, cache.batch + 1, "cu_q"), None, None,
+                   n, max_q, 0, qr, qh, orow, oh, heads, dtype_code(q), scale, 1.0)
+
+
+def _bounds(cache: KVCache, bounds: torch.Tensor):
+    n, h, _, d = cache.k_codes.shape
+    if bounds.dtype != torch.int8 or bounds.shape != (n, h, 2, d) or not bounds.is_contiguous():
+        raise ValueError(f"bounds must be contiguous int8 [{n}, {h}, 2, {d}]")
+    return _at(bounds)
+
+
+def _columns(cache: KVCache, columns: torch.Tensor) -> int:
+    """How many columns the lists hold."""
+    if columns.dim() != 3 or columns.dtype != torch.int32 or not columns.is_contiguous() or \
+            columns.shape[:2] != (cache.batch, cache.n_heads):
+        raise ValueError("columns must be contiguous int32 [batch, n_heads, pages]")
+    return columns.shape[2]
+
+
 def kv_attention_scratch_bytes(cache: KVCache, n_rows: int, max_q: int, q_heads: int,
                                with_weights: bool) -> int:
     out = ctypes.c_size_t(0)
@@ -748,13 +791,6 @@ def kv_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scale: floa
     [n_rows, q_heads] float32; ``weights`` [batch, n_heads, >= capacity] float32 receives
     decay * weights_in + the probabilities summed over rows and shared heads."""
     n, heads = q.shape[0], q.shape[1]
-    qr, qh = _head_rows(q, cache, heads, "q")
-    orow, oh = _head_rows(out, cache, heads, "out")
-    if out.dtype != q.dtype or out.shape[0] != n:
-        raise ValueError("out must have q's dtype and shape")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * heads or
-                            not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 tensor [n_rows, q_heads]")
     stride = 0
     if weights is not None:
         stride = weights.shape[-1]
@@ -762,16 +798,67 @@ def kv_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scale: floa
             if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
                                   t.shape != (cache.batch, cache.n_heads, stride)):
                 raise ValueError("weights must be contiguous float32 [batch, n_heads, stride]")
-    if max_q is None:
-        if cu_q is not None:
-            raise ValueError("cu_q needs max_q, the most rows that a sequence has")
-        max_q = n // max(cache.batch, 1)
-    query = KVQuery(_at(q), _at(out), _at(lse), _int32(cu_q, cache.batch + 1, "cu_q"),
-                    _at(weights_in), _at(weights), n, max_q, stride, qr, qh, orow, oh, heads,
-                    dtype_code(q), scale, decay)
+    query = _query(cache, q, out, scale, cu_q, max_q, lse)
+    query.d_weights_in, query.d_weights = _at(weights_in), _at(weights)
+    query.weights_stride, query.decay = stride, decay
     _check(load().ibp_kv_attention(cache.address, ctypes.addressof(query), _at(scratch),
                                    scratch.numel() * scratch.element_size(), _at(status),
                                    _raw_stream(stream)), "ibp_kv_attention")
+
+
+def kv_bounds(cache: KVCache, bounds: torch.Tensor, begin: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None) -> None:
+    """ibp_kv_bounds: least and largest K code of each element over a page's tokens into
+    ``bounds`` (int8 [n_pages, n_heads, 2, head_dim]), for the pages of tokens begin[b] (0 when
+    None) and on of every sequence."""
+    _check(load().ibp_kv_bounds(cache.address, _bounds(cache, bounds),
+                                _int32(begin, cache.batch, "begin"), _at(status),
+                                _raw_stream(stream)), "ibp_kv_bounds")
+
+
+def kv_select_scratch_bytes(cache: KVCache) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ibp_kv_select_scratch_bytes(cache.address, ctypes.byref(out)),
+           "ibp_kv_select_scratch_bytes")
+    return out.value
+
+
+def kv_select(cache: KVCache, bounds: torch.Tensor, q: torch.Tensor, columns: torch.Tensor,
+              scratch: torch.Tensor, cu_q: torch.Tensor | None = None, max_q: int | None = None,
+              status: torch.Tensor | None = None, stream=None) -> None:
+    """ibp_kv_select: the pages of every sequence and K/V head that the query rows ``q`` (as in
+    ``kv_attention``) score highest by ``bounds``, the first page and the rows' own among them,
+    as columns of the page table into ``columns`` (int32 [batch, n_heads, pages], rising, then
+    -1)."""
+    query = _query(cache, q, None, 1.0, cu_q, max_q, None)
+    _check(load().ibp_kv_select(cache.address, _bounds(cache, bounds), ctypes.addressof(query),
+                                _columns(cache, columns), _at(columns), _at(scratch),
+                                scratch.numel() * scratch.element_size(), _at(status),
+                                _raw_stream(stream)), "ibp_kv_select")
+
+
+def kv_attention_selected_scratch_bytes(cache: KVCache, n_rows: int, max_q: int, q_heads: int,
+                                        pages: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ibp_kv_attention_selected_scratch_bytes(cache.address, int(n_rows), int(max_q),
+                                                          int(q_heads), int(pages),
+                                                          ctypes.byref(out)),
+           "ibp_kv_attention_selected_scratch_bytes")
+    return out.value
+
+
+def kv_attention_selected(cache: KVCache, columns: torch.Tensor, q: torch.Tensor,
+                          out: torch.Tensor, scale: float, scratch: torch.Tensor,
+                          cu_q: torch.Tensor | None = None, max_q: int | None = None,
+                          lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                          stream=None) -> None:
+    """ibp_kv_attention_selected: ``kv_attention`` over the pages that ``columns`` (as
+    ``kv_select`` writes it) names."""
+    query = _query(cache, q, out, scale, cu_q, max_q, lse)
+    _check(load().ibp_kv_attention_selected(cache.address, ctypes.addressof(query), _at(columns),
+                                            _columns(cache, columns), _at(scratch),
+                                            scratch.numel() * scratch.element_size(), _at(status),
+                                            _raw_stream(stream)), "ibp_kv_attention_selected")
 
 
 def kv_evict_scratch_bytes(cache: KVCache, budget: int) -> int:

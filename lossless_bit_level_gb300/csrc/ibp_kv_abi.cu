@@ -170,20 +170,33 @@ int ibp_kv_attention_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, in
   return IBP_OK;
 }
 
-int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void *d_scratch,
-                     size_t scratch_bytes, int32_t *d_status, ibp_stream_t s) {
+// Query rows as every call takes them (no CUDA call).
+static int kv_query_rows(const ibp_kv_cache *cache, const ibp_kv_query *query) {
   if (!query) return IBP_ERR_ARG;
   if (int rc = kv_query_sizes(cache, query->n_rows, query->max_q, query->q_heads)) return rc;
   const ibp_kv_query &q = *query;
   if (q.dtype != IBP_FP16 && q.dtype != IBP_BF16) return IBP_ERR_DTYPE;
-  if (!stride_ok(q.q_row_stride, 2) || !stride_ok(q.q_head_stride, 2) ||
-      !stride_ok(q.out_row_stride, 2) || !stride_ok(q.out_head_stride, 2))
-    return IBP_ERR_ARG;
-  if (heads_overlap(q.n_rows, q.out_row_stride, q.q_heads, q.out_head_stride, cache->head_dim))
-    return IBP_ERR_ARG;
+  if (!stride_ok(q.q_row_stride, 2) || !stride_ok(q.q_head_stride, 2)) return IBP_ERR_ARG;
   if (!q.d_cu && q.n_rows != cache->batch * q.max_q) return IBP_ERR_ARG;
   if (q.n_rows > 0 && q.max_q == 0) return IBP_ERR_ARG;
-  if (!(q.scale == q.scale) || (q.d_weights && !(q.decay == q.decay))) return IBP_ERR_ARG;
+  return IBP_OK;
+}
+
+// And where attention writes for them.
+static int kv_query_out(const ibp_kv_cache *cache, const ibp_kv_query &q) {
+  if (!stride_ok(q.out_row_stride, 2) || !stride_ok(q.out_head_stride, 2) ||
+      heads_overlap(q.n_rows, q.out_row_stride, q.q_heads, q.out_head_stride, cache->head_dim) ||
+      !(q.scale == q.scale))
+    return IBP_ERR_ARG;
+  return IBP_OK;
+}
+
+int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void *d_scratch,
+                     size_t scratch_bytes, int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_query_rows(cache, query)) return rc;
+  const ibp_kv_query &q = *query;
+  if (int rc = kv_query_out(cache, q)) return rc;
+  if (q.d_weights && !(q.decay == q.decay)) return IBP_ERR_ARG;
   if (q.d_weights_in && !q.d_weights) return IBP_ERR_ARG;
   if (q.d_weights && q.weights_stride < 0) return IBP_ERR_ARG;
   if (cache->batch == 0 || (q.n_rows == 0 && !q.d_weights)) return IBP_OK;
@@ -199,6 +212,74 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
     return IBP_ERR_ARG;
   if (q.n_rows > 0 && (!device_ptr(q.q, 16) || !device_ptr(q.out, 16))) return IBP_ERR_ARG;
   return launch_kv_attention(*cache, q, d_scratch, d_status, reinterpret_cast<cudaStream_t>(s));
+}
+
+int ibp_kv_bounds(const ibp_kv_cache *cache, int8_t *d_bounds, const int32_t *d_begin,
+                  int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_geometry(cache)) return rc;
+  if (cache->batch == 0) return IBP_OK;
+  if (!kv_pointers(cache) || !device_ptr(d_bounds, 16) || !device_or_null(d_begin, 4) ||
+      !device_or_null(d_status, 4))
+    return IBP_ERR_ARG;
+  return launch_kv_bounds(*cache, d_bounds, d_begin, d_status, reinterpret_cast<cudaStream_t>(s));
+}
+
+// Whether lists of `pages` hold a sequence's first page and those of its rows.
+static int kv_pages_ok(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q, int64_t pages) {
+  const int64_t most = max_q < n_rows ? max_q : n_rows, P = cache->page_tokens;
+  const int64_t own = most > 0 ? (most - 1 + P - 1) / P + 1 : 0;
+  if (pages < own + 1 || pages > KV_MAX_CAPACITY / P) return IBP_ERR_ARG;
+  return IBP_OK;
+}
+
+int ibp_kv_select_scratch_bytes(const ibp_kv_cache *cache, size_t *bytes) {
+  if (!bytes) return IBP_ERR_ARG;
+  if (int rc = kv_geometry(cache)) return rc;
+  *bytes = kv_select_scratch_bytes(*cache);
+  return IBP_OK;
+}
+
+int ibp_kv_select(const ibp_kv_cache *cache, const int8_t *d_bounds, const ibp_kv_query *query,
+                  int64_t pages, int32_t *d_columns, void *d_scratch, size_t scratch_bytes,
+                  int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_query_rows(cache, query)) return rc;
+  const ibp_kv_query &q = *query;
+  if (int rc = kv_pages_ok(cache, q.n_rows, q.max_q, pages)) return rc;
+  if (scratch_bytes < kv_select_scratch_bytes(*cache)) return IBP_ERR_ARG;
+  if (cache->batch == 0) return IBP_OK;
+  if (!kv_pointers(cache) || !device_ptr(d_bounds, 16) || !device_ptr(d_columns, 4) ||
+      !device_or_null(q.d_cu, 4) || !device_ptr(d_scratch, 16) || !device_or_null(d_status, 4))
+    return IBP_ERR_ARG;
+  if (q.n_rows > 0 && !device_ptr(q.q, 16)) return IBP_ERR_ARG;
+  return launch_kv_select(*cache, d_bounds, q, pages, d_columns, d_scratch, d_status,
+                          reinterpret_cast<cudaStream_t>(s));
+}
+
+int ibp_kv_attention_selected_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
+                                            int32_t q_heads, int64_t pages, size_t *bytes) {
+  if (!bytes) return IBP_ERR_ARG;
+  if (int rc = kv_query_sizes(cache, n_rows, max_q, q_heads)) return rc;
+  if (int rc = kv_pages_ok(cache, n_rows, max_q, pages)) return rc;
+  *bytes = kv_selected_scratch_bytes(*cache, n_rows, max_q, q_heads);
+  return IBP_OK;
+}
+
+int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *query,
+                              const int32_t *d_columns, int64_t pages, void *d_scratch,
+                              size_t scratch_bytes, int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_query_rows(cache, query)) return rc;
+  const ibp_kv_query &q = *query;
+  if (int rc = kv_query_out(cache, q)) return rc;
+  if (q.d_weights || q.d_weights_in) return IBP_ERR_ARG;
+  if (int rc = kv_pages_ok(cache, q.n_rows, q.max_q, pages)) return rc;
+  if (cache->batch == 0 || q.n_rows == 0) return IBP_OK;
+  if (scratch_bytes < kv_selected_scratch_bytes(*cache, q.n_rows, q.max_q, q.q_heads)) return IBP_ERR_ARG;
+  if (!kv_pointers(cache) || !device_ptr(d_scratch, 16) || !device_or_null(q.d_lse, 4) ||
+      !device_or_null(q.d_cu, 4) || !device_ptr(d_columns, 4) || !device_or_null(d_status, 4) ||
+      !device_ptr(q.q, 16) || !device_ptr(q.out, 16))
+    return IBP_ERR_ARG;
+  return launch_kv_attention_selected(*cache, q, d_columns, pages, d_scratch, d_status,
+                                      reinterpret_cast<cudaStream_t>(s));
 }
 
 int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes) {

@@ -53,6 +53,20 @@ struct Cut {
   int b, head, block, tile, tiles, unused;
 };
 
+// What a call goes over. ALL: every token that a sequence holds. SELECTED: the tokens of the
+// pages that a list names for each sequence and K/V head, one after another as if they were
+// the sequence (the last pages, where its rows stand, are among them, so that what a row sees
+// is a matter of places as before). SHARED: spans of tokens with rows of one or more sequences.
+enum class Over { ALL, SELECTED, SHARED };
+
+// Rows [row0, row0 + n) go over len tokens in the pages from d_table[table_at] on; row i sees
+// those up to at + i.
+struct Span {
+  int64_t row0, table_at;
+  int64_t before;  // tiles of the launch before this span's
+  int n, len, at, group;
+};
+
 struct AttentionArgs {
   ibp_kv_cache c;
   ibp_kv_query q;
@@ -65,6 +79,10 @@ struct AttentionArgs {
   float *lse2;      // of segments that one CTA finished, in the order of score_row
   float *scores;    // [rows * q_heads][score_cols] in that order, or null
   Cut *cuts;        // [ctas] (many rows)
+  const int32_t *columns;  // SELECTED: [batch][n_heads][pages] columns of the page table
+  int pages;
+  const Span *spans;  // SHARED: [batch], and where segments that one CTA finished leave
+  float *side, *side_lse2;  // their normalised rows [row][q_head][D] and log2 of their sums
 };
 
 struct Sequence {
@@ -72,8 +90,29 @@ struct Sequence {
   int n, len;    // query rows, tokens
 };
 
+// Pages that a sequence of len > 0 tokens has, and of them the first that its last n tokens
+// (its query rows) lie in; SELECTED lists hold `count` columns, those from `first_own` on last.
+struct PageList {
+  int all, first_own, count;
+};
+__device__ __forceinline__ PageList page_list(const ibp_kv_cache &c, int len, int n, int pages) {
+  PageList p;
+  p.all = (len + c.page_tokens - 1) / c.page_tokens;
+  p.first_own = min(max(len - n, 0) / c.page_tokens, p.all - 1);
+  p.count = min(pages, p.all);
+  return p;
+}
+
+template <Over OVER = Over::ALL>
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, int32_t *status) {
   Sequence s;
+  if constexpr (OVER == Over::SHARED) {
+    const Span &from = a.spans[a.b0 + b];
+    s.row0 = from.row0;
+    s.n = from.n;
+    s.len = from.len;
+    return s;
+  }
   int64_t lo, hi;
   kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + b, status, &lo, &hi);
   if (hi - lo > a.q.max_q) {
@@ -83,7 +122,38 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, i
   s.row0 = lo;
   s.n = (int)(hi - lo);
   s.len = kv_len(a.c, a.b0 + b, status);
+  if constexpr (OVER == Over::SELECTED) {  // whole pages but the last
+    const PageList p = page_list(a.c, s.len, s.n, a.pages);
+    s.len -= (p.all - p.count) * a.c.page_tokens;
+  }
   return s;
+}
+
+// The page of tokens that are `col` pages into what sequence b's K/V head goes over, or -1
+// (recorded) where there is none.
+template <Over OVER>
+__device__ __forceinline__ int page_of(const AttentionArgs &a, int b, int head, int col) {
+  if constexpr (OVER == Over::SHARED) {
+    const int p = __ldg(a.c.d_table + a.spans[a.b0 + b].table_at + col);
+    if (p >= 0 && p < a.c.n_pages) return p;
+    report(a.status, IBP_ERR_INDEX);
+    return -1;
+  }
+  if constexpr (OVER == Over::SELECTED) {
+    const int len = kv_len(a.c, a.b0 + b, nullptr), n = sequence_of(a, b, nullptr).n;
+    const PageList p = page_list(a.c, len, n, a.pages);
+    const int listed =
+        __ldg(a.columns + ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.pages + col);
+    // the rows' own pages are the list's last, in order; no other entry is one of them, so that
+    // no token past the length counts and none that a row does not see
+    const int own = p.all - p.first_own, left = p.count - col;
+    if (left <= own ? listed != p.all - left : listed < 0 || listed >= p.first_own) {
+      report(a.status, IBP_ERR_INDEX);
+      return -1;
+    }
+    col = listed;
+  }
+  return kv_page(a.c, a.b0 + b, col, a.status);
 }
 
 // The rows of a sequence that the launch is for: all but where scores are kept for the weights
@@ -91,11 +161,11 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, i
 struct Slice : Sequence {
   int at;  // position of the first of them: row i sees the tokens up to at + i
 };
-template <bool SCORES>
+template <bool SCORES, Over OVER = Over::ALL>
 __device__ __forceinline__ Slice slice_of(const AttentionArgs &a, int b, int32_t *status) {
   Slice s;
-  static_cast<Sequence &>(s) = sequence_of(a, b, status);
-  s.at = s.len - s.n;
+  static_cast<Sequence &>(s) = sequence_of<OVER>(a, b, status);
+  s.at = OVER == Over::SHARED ? a.spans[a.b0 + b].at : s.len - s.n;
   if (SCORES && a.slice_rows) {
     const int skip = min(a.slice0, s.n);
     s.row0 += skip;
@@ -258,7 +328,7 @@ constexpr int JOIN_AHEAD = SCORES || Plan::MB > 16 ? 4 : 16;
 // HBM): 23 us alone, waiting for loads; it starts while the attending kernel ends. Every
 // block waits for that kernel before it returns, with work or without: what comes next in
 // the stream or a graph may be ordered behind this grid alone.
-template <int D, int DT, typename Plan, bool SCORES>
+template <int D, int DT, typename Plan, bool SCORES, Over OVER = Over::ALL>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
@@ -269,13 +339,13 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
   const int group = a.q.q_heads / a.c.n_heads;
   // what follows from the lengths alone is worked out before the attending kernel ends
   // (whatever wrote the lengths ended before that one began)
-  const Slice s = slice_of<SCORES>(a, b, nullptr);
+  const Slice s = slice_of<SCORES, OVER>(a, b, nullptr);
   const Plan plan(s, group);
   const int all = s.n * group;
   if (threadIdx.x < 32) {
     int64_t before = 0, total = 0;
     for (int k = threadIdx.x; k < a.batch; k += 32) {
-      const Slice other = slice_of<SCORES>(a, k, nullptr);
+      const Slice other = slice_of<SCORES, OVER>(a, k, nullptr);
       const Plan theirs(other, group);
       const int64_t tiles = a.c.n_heads * theirs.before(theirs.blocks);
       total += tiles;

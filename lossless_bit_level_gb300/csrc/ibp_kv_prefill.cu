@@ -1,6 +1,6 @@
 // Attention of many query rows over the 8-bit paged key/value cache, on the fifth
 // generation's matrix unit (declared in include/ibp.h; the formulas stand at the head of
-// ibp_kv_attention.cu).
+// ibp_kv_attend.cuh).
 //
 // A CTA takes 256 query rows of one K/V head (the rows of all query heads that share it,
 // so shared heads fill the matrix unit) over tiles of 128 tokens. Codes become fp16 in
@@ -244,7 +244,7 @@ __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64
   }
 }
 
-// Codes to fp16, exactly (as in ibp_kv_attention.cu).
+// Codes to fp16, exactly (as in ibp_kv_attend.cuh).
 template <int CODE, int HIGH>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   if constexpr (CODE == IBP_KV_INT8) {
