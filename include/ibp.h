@@ -616,6 +616,25 @@ int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *que
                               const int32_t *d_columns, int64_t pages, void *d_scratch,
                               size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
 
+/* Attention of a batch whose sequences share beginnings, as ibp_kv_attention (without
+ * weights: IBP_ERR_ARG). Group g is the sequences d_groups[g] .. d_groups[g+1] - 1 (d_groups
+ * [n_groups + 1] rising within [0, batch], else IBP_ERR_INDEX; sequences of no group share
+ * nothing); their first d_prefix[g] tokens are the same, and for the whole pages of these
+ * their tables name the same pages (those of the group's first sequence are read; pages in
+ * use may be named more than once in calls that only read). A prefix longer than a
+ * sequence, or than what the first of its rows sees, counts as far as all rows of the group
+ * see it. Each beginning is gone over once for all rows of its group, in slabs of 128
+ * sequences. group_rows: the most query rows that the sequences of one group have together;
+ * it chooses the kernel, no result depends on its being right. d_scratch: the size
+ * ibp_kv_attention_shared_scratch_bytes gives for the same cache, query shapes and groups.
+ * Asynchronous on s, capturable. */
+int ibp_kv_attention_shared_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
+                                          int32_t q_heads, int64_t n_groups, int64_t group_rows,
+                                          size_t *bytes);
+int ibp_kv_attention_shared(const ibp_kv_cache *cache, const ibp_kv_query *query, const int32_t *d_groups,
+                            const int32_t *d_prefix, int64_t n_groups, int64_t group_rows,
+                            void *d_scratch, size_t scratch_bytes, int32_t *d_status, ibp_stream_t s);
+
 /* Eviction by accumulated weight: of every sequence b and head h longer than budget,
  * keeps the last `recent` tokens and, of the others, the budget - recent with the
  * largest d_weights[b][h][t] (equal weights: the lowest t first; a NaN counts as the

@@ -129,7 +129,8 @@ SYMBOLS = ("ibp_status_string", "ibp_slot_bytes", "ibp_meta_scratch_bytes", "ibp
            "ibp_kv_attention_scratch_bytes", "ibp_kv_attention", "ibp_kv_evict_scratch_bytes",
            "ibp_kv_evict", "ibp_kv_append_rotated", "ibp_kv_bounds",
            "ibp_kv_select_scratch_bytes", "ibp_kv_select",
-           "ibp_kv_attention_selected_scratch_bytes", "ibp_kv_attention_selected")
+           "ibp_kv_attention_selected_scratch_bytes", "ibp_kv_attention_selected",
+           "ibp_kv_attention_shared_scratch_bytes", "ibp_kv_attention_shared")
 
 # declared in include/ibp_testing.h (a testing hook, not part of the codec)
 TESTING_SYMBOLS = ("ibp_testing_set_wait_limit_ns", "ibp_testing_withhold_plans")
@@ -199,6 +200,8 @@ def load() -> ctypes.CDLL:
     lib.ibp_kv_bounds.argtypes = [vp, vp, vp, vp, vp]
     lib.ibp_kv_select_scratch_bytes.argtypes = [vp, szp]
     lib.ibp_kv_select.argtypes = [vp, vp, vp, i64, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.ibp_kv_attention_shared_scratch_bytes.argtypes = [vp, i64, i64, i32, i64, i64, szp]
+    lib.ibp_kv_attention_shared.argtypes = [vp, vp, vp, vp, i64, i64, vp, ctypes.c_size_t, vp, vp]
     lib.ibp_kv_attention_selected_scratch_bytes.argtypes = [vp, i64, i64, i32, i64, szp]
     lib.ibp_kv_attention_selected.argtypes = [vp, vp, vp, i64, vp, ctypes.c_size_t, vp, vp]
     for name in SYMBOLS[1:]:
@@ -859,6 +862,34 @@ def kv_attention_selected(cache: KVCache, columns: torch.Tensor, q: torch.Tensor
                                             _columns(cache, columns), _at(scratch),
                                             scratch.numel() * scratch.element_size(), _at(status),
                                             _raw_stream(stream)), "ibp_kv_attention_selected")
+
+
+def kv_attention_shared_scratch_bytes(cache: KVCache, n_rows: int, max_q: int, q_heads: int,
+                                      n_groups: int, group_rows: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ibp_kv_attention_shared_scratch_bytes(cache.address, int(n_rows), int(max_q),
+                                                        int(q_heads), int(n_groups),
+                                                        int(group_rows), ctypes.byref(out)),
+           "ibp_kv_attention_shared_scratch_bytes")
+    return out.value
+
+
+def kv_attention_shared(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scale: float,
+                        scratch: torch.Tensor, groups: torch.Tensor, prefix: torch.Tensor,
+                        group_rows: int, cu_q: torch.Tensor | None = None,
+                        max_q: int | None = None, lse: torch.Tensor | None = None,
+                        status: torch.Tensor | None = None, stream=None) -> None:
+    """ibp_kv_attention_shared: ``kv_attention`` where the sequences groups[g]..groups[g+1]-1
+    (int32 [n_groups + 1]) share their first prefix[g] tokens (int32 [n_groups]) and the pages
+    of these, each beginning gone over once for the whole group; ``group_rows``: the most
+    query rows of one group."""
+    query = _query(cache, q, out, scale, cu_q, max_q, lse)
+    n = prefix.numel()
+    _check(load().ibp_kv_attention_shared(
+        cache.address, ctypes.addressof(query), _int32(groups, n + 1, "groups"),
+        _int32(prefix, n, "prefix"), n, int(group_rows), _at(scratch),
+        scratch.numel() * scratch.element_size(), _at(status), _raw_stream(stream)),
+        "ibp_kv_attention_shared")
 
 
 def kv_evict_scratch_bytes(cache: KVCache, budget: int) -> int:

@@ -282,6 +282,41 @@ int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *que
                                       reinterpret_cast<cudaStream_t>(s));
 }
 
+static int kv_groups_ok(const ibp_kv_cache *cache, int64_t n_groups, int64_t group_rows) {
+  return n_groups < 0 || n_groups > cache->batch || group_rows < 0 || group_rows > KV_MAX_CAPACITY
+             ? IBP_ERR_ARG
+             : IBP_OK;
+}
+
+int ibp_kv_attention_shared_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
+                                          int32_t q_heads, int64_t n_groups, int64_t group_rows,
+                                          size_t *bytes) {
+  if (!bytes) return IBP_ERR_ARG;
+  if (int rc = kv_query_sizes(cache, n_rows, max_q, q_heads)) return rc;
+  if (int rc = kv_groups_ok(cache, n_groups, group_rows)) return rc;
+  *bytes = kv_shared_scratch_bytes(*cache, n_rows, max_q, q_heads, group_rows);
+  return IBP_OK;
+}
+
+int ibp_kv_attention_shared(const ibp_kv_cache *cache, const ibp_kv_query *query, const int32_t *d_groups,
+                            const int32_t *d_prefix, int64_t n_groups, int64_t group_rows,
+                            void *d_scratch, size_t scratch_bytes, int32_t *d_status, ibp_stream_t s) {
+  if (int rc = kv_query_rows(cache, query)) return rc;
+  const ibp_kv_query &q = *query;
+  if (int rc = kv_query_out(cache, q)) return rc;
+  if (int rc = kv_groups_ok(cache, n_groups, group_rows)) return rc;
+  if (q.d_weights || q.d_weights_in) return IBP_ERR_ARG;
+  if (cache->batch == 0 || q.n_rows == 0) return IBP_OK;
+  if (scratch_bytes < kv_shared_scratch_bytes(*cache, q.n_rows, q.max_q, q.q_heads, group_rows))
+    return IBP_ERR_ARG;
+  if (!kv_pointers(cache) || !device_ptr(d_scratch, 16) || !device_or_null(q.d_lse, 4) ||
+      !device_or_null(q.d_cu, 4) || !device_or_null(d_status, 4) || !device_ptr(q.q, 16) ||
+      !device_ptr(q.out, 16) || (n_groups > 0 && (!device_ptr(d_groups, 4) || !device_ptr(d_prefix, 4))))
+    return IBP_ERR_ARG;
+  return launch_kv_attention_shared(*cache, q, d_groups, d_prefix, n_groups, group_rows, d_scratch, d_status,
+                                    reinterpret_cast<cudaStream_t>(s));
+}
+
 int ibp_kv_evict_scratch_bytes(const ibp_kv_cache *cache, int64_t budget, size_t *bytes) {
   if (!bytes) return IBP_ERR_ARG;
   if (int rc = kv_geometry(cache)) return rc;

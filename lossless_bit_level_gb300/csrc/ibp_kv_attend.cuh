@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads, cta = blockIdx.x;
   grid_launch_dependents();
+  if constexpr (OVER == Over::SHARED) grid_dependency_wait();  // the spans
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
           const int qh = head * group + rr % group;
           const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
           if constexpr (OVER == Over::SHARED) {  // joined with the rows' other span later
-            const int64_t at = row * a.q.q_heads + qh;
+            const int64_t at = row * a.q.q_heads + qh + (a.b0 + b < SHARE_SLAB ? 0 : a.side_rows);
             reinterpret_cast<float4 *>(a.side)[at * (D / 4) + piece] = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
             if (piece == 0) a.side_lse2[at] = sum > 0.0f ? top + log2f(sum) : -INFINITY;
             continue;
@@ -609,16 +610,23 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   const int group = a.q.q_heads / a.c.n_heads;
   const int64_t blocks = (launch_rows_of(a) * group + S::MB - 1) / S::MB;
   const int64_t most = (int64_t)a.batch * a.c.n_heads * blocks * (a.score_cols / TILE);
-  a.ctas = (int)std::min<int64_t>(std::min(S::per_sm * dev.sm_count, MAX_CTAS), std::max<int64_t>(most, 1));
-  kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
-  if constexpr (OVER == Over::SHARED) return IBP_OK;  // joined by a kernel of its own
-  const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
-  if (launch_dependent(kv_finish_kernel<D, DT, typename S::Plan, SCORES, OVER>,
-                       dim3((unsigned)(blocks + chunks), (unsigned)a.c.n_heads, (unsigned)a.batch),
-                       dim3(FINISH_THREADS), 0, s, a, (int)blocks) != cudaSuccess)
-    return IBP_ERR_CUDA;
-  return IBP_OK;
+  // (SHARED: how many the spans are for is known to their plan alone, which the joining goes by)
+  a.ctas = std::min(S::per_sm * dev.sm_count, MAX_CTAS);
+  if (OVER != Over::SHARED) a.ctas = (int)std::min<int64_t>(a.ctas, std::max<int64_t>(most, 1));
+  if constexpr (OVER == Over::SHARED) {  // after the kernel that lays out the spans; joined by one of its own
+    return launch_dependent(kernel, dim3((unsigned)a.ctas), dim3(THREADS), S::smem, s, a) == cudaSuccess
+               ? IBP_OK
+               : IBP_ERR_CUDA;
+  } else {
+    kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
+    if (launch_dependent(kv_finish_kernel<D, DT, typename S::Plan, SCORES, OVER>,
+                         dim3((unsigned)(blocks + chunks), (unsigned)a.c.n_heads, (unsigned)a.batch),
+                         dim3(FINISH_THREADS), 0, s, a, (int)blocks) != cudaSuccess)
+      return IBP_ERR_CUDA;
+    return IBP_OK;
+  }
 }
 
 }  // namespace

@@ -46,6 +46,8 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+}  // namespace
+
 // What the joining kernel for many rows needs of a CTA's place: the segment its stretch
 // begins in (tile: how many of the segment's tiles lie before it; 0: none).
 struct Cut {
@@ -59,6 +61,9 @@ struct Cut {
 // is a matter of places as before). SHARED: spans of tokens with rows of one or more sequences.
 enum class Over { ALL, SELECTED, SHARED };
 
+// Sequences whose spans are laid out together: at most so many beginnings that several of them
+// share come first, each with the rows of all its sequences, then what each sequence has behind.
+constexpr int SHARE_SLAB = 128;
 // Rows [row0, row0 + n) go over len tokens in the pages from d_table[table_at] on; row i sees
 // those up to at + i.
 struct Span {
@@ -81,9 +86,21 @@ struct AttentionArgs {
   Cut *cuts;        // [ctas] (many rows)
   const int32_t *columns;  // SELECTED: [batch][n_heads][pages] columns of the page table
   int pages;
-  const Span *spans;  // SHARED: [batch], and where segments that one CTA finished leave
-  float *side, *side_lse2;  // their normalised rows [row][q_head][D] and log2 of their sums
+  // SHARED: [batch], and where segments that one CTA finished leave their normalised rows
+  // [row][q_head][D] and log2 of their sums, for beginnings and (side_rows further) the rest
+  const Span *spans;
+  float *side, *side_lse2;
+  int64_t side_rows;
 };
+
+// Many query rows over SHARED spans (ibp_kv_prefill.cu): a.spans, a.side and a.part are set.
+struct PrefillShape {
+  int rows, tile, ctas;  // of a segment, tokens of a tile, how many CTAs share the tiles
+};
+PrefillShape prefill_shape();
+int launch_kv_prefill_shared(AttentionArgs a, cudaStream_t s);
+
+namespace {
 
 struct Sequence {
   int64_t row0;  // its first query row

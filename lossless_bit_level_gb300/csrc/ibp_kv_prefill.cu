@@ -25,6 +25,7 @@
 // against 270). Two places for scores with P over them took 272 us with a wait for the product
 // that reads P.
 #include <algorithm>
+#include <type_traits>
 
 #include "ibp_kv_attention.cuh"
 
@@ -54,7 +55,9 @@ constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 // factors: between that and 2^4 times it). Lower than SHIFT: here a row that outgrows its
 // reference costs the whole warp (2048 rows over 8192 tokens: 306 us with 7, 277 with 4).
 constexpr float ROW_SHIFT = 2.0f;
-using Plan = CausalPlan<MB, TILE>;
+// SHARED spans are seen whole by all their rows.
+template <Over OVER>
+using PlanOf = std::conditional_t<OVER == Over::SHARED, EvenPlan<MB, TILE>, CausalPlan<MB, TILE>>;
 
 // ---- tensor memory and the matrix instruction
 __device__ __forceinline__ void tmem_alloc(uint32_t *at) {
@@ -208,12 +211,13 @@ struct __align__(16) Cursor {
   int b, head, block, tile, tiles;
   Sequence seq;
 };
+template <Over OVER>
 __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_t *prefix, int group,
                                             int64_t x) {
   Cursor c;
   c.b = find_sequence(prefix, a.batch, x);
-  c.seq = sequence_of(a, c.b, nullptr);
-  const Plan plan(c.seq, group);
+  c.seq = sequence_of<OVER>(a, c.b, nullptr);
+  const PlanOf<OVER> plan(c.seq, group);
   const int64_t local = x - prefix[c.b], per_head = (prefix[c.b + 1] - prefix[c.b]) / a.c.n_heads;
   c.head = (int)(local / per_head);
   const int64_t in = local - c.head * per_head;
@@ -224,11 +228,12 @@ __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_
 }
 static_assert(sizeof(Cursor) <= 48, "the place kept for it");
 // The first tile of the next segment that has one (there is one: the caller's x < total).
+template <Over OVER>
 __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64_t *prefix, int group,
                                              Cursor &c) {
   c.tile = 0;
   for (;;) {
-    const Plan plan(c.seq, group);
+    const PlanOf<OVER> plan(c.seq, group);
     if (++c.block == plan.blocks) {
       c.block = 0;
       if (++c.head == a.c.n_heads) {
@@ -236,10 +241,10 @@ __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64
         do {
           ++c.b;
         } while (prefix[c.b] == prefix[c.b + 1]);
-        c.seq = sequence_of(a, c.b, nullptr);
+        c.seq = sequence_of<OVER>(a, c.b, nullptr);
       }
     }
-    c.tiles = Plan(c.seq, group).tiles(c.block);
+    c.tiles = PlanOf<OVER>(c.seq, group).tiles(c.block);
     if (c.tiles > 0) return;
   }
 }
@@ -259,9 +264,10 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   }
 }
 
-template <int D, int CODE, int DT>
+template <int D, int CODE, int DT, Over OVER>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ AttentionArgs a) {
   using M = Memory<D>;
+  using Plan = PlanOf<OVER>;
   static_assert(M::info % alignof(TileInfo) == 0 && M::bars % 8 == 0 && M::prefix % 8 == 0 &&
                     M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0 && M::bytes <= 227 * 1024,
                 "what lies in shared memory is aligned and fits");
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads;
   grid_launch_dependents();
+  if constexpr (OVER == Over::SHARED) grid_dependency_wait();  // the spans
   if (smem_u32(smem) & 1023) {  // the operands' rows would be swizzled otherwise than written
     report(a.status, IBP_ERR_CUDA);
     if (threadIdx.x == 0) a.cuts[cta] = Cut();
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const int b = k0 + lane;
       int64_t tiles = 0;
       if (b < a.batch) {
-        const Plan plan(sequence_of(a, b, cta == 0 ? a.status : nullptr), group);
+        const Plan plan(sequence_of<OVER>(a, b, cta == 0 ? a.status : nullptr), group);
         tiles = c.n_heads * plan.before(plan.blocks);
       }
       int64_t sum = tiles;
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         tc_commit(&s_full[2 * w + h], mine);
         if (h) tc_commit(&k_free[s], mine);
       };
-      Cursor cur = cursor_at(a, prefix, group, lo);
+      Cursor cur = cursor_at<OVER>(a, prefix, group, lo);
       const int n = (int)(hi - lo);
       int g = 0;  // tiles of the stretch begun
       uint32_t segment = 0;
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           }
         }
         ++segment;
-        if (ok && g < n) next_segment(a, prefix, group, cur);
+        if (ok && g < n) next_segment<OVER>(a, prefix, group, cur);
       }
       // nothing may be left running when this CTA gives its memory back
       tc_commit(&last[w], mine);
@@ -495,14 +502,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         int b, head, t0, len;
       };
       Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + 8;  // one for all lanes
-      if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+      if (lane == 0) *cur = cursor_at<OVER>(a, prefix, group, lo);
       __syncwarp();
       int ahead = 0;  // tiles of the stretch taken
       auto take = [&] {
         const Place p = {cur->b, cur->head, cur->tile * TILE, cur->seq.len};
         ++ahead;
         __syncwarp();
-        if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment(a, prefix, group, *cur);
+        if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment<OVER>(a, prefix, group, *cur);
         __syncwarp();
         return p;
       };
@@ -514,6 +521,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       };
       auto ask = [&](const Place &p) {
         const int t = p.t0 + (lane & 7) * 16;
+        if constexpr (OVER == Over::SHARED)
+          return t < p.len ? __ldg(c.d_table + a.spans[a.b0 + p.b].table_at + t / c.page_tokens) : -1;
         return t < p.len ? __ldg(c.d_table + (int64_t)(a.b0 + p.b) * c.table_stride + t / c.page_tokens) : -1;
       };
       auto look_up = [&](const Place &p, int page) {
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
       unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
       Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
-      if (lane == 0) *cur = cursor_at(a, prefix, group, lo);
+      if (lane == 0) *cur = cursor_at<OVER>(a, prefix, group, lo);
       __syncwarp();
       if (threadIdx.x == 0) {
         const Cut cut = {prefix[a.batch], cur->b, cur->head, cur->block, cur->tile, cur->tiles, 0};
@@ -668,7 +677,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full[w]);
         }
-        const int limit = live ? max(cur->seq.len - cur->seq.n + rr / group + 1, 0) : 0x7FFFFFFF;
+        const int limit = !live ? 0x7FFFFFFF
+                          : OVER == Over::SHARED ? cur->seq.len
+                                                 : max(cur->seq.len - cur->seq.n + rr / group + 1, 0);
         float m = NONE, mv = NONE, over = 0.0f;  // over: what the references are to rise by,
         bool pending = false;                     // if any row's are
         uint64_t l = 0;                           // two halves of the sum
@@ -809,7 +820,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           float y[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(s[e]) * f;
-          if (done) {
+          if (OVER == Over::SHARED && done) {  // joined with the rows' other span later
+            float4 *side = reinterpret_cast<float4 *>(a.side + (q_row * a.q.q_heads + q_head) * D + 32 * q4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) side[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          } else if (done) {
             store16<DT>(out + 64 * q4, y);
             store16<DT>(out + 64 * q4 + 32, y + 16);
           } else {
@@ -821,7 +836,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         tc_fence_before();
         if (live) {
-          if (done) {
+          if (OVER == Over::SHARED && done) {
+            a.side_lse2[q_row * a.q.q_heads + q_head] = sum > 0.0f ? m + log2f(sum) : -INFINITY;
+          } else if (done) {
             if (a.q.d_lse)
               a.q.d_lse[q_row * a.q.q_heads + q_head] = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
           } else {
@@ -830,7 +847,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         x += count;
         __syncwarp();
-        if (lane == 0 && x < n_tiles) next_segment(a, prefix, group, *cur);
+        if (lane == 0 && x < n_tiles) next_segment<OVER>(a, prefix, group, *cur);
         __syncwarp();
       }
     } else if (threadIdx.x == 0) {
@@ -838,9 +855,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       a.cuts[cta] = none;
     }
     // blocks of rows that see nothing have no tiles: the CTAs share them out by heads
-    for (int i = cta; i < a.batch * c.n_heads; i += gridDim.x) {
+    for (int i = cta; OVER == Over::ALL && i < a.batch * c.n_heads; i += gridDim.x) {
       const int b = i / c.n_heads, head = i % c.n_heads;
-      const Sequence sq = sequence_of(a, b, nullptr);
+      const Sequence sq = sequence_of<OVER>(a, b, nullptr);
       if (sq.n <= sq.len) continue;
       const Plan plan(sq, group);
       for (int block = 0; block < plan.blocks && plan.tiles(block) == 0; ++block) {
@@ -910,9 +927,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 8) kv_join_kernel(const __grid_c
   }
 }
 
-template <int D, int CODE, int DT>
+template <int D, int CODE, int DT, Over OVER>
 int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
-  const auto kernel = kv_prefill_kernel<D, CODE, DT>;
+  const auto kernel = kv_prefill_kernel<D, CODE, DT, OVER>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Memory<D>::bytes) !=
       cudaSuccess)
     return IBP_ERR_CUDA;
@@ -923,22 +940,28 @@ int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
       16 * attr.numRegs < 8 * ROW_REGS + 4 * CONVERT_REGS + 4 * ISSUE_REGS)
     return IBP_ERR_CUDA;
   a.ctas = std::min(dev.sm_count, MAX_PREFILL_CTAS);
-  kernel<<<a.ctas, THREADS, Memory<D>::bytes, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
-  if (a.ctas > 1 &&
-      launch_dependent(kv_join_kernel<D, DT>, dim3(JOIN_SHARE, (unsigned)(a.ctas - 1)), dim3(JOIN_THREADS),
-                       0, s, a) != cudaSuccess)
-    return IBP_ERR_CUDA;
-  return IBP_OK;
+  if constexpr (OVER == Over::SHARED) {  // after the kernel that lays out the spans; joined by one of its own
+    return launch_dependent(kernel, dim3((unsigned)a.ctas), dim3(THREADS), Memory<D>::bytes, s, a) == cudaSuccess
+               ? IBP_OK
+               : IBP_ERR_CUDA;
+  } else {
+    kernel<<<a.ctas, THREADS, Memory<D>::bytes, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    if (a.ctas > 1 &&
+        launch_dependent(kv_join_kernel<D, DT>, dim3(JOIN_SHARE, (unsigned)(a.ctas - 1)), dim3(JOIN_THREADS),
+                         0, s, a) != cudaSuccess)
+      return IBP_ERR_CUDA;
+    return IBP_OK;
+  }
 }
 
-template <int D>
+template <int D, Over OVER>
 int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   if (a.c.code == IBP_KV_INT8)
-    return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_INT8, IBP_BF16>(a, dev, s)
-                                 : launch_for<D, IBP_KV_INT8, IBP_FP16>(a, dev, s);
-  return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_E4M3, IBP_BF16>(a, dev, s)
-                               : launch_for<D, IBP_KV_E4M3, IBP_FP16>(a, dev, s);
+    return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_INT8, IBP_BF16, OVER>(a, dev, s)
+                                 : launch_for<D, IBP_KV_INT8, IBP_FP16, OVER>(a, dev, s);
+  return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_E4M3, IBP_BF16, OVER>(a, dev, s)
+                               : launch_for<D, IBP_KV_E4M3, IBP_FP16, OVER>(a, dev, s);
 }
 
 }  // namespace
@@ -961,10 +984,22 @@ int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scra
   a.part = reinterpret_cast<float *>(a.cuts + MAX_PREFILL_CTAS);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += BATCH) {
     a.batch = std::min(c.batch - a.b0, BATCH);
-    if (int rc = c.head_dim == 64 ? launch_types<64>(a, dev, s) : launch_types<128>(a, dev, s))
+    if (int rc = c.head_dim == 64 ? launch_types<64, Over::ALL>(a, dev, s)
+                                 : launch_types<128, Over::ALL>(a, dev, s))
       return rc;
   }
   return IBP_OK;
+}
+
+int launch_kv_prefill_shared(AttentionArgs a, cudaStream_t s) {
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  return a.c.head_dim == 64 ? launch_types<64, Over::SHARED>(a, dev, s)
+                            : launch_types<128, Over::SHARED>(a, dev, s);
+}
+PrefillShape prefill_shape() {
+  DeviceInfo dev;
+  return {MB, TILE, device_info(&dev) == IBP_OK ? std::min(dev.sm_count, MAX_PREFILL_CTAS) : 0};
 }
 
 }  // namespace ibp

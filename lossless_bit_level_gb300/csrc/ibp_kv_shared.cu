@@ -1,0 +1,385 @@
+// Attention of a batch whose sequences share beginnings, over the 8-bit paged key/value cache
+// (declared in include/ibp.h).
+//
+// A row's softmax over a shared beginning and over the rest of its sequence are joined by
+// their sums of exponentials: with z_i = log2 of the i-th sum and o_i its normalised output,
+//   z = log2(2^z_0 + 2^z_1),  out = o_0 2^(z_0 - z) + o_1 2^(z_1 - z).
+// So a beginning is gone over once for the rows of all its sequences together, which fill the
+// matrix unit, where each sequence by itself would read and convert it again.
+#include "ibp_kv_attend.cuh"
+
+namespace ibp {
+
+namespace {
+
+constexpr int PLAN_THREADS = SHARE_SLAB;
+constexpr int JOIN_WARPS = 4, JOIN_PARTS = 4;
+
+struct Side {
+  int mb, tile, ctas;  // rows of a segment, tokens of a tile, CTAs of the launch
+  const float *part;
+};
+
+struct ShareArgs {
+  ibp_kv_cache c;
+  ibp_kv_query q;
+  int32_t *status;
+  const int32_t *groups, *prefix;
+  int n_groups, b0, batch;
+  Side side[2];     // beginnings, the rest
+  int together;     // both in one launch: tiles of the rest follow those of the beginnings
+  Span *spans;      // [2 * SHARE_SLAB]
+  int64_t *total;   // [2] tiles of each side's launch
+  const float *result, *result_lse2;  // as AttentionArgs::side
+  int64_t side_rows;
+};
+
+// Exclusive sum over the block's threads; *all: the sum.
+__device__ __forceinline__ int64_t sum_before(int64_t x, int64_t *warp_sum, int64_t *all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t run = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(FULL, run, o);
+    if (lane >= o) run += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = run;
+  __syncthreads();
+  int64_t before = 0, sum = 0;
+  for (int k = 0; k < PLAN_THREADS / 32; ++k) {
+    if (k < warp) before += warp_sum[k];
+    sum += warp_sum[k];
+  }
+  *all = sum;
+  return before + run - x;
+}
+
+// One CTA lays out the spans of up to SHARE_SLAB sequences. A run of sequences of one group
+// shares the whole pages of its prefix that none of its rows may not see; a run of one
+// sequence shares nothing.
+__global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __grid_constant__ ShareArgs a) {
+  __shared__ int group_of[SHARE_SLAB], seen[SHARE_SLAB], members[SHARE_SLAB];
+  __shared__ int first[SHARE_SLAB], last[SHARE_SLAB];
+  __shared__ int64_t warp_sum[PLAN_THREADS / 32];
+  const int t = threadIdx.x, b = a.b0 + t, heads = a.c.n_heads, group = a.q.q_heads / heads;
+  const int P = a.c.page_tokens;
+  const bool live = t < a.batch;
+  grid_launch_dependents();
+  // the last group that does not begin after the sequence, if it has it
+  int mine = -1;
+  if (live) {
+    int lo = -1, hi = a.n_groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(a.groups + mid) <= b) lo = mid; else hi = mid;
+    }
+    if (lo >= 0 && b < __ldg(a.groups + lo + 1)) mine = lo;
+  }
+  if (a.b0 == 0)
+    for (int g = t; g < a.n_groups; g += PLAN_THREADS) {
+      const int x = __ldg(a.groups + g), y = __ldg(a.groups + g + 1);
+      if (x < 0 || y < x || y > a.c.batch) report(a.status, IBP_ERR_INDEX);
+    }
+  group_of[t] = mine;
+  seen[t] = 0x7FFFFFFF;
+  members[t] = first[t] = last[t] = 0;
+  __syncthreads();
+  const bool starts = live && (t == 0 || mine < 0 || group_of[t - 1] != mine);
+  int64_t runs;
+  const int run = (int)sum_before(starts, warp_sum, &runs) + starts - 1;
+  Span s = {};
+  int n = 0, len = 0;
+  int64_t lo = 0, hi = 0;
+  if (live) {
+    kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, b, a.status, &lo, &hi);
+    if (hi - lo > a.q.max_q) report(a.status, IBP_ERR_INDEX);
+    n = (int)min(hi - lo, a.q.max_q);
+    len = kv_len(a.c, b, a.status);
+    if (starts) first[run] = t;
+    if (t + 1 == a.batch || mine < 0 || group_of[t + 1] != mine) last[run] = t;
+    if (n > 0) {
+      const int whole = mine >= 0 ? __ldg(a.prefix + mine) : 0;
+      atomicMin(&seen[run], max(min(whole, len - n + 1), 0) / P * P);
+      atomicAdd(&members[run], 1);
+    }
+  }
+  __syncthreads();
+  const int shared_tokens = live && members[run] > 1 ? seen[run] : 0;
+  // beginnings: thread t lays out run t
+  int64_t tiles = 0, total;
+  if (t < (int)runs && members[t] > 1 && seen[t] > 0) {
+    int64_t x, y, z, end;
+    kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + first[t], nullptr, &x, &y);
+    kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + last[t], nullptr, &z, &end);
+    s.row0 = x;
+    s.n = (int)max(min(end - x, (int64_t)0x3FFFFFFF), (int64_t)0);
+    s.len = s.at = seen[t];
+    s.table_at = (int64_t)(a.b0 + first[t]) * a.c.table_stride;
+    const int64_t blocks = ((int64_t)s.n * group + a.side[0].mb - 1) / a.side[0].mb;
+    tiles = heads * blocks * ((s.len + a.side[0].tile - 1) / a.side[0].tile);
+  }
+  s.before = sum_before(tiles, warp_sum, &total);
+  s.group = t;
+  a.spans[t] = s;
+  const int64_t behind = a.together ? total : 0;
+  if (t == 0) a.total[0] = total;
+  // the rest of each sequence
+  s = Span();
+  tiles = 0;
+  if (live) {
+    s.row0 = lo;
+    s.n = n;
+    s.len = len - shared_tokens;
+    s.at = s.len - n;
+    s.table_at = (int64_t)b * a.c.table_stride + shared_tokens / P;
+    s.group = run;
+    const int64_t blocks = ((int64_t)n * group + a.side[1].mb - 1) / a.side[1].mb;
+    tiles = heads * blocks * ((s.len + a.side[1].tile - 1) / a.side[1].tile);
+  }
+  s.before = behind + sum_before(tiles, warp_sum, &total);
+  a.spans[SHARE_SLAB + t] = s;
+  if (t == 0) {
+    a.total[1] = behind + total;
+    if (a.together) a.total[0] = behind + total;
+  }
+}
+
+// One row's result of one side: D/32 elements a lane, and log2 of its sum.
+template <int D>
+struct Half {
+  static constexpr int V = D / 32;
+  float y[V], z;
+};
+
+template <int V>
+__device__ __forceinline__ void load_lane(const float *from, float *y) {
+  if constexpr (V == 4) {
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(from));
+    y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
+  } else {
+    const float2 v = __ldcg(reinterpret_cast<const float2 *>(from));
+    y[0] = v.x; y[1] = v.y;
+  }
+}
+
+// A segment that one CTA finished left its rows; the parts of the others are joined in their
+// order, so that results do not depend on timing.
+template <int D>
+__device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const Span &s, int64_t row, int qh) {
+  constexpr int V = Half<D>::V;
+  Half<D> h;
+  for (int e = 0; e < V; ++e) h.y[e] = 0.0f;
+  h.z = -INFINITY;
+  // (rows outside the span: offsets that do not rise, recorded already)
+  if (s.len <= 0 || row < s.row0 || row >= s.row0 + s.n) return h;
+  const Side &side = a.side[which];
+  const int lane = threadIdx.x & 31, group = a.q.q_heads / a.c.n_heads;
+  const int64_t rr = (row - s.row0) * group + qh % group;
+  const int64_t blocks = ((int64_t)s.n * group + side.mb - 1) / side.mb;
+  const int tiles = (s.len + side.tile - 1) / side.tile, r = (int)(rr % side.mb);
+  const Parts p = parts_of(a.total[which], s.before + (qh / group * blocks + rr / side.mb) * tiles, tiles, side.ctas);
+  if (p.first == p.last) {
+    const int64_t at = row * a.q.q_heads + qh + which * a.side_rows;
+    load_lane<V>(a.result + at * D + lane * V, h.y);
+    h.z = __ldcg(a.result_lse2 + at);
+    return h;
+  }
+  const int64_t stride = (int64_t)side.mb * (D + 4);
+  float top = NONE, topv = NONE, sum = 0.0f;
+  for (int k0 = p.first; k0 <= p.last; k0 += JOIN_PARTS) {
+    float4 st[JOIN_PARTS];
+    float y[JOIN_PARTS][V];
+#pragma unroll
+    for (int k = 0; k < JOIN_PARTS; ++k) {
+      const int cta = min(k0 + k, p.last);
+      const float *part = side.part + ((int64_t)cta * 2 + (cta == p.first ? p.second : 0)) * stride;
+      st[k] = __ldcg(reinterpret_cast<const float4 *>(part + side.mb * D) + r);
+      load_lane<V>(part + r * D + lane * V, y[k]);
+    }
+    float m = top, mv = topv;
+#pragma unroll
+    for (int k = 0; k < JOIN_PARTS; ++k) {
+      m = fmaxf(m, st[k].x);  // a part read twice does not raise it
+      mv = fmaxf(mv, st[k].y);
+    }
+    const float fl = exp2_fast(top - m), fo = exp2_fast(topv - mv);
+    sum *= fl;
+#pragma unroll
+    for (int e = 0; e < V; ++e) h.y[e] *= fo;
+#pragma unroll
+    for (int k = 0; k < JOIN_PARTS; ++k)
+      if (k0 + k <= p.last) {
+        const float f = exp2_fast(st[k].y - mv);
+        sum += st[k].z * exp2_fast(st[k].x - m);
+#pragma unroll
+        for (int e = 0; e < V; ++e) h.y[e] += y[k][e] * f;
+      }
+    top = m;
+    topv = mv;
+  }
+  const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) h.y[e] *= f;
+  h.z = sum > 0.0f ? top + log2f(sum) : -INFINITY;
+  return h;
+}
+
+// A warp to a row and query head: its two halves into one.
+template <int D, int DT>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __grid_constant__ ShareArgs a) {
+  constexpr int V = Half<D>::V;
+  const int lane = threadIdx.x & 31;
+  const int64_t x = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), each = a.q.max_q * a.q.q_heads;
+  const int i = (int)(x / each), j = (int)(x % each / a.q.q_heads), qh = (int)(x % a.q.q_heads);
+  grid_dependency_wait();
+  if (i >= a.batch) return;
+  const Span s = a.spans[SHARE_SLAB + i];
+  if (j >= s.n) return;
+  const int64_t row = s.row0 + j;
+  const Half<D> u = half_of<D>(a, 0, a.spans[s.group], row, qh), v = half_of<D>(a, 1, s, row, qh);
+  const float top = fmaxf(u.z, v.z);
+  float z = -INFINITY, y[V];
+  if (top == -INFINITY) {  // a row that sees nothing
+    for (int e = 0; e < V; ++e) y[e] = 0.0f;
+  } else {
+    const float fu = exp2_fast(u.z - top), fv = exp2_fast(v.z - top), f = 1.0f / (fu + fv);
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = (u.y[e] * fu + v.y[e] * fv) * f;
+    z = top + log2f(fu + fv);
+  }
+  char *out = static_cast<char *>(a.q.out) +
+              2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + lane * V);
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]));
+  else
+    *reinterpret_cast<uint32_t *>(out) = pack2<DT>(y[0], y[1]);
+  if (lane == 0 && a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
+}
+
+// ---- host side
+
+template <int D, int CODE, int DT>
+int attend_rows(const AttentionArgs &a, int mb, const DeviceInfo &dev, cudaStream_t s) {
+  switch (mb) {
+    case 8: return launch_shape<D, CODE, DT, 1, 1, false, Over::SHARED>(a, dev, s);
+    case 16: return launch_shape<D, CODE, DT, 2, 1, false, Over::SHARED>(a, dev, s);
+    case 32: return launch_shape<D, CODE, DT, 2, 2, false, Over::SHARED>(a, dev, s);
+    default: return launch_shape<D, CODE, DT, 2, 4, false, Over::SHARED>(a, dev, s);
+  }
+}
+template <int D>
+int attend_types(const AttentionArgs &a, int mb, const DeviceInfo &dev, cudaStream_t s) {
+  if (a.c.code == IBP_KV_INT8)
+    return a.q.dtype == IBP_BF16 ? attend_rows<D, IBP_KV_INT8, IBP_BF16>(a, mb, dev, s)
+                                 : attend_rows<D, IBP_KV_INT8, IBP_FP16>(a, mb, dev, s);
+  return a.q.dtype == IBP_BF16 ? attend_rows<D, IBP_KV_E4M3, IBP_BF16>(a, mb, dev, s)
+                               : attend_rows<D, IBP_KV_E4M3, IBP_FP16>(a, mb, dev, s);
+}
+
+// CTAs of the kernel for few rows in segments of mb.
+int attend_ctas(int mb, const DeviceInfo &dev) { return std::min((mb == 8 ? 3 : 2) * dev.sm_count, MAX_CTAS); }
+
+// How a call is divided: rows of a segment, and whether beginnings go to the kernel for many
+// rows or along with the rest. alone: not divided at all.
+struct Division {
+  bool alone, many;
+  int mb;
+};
+Division division_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, int64_t group_rows) {
+  const int64_t group = q_heads / c.n_heads, each = std::min(max_q, n_rows) * group;
+  const int64_t all = std::max(std::min(group_rows, n_rows) * group, each);
+  Division d;
+  d.alone = each > 64;
+  d.many = all > 32;
+  d.mb = rows_of(d.many ? each : all);
+  return d;
+}
+
+struct ShareLayout {
+  size_t spans, parts[2], result, lse2, bytes;
+};
+ShareLayout share_layout(const ibp_kv_cache &c, const Division &d, int64_t n_rows, int q_heads) {
+  const size_t row = (c.head_dim + 4) * sizeof(float), rows = (size_t)n_rows * q_heads;
+  ShareLayout y;
+  y.spans = 0;
+  y.parts[1] = (2 * SHARE_SLAB * sizeof(Span) + 2 * sizeof(int64_t) + 255) / 256 * 256;
+  y.parts[0] = y.parts[1] + (size_t)MAX_CTAS * 2 * d.mb * row;
+  y.result = y.parts[0] + (d.many ? (size_t)MAX_PREFILL_CTAS * 2 * prefill_shape().rows * row + MAX_PREFILL_CTAS * sizeof(Cut) : 0);
+  y.lse2 = y.result + 2 * rows * c.head_dim * sizeof(float);
+  y.bytes = y.lse2 + (2 * rows * sizeof(float) + 255) / 256 * 256;
+  return y;
+}
+
+}  // namespace
+
+size_t kv_shared_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads,
+                               int64_t group_rows) {
+  const Division d = division_of(c, n_rows, max_q, q_heads, group_rows);
+  if (d.alone) return kv_attention_scratch_bytes(c, n_rows, max_q, q_heads, false);
+  return share_layout(c, d, n_rows, q_heads).bytes;
+}
+
+int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query, const int32_t *d_groups,
+                               const int32_t *d_prefix, int64_t n_groups, int64_t group_rows, void *d_scratch,
+                               int32_t *d_status, cudaStream_t s) {
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
+  const Division d = division_of(c, query.n_rows, query.max_q, query.q_heads, group_rows);
+  if (d.alone) return launch_kv_attention(c, query, d_scratch, d_status, s);
+  const ShareLayout y = share_layout(c, d, query.n_rows, query.q_heads);
+  char *base = static_cast<char *>(d_scratch);
+  ShareArgs a = {};
+  a.c = c;
+  a.q = query;
+  a.q.max_q = std::min(query.max_q, query.n_rows);
+  a.status = d_status;
+  a.groups = d_groups;
+  a.prefix = d_prefix;
+  a.n_groups = (int)n_groups;
+  a.together = !d.many;
+  a.spans = reinterpret_cast<Span *>(base + y.spans);
+  a.total = reinterpret_cast<int64_t *>(a.spans + 2 * SHARE_SLAB);
+  a.result = reinterpret_cast<float *>(base + y.result);
+  a.result_lse2 = reinterpret_cast<float *>(base + y.lse2);
+  a.side_rows = query.n_rows * query.q_heads;
+  a.side[1] = {d.mb, TILE, attend_ctas(d.mb, dev), reinterpret_cast<float *>(base + y.parts[1])};
+  a.side[0] = a.side[1];
+  const PrefillShape many = prefill_shape();
+  if (d.many) a.side[0] = {many.rows, many.tile, many.ctas, reinterpret_cast<float *>(base + y.parts[0])};
+
+  AttentionArgs t = {};
+  t.c = c;
+  t.q = a.q;
+  t.status = d_status;
+  t.wait_ns = gather_wait_limit_ns();
+  t.withhold = withhold_plans();
+  t.spans = a.spans;
+  t.side = const_cast<float *>(a.result);
+  t.side_lse2 = const_cast<float *>(a.result_lse2);
+  t.side_rows = a.side_rows;
+  const auto join = c.head_dim == 64 ? (query.dtype == IBP_BF16 ? kv_share_join_kernel<64, IBP_BF16> : kv_share_join_kernel<64, IBP_FP16>)
+                                     : (query.dtype == IBP_BF16 ? kv_share_join_kernel<128, IBP_BF16> : kv_share_join_kernel<128, IBP_FP16>);
+  for (a.b0 = 0; a.b0 < c.batch; a.b0 += SHARE_SLAB) {
+    a.batch = std::min(c.batch - a.b0, SHARE_SLAB);
+    kv_share_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    if (d.many) {
+      t.b0 = 0;
+      t.batch = SHARE_SLAB;
+      t.part = const_cast<float *>(a.side[0].part);
+      t.cuts = reinterpret_cast<Cut *>(t.part + (size_t)MAX_PREFILL_CTAS * 2 * many.rows * (c.head_dim + 4));
+      if (int rc = launch_kv_prefill_shared(t, s)) return rc;
+    }
+    t.b0 = d.many ? SHARE_SLAB : 0;
+    t.batch = SHARE_SLAB + a.batch - t.b0;
+    t.part = const_cast<float *>(a.side[1].part);
+    if (int rc = c.head_dim == 64 ? attend_types<64>(t, d.mb, dev, s) : attend_types<128>(t, d.mb, dev, s)) return rc;
+    const int64_t warps = a.batch * a.q.max_q * query.q_heads, blocks = (warps + JOIN_WARPS - 1) / JOIN_WARPS;
+    if (blocks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
+    if (launch_dependent(join, dim3((unsigned)blocks), dim3(32 * JOIN_WARPS), 0, s, a) != cudaSuccess)
+      return IBP_ERR_CUDA;
+  }
+  return IBP_OK;
+}
+
+}  // namespace ibp
