@@ -522,7 +522,7 @@ typedef struct {
  * after the rotation), values as they are. queries (nullable): rotated too and rounded once
  * to their type, whether or not there was room for their tokens; rows that belong to no
  * sequence (before d_cu[0], at or past d_cu[batch]) are left as they are. Asynchronous on s,
- * one launch. */
+ * one launch or two, capturable. */
 int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_rows *rows,
                           const ibp_kv_rotation *rotation, const ibp_kv_turned *queries,
                           int32_t *d_new_lens, int32_t *d_status, ibp_stream_t s);

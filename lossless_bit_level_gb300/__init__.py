@@ -379,7 +379,7 @@ def decompress_gather_dedup(slots: torch.Tensor, n_rows: int, row_elems: int, dt
     _check(load().ibp_decompress_gather_dedup(
         _ptr(slots), sb, int(n_rows), int(row_elems), int(dtype), int(block_elems), _ptr(bitmask),
         _ptr(meta), _ptr(idx), idx.numel(), _ptr(out), _ptr(scratch),
-        scratch.numel() * scratch.element_size(), _ptr(status), _stream(stream)),
+        scratch.nbytes, _ptr(status), _stream(stream)),
         "ibp_decompress_gather_dedup")
 
 
@@ -616,14 +616,12 @@ class KVCache:
 
 def _head_rows(t: torch.Tensor, cache: KVCache, heads: int, what: str) -> tuple[int, int]:
     """Row and head strides of [n_rows, heads, head_dim] rows (elements of a head contiguous)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim or \
-            (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{what} must be [n_rows, {heads}, {cache.head_dim}] with the elements "
-                         "of a head contiguous")
-    if t.shape[0] <= 1 and not t.numel():
-        return heads * cache.head_dim, cache.head_dim
-    return (t.stride(0) if t.shape[0] > 1 else heads * cache.head_dim,
-            t.stride(1) if heads > 1 else cache.head_dim)
+    shape, strides, d = t.shape, t.stride(), cache.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or (strides[2] != 1 and t.numel()):
+        raise ValueError(f"{what} must be [n_rows, {heads}, {d}] with the elements of a head "
+                         "contiguous")
+    n = shape[0]
+    return strides[0] if n > 1 else heads * d, strides[1] if n and heads > 1 else d
 
 
 def _int32(t: torch.Tensor | None, n: int, what: str):
@@ -695,7 +693,8 @@ def kv_append_rotated(cache: KVCache, k: torch.Tensor, v: torch.Tensor, rotation
     kr, kh = _head_rows(k, cache, cache.n_heads, "k")
     vr, vh = _head_rows(v, cache, cache.n_heads, "v")
     n = k.shape[0]
-    if v.dtype != k.dtype or v.shape[0] != n:
+    dtype = k.dtype
+    if v.dtype != dtype or v.shape[0] != n:
         raise ValueError("k and v must have one dtype and row count")
     rows = KVRows(_at(k), _at(v), _int32(cu, cache.batch + 1, "cu"), n, kr, kh, vr, vh,
                   dtype_code(k))
@@ -703,12 +702,17 @@ def kv_append_rotated(cache: KVCache, k: torch.Tensor, v: torch.Tensor, rotation
     turn.d_positions = _int32(positions, n * rotation.axes, "positions")
     queries = None
     if q is not None:
-        q_out = q if q_out is None else q_out
-        if q.dtype != k.dtype or q.shape[0] != n or q_out.dtype != q.dtype or q_out.shape != q.shape:
-            raise ValueError("q and q_out must have k's dtype and row count, and one shape")
-        qr, qh = _head_rows(q, cache, q.shape[1], "q")
-        orow, oh = _head_rows(q_out, cache, q.shape[1], "q_out")
-        queries = KVTurned(_at(q), _at(q_out), qr, qh, orow, oh, q.shape[1])
+        shape = q.shape
+        if q_out is None:
+            q_out = q
+        elif q_out.dtype != dtype or q_out.shape != shape:
+            raise ValueError("q_out must have q's dtype and shape")
+        if q.dtype != dtype or shape[0] != n:
+            raise ValueError("q must have k's dtype and row count")
+        heads = shape[1] if len(shape) == 3 else 0
+        qr, qh = _head_rows(q, cache, heads, "q")
+        orow, oh = (qr, qh) if q_out is q else _head_rows(q_out, cache, heads, "q_out")
+        queries = KVTurned(_at(q), _at(q_out), qr, qh, orow, oh, heads)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     _check(load().ibp_kv_append_rotated(
@@ -740,7 +744,8 @@ def kv_read(cache: KVCache, k_out: torch.Tensor | None, v_out: torch.Tensor | No
 def _query(cache: KVCache, q: torch.Tensor, out: torch.Tensor | None, scale: float, cu_q, max_q,
            lse) -> KVQuery:
     """ibp_kv_query of query rows, without weights."""
-    n, heads = q.shape[0], q.shape[1]
+    shape = q.shape
+    n, heads = shape[0], shape[1]
     qr, qh = _head_rows(q, cache, heads, "q")
     orow = oh = 0
     if out is not None:
@@ -805,7 +810,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scale: floa
     query.d_weights_in, query.d_weights = _at(weights_in), _at(weights)
     query.weights_stride, query.decay = stride, decay
     _check(load().ibp_kv_attention(cache.address, ctypes.addressof(query), _at(scratch),
-                                   scratch.numel() * scratch.element_size(), _at(status),
+                                   scratch.nbytes, _at(status),
                                    _raw_stream(stream)), "ibp_kv_attention")
 
 
@@ -836,7 +841,7 @@ def kv_select(cache: KVCache, bounds: torch.Tensor, q: torch.Tensor, columns: to
     query = _query(cache, q, None, 1.0, cu_q, max_q, None)
     _check(load().ibp_kv_select(cache.address, _bounds(cache, bounds), ctypes.addressof(query),
                                 _columns(cache, columns), _at(columns), _at(scratch),
-                                scratch.numel() * scratch.element_size(), _at(status),
+                                scratch.nbytes, _at(status),
                                 _raw_stream(stream)), "ibp_kv_select")
 
 
@@ -860,7 +865,7 @@ def kv_attention_selected(cache: KVCache, columns: torch.Tensor, q: torch.Tensor
     query = _query(cache, q, out, scale, cu_q, max_q, lse)
     _check(load().ibp_kv_attention_selected(cache.address, ctypes.addressof(query), _at(columns),
                                             _columns(cache, columns), _at(scratch),
-                                            scratch.numel() * scratch.element_size(), _at(status),
+                                            scratch.nbytes, _at(status),
                                             _raw_stream(stream)), "ibp_kv_attention_selected")
 
 
@@ -888,7 +893,7 @@ def kv_attention_shared(cache: KVCache, q: torch.Tensor, out: torch.Tensor, scal
     _check(load().ibp_kv_attention_shared(
         cache.address, ctypes.addressof(query), _int32(groups, n + 1, "groups"),
         _int32(prefix, n, "prefix"), n, int(group_rows), _at(scratch),
-        scratch.numel() * scratch.element_size(), _at(status), _raw_stream(stream)),
+        scratch.nbytes, _at(status), _raw_stream(stream)),
         "ibp_kv_attention_shared")
 
 
@@ -916,7 +921,7 @@ def kv_evict(cache: KVCache, weights: torch.Tensor, budget: int, recent: int, ds
         cache.address, _at(weights), weights.shape[2], int(budget), int(recent), dst.address,
         _at(dst.lens), _at(new_weights), 0 if new_weights is None else new_weights.shape[2],
         _int32(kept, cache.batch * cache.n_heads * int(budget), "kept"), _at(scratch),
-        scratch.numel() * scratch.element_size(), _at(status), _raw_stream(stream)),
+        scratch.nbytes, _at(status), _raw_stream(stream)),
         "ibp_kv_evict")
 
 

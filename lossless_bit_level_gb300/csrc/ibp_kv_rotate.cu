@@ -1,5 +1,8 @@
 // Append to the 8-bit paged key/value cache with the position rotation applied on the way
 // (declared in include/ibp.h).
+#include <algorithm>
+#include <type_traits>
+
 #include "ibp_kv_append.cuh"
 
 namespace ibp {
@@ -13,8 +16,9 @@ namespace {
 // A unit is 16 elements of a head in two pieces of 8: those that a unit's eight pairs (8 u to
 // 8 u + 7) lie in. Pairs of two halves have pieces dim/2 apart, neighbouring pairs and what
 // is not rotated lie in 16 consecutive elements.
-constexpr int GROUPS = 4;       // units a thread holds (rotated: 16 floats each)
-constexpr int MAX_THREADS = 256;  // a page of 128 tokens of 128 elements
+constexpr int MAX_THREADS = 512;
+constexpr int GROUPS = 2;  // units of a head that a thread holds (rotated: 16 floats each)
+constexpr int TURN_THREADS = 256;
 constexpr int FEW_WARPS = 4;
 
 struct RotateArgs {
@@ -25,6 +29,7 @@ struct RotateArgs {
   int64_t each, items_each, items;
   int64_t kv_blocks;   // blocks that append; those after them rotate queries
   int q_chunks;        // blocks that share the heads of a query row
+  int kv_chunks;       // blocks that share the heads of a page, of K or V
   int mixed;           // a unit's pairs are not all on one axis
   int shift;           // log2 of the page size
   int32_t *new_lens, *status;
@@ -49,7 +54,7 @@ __device__ __forceinline__ Unit unit_of(const ibp_kv_rotation &t, int u) {
 }
 
 template <int DT>
-__device__ __forceinline__ void load_unit(const char *row, const Unit &u, float *x) {
+__device__ __forceinline__ Raw16<DT> load_unit(const char *row, const Unit &u) {
   constexpr int ES = DT == IBP_FP32 ? 4 : 2, V = DT == IBP_FP32 ? 2 : 1;
   Raw16<DT> r;
 #pragma unroll
@@ -57,13 +62,12 @@ __device__ __forceinline__ void load_unit(const char *row, const Unit &u, float 
     r.v[i] = __ldg(reinterpret_cast<const uint4 *>(row + u.a * ES) + i);
     r.v[V + i] = __ldg(reinterpret_cast<const uint4 *>(row + u.b * ES) + i);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.four(i, x + 4 * i);
+  return r;
 }
 
-// Cosines and sines of a unit's pairs.
+// Cosines and sines of a unit's pairs, two to a register pair.
 struct Angles {
-  float2 y[8];
+  uint64_t c[4], s[4];
 };
 // Position of a row on an axis; `place`: its token's number in the sequence.
 __device__ __forceinline__ int64_t position_of(const RotateArgs &a, int64_t row, int64_t place, int axis) {
@@ -81,31 +85,52 @@ __device__ __forceinline__ Angles angles_of(const RotateArgs &a, int u, int64_t 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 z = __ldg(from + i);
-      g.y[2 * i] = make_float2(z.x, z.y);
-      g.y[2 * i + 1] = make_float2(z.z, z.w);
+      g.c[i] = pair(z.x, z.z);
+      g.s[i] = pair(z.y, z.w);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      g.y[i] = __ldg(reinterpret_cast<const float2 *>(
-          a.t.d_table + 2 * (position_of(a, row, place, a.t.axis[8 * u + i]) * pairs + 8 * u + i)));
+    for (int i = 0; i < 4; ++i) {
+      float2 z[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = 8 * u + 2 * i + k;
+        z[k] = __ldg(reinterpret_cast<const float2 *>(
+            a.t.d_table + 2 * (position_of(a, row, place, a.t.axis[at]) * pairs + at)));
+      }
+      g.c[i] = pair(z[0].x, z[1].x);
+      g.s[i] = pair(z[0].y, z[1].y);
+    }
   }
   return g;
 }
 
-__device__ __forceinline__ void turn(float &x, float &y, float2 g) {
-  const float u = __fsub_rn(__fmul_rn(x, g.x), __fmul_rn(y, g.y));
-  y = __fadd_rn(__fmul_rn(y, g.x), __fmul_rn(x, g.y));
-  x = u;
+// Two pairs (x, y): products two at a time, sums one by one (a packed product and sum could
+// become one operation with one rounding).
+__device__ __forceinline__ void turn2(float &x0, float &y0, float &x1, float &y1, uint64_t c, uint64_t s) {
+  const uint64_t x = pair(x0, x1), y = pair(y0, y1);
+  const uint64_t xc = mul2(x, c), ys = mul2(y, s), yc = mul2(y, c), xs = mul2(x, s);
+  x0 = __fsub_rn(low(xc), low(ys));
+  x1 = __fsub_rn(high(xc), high(ys));
+  y0 = __fadd_rn(low(yc), low(xs));
+  y1 = __fadd_rn(high(yc), high(xs));
 }
 __device__ __forceinline__ void turn_unit(float *x, const Angles &g, bool interleaved) {
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], g.y[i]);
+    for (int i = 0; i < 4; ++i) turn2(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], g.c[i], g.s[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], g.y[i]);
+    for (int i = 0; i < 4; ++i) turn2(x[2 * i], x[8 + 2 * i], x[2 * i + 1], x[9 + 2 * i], g.c[i], g.s[i]);
   }
+}
+
+// The larger of m and the magnitudes of 16 values, NaN if one is.
+__device__ __forceinline__ float largest16(float m, const float *x) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x[i]), "f"(x[i + 1]));
+  return m;
 }
 
 __device__ __forceinline__ Raw16<IBP_FP32> as_raw(const float *x) {
@@ -131,8 +156,15 @@ __device__ __forceinline__ Item even_item(const RotateArgs &a, int64_t item) {
 template <int D, int DT>
 __device__ __forceinline__ void turn_queries(const RotateArgs &a, int64_t block) {
   constexpr int GD = D / 16, ES = DT == IBP_FP32 ? 4 : 2;
+  constexpr int KEPT = 255;  // offsets that are searched in shared memory
+  __shared__ int32_t starts[KEPT + 1];
   const int64_t row = block / a.q_chunks * (blockDim.x / GD) + threadIdx.x / GD;
   const int chunk = (int)(block % a.q_chunks);
+  const bool kept = a.r.d_cu && a.c.batch <= KEPT;
+  if (kept) {
+    for (int i = threadIdx.x; i <= a.c.batch; i += blockDim.x) starts[i] = __ldg(a.r.d_cu + i);
+    __syncthreads();
+  }
   if (row >= a.r.n_rows) return;
   const Unit u = unit_of<D>(a.t, threadIdx.x % GD);
   int64_t place = 0;
@@ -141,10 +173,10 @@ __device__ __forceinline__ void turn_queries(const RotateArgs &a, int64_t block)
     int lo = 0, hi = a.c.batch;  // the last sequence that does not begin after the row
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (__ldg(a.r.d_cu + mid) <= row) lo = mid; else hi = mid;
+      if ((kept ? starts[mid] : __ldg(a.r.d_cu + mid)) <= row) lo = mid; else hi = mid;
     }
     b = lo;
-    const int64_t first = __ldg(a.r.d_cu + b), end = __ldg(a.r.d_cu + b + 1);
+    const int64_t first = kept ? starts[b] : __ldg(a.r.d_cu + b), end = kept ? starts[b + 1] : __ldg(a.r.d_cu + b + 1);
     if (row < first || row >= end) return;  // no sequence's row
     place = row - first;
   } else {
@@ -163,7 +195,9 @@ __device__ __forceinline__ void turn_queries(const RotateArgs &a, int64_t block)
 #pragma unroll 4
   for (int h = h0; h < h1; ++h) {
     float x[16];
-    load_unit<DT>(from + h * a.q.q_head_stride * ES, u, x);
+    const Raw16<DT> r = load_unit<DT>(from + h * a.q.q_head_stride * ES, u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.four(i, x + 4 * i);
     if (u.turned) turn_unit(x, g, a.t.interleaved);
     char *out = to + h * a.q.out_head_stride * ES;
     if constexpr (DT == IBP_FP32) {
@@ -184,91 +218,182 @@ __device__ __forceinline__ void turn_queries(const RotateArgs &a, int64_t block)
   }
 }
 
-// One thread block quantises what one (page, head) tile receives, as in the append without a
-// rotation; the values stay in registers between the maximum and the rounding, keys as rotated.
-template <int D, int DT, int CODE, bool KEYS>
-__device__ __forceinline__ void append_tile(const RotateArgs &a, const AppendPlace &p, int head,
-                                            uint32_t *sm) {
+// Rows on their way: a thread copies its own units of the next heads into places of its own in
+// shared memory, so that they wait for no barrier and take no registers.
+template <int DT>
+struct Ahead {
+  static constexpr int vecs = Raw16<DT>::vecs, thread_bytes = GROUPS * vecs * 16;
+  static constexpr int stages = DT == IBP_FP32 ? 3 : 4;  // heads, the one at hand among them
+};
+__device__ __forceinline__ void copy16(uint4 *to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+// Largest of the block's values; every thread gets it. `sm`: a place for each warp.
+__device__ __forceinline__ uint32_t largest_of_block(uint32_t v, uint32_t *sm) {
+  v = __reduce_max_sync(FULL, v);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_max_sync(FULL, lane < (int)(blockDim.x >> 5) ? sm[lane] : 0u);
+}
+
+// One thread block quantises what a page receives in some heads of K or V, one head after
+// another: what follows from the place alone (sequence, page, the angles of its tokens) is worked
+// out once for all of them, the next head's rows are asked for before this one's are rounded,
+// and the values stay in registers between the maximum and the rounding, keys as rotated.
+// PLAIN: the rows fill the page, and keys are rotated whole in halves, so that nothing is asked
+// for each unit (the code between the copies and the stores is what bounds it: 25 % fewer
+// instructions).
+template <int D, int DT, int CODE, bool KEYS, bool PLAIN>
+__device__ __forceinline__ void append_heads(const RotateArgs &a, const AppendPlace &p, int h0, int h1,
+                                             uint32_t (*sm)[32]) {
   constexpr int GD = D / 16, ES = DT == IBP_FP32 ? 4 : 2, HELD = KEYS ? IBP_FP32 : DT;
+  using Held = Raw16<HELD>;
+  using A = Ahead<DT>;
+  extern __shared__ uint4 rows[];  // [stage][group][16 bytes][thread]
   const int P = 1 << a.shift, T = blockDim.x, STEP = T / GD;
-  const int64_t row_stride = KEYS ? a.r.k_row_stride : a.r.v_row_stride;
-  const int64_t head_stride = KEYS ? a.r.k_head_stride : a.r.v_head_stride;
-  float *scale_at = (KEYS ? a.c.k_scales : a.c.v_scales) + (int64_t)p.page * a.c.n_heads + head;
-  char *codes = static_cast<char *>(KEYS ? a.c.k_codes : a.c.v_codes) + kv_tile(a.c, p.page, head);
-  const float before = p.t0 < p.len ? *scale_at : 0.0f;
+  const int64_t row_stride = (KEYS ? a.r.k_row_stride : a.r.v_row_stride) * ES;
+  const int64_t head_stride = (KEYS ? a.r.k_head_stride : a.r.v_head_stride) * ES;
+  float *scale_at = (KEYS ? a.c.k_scales : a.c.v_scales) + (int64_t)p.page * a.c.n_heads + h0;
+  char *codes = static_cast<char *>(KEYS ? a.c.k_codes : a.c.v_codes) + kv_tile(a.c, p.page, h0);
   // tokens of the tile: [old, fresh) are the new rows
-  const int old = (int)max((int64_t)p.len - p.t0, (int64_t)0), fresh = (int)min(p.end - p.t0, (int64_t)P);
-  const int tok = threadIdx.x / GD;
-  const Unit u = KEYS ? unit_of<D>(a.t, threadIdx.x % GD)
-                      : Unit{(int)threadIdx.x % GD, 16 * ((int)threadIdx.x % GD), 0, false};
+  const int old = PLAIN ? 0 : (int)max((int64_t)p.len - p.t0, (int64_t)0);
+  const int fresh = (int)min(p.end - p.t0, (int64_t)P);
+  const int tok = threadIdx.x / GD, piece = threadIdx.x % GD;
+  const Unit u = KEYS ? unit_of<D>(a.t, piece) : Unit{piece, 16 * piece, 16 * piece + 8, false};
   const int64_t row0 = p.lo + (p.t0 - p.len) + tok;
-  const char *src = static_cast<const char *>(KEYS ? a.r.k : a.r.v) +
-                    (row0 * row_stride + head * head_stride) * ES;
-  Raw16<HELD> x[GROUPS];
-  uint32_t bits = 0;
+  const char *src = static_cast<const char *>(KEYS ? a.r.k : a.r.v) + row0 * row_stride + h0 * head_stride;
+  const int64_t step = STEP * row_stride;
+  auto live = [&](int i) { return PLAIN || (tok + i * STEP >= old && tok + i * STEP < fresh); };
+  const int stage = GROUPS * A::vecs * T;
+  uint4 *const first = rows + threadIdx.x, *const past = first + A::stages * stage;
+  uint4 *to = first;
+  int asked = h0;
+  auto ask = [&] {  // for the next head's rows
+    if (asked < h1) {
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    x[g].clear();
-    const int t = tok + g * STEP;
-    if (t >= old && t < fresh) {
-      const char *at = src + (int64_t)g * STEP * row_stride * ES;
-      if constexpr (KEYS) {
+      for (int i = 0; i < GROUPS; ++i)
+        if (live(i)) {
+#pragma unroll
+          for (int k = 0; k < A::vecs; ++k)
+            copy16(to + (i * A::vecs + k) * T,
+                   src + i * step + (k < A::vecs / 2 ? u.a * ES + 16 * k : u.b * ES + 16 * (k - A::vecs / 2)));
+        }
+      src += head_stride;
+      ++asked;
+      to += stage;
+      if (to == past) to = first;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 1; k < A::stages; ++k) ask();
+  Angles g[KEYS ? GROUPS : 1];
+  if constexpr (KEYS) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
+      if (live(i) && u.turned) g[i] = angles_of(a, u.u, row0 + i * STEP, p.t0 + tok + i * STEP);
+  }
+  const uint4 *at = first;
+  float next_before = old ? *scale_at : 0.0f;
+  char *put_a = codes + tok * D + u.a, *put_b = codes + tok * D + u.b;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const float before = next_before;
+    cp_async_wait<A::stages - 2>();  // this head's rows (a thread reads none but its own copies)
+    Raw16<DT> r[GROUPS];
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      if constexpr (!PLAIN) r[i].clear();
+      if (live(i))
+#pragma unroll
+        for (int k = 0; k < A::vecs; ++k) r[i].v[k] = at[(i * A::vecs + k) * T];
+    }
+    at += stage;
+    if (at == past) at = first;
+    Held x[GROUPS];
+    uint32_t bits = 0;
+    if constexpr (KEYS) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) {
         float y[16];
-        load_unit<DT>(at, u, y);
-        if (u.turned) turn_unit(y, angles_of(a, u.u, row0 + g * STEP, p.t0 + t), a.t.interleaved);
-        x[g] = as_raw(y);
-      } else {
-        x[g].load(at + u.a * ES);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[i].four(e, y + 4 * e);
+        if (PLAIN || (live(i) && u.turned)) turn_unit(y, g[i], !PLAIN && a.t.interleaved);
+        most = largest16(most, y);
+        x[i] = as_raw(y);
       }
-    }
-  }
+      bits = __float_as_uint(most);
+    } else {
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) bits = x[g].largest(bits);
-  bits = block_max(Raw16<HELD>::fold(bits), sm);
-  float largest = Raw16<HELD>::value(bits);
-  const bool odd = bits >= Raw16<HELD>::inf;  // infinities or NaN among the values
-  if (odd) {
-    float most = 0.0f;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) most = largest_finite<HELD>(x[g], most);
-    __syncthreads();
-    largest = __uint_as_float(block_max(__float_as_uint(most), sm));
-  }
-  const float scale = fmaxf(before, kv_scale<CODE>(largest));
-  const float inverse = kv_inverse(scale);
-  if (threadIdx.x == 0) *scale_at = scale;
-  const bool any = odd || !(scale < 0x1p120f);
-#pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    const int t = tok + g * STEP;
-    if (t >= old && t < fresh) {
-      const uint4 w = any ? encode16<HELD, CODE, true>(x[g], inverse) : encode16<HELD, CODE, false>(x[g], inverse);
-      char *to = codes + t * D;
-      if constexpr (KEYS) {
-        *reinterpret_cast<uint2 *>(to + u.a) = make_uint2(w.x, w.y);
-        *reinterpret_cast<uint2 *>(to + u.b) = make_uint2(w.z, w.w);
-      } else {
-        *reinterpret_cast<uint4 *>(to + u.a) = w;
+      for (int i = 0; i < GROUPS; ++i) {
+        x[i] = r[i];
+        bits = x[i].largest(bits);
       }
+      bits = Held::fold(bits);
     }
-  }
-  if (old && scale > before) {
-    const float ratio = __fdiv_rn(before, scale);
-    uint4 *there = reinterpret_cast<uint4 *>(codes) + threadIdx.x;
-    for (int g = 0; tok + g * STEP < old; ++g) there[g * T] = rescale16<CODE>(there[g * T], ratio);
+    ask();
+    if (old && h + 1 < h1) next_before = scale_at[1];
+    // (two places in turn: a thread may be one barrier ahead of one that still reads)
+    bits = largest_of_block(bits, sm[h & 1]);
+    float largest = Held::value(bits);
+    const bool odd = bits >= Held::inf;  // infinities or NaN among the values
+    if (odd) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) most = largest_finite<HELD>(x[i], most);
+      __syncthreads();
+      largest = __uint_as_float(largest_of_block(__float_as_uint(most), sm[h & 1]));
+    }
+    const float scale = fmaxf(before, kv_scale<CODE>(largest));
+    const float inverse = scale > 0.0f ? __frcp_rn(scale) : 0.0f;
+    if (threadIdx.x == 0) *scale_at = scale;
+    ++scale_at;
+    auto put = [&](auto any) {
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i)
+        if (live(i)) {
+          const uint4 w = encode16<HELD, CODE, decltype(any)::value>(x[i], inverse);
+          if constexpr (KEYS) {
+            *reinterpret_cast<uint2 *>(put_a + i * STEP * D) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2 *>(put_b + i * STEP * D) = make_uint2(w.z, w.w);
+          } else {
+            *reinterpret_cast<uint4 *>(put_a + i * STEP * D) = w;
+          }
+        }
+    };
+    if (!odd && scale < 0x1p120f)
+      put(std::false_type());
+    else
+      put(std::true_type());
+    if (old && scale > before) {
+      const float ratio = __fdiv_rn(before, scale);
+      uint4 *there = reinterpret_cast<uint4 *>(codes) + threadIdx.x;
+      for (int i = 0; tok + i * STEP < old; ++i) there[i * T] = rescale16<CODE>(there[i * T], ratio);
+    }
+    if constexpr (!PLAIN) codes += P * D;
+    put_a += P * D;
+    put_b += P * D;
   }
 }
 
+// Rows that queries are rotated in, after (and along with the end of) the kernel that appends.
+template <int D, int DT>
+__global__ void __launch_bounds__(TURN_THREADS, 4) kv_turn_kernel(const __grid_constant__ RotateArgs a) {
+  turn_queries<D, DT>(a, blockIdx.x);
+  grid_dependency_wait();  // what comes next in the stream may be ordered behind this grid alone
+}
+
 template <int D, int DT, int CODE>
-__global__ void __launch_bounds__(MAX_THREADS) kv_rotate_kernel(const __grid_constant__ RotateArgs a) {
-  __shared__ uint32_t sm[32];
-  if ((int64_t)blockIdx.x >= a.kv_blocks) {
-    turn_queries<D, DT>(a, (int64_t)blockIdx.x - a.kv_blocks);
-    return;
-  }
+__global__ void __launch_bounds__(MAX_THREADS)
+    kv_rotate_kernel(const __grid_constant__ RotateArgs a) {
+  __shared__ uint32_t sm[2][32];
+  grid_launch_dependents();
   const int T = blockDim.x;
-  const int64_t item = blockIdx.x / (2 * a.c.n_heads);
-  const int which = (int)(blockIdx.x % (2 * a.c.n_heads)), head = which >> 1;
+  const int64_t item = blockIdx.x / (2 * a.kv_chunks);
+  const int which = (int)(blockIdx.x % (2 * a.kv_chunks)), chunk = which >> 1;
   Item i;
   if (a.r.d_cu) {
     int below = 0;  // starts rise with b: the last one that is not past the item
@@ -284,10 +409,22 @@ __global__ void __launch_bounds__(MAX_THREADS) kv_rotate_kernel(const __grid_con
   const AppendPlace p = place_of(a.c, a.r, a.each, i.b, i.nth, a.shift, which == 0 && threadIdx.x == 0,
                                  a.new_lens, a.status);
   if (p.page < 0) return;
-  if (which & 1)
-    append_tile<D, DT, CODE, false>(a, p, head, sm);
-  else
-    append_tile<D, DT, CODE, true>(a, p, head, sm);
+  const int per = (a.c.n_heads + a.kv_chunks - 1) / a.kv_chunks, h0 = chunk * per,
+            h1 = min(h0 + per, a.c.n_heads);
+  if (h0 >= h1) return;
+  const bool covers = T * GROUPS * 16 == D << a.shift;  // (a page of 16 tokens of 64 elements is less than a warp's)
+  const bool full = p.t0 >= p.len && p.end - p.t0 >= 1 << a.shift;
+  if (which & 1) {
+    if (full && covers)
+      append_heads<D, DT, CODE, false, true>(a, p, h0, h1, sm);
+    else
+      append_heads<D, DT, CODE, false, false>(a, p, h0, h1, sm);
+  } else {
+    if (full && a.t.dim == D && !a.t.interleaved && covers)
+      append_heads<D, DT, CODE, true, true>(a, p, h0, h1, sm);
+    else
+      append_heads<D, DT, CODE, true, false>(a, p, h0, h1, sm);
+  }
 }
 
 // The same for a few rows a sequence: one warp to a tile, which reads its rows twice (the
@@ -310,7 +447,9 @@ __device__ __forceinline__ void append_few(const RotateArgs &a, const AppendPlac
     const char *at = src + (int64_t)(i / GD) * row_stride * ES;
     if constexpr (KEYS) {
       float y[16];
-      load_unit<DT>(at, u, y);
+      const Raw16<DT> r = load_unit<DT>(at, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.four(e, y + 4 * e);
       if (u.turned) turn_unit(y, angles_of(a, u.u, row0 + i / GD, from + i / GD), a.t.interleaved);
       x = as_raw(y);
     } else {
@@ -380,40 +519,62 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) kv_rotate_few_kernel(const __g
     append_few<D, DT, CODE, true>(a, p, head, lane);
 }
 
-// Blocks that rotate queries, `threads` each.
-int64_t query_blocks(RotateArgs &a, int threads, int heads_each) {
+// Blocks of `threads` that rotate queries: up to 16 heads to a thread (its angles are loaded
+// once), fewer while no more than `most` blocks come of it (those that run at once).
+int64_t query_blocks(RotateArgs &a, int threads, int64_t most) {
   if (!a.q.q || a.r.n_rows == 0) return 0;
   const int rows = threads / (a.c.head_dim / 16);
-  a.q_chunks = (a.q.q_heads + heads_each - 1) / heads_each;
-  return (a.r.n_rows + rows - 1) / rows * a.q_chunks;
+  const int64_t blocks = (a.r.n_rows + rows - 1) / rows;
+  a.q_chunks = (int)std::min<int64_t>(std::max<int64_t>(most / blocks, (a.q.q_heads + 15) / 16),
+                                      a.q.q_heads);
+  return blocks * a.q_chunks;
 }
 
 template <int D, int DT>
-int launch_code(RotateArgs &a, cudaStream_t s) {
+int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const int P = a.c.page_tokens;
   a.each = a.r.d_cu ? 0 : a.r.n_rows / a.c.batch;
   a.items_each = a.each > 0 ? (a.each - 1) / P + 2 : 1;
   a.items = a.r.d_cu ? a.r.n_rows / P + 2 * (int64_t)a.c.batch : a.items_each * a.c.batch;
+  if (a.items > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
   const bool int8 = a.c.code == IBP_KV_INT8;
   // A warp to a tile while a sequence brings less than a quarter of a page (the rule of the
   // append without a rotation, for the same reasons).
-  const bool few = a.r.n_rows < (int64_t)a.c.batch * (P / 4);
-  const int threads = few ? 32 * FEW_WARPS : P * D / 16 / GROUPS < 32 ? 32 : P * D / 16 / GROUPS;
-  a.kv_blocks = few ? (a.items * 2 * a.c.n_heads + FEW_WARPS - 1) / FEW_WARPS : a.items * 2 * a.c.n_heads;
-  const int64_t blocks = a.kv_blocks + query_blocks(a, threads, few ? 4 : 8);
-  if (a.items > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
-  const auto kernel = few ? (int8 ? kv_rotate_few_kernel<D, DT, IBP_KV_INT8> : kv_rotate_few_kernel<D, DT, IBP_KV_E4M3>)
-                          : (int8 ? kv_rotate_kernel<D, DT, IBP_KV_INT8> : kv_rotate_kernel<D, DT, IBP_KV_E4M3>);
-  kernel<<<(unsigned)blocks, threads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? IBP_OK : IBP_ERR_CUDA;
+  if (a.r.n_rows < (int64_t)a.c.batch * (P / 4)) {
+    constexpr int threads = 32 * FEW_WARPS;
+    a.kv_blocks = (a.items * 2 * a.c.n_heads + FEW_WARPS - 1) / FEW_WARPS;
+    const int64_t blocks = a.kv_blocks + query_blocks(a, threads, dev.sm_count);
+    if (blocks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
+    const auto kernel = int8 ? kv_rotate_few_kernel<D, DT, IBP_KV_INT8> : kv_rotate_few_kernel<D, DT, IBP_KV_E4M3>;
+    kernel<<<(unsigned)blocks, threads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? IBP_OK : IBP_ERR_CUDA;
+  }
+  const int threads = std::max(P * D / 16 / GROUPS, 32);
+  // Up to 16 heads to a block (8 x 4,096 tokens, 32 heads of 128: 215 us with 8, 207 with 16,
+  // 211 with 32). What a block looks up before its first row arrives takes as long as several
+  // heads, so no more blocks than run at once where there are few pages.
+  const int64_t at_once = (int64_t)dev.sm_count * std::min(512 / threads, 32);
+  a.kv_chunks = (int)std::min<int64_t>(std::max<int64_t>(at_once / (a.items * 2), (a.c.n_heads + 15) / 16),
+                                       a.c.n_heads);
+  const int64_t blocks = a.items * 2 * a.kv_chunks, turns = query_blocks(a, TURN_THREADS, 4 * (int64_t)dev.sm_count);
+  if (blocks > 0x7FFFFFFF || turns > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
+  const auto kernel = int8 ? kv_rotate_kernel<D, DT, IBP_KV_INT8> : kv_rotate_kernel<D, DT, IBP_KV_E4M3>;
+  const int smem = threads * Ahead<DT>::thread_bytes * Ahead<DT>::stages;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return IBP_ERR_CUDA;
+  kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+  if (turns > 0 && launch_dependent(kv_turn_kernel<D, DT>, dim3((unsigned)turns), dim3(TURN_THREADS), 0, s, a) != cudaSuccess)
+    return IBP_ERR_CUDA;
+  return IBP_OK;
 }
 
 template <int D>
-int launch_dtype(RotateArgs &a, cudaStream_t s) {
+int launch_dtype(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   switch (a.r.dtype) {
-    case IBP_FP32: return launch_code<D, IBP_FP32>(a, s);
-    case IBP_FP16: return launch_code<D, IBP_FP16>(a, s);
-    default: return launch_code<D, IBP_BF16>(a, s);
+    case IBP_FP32: return launch_code<D, IBP_FP32>(a, dev, s);
+    case IBP_FP16: return launch_code<D, IBP_FP16>(a, dev, s);
+    default: return launch_code<D, IBP_BF16>(a, dev, s);
   }
 }
 
@@ -422,6 +583,8 @@ int launch_dtype(RotateArgs &a, cudaStream_t s) {
 int launch_kv_append_rotated(const ibp_kv_cache &c, const ibp_kv_rows &r, const ibp_kv_rotation &t,
                              const ibp_kv_turned *q, int32_t *d_new_lens, int32_t *d_status,
                              cudaStream_t s) {
+  DeviceInfo dev;
+  if (int rc = device_info(&dev)) return rc;
   RotateArgs a = {};
   a.c = c;
   a.r = r;
@@ -432,7 +595,7 @@ int launch_kv_append_rotated(const ibp_kv_cache &c, const ibp_kv_rows &r, const 
   for (int i = 0; i < t.dim / 2; ++i) a.mixed |= t.axis[i] != t.axis[i & ~7];
   a.new_lens = d_new_lens;
   a.status = d_status;
-  return c.head_dim == 64 ? launch_dtype<64>(a, s) : launch_dtype<128>(a, s);
+  return c.head_dim == 64 ? launch_dtype<64>(a, dev, s) : launch_dtype<128>(a, dev, s);
 }
 
 }  // namespace ibp
