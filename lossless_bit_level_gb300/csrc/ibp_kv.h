@@ -31,7 +31,7 @@ size_t kv_selected_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t 
 int launch_kv_attention_selected(const ibp_kv_cache &c, const ibp_kv_query &q, const int32_t *d_columns,
                                  int64_t pages, void *d_scratch, int32_t *d_status, cudaStream_t s);
 size_t kv_shared_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads,
-                               int64_t group_rows);
+                               int64_t n_groups, int64_t group_rows);
 int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &q, const int32_t *d_groups,
                                const int32_t *d_prefix, int64_t n_groups, int64_t group_rows, void *d_scratch,
                                int32_t *d_status, cudaStream_t s);

@@ -294,7 +294,7 @@ int ibp_kv_attention_shared_scratch_bytes(const ibp_kv_cache *cache, int64_t n_r
   if (!bytes) return IBP_ERR_ARG;
   if (int rc = kv_query_sizes(cache, n_rows, max_q, q_heads)) return rc;
   if (int rc = kv_groups_ok(cache, n_groups, group_rows)) return rc;
-  *bytes = kv_shared_scratch_bytes(*cache, n_rows, max_q, q_heads, group_rows);
+  *bytes = kv_shared_scratch_bytes(*cache, n_rows, max_q, q_heads, n_groups, group_rows);
   return IBP_OK;
 }
 
@@ -307,7 +307,7 @@ int ibp_kv_attention_shared(const ibp_kv_cache *cache, const ibp_kv_query *query
   if (int rc = kv_groups_ok(cache, n_groups, group_rows)) return rc;
   if (q.d_weights || q.d_weights_in) return IBP_ERR_ARG;
   if (cache->batch == 0 || q.n_rows == 0) return IBP_OK;
-  if (scratch_bytes < kv_shared_scratch_bytes(*cache, q.n_rows, q.max_q, q.q_heads, group_rows))
+  if (scratch_bytes < kv_shared_scratch_bytes(*cache, q.n_rows, q.max_q, q.q_heads, n_groups, group_rows))
     return IBP_ERR_ARG;
   if (!kv_pointers(cache) || !device_ptr(d_scratch, 16) || !device_or_null(q.d_lse, 4) ||
       !device_or_null(q.d_cu, 4) || !device_or_null(d_status, 4) || !device_ptr(q.q, 16) ||

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
           const int qh = head * group + rr % group;
           const float f = sum > 0.0f ? exp2_fast(topv - top) / sum : 0.0f;
           if constexpr (OVER == Over::SHARED) {  // joined with the rows' other span later
-            const int64_t at = row * a.q.q_heads + qh + (a.b0 + b < SHARE_SLAB ? 0 : a.side_rows);
+            const int64_t at = row * a.q.q_heads + qh + (a.b0 + b < a.beginnings ? 0 : a.side_rows);
             reinterpret_cast<float4 *>(a.side)[at * (D / 4) + piece] = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
             if (piece == 0) a.side_lse2[at] = sum > 0.0f ? top + log2f(sum) : -INFINITY;
             continue;

@@ -87,18 +87,21 @@ struct AttentionArgs {
   const int32_t *columns;  // SELECTED: [batch][n_heads][pages] columns of the page table
   int pages;
   // SHARED: [batch], and where segments that one CTA finished leave their normalised rows
-  // [row][q_head][D] and log2 of their sums, for beginnings and (side_rows further) the rest
+  // [row][q_head][D] and log2 of their sums, for beginnings, (side_rows further) the rest and
+  // (after that) the second results of beginnings
   const Span *spans;
   float *side, *side_lse2;
   int64_t side_rows;
+  int beginnings;  // the spans before this one are beginnings
 };
 
 // Many query rows over SHARED spans (ibp_kv_prefill.cu): a.spans, a.side and a.part are set.
+// split: for no more than 128 rows, in two results a part: rows r and 128 + r.
 struct PrefillShape {
-  int rows, tile, ctas;  // of a segment, tokens of a tile, how many CTAs share the tiles
+  int rows, part_rows, tile, ctas;  // of a segment, of a part; tokens of a tile; CTAs that share them
 };
-PrefillShape prefill_shape();
-int launch_kv_prefill_shared(AttentionArgs a, cudaStream_t s);
+PrefillShape prefill_shape(bool split);
+int launch_kv_prefill_shared(AttentionArgs a, bool split, cudaStream_t s);
 
 namespace {
 

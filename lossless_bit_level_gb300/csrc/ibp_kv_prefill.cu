@@ -55,9 +55,14 @@ constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 // factors: between that and 2^4 times it). Lower than SHIFT: here a row that outgrows its
 // reference costs the whole warp (2048 rows over 8192 tokens: 306 us with 7, 277 with 4).
 constexpr float ROW_SHIFT = 2.0f;
-// SHARED spans are seen whole by all their rows.
-template <Over OVER>
-using PlanOf = std::conditional_t<OVER == Over::SHARED, EvenPlan<MB, TILE>, CausalPlan<MB, TILE>>;
+// SHARED spans are seen whole by all their rows. SPLIT (of SHARED): no more than 128 rows, which
+// both halves of the CTA hold: half w takes the tiles of its stretch whose number has its parity,
+// so that neither waits for the other and no half is without rows. Each half leaves results of
+// its own, in the place of 128 rows each, and the joining adds them up.
+template <bool SPLIT>
+constexpr int ROWS_OF = SPLIT ? MB / 2 : MB;
+template <Over OVER, bool SPLIT>
+using PlanOf = std::conditional_t<OVER == Over::SHARED, EvenPlan<ROWS_OF<SPLIT>, TILE>, CausalPlan<MB, TILE>>;
 
 // ---- tensor memory and the matrix instruction
 __device__ __forceinline__ void tmem_alloc(uint32_t *at) {
@@ -198,7 +203,7 @@ struct Memory {
   static constexpr int q = 0, k = 2 * q_bytes, v = k + STAGES * kv_bytes, raw_k = v + V_HALVES * half_bytes,
                        raw_v = raw_k + STAGES * code_bytes;
   static constexpr int info = raw_v + STAGES * code_bytes, bars = info + INFOS * (int)sizeof(TileInfo);
-  static constexpr int barriers = 36 + INFOS;  // see the kernel's list of them
+  static constexpr int barriers = 38 + INFOS;  // see the kernel's list of them
   static constexpr int prefix = bars + barriers * 8;
   static constexpr int cursors = (prefix + (BATCH + 1) * 8 + 15) / 16 * 16;
   static constexpr int words = cursors + 9 * 48;
@@ -211,13 +216,13 @@ struct __align__(16) Cursor {
   int b, head, block, tile, tiles;
   Sequence seq;
 };
-template <Over OVER>
+template <Over OVER, bool SPLIT>
 __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_t *prefix, int group,
                                             int64_t x) {
   Cursor c;
   c.b = find_sequence(prefix, a.batch, x);
   c.seq = sequence_of<OVER>(a, c.b, nullptr);
-  const PlanOf<OVER> plan(c.seq, group);
+  const PlanOf<OVER, SPLIT> plan(c.seq, group);
   const int64_t local = x - prefix[c.b], per_head = (prefix[c.b + 1] - prefix[c.b]) / a.c.n_heads;
   c.head = (int)(local / per_head);
   const int64_t in = local - c.head * per_head;
@@ -228,12 +233,12 @@ __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_
 }
 static_assert(sizeof(Cursor) <= 48, "the place kept for it");
 // The first tile of the next segment that has one (there is one: the caller's x < total).
-template <Over OVER>
+template <Over OVER, bool SPLIT>
 __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64_t *prefix, int group,
                                              Cursor &c) {
   c.tile = 0;
   for (;;) {
-    const PlanOf<OVER> plan(c.seq, group);
+    const PlanOf<OVER, SPLIT> plan(c.seq, group);
     if (++c.block == plan.blocks) {
       c.block = 0;
       if (++c.head == a.c.n_heads) {
@@ -244,7 +249,7 @@ __device__ __forceinline__ void next_segment(const AttentionArgs &a, const int64
         c.seq = sequence_of<OVER>(a, c.b, nullptr);
       }
     }
-    c.tiles = PlanOf<OVER>(c.seq, group).tiles(c.block);
+    c.tiles = PlanOf<OVER, SPLIT>(c.seq, group).tiles(c.block);
     if (c.tiles > 0) return;
   }
 }
@@ -264,10 +269,10 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   }
 }
 
-template <int D, int CODE, int DT, Over OVER>
+template <int D, int CODE, int DT, Over OVER, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_constant__ AttentionArgs a) {
   using M = Memory<D>;
-  using Plan = PlanOf<OVER>;
+  using Plan = PlanOf<OVER, SPLIT>;
   static_assert(M::info % alignof(TileInfo) == 0 && M::bars % 8 == 0 && M::prefix % 8 == 0 &&
                     M::cursors % alignof(Cursor) == 0 && M::words % 8 == 0 && M::bytes <= 227 * 1024,
                 "what lies in shared memory is aligned and fits");
@@ -280,10 +285,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   // [2 w + half]: a row's thread may be two instructions ahead of the last one done
   uint64_t *s_full = bars + 20, *p_full = bars + 24, *o_done = bars + 28, *s_free = bars + 32,
            *info_full = bars + 36;
+  // SPLIT: a half's tiles have their own (it would not tell the phases of the other's apart)
+  auto v_full_of = [&](int tile, int half) {
+    return SPLIT && (tile & 1) ? bars + 36 + INFOS + half : v_full + half;
+  };
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + M::prefix);
   uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + M::words);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + M::words + 4);
 
+  constexpr int STEP = SPLIT ? 2 : 1;  // between tiles of a half
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads;
@@ -297,13 +307,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_free[i], 2);
+      mbar_init(&k_free[i], SPLIT ? 1 : 2);
       mbar_init(&raw_k_full[i], 1);
       mbar_init(&raw_k_free[i], 4);
       mbar_init(&raw_v_full[i], 1);
       mbar_init(&raw_v_free[i], 4);
-      mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 2);
+      mbar_init(v_full_of(0, i), 4);
+      mbar_init(&v_free[i], SPLIT ? 1 : 2);
+      mbar_init(v_full_of(1, i), 4);
       mbar_init(&q_full[i], 4);
       mbar_init(&last[i], 1);
     }
@@ -370,8 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     for (int h = 0; h < 2; ++h) to[h] = key0 * 128 + (((2 * piece + h) ^ key0) & 7) * 16;
     int held = 0;
     uint32_t bad = 0;
-    auto convert = [&](const unsigned char *raw, unsigned char *out, int half) {
-      uint4 w[N];
+    auto load = [&](uint4 *w, const unsigned char *raw, int half) {
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + from + i * (STEP * D));
       if (held < TILE || bad) {  // what no page gave is not a number of ours
@@ -381,6 +391,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           if (key >= held || ((bad >> (key / 16)) & 1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
+    };
+    auto store = [&](const uint4 *w, unsigned char *out) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -411,9 +423,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         held = info[(g + 1) & (INFOS - 1)].held;
         bad = info[(g + 1) & (INFOS - 1)].bad;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-          convert(smem + M::raw_k + s * M::code_bytes + half * (HALF * D),
-                  smem + M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128), half);
+        for (int half = 0; half < 2; ++half) {
+          uint4 w[N];
+          load(w, smem + M::raw_k + s * M::code_bytes + half * (HALF * D), half);
+          store(w, smem + M::k + s * M::kv_bytes + block * (TILE * 128) + half * (HALF * 128));
+        }
         done(&k_full[s], &raw_k_free[s]);
       }
       if (g >= 0) {
@@ -425,9 +439,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         for (int half = 0; half < 2; ++half) {
           if (g >= 1) ok = ok && ready(&v_free[half], (uint32_t)(g - 1) & 1);
           if (!ok) break;
-          convert(smem + M::raw_v + s * M::code_bytes + half * (HALF * D),
-                  smem + M::v + half * M::half_bytes + block * (HALF * 128), half);
-          done(&v_full[half], half ? &raw_v_free[s] : nullptr);
+          uint4 w[N];
+          load(w, smem + M::raw_v + s * M::code_bytes + half * (HALF * D), half);
+          store(w, smem + M::v + half * M::half_bytes + block * (HALF * 128));
+          done(v_full_of(g, half), half ? &raw_v_free[s] : nullptr);
         }
         if (!ok) break;
       }
@@ -452,42 +467,48 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         tc_commit(&s_full[2 * w + h], mine);
         if (h) tc_commit(&k_free[s], mine);
       };
-      Cursor cur = cursor_at<OVER>(a, prefix, group, lo);
+      Cursor cur = cursor_at<OVER, SPLIT>(a, prefix, group, lo);
       const int n = (int)(hi - lo);
       int g = 0;  // tiles of the stretch begun
       uint32_t segment = 0;
       bool ok = true;
       while (ok && g < n) {
         const int count = min(cur.tiles - cur.tile, n - g);
-        ok = ready(&k_full[g & 1], (g >> 1) & 1) && ready(&q_full[w], segment & 1);
-        if (!ok) break;
-        tc_fence_after();
-        scores(g & 1, 0);
-        for (int j = 0; j < count && ok; ++j, ++g) {
+        const int skip = SPLIT ? (g ^ w) & 1 : 0, mine_of = SPLIT ? (count - skip + 1) / 2 : count;
+        int x = g + skip;  // the half's own tiles: every STEP-th from here
+        g += count;
+        if (mine_of > 0) {
+          ok = ready(&k_full[x & 1], (x >> 1) & 1) && ready(&q_full[w], segment & 1);
+          if (!ok) break;
+          tc_fence_after();
+          scores(x & 1, 0);
+          for (int j = 0; j < mine_of && ok; ++j, x += STEP) {
+            const uint32_t turn = SPLIT ? (x >> 1) & 1 : x & 1;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (h == 0 || j + 1 < count) {  // the scores after these, once these have been read
-              const int next = g + h;
-              if (h) ok = ready(&k_full[next & 1], (next >> 1) & 1);
-              ok = ok && ready(&s_free[2 * w + h], g & 1);
+            for (int h = 0; h < 2; ++h) {
+              if (h == 0 || j + 1 < mine_of) {  // the scores after these, once these have been read
+                const int next = x + h * STEP;
+                if (h) ok = ready(&k_full[next & 1], (next >> 1) & 1);
+                ok = ok && ready(&s_free[2 * w + h], turn);
+                if (!ok) break;
+                tc_fence_after();
+                scores(next & 1, h ^ 1);
+              }
+              ok = ready(v_full_of(x, h), turn) && ready(&p_full[2 * w + h], turn);
               if (!ok) break;
               tc_fence_after();
-              scores(next & 1, h ^ 1);
-            }
-            ok = ready(&v_full[h], g & 1) && ready(&p_full[2 * w + h], g & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v = v_at + h * (M::half_bytes >> 4), first = j > 0 || h > 0;
+              const uint32_t v = v_at + h * (M::half_bytes >> 4), first = j > 0 || h > 0;
 #pragma unroll
-            for (int e = 0; e < HALF / 16; ++e)
-              mma_ts(o_at, s_at + HALF + 32 * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first,
-                     mine);
-            tc_commit(&o_done[2 * w + h], mine);
-            tc_commit(&v_free[h], mine);
+              for (int e = 0; e < HALF / 16; ++e)
+                mma_ts(o_at, s_at + HALF + 32 * h + 8 * e, operand_at(v, e * 2048), io, e > 0 ? 1u : first,
+                       mine);
+              tc_commit(&o_done[2 * w + h], mine);
+              tc_commit(&v_free[h], mine);
+            }
           }
+          ++segment;
         }
-        ++segment;
-        if (ok && g < n) next_segment<OVER>(a, prefix, group, cur);
+        if (ok && g < n) next_segment<OVER, SPLIT>(a, prefix, group, cur);
       }
       // nothing may be left running when this CTA gives its memory back
       tc_commit(&last[w], mine);
@@ -502,14 +523,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         int b, head, t0, len;
       };
       Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + 8;  // one for all lanes
-      if (lane == 0) *cur = cursor_at<OVER>(a, prefix, group, lo);
+      if (lane == 0) *cur = cursor_at<OVER, SPLIT>(a, prefix, group, lo);
       __syncwarp();
       int ahead = 0;  // tiles of the stretch taken
       auto take = [&] {
         const Place p = {cur->b, cur->head, cur->tile * TILE, cur->seq.len};
         ++ahead;
         __syncwarp();
-        if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment<OVER>(a, prefix, group, *cur);
+        if (lane == 0 && ++cur->tile == cur->tiles && ahead < n) next_segment<OVER, SPLIT>(a, prefix, group, *cur);
         __syncwarp();
         return p;
       };
@@ -539,17 +560,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         return y;
       };
+      // The first tile's keys are asked for before anything of the second is looked up.
       Place now = take(), next = now, after = now;  // tiles g, g + 1 and g + 2
-      Pages py = look_up(now, ask(now)), ny = py;
-      int asked = -1;
+      const int first_page = ask(now);
+      int next_page = -1, asked = -1;
       if (n > 1) {
         next = take();
-        ny = look_up(next, ask(next));
+        next_page = ask(next);
       }
-      if (n > 2) {
-        after = take();
-        asked = ask(after);
-      }
+      Pages py = look_up(now, first_page), ny = py;
       auto copy = [&](const char *codes, const Place &p, const Pages &y, unsigned char *to, uint64_t *bar) {
         const bool starts = lane < GROUPS && (lane * 16) % PP == 0 && y.page >= 0;
         const unsigned copies = __ballot_sync(FULL, starts);
@@ -581,6 +600,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       int k_sent = 0, v_sent = 0;
       bool ok = fetch_k(0, now, py);
       k_sent = ok;
+      if (n > 1) ny = look_up(next, next_page);
+      if (n > 2) {
+        after = take();
+        asked = ask(after);
+      }
       const int upto = a.withhold ? 1 : n;
       for (int g = 0; g < upto && ok; ++g) {
         if (g + 1 < n) {
@@ -620,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       const uint32_t sp = tmem + 128 * w + lanes, op = tmem + O_COL + 128 * w + lanes;
       unsigned char *q_to = smem + M::q + w * M::q_bytes + row * 128;
       Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
-      if (lane == 0) *cur = cursor_at<OVER>(a, prefix, group, lo);
+      if (lane == 0) *cur = cursor_at<OVER, SPLIT>(a, prefix, group, lo);
       __syncwarp();
       if (threadIdx.x == 0) {
         const Cut cut = {prefix[a.batch], cur->b, cur->head, cur->block, cur->tile, cur->tiles, 0};
@@ -631,12 +655,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       bool ok = true;
       while (ok && x < n_tiles) {
         const int tile0 = cur->tile, count = min(cur->tiles - tile0, n_tiles - x);
-        const bool live = cur->block * MB + r < cur->seq.n * group;
-        const int rr = cur->block * MB + r;
+        const int skip = SPLIT ? (x ^ w) & 1 : 0, mine_of = SPLIT ? (count - skip + 1) / 2 : count;
+        const int rr = cur->block * ROWS_OF<SPLIT> + (SPLIT ? row : r);
+        const bool live = rr < cur->seq.n * group;
         // the row in fp16, brought to a largest magnitude in [1, 2) by a power of two (bf16);
         // the sign of the scale goes with it, so that factors of scores are never negative
         float rowc = 0.0f;
-        {
+        if (!SPLIT || mine_of > 0) {
           const char *src = static_cast<const char *>(a.q.q) +
                             2 * ((cur->seq.row0 + rr / group) * a.q.q_row_stride +
                                  (cur->head * group + rr % group) * a.q.q_head_stride);
@@ -698,15 +723,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           tmem_wait_store();
         };
 #pragma unroll 1
-        for (int j = 0; j < 2 * count; ++j) {
-          const int u = 2 * x + j, g = u >> 1, h = u & 1;  // halves of tiles done, the tile, its half
+        for (int j = 0; j < 2 * mine_of; ++j) {
+          const int at_tile = skip + (j >> 1) * STEP, g = x + at_tile, h = j & 1;  // of the segment, the stretch; its half
+          const int done_of = SPLIT ? g >> 1 : g, u = 2 * done_of + h;  // own tiles before, halves of tiles
           ok = __all_sync(FULL, (h || wait(&info_full[g & (INFOS - 1)], (uint32_t)((g / INFOS) & 1))) &&
-                                    wait(&s_full[2 * w + h], (uint32_t)(g & 1)));
+                                    wait(&s_full[2 * w + h], (uint32_t)(done_of & 1)));
           if (!ok) break;
           tc_fence_after();
           const float2 *scale = info[g & (INFOS - 1)].scale + 4 * h;
           const uint32_t bad = (info[g & (INFOS - 1)].bad >> (4 * h)) & 15u;
-          const int seen = limit - (tile0 + (j >> 1)) * TILE - h * HALF;  // columns this row sees
+          const int seen = limit - (tile0 + at_tile) * TILE - h * HALF;  // columns this row sees
           uint32_t s[HALF], p[HALF / 2];
           tmem_read64(sp, s);
           tc_fence_before();
@@ -801,9 +827,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         if (!ok) break;
         // ---- finish the segment, or leave a part
-        ok = __all_sync(FULL, wait(&o_done[2 * w + 1], (uint32_t)(x + count - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
+        const bool some = !SPLIT || mine_of > 0;
+        if (some) {
+          const int end = x + skip + (mine_of - 1) * STEP;  // the last of the half's tiles
+          ok = __all_sync(FULL, wait(&o_done[2 * w + 1], (uint32_t)(SPLIT ? end >> 1 : end) & 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
         const float sum = low(l) + high(l);
         const bool done = tile0 == 0 && count == cur->tiles;
         const int64_t q_row = cur->seq.row0 + rr / group;
@@ -819,9 +849,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
           if (!live) continue;
           float y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(s[e]) * f;
+          for (int e = 0; e < 32; ++e) y[e] = some ? __uint_as_float(s[e]) * f : 0.0f;
           if (OVER == Over::SHARED && done) {  // joined with the rows' other span later
-            float4 *side = reinterpret_cast<float4 *>(a.side + (q_row * a.q.q_heads + q_head) * D + 32 * q4);
+            const int64_t at = q_row * a.q.q_heads + q_head + (SPLIT && w ? 2 * a.side_rows : 0);
+            float4 *side = reinterpret_cast<float4 *>(a.side + at * D + 32 * q4);
 #pragma unroll
             for (int e = 0; e < 8; ++e) side[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           } else if (done) {
@@ -837,7 +868,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         tc_fence_before();
         if (live) {
           if (OVER == Over::SHARED && done) {
-            a.side_lse2[q_row * a.q.q_heads + q_head] = sum > 0.0f ? m + log2f(sum) : -INFINITY;
+            a.side_lse2[q_row * a.q.q_heads + q_head + (SPLIT && w ? 2 * a.side_rows : 0)] = sum > 0.0f ? m + log2f(sum) : -INFINITY;
           } else if (done) {
             if (a.q.d_lse)
               a.q.d_lse[q_row * a.q.q_heads + q_head] = sum > 0.0f ? (m + log2f(sum)) * LN2 : -INFINITY;
@@ -847,7 +878,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         }
         x += count;
         __syncwarp();
-        if (lane == 0 && x < n_tiles) next_segment<OVER>(a, prefix, group, *cur);
+        if (lane == 0 && x < n_tiles) next_segment<OVER, SPLIT>(a, prefix, group, *cur);
         __syncwarp();
       }
     } else if (threadIdx.x == 0) {
@@ -927,9 +958,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 8) kv_join_kernel(const __grid_c
   }
 }
 
-template <int D, int CODE, int DT, Over OVER>
+template <int D, int CODE, int DT, Over OVER, bool SPLIT>
 int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
-  const auto kernel = kv_prefill_kernel<D, CODE, DT, OVER>;
+  const auto kernel = kv_prefill_kernel<D, CODE, DT, OVER, SPLIT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Memory<D>::bytes) !=
       cudaSuccess)
     return IBP_ERR_CUDA;
@@ -955,13 +986,13 @@ int launch_for(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
   }
 }
 
-template <int D, Over OVER>
+template <int D, Over OVER, bool SPLIT>
 int launch_types(const AttentionArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   if (a.c.code == IBP_KV_INT8)
-    return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_INT8, IBP_BF16, OVER>(a, dev, s)
-                                 : launch_for<D, IBP_KV_INT8, IBP_FP16, OVER>(a, dev, s);
-  return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_E4M3, IBP_BF16, OVER>(a, dev, s)
-                               : launch_for<D, IBP_KV_E4M3, IBP_FP16, OVER>(a, dev, s);
+    return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_INT8, IBP_BF16, OVER, SPLIT>(a, dev, s)
+                                 : launch_for<D, IBP_KV_INT8, IBP_FP16, OVER, SPLIT>(a, dev, s);
+  return a.q.dtype == IBP_BF16 ? launch_for<D, IBP_KV_E4M3, IBP_BF16, OVER, SPLIT>(a, dev, s)
+                               : launch_for<D, IBP_KV_E4M3, IBP_FP16, OVER, SPLIT>(a, dev, s);
 }
 
 }  // namespace
@@ -984,22 +1015,26 @@ int launch_kv_prefill(const ibp_kv_cache &c, const ibp_kv_query &q, void *d_scra
   a.part = reinterpret_cast<float *>(a.cuts + MAX_PREFILL_CTAS);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += BATCH) {
     a.batch = std::min(c.batch - a.b0, BATCH);
-    if (int rc = c.head_dim == 64 ? launch_types<64, Over::ALL>(a, dev, s)
-                                 : launch_types<128, Over::ALL>(a, dev, s))
+    if (int rc = c.head_dim == 64 ? launch_types<64, Over::ALL, false>(a, dev, s)
+                                 : launch_types<128, Over::ALL, false>(a, dev, s))
       return rc;
   }
   return IBP_OK;
 }
 
-int launch_kv_prefill_shared(AttentionArgs a, cudaStream_t s) {
+int launch_kv_prefill_shared(AttentionArgs a, bool split, cudaStream_t s) {
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
-  return a.c.head_dim == 64 ? launch_types<64, Over::SHARED>(a, dev, s)
-                            : launch_types<128, Over::SHARED>(a, dev, s);
+  if (split)
+    return a.c.head_dim == 64 ? launch_types<64, Over::SHARED, true>(a, dev, s)
+                              : launch_types<128, Over::SHARED, true>(a, dev, s);
+  return a.c.head_dim == 64 ? launch_types<64, Over::SHARED, false>(a, dev, s)
+                            : launch_types<128, Over::SHARED, false>(a, dev, s);
 }
-PrefillShape prefill_shape() {
+PrefillShape prefill_shape(bool split) {
   DeviceInfo dev;
-  return {MB, TILE, device_info(&dev) == IBP_OK ? std::min(dev.sm_count, MAX_PREFILL_CTAS) : 0};
+  return {split ? ROWS_OF<true> : ROWS_OF<false>, MB, TILE,
+          device_info(&dev) == IBP_OK ? std::min(dev.sm_count, MAX_PREFILL_CTAS) : 0};
 }
 
 }  // namespace ibp

@@ -13,10 +13,17 @@ namespace ibp {
 namespace {
 
 constexpr int PLAN_THREADS = SHARE_SLAB;
-constexpr int JOIN_WARPS = 4, JOIN_PARTS = 4;
+constexpr int JOIN_WARPS = 4, JOIN_PARTS = 8;
+
+// a / b of numbers that are not negative: a division in 64 bits takes several times as long
+// as one in 32, which most of these fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 struct Side {
-  int mb, tile, ctas;  // rows of a segment, tokens of a tile, CTAs of the launch
+  int mb, part_rows, tile, ctas;  // rows of a segment and of a part, tokens of a tile, CTAs of the launch
+  int split;                      // a part and a finished segment are in two results, mb rows apart
   const float *part;
 };
 
@@ -28,7 +35,8 @@ struct ShareArgs {
   int n_groups, b0, batch;
   Side side[2];     // beginnings, the rest
   int together;     // both in one launch: tiles of the rest follow those of the beginnings
-  Span *spans;      // [2 * SHARE_SLAB]
+  int beginnings;   // spans kept for beginnings, the rest behind them
+  Span *spans;      // [beginnings + batch]
   int64_t *total;   // [2] tiles of each side's launch
   const float *result, *result_lse2;  // as AttentionArgs::side
   int64_t side_rows;
@@ -59,7 +67,7 @@ __device__ __forceinline__ int64_t sum_before(int64_t x, int64_t *warp_sum, int6
 // sequence shares nothing.
 __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __grid_constant__ ShareArgs a) {
   __shared__ int group_of[SHARE_SLAB], seen[SHARE_SLAB], members[SHARE_SLAB];
-  __shared__ int first[SHARE_SLAB], last[SHARE_SLAB];
+  __shared__ int first[SHARE_SLAB], last[SHARE_SLAB], place[SHARE_SLAB];
   __shared__ int64_t warp_sum[PLAN_THREADS / 32];
   const int t = threadIdx.x, b = a.b0 + t, heads = a.c.n_heads, group = a.q.q_heads / heads;
   const int P = a.c.page_tokens;
@@ -104,10 +112,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
     }
   }
   __syncthreads();
-  const int shared_tokens = live && members[run] > 1 ? seen[run] : 0;
-  // beginnings: thread t lays out run t
-  int64_t tiles = 0, total;
-  if (t < (int)runs && members[t] > 1 && seen[t] > 0) {
+  // beginnings: thread t lays out run t, those that are shared one after another
+  bool shares = t < (int)runs && members[t] > 1 && seen[t] > 0;
+  int64_t beginnings, total;
+  const int at = (int)sum_before(shares, warp_sum, &beginnings);
+  shares = shares && at < a.beginnings;  // (more of them: offsets that do not rise, recorded already)
+  place[t] = shares ? at : -1;
+  int64_t tiles = 0;
+  if (shares) {
     int64_t x, y, z, end;
     kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + first[t], nullptr, &x, &y);
     kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + last[t], nullptr, &z, &end);
@@ -115,29 +127,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
     s.n = (int)max(min(end - x, (int64_t)0x3FFFFFFF), (int64_t)0);
     s.len = s.at = seen[t];
     s.table_at = (int64_t)(a.b0 + first[t]) * a.c.table_stride;
-    const int64_t blocks = ((int64_t)s.n * group + a.side[0].mb - 1) / a.side[0].mb;
+    const int64_t blocks = quotient((int64_t)s.n * group + a.side[0].mb - 1, a.side[0].mb);
     tiles = heads * blocks * ((s.len + a.side[0].tile - 1) / a.side[0].tile);
   }
   s.before = sum_before(tiles, warp_sum, &total);
-  s.group = t;
-  a.spans[t] = s;
+  if (shares) a.spans[at] = s;
+  if (t >= (int)beginnings && t < a.beginnings) a.spans[t] = Span();
   const int64_t behind = a.together ? total : 0;
   if (t == 0) a.total[0] = total;
+  __syncthreads();
   // the rest of each sequence
   s = Span();
   tiles = 0;
   if (live) {
+    s.group = place[run];
+    const int shared_tokens = s.group >= 0 ? seen[run] : 0;
     s.row0 = lo;
     s.n = n;
     s.len = len - shared_tokens;
     s.at = s.len - n;
     s.table_at = (int64_t)b * a.c.table_stride + shared_tokens / P;
-    s.group = run;
-    const int64_t blocks = ((int64_t)n * group + a.side[1].mb - 1) / a.side[1].mb;
+    const int64_t blocks = quotient((int64_t)n * group + a.side[1].mb - 1, a.side[1].mb);
     tiles = heads * blocks * ((s.len + a.side[1].tile - 1) / a.side[1].tile);
   }
   s.before = behind + sum_before(tiles, warp_sum, &total);
-  a.spans[SHARE_SLAB + t] = s;
+  if (live) a.spans[a.beginnings + t] = s;
   if (t == 0) {
     a.total[1] = behind + total;
     if (a.together) a.total[0] = behind + total;
@@ -162,6 +176,20 @@ __device__ __forceinline__ void load_lane(const float *from, float *y) {
   }
 }
 
+// Two results of one row over different tokens.
+template <int D>
+__device__ __forceinline__ Half<D> joined(const Half<D> &u, const Half<D> &v) {
+  Half<D> h;
+  const float top = fmaxf(u.z, v.z);
+  const bool none = top == -INFINITY;  // neither has seen a token
+  const float fu = none ? 0.0f : exp2_fast(u.z - top), fv = none ? 0.0f : exp2_fast(v.z - top);
+  const float f = none ? 0.0f : 1.0f / (fu + fv);
+#pragma unroll
+  for (int e = 0; e < Half<D>::V; ++e) h.y[e] = (u.y[e] * fu + v.y[e] * fv) * f;
+  h.z = none ? -INFINITY : top + log2f(fu + fv);
+  return h;
+}
+
 // A segment that one CTA finished left its rows; the parts of the others are joined in their
 // order, so that results do not depend on timing.
 template <int D>
@@ -174,27 +202,34 @@ __device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const 
   if (s.len <= 0 || row < s.row0 || row >= s.row0 + s.n) return h;
   const Side &side = a.side[which];
   const int lane = threadIdx.x & 31, group = a.q.q_heads / a.c.n_heads;
-  const int64_t rr = (row - s.row0) * group + qh % group;
-  const int64_t blocks = ((int64_t)s.n * group + side.mb - 1) / side.mb;
-  const int tiles = (s.len + side.tile - 1) / side.tile, r = (int)(rr % side.mb);
-  const Parts p = parts_of(a.total[which], s.before + (qh / group * blocks + rr / side.mb) * tiles, tiles, side.ctas);
+  const int64_t rr = (row - s.row0) * group + qh % group, block = quotient(rr, side.mb);
+  const int64_t blocks = quotient((int64_t)s.n * group + side.mb - 1, side.mb);
+  const int tiles = (s.len + side.tile - 1) / side.tile, r = (int)(rr - block * side.mb);
+  const Parts p = parts_of(a.total[which], s.before + (qh / group * blocks + block) * tiles, tiles, side.ctas);
   if (p.first == p.last) {
-    const int64_t at = row * a.q.q_heads + qh + which * a.side_rows;
+    const int64_t at = row * a.q.q_heads + qh + which * a.side_rows, second = at + 2 * a.side_rows;
     load_lane<V>(a.result + at * D + lane * V, h.y);
     h.z = __ldcg(a.result_lse2 + at);
+    if (side.split) {
+      Half<D> k;
+      load_lane<V>(a.result + second * D + lane * V, k.y);
+      k.z = __ldcg(a.result_lse2 + second);
+      h = joined<D>(h, k);
+    }
     return h;
   }
-  const int64_t stride = (int64_t)side.mb * (D + 4);
+  const int64_t stride = (int64_t)side.part_rows * (D + 4);
+  const int shift = side.split, n = (p.last - p.first + 1) << shift;
   float top = NONE, topv = NONE, sum = 0.0f;
-  for (int k0 = p.first; k0 <= p.last; k0 += JOIN_PARTS) {
+  for (int k0 = 0; k0 < n; k0 += JOIN_PARTS) {
     float4 st[JOIN_PARTS];
     float y[JOIN_PARTS][V];
 #pragma unroll
     for (int k = 0; k < JOIN_PARTS; ++k) {
-      const int cta = min(k0 + k, p.last);
+      const int at = min(k0 + k, n - 1), cta = p.first + (at >> shift), rk = r + (shift ? at & 1 : 0) * side.mb;
       const float *part = side.part + ((int64_t)cta * 2 + (cta == p.first ? p.second : 0)) * stride;
-      st[k] = __ldcg(reinterpret_cast<const float4 *>(part + side.mb * D) + r);
-      load_lane<V>(part + r * D + lane * V, y[k]);
+      st[k] = __ldcg(reinterpret_cast<const float4 *>(part + side.part_rows * D) + rk);
+      load_lane<V>(part + rk * D + lane * V, y[k]);
     }
     float m = top, mv = topv;
 #pragma unroll
@@ -208,7 +243,7 @@ __device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const 
     for (int e = 0; e < V; ++e) h.y[e] *= fo;
 #pragma unroll
     for (int k = 0; k < JOIN_PARTS; ++k)
-      if (k0 + k <= p.last) {
+      if (k0 + k < n) {
         const float f = exp2_fast(st[k].y - mv);
         sum += st[k].z * exp2_fast(st[k].x - m);
 #pragma unroll
@@ -230,30 +265,21 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
   constexpr int V = Half<D>::V;
   const int lane = threadIdx.x & 31;
   const int64_t x = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), each = a.q.max_q * a.q.q_heads;
-  const int i = (int)(x / each), j = (int)(x % each / a.q.q_heads), qh = (int)(x % a.q.q_heads);
+  const int i = (int)quotient(x, each), in = (int)(x - i * each), j = in / a.q.q_heads, qh = in % a.q.q_heads;
   grid_dependency_wait();
   if (i >= a.batch) return;
-  const Span s = a.spans[SHARE_SLAB + i];
+  const Span s = a.spans[a.beginnings + i];
   if (j >= s.n) return;
   const int64_t row = s.row0 + j;
-  const Half<D> u = half_of<D>(a, 0, a.spans[s.group], row, qh), v = half_of<D>(a, 1, s, row, qh);
-  const float top = fmaxf(u.z, v.z);
-  float z = -INFINITY, y[V];
-  if (top == -INFINITY) {  // a row that sees nothing
-    for (int e = 0; e < V; ++e) y[e] = 0.0f;
-  } else {
-    const float fu = exp2_fast(u.z - top), fv = exp2_fast(v.z - top), f = 1.0f / (fu + fv);
-#pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = (u.y[e] * fu + v.y[e] * fv) * f;
-    z = top + log2f(fu + fv);
-  }
+  const Half<D> h = joined<D>(half_of<D>(a, 0, s.group < 0 ? Span() : a.spans[s.group], row, qh),
+                                   half_of<D>(a, 1, s, row, qh));
   char *out = static_cast<char *>(a.q.out) +
               2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + lane * V);
   if constexpr (V == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]));
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<DT>(h.y[0], h.y[1]), pack2<DT>(h.y[2], h.y[3]));
   else
-    *reinterpret_cast<uint32_t *>(out) = pack2<DT>(y[0], y[1]);
-  if (lane == 0 && a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = z * LN2;
+    *reinterpret_cast<uint32_t *>(out) = pack2<DT>(h.y[0], h.y[1]);
+  if (lane == 0 && a.q.d_lse) a.q.d_lse[row * a.q.q_heads + qh] = h.z * LN2;
 }
 
 // ---- host side
@@ -282,15 +308,17 @@ int attend_ctas(int mb, const DeviceInfo &dev) { return std::min((mb == 8 ? 3 : 
 // How a call is divided: rows of a segment, and whether beginnings go to the kernel for many
 // rows or along with the rest. alone: not divided at all.
 struct Division {
-  bool alone, many;
+  bool alone, many, split;
   int mb;
 };
-Division division_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, int64_t group_rows) {
+Division division_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads, int64_t n_groups,
+                     int64_t group_rows) {
   const int64_t group = q_heads / c.n_heads, each = std::min(max_q, n_rows) * group;
   const int64_t all = std::max(std::min(group_rows, n_rows) * group, each);
   Division d;
-  d.alone = each > 64;
+  d.alone = each > 64 || n_groups == 0;
   d.many = all > 32;
+  d.split = all <= prefill_shape(true).rows;
   d.mb = rows_of(d.many ? each : all);
   return d;
 }
@@ -304,17 +332,17 @@ ShareLayout share_layout(const ibp_kv_cache &c, const Division &d, int64_t n_row
   y.spans = 0;
   y.parts[1] = (2 * SHARE_SLAB * sizeof(Span) + 2 * sizeof(int64_t) + 255) / 256 * 256;
   y.parts[0] = y.parts[1] + (size_t)MAX_CTAS * 2 * d.mb * row;
-  y.result = y.parts[0] + (d.many ? (size_t)MAX_PREFILL_CTAS * 2 * prefill_shape().rows * row + MAX_PREFILL_CTAS * sizeof(Cut) : 0);
-  y.lse2 = y.result + 2 * rows * c.head_dim * sizeof(float);
-  y.bytes = y.lse2 + (2 * rows * sizeof(float) + 255) / 256 * 256;
+  y.result = y.parts[0] + (d.many ? (size_t)MAX_PREFILL_CTAS * 2 * prefill_shape(d.split).part_rows * row + MAX_PREFILL_CTAS * sizeof(Cut) : 0);
+  y.lse2 = y.result + 3 * rows * c.head_dim * sizeof(float);
+  y.bytes = y.lse2 + (3 * rows * sizeof(float) + 255) / 256 * 256;
   return y;
 }
 
 }  // namespace
 
 size_t kv_shared_scratch_bytes(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q_heads,
-                               int64_t group_rows) {
-  const Division d = division_of(c, n_rows, max_q, q_heads, group_rows);
+                               int64_t n_groups, int64_t group_rows) {
+  const Division d = division_of(c, n_rows, max_q, q_heads, n_groups, group_rows);
   if (d.alone) return kv_attention_scratch_bytes(c, n_rows, max_q, q_heads, false);
   return share_layout(c, d, n_rows, q_heads).bytes;
 }
@@ -324,7 +352,7 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
                                int32_t *d_status, cudaStream_t s) {
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
-  const Division d = division_of(c, query.n_rows, query.max_q, query.q_heads, group_rows);
+  const Division d = division_of(c, query.n_rows, query.max_q, query.q_heads, n_groups, group_rows);
   if (d.alone) return launch_kv_attention(c, query, d_scratch, d_status, s);
   const ShareLayout y = share_layout(c, d, query.n_rows, query.q_heads);
   char *base = static_cast<char *>(d_scratch);
@@ -342,10 +370,11 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
   a.result = reinterpret_cast<float *>(base + y.result);
   a.result_lse2 = reinterpret_cast<float *>(base + y.lse2);
   a.side_rows = query.n_rows * query.q_heads;
-  a.side[1] = {d.mb, TILE, attend_ctas(d.mb, dev), reinterpret_cast<float *>(base + y.parts[1])};
+  a.side[1] = {d.mb, d.mb, TILE, attend_ctas(d.mb, dev), 0, reinterpret_cast<float *>(base + y.parts[1])};
   a.side[0] = a.side[1];
-  const PrefillShape many = prefill_shape();
-  if (d.many) a.side[0] = {many.rows, many.tile, many.ctas, reinterpret_cast<float *>(base + y.parts[0])};
+  const PrefillShape many = prefill_shape(d.split);
+  if (d.many)
+    a.side[0] = {many.rows, many.part_rows, many.tile, many.ctas, d.split, reinterpret_cast<float *>(base + y.parts[0])};
 
   AttentionArgs t = {};
   t.c = c;
@@ -361,17 +390,19 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
                                      : (query.dtype == IBP_BF16 ? kv_share_join_kernel<128, IBP_BF16> : kv_share_join_kernel<128, IBP_FP16>);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += SHARE_SLAB) {
     a.batch = std::min(c.batch - a.b0, SHARE_SLAB);
+    // of a slab's sequences, two at least have each shared beginning
+    a.beginnings = t.beginnings = (int)std::min<int64_t>(n_groups, (a.batch + 1) / 2);
     kv_share_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
     if (d.many) {
       t.b0 = 0;
-      t.batch = SHARE_SLAB;
+      t.batch = a.beginnings;
       t.part = const_cast<float *>(a.side[0].part);
-      t.cuts = reinterpret_cast<Cut *>(t.part + (size_t)MAX_PREFILL_CTAS * 2 * many.rows * (c.head_dim + 4));
-      if (int rc = launch_kv_prefill_shared(t, s)) return rc;
+      t.cuts = reinterpret_cast<Cut *>(t.part + (size_t)MAX_PREFILL_CTAS * 2 * many.part_rows * (c.head_dim + 4));
+      if (int rc = launch_kv_prefill_shared(t, d.split, s)) return rc;
     }
-    t.b0 = d.many ? SHARE_SLAB : 0;
-    t.batch = SHARE_SLAB + a.batch - t.b0;
+    t.b0 = d.many ? a.beginnings : 0;
+    t.batch = a.beginnings + a.batch - t.b0;
     t.part = const_cast<float *>(a.side[1].part);
     if (int rc = c.head_dim == 64 ? attend_types<64>(t, d.mb, dev, s) : attend_types<128>(t, d.mb, dev, s)) return rc;
     const int64_t warps = a.batch * a.q.max_q * query.q_heads, blocks = (warps + JOIN_WARPS - 1) / JOIN_WARPS;
