@@ -130,8 +130,14 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads, cta = blockIdx.x;
-  grid_launch_dependents();
-  if constexpr (OVER == Over::SHARED) grid_dependency_wait();  // the spans
+  if constexpr (OVER != Over::SHARED) grid_launch_dependents();
+  // SHARED beside the kernel for many rows, which this one need not wait for before its end: that
+  // one let it start once the spans were there
+  if constexpr (OVER == Over::SHARED) {
+    if (!a.beside) grid_dependency_wait();
+    grid_launch_dependents();  // the spans are there for the joining too
+    if ((int)blockIdx.x >= ctas_of<OVER>(a)) return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
@@ -162,8 +168,12 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   }
   __syncthreads();
   const int64_t total = prefix[a.batch];
-  const Split split(total, a.ctas);
-  if (cta >= split.ctas) return;
+  const Split split(total, ctas_of<OVER>(a));
+  // (what comes next is ordered behind this grid alone: its first CTA ends after the one beside it)
+  auto leave = [&] {
+    if (OVER == Over::SHARED && a.beside && cta == 0) grid_dependency_wait();
+  };
+  if (cta >= split.ctas) return leave();
   const int64_t lo = split.start(cta), hi = split.start(cta + 1);
 
   if (warp == CONSUMERS) {
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
 #pragma unroll 1
     for (int64_t k = i > ST ? i - ST : 0; k < i; ++k)
       drain(&full[k % ST], (uint32_t)((k / ST) & 1), a.status);
-    return;
+    return leave();
   }
 
   // ---- computing warps: S^T = K q^T (16 tokens x 8 NT rows), then O^T += V^T P^T
@@ -585,6 +595,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
     }
     x += count;
   }
+  leave();
 }
 
 // ---- host side -------------------------------------------------------------------

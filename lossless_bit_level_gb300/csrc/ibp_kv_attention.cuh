@@ -93,6 +93,8 @@ struct AttentionArgs {
   float *side, *side_lse2;
   int64_t side_rows;
   int beginnings;  // the spans before this one are beginnings
+  const int *active;  // SHARED: of the launched CTAs, how many share the tiles
+  int beside;         // SHARED, few rows: the kernel for many rows is launched before it
 };
 
 // Many query rows over SHARED spans (ibp_kv_prefill.cu): a.spans, a.side and a.part are set.
@@ -127,10 +129,10 @@ template <Over OVER = Over::ALL>
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, int32_t *status) {
   Sequence s;
   if constexpr (OVER == Over::SHARED) {
-    const Span &from = a.spans[a.b0 + b];
-    s.row0 = from.row0;
-    s.n = from.n;
-    s.len = from.len;
+    const Span *from = a.spans + a.b0 + b;
+    s.row0 = __ldcg(&from->row0);
+    s.n = __ldcg(&from->n);
+    s.len = __ldcg(&from->len);
     return s;
   }
   int64_t lo, hi;
@@ -154,7 +156,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b, i
 template <Over OVER>
 __device__ __forceinline__ int page_of(const AttentionArgs &a, int b, int head, int col) {
   if constexpr (OVER == Over::SHARED) {
-    const int p = __ldg(a.c.d_table + a.spans[a.b0 + b].table_at + col);
+    const int p = __ldg(a.c.d_table + __ldcg(&a.spans[a.b0 + b].table_at) + col);
     if (p >= 0 && p < a.c.n_pages) return p;
     report(a.status, IBP_ERR_INDEX);
     return -1;
@@ -185,7 +187,7 @@ template <bool SCORES, Over OVER = Over::ALL>
 __device__ __forceinline__ Slice slice_of(const AttentionArgs &a, int b, int32_t *status) {
   Slice s;
   static_cast<Sequence &>(s) = sequence_of<OVER>(a, b, status);
-  s.at = OVER == Over::SHARED ? a.spans[a.b0 + b].at : s.len - s.n;
+  s.at = OVER == Over::SHARED ? __ldcg(&a.spans[a.b0 + b].at) : s.len - s.n;
   if (SCORES && a.slice_rows) {
     const int skip = min(a.slice0, s.n);
     s.row0 += skip;
@@ -279,6 +281,14 @@ struct CausalPlan {
     return lo;
   }
 };
+
+// (Loads that pass the first-level cache: the spans' plan may have ended within the life of the
+// grid before this one, which waited for it and let this one start after that.)
+template <Over OVER>
+__device__ __forceinline__ int ctas_of(const AttentionArgs &a) {
+  if constexpr (OVER == Over::SHARED) return __ldcg(a.active);
+  return a.ctas;
+}
 
 __device__ __forceinline__ int find_sequence(const int64_t *prefix, int batch, int64_t x) {
   int lo = 0, hi = batch;  // the last b with prefix[b] <= x (empty ones come before it)

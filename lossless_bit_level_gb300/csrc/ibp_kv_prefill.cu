@@ -223,6 +223,15 @@ __device__ __forceinline__ Cursor cursor_at(const AttentionArgs &a, const int64_
   c.b = find_sequence(prefix, a.batch, x);
   c.seq = sequence_of<OVER>(a, c.b, nullptr);
   const PlanOf<OVER, SPLIT> plan(c.seq, group);
+  if constexpr (OVER == Over::SHARED)
+    if (((x | prefix[c.b + 1]) >> 31) == 0) {  // divisions in 32 bits take a fraction of the time
+      const uint32_t local = (uint32_t)(x - prefix[c.b]), segment = local / (uint32_t)plan.tiles_each;
+      c.head = (int)(segment / (uint32_t)plan.blocks);
+      c.block = (int)segment - c.head * plan.blocks;
+      c.tile = (int)(local - segment * (uint32_t)plan.tiles_each);
+      c.tiles = plan.tiles_each;
+      return c;
+    }
   const int64_t local = x - prefix[c.b], per_head = (prefix[c.b + 1] - prefix[c.b]) / a.c.n_heads;
   c.head = (int)(local / per_head);
   const int64_t in = local - c.head * per_head;
@@ -297,11 +306,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads;
-  grid_launch_dependents();
-  if constexpr (OVER == Over::SHARED) grid_dependency_wait();  // the spans
+  if constexpr (OVER == Over::ALL) grid_launch_dependents();
   if (smem_u32(smem) & 1023) {  // the operands' rows would be swizzled otherwise than written
     report(a.status, IBP_ERR_CUDA);
-    if (threadIdx.x == 0) a.cuts[cta] = Cut();
+    if (OVER == Over::ALL && threadIdx.x == 0) a.cuts[cta] = Cut();
+    if constexpr (OVER == Over::SHARED) grid_dependency_wait();
     return;
   }
   if (threadIdx.x == 0) {
@@ -328,6 +337,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
     *abort = 0;
     mbar_init_fence();
   }
+  if constexpr (OVER == Over::SHARED) {
+    grid_dependency_wait();  // the spans
+    grid_launch_dependents();  // they are there for the next grid too
+    if (cta >= ctas_of<OVER>(a)) return;  // the SM is for that one
+  }
   if (warp == ISSUE_WARP) {
     tmem_alloc(tmem_at);
     int64_t base = 0;
@@ -352,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  const Split split(prefix[a.batch], a.ctas);
+  const Split split(prefix[a.batch], ctas_of<OVER>(a));
   const bool work = cta < split.ctas;
   const int64_t lo = work ? split.start(cta) : 0, hi = work ? split.start(cta + 1) : 0;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       auto ask = [&](const Place &p) {
         const int t = p.t0 + (lane & 7) * 16;
         if constexpr (OVER == Over::SHARED)
-          return t < p.len ? __ldg(c.d_table + a.spans[a.b0 + p.b].table_at + t / c.page_tokens) : -1;
+          return t < p.len ? __ldg(c.d_table + __ldcg(&a.spans[a.b0 + p.b].table_at) + t / c.page_tokens) : -1;
         return t < p.len ? __ldg(c.d_table + (int64_t)(a.b0 + p.b) * c.table_stride + t / c.page_tokens) : -1;
       };
       auto look_up = [&](const Place &p, int page) {
@@ -646,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
       Cursor *cur = reinterpret_cast<Cursor *>(smem + M::cursors) + warp;
       if (lane == 0) *cur = cursor_at<OVER, SPLIT>(a, prefix, group, lo);
       __syncwarp();
-      if (threadIdx.x == 0) {
+      if (OVER == Over::ALL && threadIdx.x == 0) {
         const Cut cut = {prefix[a.batch], cur->b, cur->head, cur->block, cur->tile, cur->tiles, 0};
         a.cuts[cta] = cut;
       }
@@ -881,7 +895,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const __grid_con
         if (lane == 0 && x < n_tiles) next_segment<OVER, SPLIT>(a, prefix, group, *cur);
         __syncwarp();
       }
-    } else if (threadIdx.x == 0) {
+    } else if (OVER == Over::ALL && threadIdx.x == 0) {
       const Cut none = {prefix[a.batch], 0, 0, 0, 0, 0, 0};
       a.cuts[cta] = none;
     }

@@ -23,6 +23,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 struct Side {
   int mb, part_rows, tile, ctas;  // rows of a segment and of a part, tokens of a tile, CTAs of the launch
+  int cost;                       // of a tile: time that it takes an SM, in 0.1 us
   int split;                      // a part and a finished segment are in two results, mb rows apart
   const float *part;
 };
@@ -38,6 +39,7 @@ struct ShareArgs {
   int beginnings;   // spans kept for beginnings, the rest behind them
   Span *spans;      // [beginnings + batch]
   int64_t *total;   // [2] tiles of each side's launch
+  int *active;      // [2] CTAs that share them
   const float *result, *result_lse2;  // as AttentionArgs::side
   int64_t side_rows;
 };
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
   shares = shares && at < a.beginnings;  // (more of them: offsets that do not rise, recorded already)
   place[t] = shares ? at : -1;
   int64_t tiles = 0;
+  __shared__ int segments;  // of the first beginning
   if (shares) {
     int64_t x, y, z, end;
     kv_row_range(a.q.d_cu, a.q.n_rows, a.q.max_q, a.b0 + first[t], nullptr, &x, &y);
@@ -129,6 +132,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
     s.table_at = (int64_t)(a.b0 + first[t]) * a.c.table_stride;
     const int64_t blocks = quotient((int64_t)s.n * group + a.side[0].mb - 1, a.side[0].mb);
     tiles = heads * blocks * ((s.len + a.side[0].tile - 1) / a.side[0].tile);
+    if (at == 0) segments = (int)min(heads * blocks, (int64_t)0x3FFFFFFF);
   }
   s.before = sum_before(tiles, warp_sum, &total);
   if (shares) a.spans[at] = s;
@@ -154,8 +158,40 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
   if (live) a.spans[a.beginnings + t] = s;
   if (t == 0) {
     a.total[1] = behind + total;
-    if (a.together) a.total[0] = behind + total;
+    if (a.together) {
+      a.total[0] = behind + total;
+      a.active[0] = a.active[1] = a.side[1].ctas;
+    } else {
+      // The two kernels run side by side: as many SMs to each as the tiles that it has take time
+      // (32 conversations behind 8,192 tokens: 60 us one after the other).
+      const int sms = a.side[0].ctas;
+      const int64_t work = a.total[0] * a.side[0].cost, rest = total * a.side[1].cost;
+      int mine = work == 0 ? 0 : rest == 0 ? sms : (int)min(max(sms * work / (work + rest), (int64_t)1), (int64_t)sms - 1);
+      // no more than tiles; of one beginning, a whole number to each head and block of rows, so
+      // that none goes over two (which takes it as long as four tiles more)
+      mine = (int)min((int64_t)mine, a.total[0]);
+      if (beginnings == 1 && mine > segments) mine = min((mine + segments - 1) / segments, sms / segments) * segments;
+      a.active[0] = max(mine, 1);
+      a.active[1] = max(a.side[1].ctas / sms * (sms - mine), 1);
+    }
   }
+}
+
+__device__ __forceinline__ Span span_at(const Span *p) {
+  static_assert(sizeof(Span) == 40, "five words of 64 bits");
+  Span s;
+  const long long *from = reinterpret_cast<const long long *>(p);
+  long long w[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = __ldcg(from + i);
+  s.row0 = w[0];
+  s.table_at = w[1];
+  s.before = w[2];
+  s.n = (int)w[3];
+  s.len = (int)(w[3] >> 32);
+  s.at = (int)w[4];
+  s.group = (int)(w[4] >> 32);
+  return s;
 }
 
 // One row's result of one side: D/32 elements a lane, and log2 of its sum.
@@ -190,23 +226,45 @@ __device__ __forceinline__ Half<D> joined(const Half<D> &u, const Half<D> &v) {
   return h;
 }
 
-// A segment that one CTA finished left its rows; the parts of the others are joined in their
-// order, so that results do not depend on timing.
+// Where a row's results of one side lie (n 0: it has none). A segment that one CTA finished left
+// its rows; the parts of the others are joined in their order, so that results do not depend on
+// timing.
+struct Where {
+  int n, r;    // parts, two to a CTA if split; row in a part
+  bool done;
+  Parts p;
+};
+__device__ __forceinline__ Where where_of(const ShareArgs &a, int which, const Span &s, int64_t row, int qh) {
+  Where w = {};
+  // (rows outside the span: offsets that do not rise, recorded already)
+  if (s.len <= 0 || row < s.row0 || row >= s.row0 + s.n) return w;
+  const Side &side = a.side[which];
+  const int group = a.q.q_heads / a.c.n_heads;
+  const int64_t rr = (row - s.row0) * group + qh % group, block = quotient(rr, side.mb);
+  const int64_t blocks = quotient((int64_t)s.n * group + side.mb - 1, side.mb);
+  const int tiles = (s.len + side.tile - 1) / side.tile;
+  w.r = (int)(rr - block * side.mb);
+  // as parts_of, its divisions in 32 bits where they fit
+  const int64_t total = __ldcg(a.total + which), start = s.before + (qh / group * blocks + block) * tiles;
+  const int64_t ctas = min((int64_t)__ldcg(a.active + which), total);
+  w.p.first = (int)quotient((start + 1) * ctas - 1, total);
+  w.p.last = (int)quotient((start + tiles) * ctas - 1, total);
+  w.p.second = quotient(total * w.p.first, ctas) < start;
+  w.done = w.p.first == w.p.last;
+  w.n = (w.done ? 1 : w.p.last - w.p.first + 1) << side.split;
+  return w;
+}
+
 template <int D>
-__device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const Span &s, int64_t row, int qh) {
+__device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const Where &w, int64_t row, int qh) {
   constexpr int V = Half<D>::V;
   Half<D> h;
   for (int e = 0; e < V; ++e) h.y[e] = 0.0f;
   h.z = -INFINITY;
-  // (rows outside the span: offsets that do not rise, recorded already)
-  if (s.len <= 0 || row < s.row0 || row >= s.row0 + s.n) return h;
+  if (w.n == 0) return h;
   const Side &side = a.side[which];
-  const int lane = threadIdx.x & 31, group = a.q.q_heads / a.c.n_heads;
-  const int64_t rr = (row - s.row0) * group + qh % group, block = quotient(rr, side.mb);
-  const int64_t blocks = quotient((int64_t)s.n * group + side.mb - 1, side.mb);
-  const int tiles = (s.len + side.tile - 1) / side.tile, r = (int)(rr - block * side.mb);
-  const Parts p = parts_of(a.total[which], s.before + (qh / group * blocks + block) * tiles, tiles, side.ctas);
-  if (p.first == p.last) {
+  const int lane = threadIdx.x & 31;
+  if (w.done) {
     const int64_t at = row * a.q.q_heads + qh + which * a.side_rows, second = at + 2 * a.side_rows;
     load_lane<V>(a.result + at * D + lane * V, h.y);
     h.z = __ldcg(a.result_lse2 + at);
@@ -219,15 +277,15 @@ __device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const 
     return h;
   }
   const int64_t stride = (int64_t)side.part_rows * (D + 4);
-  const int shift = side.split, n = (p.last - p.first + 1) << shift;
+  const int shift = side.split, n = w.n;
   float top = NONE, topv = NONE, sum = 0.0f;
   for (int k0 = 0; k0 < n; k0 += JOIN_PARTS) {
     float4 st[JOIN_PARTS];
     float y[JOIN_PARTS][V];
 #pragma unroll
     for (int k = 0; k < JOIN_PARTS; ++k) {
-      const int at = min(k0 + k, n - 1), cta = p.first + (at >> shift), rk = r + (shift ? at & 1 : 0) * side.mb;
-      const float *part = side.part + ((int64_t)cta * 2 + (cta == p.first ? p.second : 0)) * stride;
+      const int at = min(k0 + k, n - 1), cta = w.p.first + (at >> shift), rk = w.r + (shift ? at & 1 : 0) * side.mb;
+      const float *part = side.part + ((int64_t)cta * 2 + (cta == w.p.first ? w.p.second : 0)) * stride;
       st[k] = __ldcg(reinterpret_cast<const float4 *>(part + side.part_rows * D) + rk);
       load_lane<V>(part + rk * D + lane * V, y[k]);
     }
@@ -266,13 +324,21 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
   const int lane = threadIdx.x & 31;
   const int64_t x = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), each = a.q.max_q * a.q.q_heads;
   const int i = (int)quotient(x, each), in = (int)(x - i * each), j = in / a.q.q_heads, qh = in % a.q.q_heads;
-  grid_dependency_wait();
-  if (i >= a.batch) return;
-  const Span s = a.spans[a.beginnings + i];
-  if (j >= s.n) return;
+  // The spans are there before the kernels that go over them let this one start (loads pass the
+  // first-level cache), so that only their results are waited for.
+  Span s = {}, from = {};
+  if (i < a.batch) s = span_at(a.spans + a.beginnings + i);
+  if (i < a.batch && s.group >= 0) from = span_at(a.spans + s.group);
   const int64_t row = s.row0 + j;
-  const Half<D> h = joined<D>(half_of<D>(a, 0, s.group < 0 ? Span() : a.spans[s.group], row, qh),
-                                   half_of<D>(a, 1, s, row, qh));
+  const bool live = i < a.batch && j < s.n;
+  Where first = {}, rest = {};
+  if (live) {
+    first = where_of(a, 0, from, row, qh);
+    rest = where_of(a, 1, s, row, qh);
+  }
+  grid_dependency_wait();
+  if (!live) return;
+  const Half<D> h = joined<D>(half_of<D>(a, 0, first, row, qh), half_of<D>(a, 1, rest, row, qh));
   char *out = static_cast<char *>(a.q.out) +
               2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + lane * V);
   if constexpr (V == 4)
@@ -330,9 +396,9 @@ ShareLayout share_layout(const ibp_kv_cache &c, const Division &d, int64_t n_row
   const size_t row = (c.head_dim + 4) * sizeof(float), rows = (size_t)n_rows * q_heads;
   ShareLayout y;
   y.spans = 0;
-  y.parts[1] = (2 * SHARE_SLAB * sizeof(Span) + 2 * sizeof(int64_t) + 255) / 256 * 256;
+  y.parts[1] = (2 * SHARE_SLAB * sizeof(Span) + 2 * sizeof(int64_t) + 2 * sizeof(int) + 255) / 256 * 256;
   y.parts[0] = y.parts[1] + (size_t)MAX_CTAS * 2 * d.mb * row;
-  y.result = y.parts[0] + (d.many ? (size_t)MAX_PREFILL_CTAS * 2 * prefill_shape(d.split).part_rows * row + MAX_PREFILL_CTAS * sizeof(Cut) : 0);
+  y.result = y.parts[0] + (d.many ? (size_t)MAX_PREFILL_CTAS * 2 * prefill_shape(d.split).part_rows * row : 0);
   y.lse2 = y.result + 3 * rows * c.head_dim * sizeof(float);
   y.bytes = y.lse2 + (3 * rows * sizeof(float) + 255) / 256 * 256;
   return y;
@@ -367,14 +433,16 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
   a.together = !d.many;
   a.spans = reinterpret_cast<Span *>(base + y.spans);
   a.total = reinterpret_cast<int64_t *>(a.spans + 2 * SHARE_SLAB);
+  a.active = reinterpret_cast<int *>(a.total + 2);
   a.result = reinterpret_cast<float *>(base + y.result);
   a.result_lse2 = reinterpret_cast<float *>(base + y.lse2);
   a.side_rows = query.n_rows * query.q_heads;
-  a.side[1] = {d.mb, d.mb, TILE, attend_ctas(d.mb, dev), 0, reinterpret_cast<float *>(base + y.parts[1])};
+  // (costs: what tiles of long sequences took when kernels had the GPU to themselves)
+  a.side[1] = {d.mb, d.mb, TILE, attend_ctas(d.mb, dev), d.mb <= 16 ? 5 : d.mb == 32 ? 9 : 18, 0, reinterpret_cast<float *>(base + y.parts[1])};
   a.side[0] = a.side[1];
   const PrefillShape many = prefill_shape(d.split);
   if (d.many)
-    a.side[0] = {many.rows, many.part_rows, many.tile, many.ctas, d.split, reinterpret_cast<float *>(base + y.parts[0])};
+    a.side[0] = {many.rows, many.part_rows, many.tile, many.ctas, d.split ? 24 : 36, d.split, reinterpret_cast<float *>(base + y.parts[0])};
 
   AttentionArgs t = {};
   t.c = c;
@@ -398,12 +466,15 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
       t.b0 = 0;
       t.batch = a.beginnings;
       t.part = const_cast<float *>(a.side[0].part);
-      t.cuts = reinterpret_cast<Cut *>(t.part + (size_t)MAX_PREFILL_CTAS * 2 * many.part_rows * (c.head_dim + 4));
+      t.active = a.active;
+      t.beside = 0;
       if (int rc = launch_kv_prefill_shared(t, d.split, s)) return rc;
     }
     t.b0 = d.many ? a.beginnings : 0;
     t.batch = a.beginnings + a.batch - t.b0;
     t.part = const_cast<float *>(a.side[1].part);
+    t.active = a.active + 1;
+    t.beside = d.many;
     if (int rc = c.head_dim == 64 ? attend_types<64>(t, d.mb, dev, s) : attend_types<128>(t, d.mb, dev, s)) return rc;
     const int64_t warps = a.batch * a.q.max_q * query.q_heads, blocks = (warps + JOIN_WARPS - 1) / JOIN_WARPS;
     if (blocks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
