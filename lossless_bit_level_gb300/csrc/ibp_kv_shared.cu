@@ -255,31 +255,31 @@ __device__ __forceinline__ Where where_of(const ShareArgs &a, int which, const S
   return w;
 }
 
+// One row's result over parts k0 .. k1 - 1.
 template <int D>
-__device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const Where &w, int64_t row, int qh) {
+__device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const Where &w, int k0, int k1,
+                                           int64_t row, int qh) {
   constexpr int V = Half<D>::V;
   Half<D> h;
   for (int e = 0; e < V; ++e) h.y[e] = 0.0f;
   h.z = -INFINITY;
-  if (w.n == 0) return h;
+  if (k0 >= k1) return h;
   const Side &side = a.side[which];
   const int lane = threadIdx.x & 31;
   if (w.done) {
-    const int64_t at = row * a.q.q_heads + qh + which * a.side_rows, second = at + 2 * a.side_rows;
-    load_lane<V>(a.result + at * D + lane * V, h.y);
-    h.z = __ldcg(a.result_lse2 + at);
-    if (side.split) {
-      Half<D> k;
-      load_lane<V>(a.result + second * D + lane * V, k.y);
-      k.z = __ldcg(a.result_lse2 + second);
-      h = joined<D>(h, k);
+    for (int k = k0; k < k1; ++k) {
+      const int64_t at = row * a.q.q_heads + qh + (which + 2 * k) * a.side_rows;
+      Half<D> one;
+      load_lane<V>(a.result + at * D + lane * V, one.y);
+      one.z = __ldcg(a.result_lse2 + at);
+      h = joined<D>(h, one);
     }
     return h;
   }
   const int64_t stride = (int64_t)side.part_rows * (D + 4);
-  const int shift = side.split, n = w.n;
+  const int shift = side.split, n = k1;
   float top = NONE, topv = NONE, sum = 0.0f;
-  for (int k0 = 0; k0 < n; k0 += JOIN_PARTS) {
+  for (; k0 < n; k0 += JOIN_PARTS) {
     float4 st[JOIN_PARTS];
     float y[JOIN_PARTS][V];
 #pragma unroll
@@ -317,12 +317,14 @@ __device__ __forceinline__ Half<D> half_of(const ShareArgs &a, int which, const 
   return h;
 }
 
-// A warp to a row and query head: its two halves into one.
-template <int D, int DT>
+// A warp to a row and query head, or (SHARE) a block of them: its warps share the parts of the
+// beginning, of which a long one has dozens, the last takes the rest, and the first joins what
+// they found.
+template <int D, int DT, bool SHARE>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __grid_constant__ ShareArgs a) {
   constexpr int V = Half<D>::V;
-  const int lane = threadIdx.x & 31;
-  const int64_t x = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), each = a.q.max_q * a.q.q_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t x = SHARE ? blockIdx.x : (int64_t)blockIdx.x * JOIN_WARPS + warp, each = a.q.max_q * a.q.q_heads;
   const int i = (int)quotient(x, each), in = (int)(x - i * each), j = in / a.q.q_heads, qh = in % a.q.q_heads;
   // The spans are there before the kernels that go over them let this one start (loads pass the
   // first-level cache), so that only their results are waited for.
@@ -338,7 +340,25 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
   }
   grid_dependency_wait();
   if (!live) return;
-  const Half<D> h = joined<D>(half_of<D>(a, 0, first, row, qh), half_of<D>(a, 1, rest, row, qh));
+  Half<D> h;
+  if constexpr (SHARE) {
+    __shared__ float found[JOIN_WARPS][D], found_z[JOIN_WARPS];
+    h = half_of<D>(a, 0, first, first.n * warp / JOIN_WARPS, first.n * (warp + 1) / JOIN_WARPS, row, qh);
+    if (warp == JOIN_WARPS - 1) h = joined<D>(h, half_of<D>(a, 1, rest, 0, rest.n, row, qh));
+    for (int e = 0; e < V; ++e) found[warp][lane * V + e] = h.y[e];
+    if (lane == 0) found_z[warp] = h.z;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int k = 1; k < JOIN_WARPS; ++k) {
+      Half<D> other;
+      for (int e = 0; e < V; ++e) other.y[e] = found[k][lane * V + e];
+      other.z = found_z[k];
+      h = joined<D>(h, other);
+    }
+  } else {
+    h = joined<D>(half_of<D>(a, 0, first, 0, first.n, row, qh), half_of<D>(a, 1, rest, 0, rest.n, row, qh));
+  }
   char *out = static_cast<char *>(a.q.out) +
               2 * (row * a.q.out_row_stride + qh * a.q.out_head_stride + lane * V);
   if constexpr (V == 4)
@@ -366,6 +386,14 @@ int attend_types(const AttentionArgs &a, int mb, const DeviceInfo &dev, cudaStre
                                  : attend_rows<D, IBP_KV_INT8, IBP_FP16>(a, mb, dev, s);
   return a.q.dtype == IBP_BF16 ? attend_rows<D, IBP_KV_E4M3, IBP_BF16>(a, mb, dev, s)
                                : attend_rows<D, IBP_KV_E4M3, IBP_FP16>(a, mb, dev, s);
+}
+
+template <int D>
+int launch_join(const ShareArgs &a, bool share, int64_t blocks, cudaStream_t s) {
+  const bool bf16 = a.q.dtype == IBP_BF16;
+  const auto join = share ? (bf16 ? kv_share_join_kernel<D, IBP_BF16, true> : kv_share_join_kernel<D, IBP_FP16, true>)
+                          : (bf16 ? kv_share_join_kernel<D, IBP_BF16, false> : kv_share_join_kernel<D, IBP_FP16, false>);
+  return launch_dependent(join, dim3((unsigned)blocks), dim3(32 * JOIN_WARPS), 0, s, a) == cudaSuccess ? IBP_OK : IBP_ERR_CUDA;
 }
 
 // CTAs of the kernel for few rows in segments of mb.
@@ -454,8 +482,6 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
   t.side = const_cast<float *>(a.result);
   t.side_lse2 = const_cast<float *>(a.result_lse2);
   t.side_rows = a.side_rows;
-  const auto join = c.head_dim == 64 ? (query.dtype == IBP_BF16 ? kv_share_join_kernel<64, IBP_BF16> : kv_share_join_kernel<64, IBP_FP16>)
-                                     : (query.dtype == IBP_BF16 ? kv_share_join_kernel<128, IBP_BF16> : kv_share_join_kernel<128, IBP_FP16>);
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += SHARE_SLAB) {
     a.batch = std::min(c.batch - a.b0, SHARE_SLAB);
     // of a slab's sequences, two at least have each shared beginning
@@ -476,10 +502,13 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
     t.active = a.active + 1;
     t.beside = d.many;
     if (int rc = c.head_dim == 64 ? attend_types<64>(t, d.mb, dev, s) : attend_types<128>(t, d.mb, dev, s)) return rc;
-    const int64_t warps = a.batch * a.q.max_q * query.q_heads, blocks = (warps + JOIN_WARPS - 1) / JOIN_WARPS;
+    // Several warps to a row while all rows are there at once (512 rows with 50 parts: 9 us, 4 with
+    // four warps to each; 4,480 with two: 5 and 11).
+    const int64_t rows = a.batch * a.q.max_q * query.q_heads;
+    const bool share = rows <= 4 * (int64_t)dev.sm_count;
+    const int64_t blocks = share ? rows : (rows + JOIN_WARPS - 1) / JOIN_WARPS;
     if (blocks > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
-    if (launch_dependent(join, dim3((unsigned)blocks), dim3(32 * JOIN_WARPS), 0, s, a) != cudaSuccess)
-      return IBP_ERR_CUDA;
+    if (int rc = c.head_dim == 64 ? launch_join<64>(a, share, blocks, s) : launch_join<128>(a, share, blocks, s)) return rc;
   }
   return IBP_OK;
 }
