@@ -608,6 +608,7 @@ class KVCache:
         stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
         self.batch, self.n_heads, self.page_tokens, self.head_dim = table.shape[0], h, p, d
         self.capacity = table.shape[1] * p
+        self.bounds_shape = (n, h, 2, d)
         self.struct = KVCacheStruct(_at(k_codes), _at(v_codes), _at(k_scales), _at(v_scales),
                                     _at(table), _at(lens), n, stride, table.shape[0],
                                     table.shape[1], h, p, d, _KV_CODES[k_codes.dtype])
@@ -743,39 +744,47 @@ def kv_read(cache: KVCache, k_out: torch.Tensor | None, v_out: torch.Tensor | No
 
 def _query(cache: KVCache, q: torch.Tensor, out: torch.Tensor | None, scale: float, cu_q, max_q,
            lse) -> KVQuery:
-    """ibp_kv_query of query rows, without weights."""
-    shape = q.shape
-    n, heads = shape[0], shape[1]
+    """ibp_kv_query of query rows, without weights. (It is on the path of every decoding step:
+    each attribute of a tensor is asked for once.)"""
+    shape, dtype = q.shape, q.dtype
+    heads = shape[1] if len(shape) == 3 else 0
     qr, qh = _head_rows(q, cache, heads, "q")
+    n = shape[0]
+    out_at = lse_at = None
     orow = oh = 0
     if out is not None:
-        orow, oh = _head_rows(out, cache, heads, "out")
-        if out.dtype != q.dtype or out.shape[0] != n:
+        if out.dtype != dtype or out.shape != shape:
             raise ValueError("out must have q's dtype and shape")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * heads or
-                            not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 tensor [n_rows, q_heads]")
+        orow, oh = _head_rows(out, cache, heads, "out")
+        out_at = out.data_ptr()
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.numel() != n * heads or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [n_rows, q_heads]")
+        lse_at = lse.data_ptr()
     if max_q is None:
         if cu_q is not None:
             raise ValueError("cu_q needs max_q, the most rows that a sequence has")
         max_q = n // max(cache.batch, 1)
-    return KVQuery(_at(q), _at(out), _at(lse), _int32(cu_q, cache.batch + 1, "cu_q"), None, None,
-                   n, max_q, 0, qr, qh, orow, oh, heads, dtype_code(q), scale, 1.0)
+    return KVQuery(q.data_ptr(), out_at, lse_at,
+                   None if cu_q is None else _int32(cu_q, cache.batch + 1, "cu_q"), None, None, n,
+                   max_q, 0, qr, qh, orow, oh, heads,
+                   _TORCH_DTYPES[dtype] if dtype in _TORCH_DTYPES else dtype_code(q), scale, 1.0)
 
 
 def _bounds(cache: KVCache, bounds: torch.Tensor):
-    n, h, _, d = cache.k_codes.shape
-    if bounds.dtype != torch.int8 or bounds.shape != (n, h, 2, d) or not bounds.is_contiguous():
-        raise ValueError(f"bounds must be contiguous int8 [{n}, {h}, 2, {d}]")
-    return _at(bounds)
+    if bounds.dtype != torch.int8 or bounds.shape != cache.bounds_shape or \
+            not bounds.is_contiguous():
+        raise ValueError(f"bounds must be contiguous int8 {list(cache.bounds_shape)}")
+    return bounds.data_ptr()
 
 
 def _columns(cache: KVCache, columns: torch.Tensor) -> int:
     """How many columns the lists hold."""
-    if columns.dim() != 3 or columns.dtype != torch.int32 or not columns.is_contiguous() or \
-            columns.shape[:2] != (cache.batch, cache.n_heads):
+    shape = columns.shape
+    if len(shape) != 3 or shape[0] != cache.batch or shape[1] != cache.n_heads or \
+            columns.dtype != torch.int32 or not columns.is_contiguous():
         raise ValueError("columns must be contiguous int32 [batch, n_heads, pages]")
-    return columns.shape[2]
+    return shape[2]
 
 
 def kv_attention_scratch_bytes(cache: KVCache, n_rows: int, max_q: int, q_heads: int,
