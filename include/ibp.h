@@ -438,9 +438,9 @@ int ibp_query_async(const uint32_t *d_row_bitmask, const uint32_t *d_row_bits, i
  * scales: [n_pages][n_heads] floats. Token t of sequence b lies in slot t % page_tokens of
  * page d_table[b*table_stride + t / page_tokens]; its value is code * scale. page_tokens
  * is 16, 32, 64 or 128, head_dim 64 or 128 (else IBP_ERR_UNSUPPORTED). A sequence holds at most table_cols *
- * page_tokens tokens (its capacity, at most 2^30). No two entries that name a page in
- * use may name the same one in a call that writes pages; entries past a sequence's last
- * page are never read.
+ * page_tokens tokens (its capacity, at most 2^30). A page that a call writes (append: those
+ * from a sequence's length on; evict: dst's) is named by one entry in use alone; others may
+ * be shared by sequences. Entries past a sequence's last page are never read.
  *
  * Quantisation of a page's tile whose largest finite magnitude is a: scale = a * (1 /
  * qmax) (qmax 127 for IBP_KV_INT8, 448 for IBP_KV_E4M3) held in [2^-100, 2^120], or 0

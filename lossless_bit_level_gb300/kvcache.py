@@ -12,11 +12,18 @@ were attended least:
                                       |  attend (adds up each token's probabilities)
                                       +--evict--> fewer pages --read--> rows again
 
+Rows may be rotated by their positions on the way in (``append`` and ``load`` with a
+``KVRotation``, their queries with them). Sequences that begin alike hold the pages of their
+beginning once (``share``) and ``attend`` goes over it once for all of them. With
+``track_bounds`` a step may attend over a few pages only, those that a cheap score finds for
+each sequence and head (``attend`` with ``pages``).
+
 The pages of all sequences come from one pool; the host knows every length, and what it
 sends goes through pinned memory, so no call waits for the GPU (``check`` does). The host's
 part of a call is Python that a graph cannot capture; the package's own calls can be. All
-arithmetic is in the library's kernels (``ibp_kv_append``,
-``ibp_kv_read``, ``ibp_kv_attention``, ``ibp_kv_evict``); this module only hands out pages
+arithmetic is in the library's kernels (``ibp_kv_append`` and ``ibp_kv_append_rotated``,
+``ibp_kv_read``, ``ibp_kv_attention``, ``.._shared`` and ``.._selected``, ``ibp_kv_bounds``,
+``ibp_kv_select``, ``ibp_kv_evict``); this module only hands out pages
 and buffers and orders launches on the current stream.
 """
 from __future__ import annotations
@@ -25,8 +32,10 @@ import contextlib
 
 import torch
 
-from . import KVCache, kv_append, kv_attention, kv_attention_scratch_bytes, kv_evict, \
-    kv_evict_scratch_bytes, kv_read
+from . import KVCache, KVRotation, kv_append, kv_append_rotated, kv_attention, \
+    kv_attention_scratch_bytes, kv_attention_selected, kv_attention_selected_scratch_bytes, \
+    kv_attention_shared, kv_attention_shared_scratch_bytes, kv_bounds, kv_evict, \
+    kv_evict_scratch_bytes, kv_read, kv_select, kv_select_scratch_bytes
 
 _CODES = {"int8": torch.int8}
 if hasattr(torch, "float8_e4m3fn"):
@@ -38,11 +47,13 @@ class DecodeCache:
 
     n_pages pages of page_tokens tokens are shared by the sequences, each of which holds at
     most max_tokens. ``track_weights`` keeps the probabilities that ``attend`` gave each
-    token, summed over steps with the factor ``decay``, for ``evict`` to go by."""
+    token, summed over steps with the factor ``decay``, for ``evict`` to go by.
+    ``track_bounds`` keeps the pages' bounds that ``attend`` selects pages by."""
 
     def __init__(self, n_pages: int, batch: int, n_heads: int, head_dim: int, max_tokens: int,
                  page_tokens: int = 64, code: str = "int8", track_weights: bool = True,
-                 decay: float = 1.0, device: torch.device | str = "cuda"):
+                 decay: float = 1.0, device: torch.device | str = "cuda",
+                 track_bounds: bool = False):
         if code not in _CODES:
             raise ValueError(f"code must be one of {sorted(_CODES)}")
         shape = (n_pages, n_heads, page_tokens, head_dim)
@@ -63,6 +74,9 @@ class DecodeCache:
         if track_weights:
             self.weights = zeros(batch, n_heads, self.max_tokens, dtype=torch.float32)
             self._weights_after = torch.zeros_like(self.weights)
+        self.bounds = zeros(*self._handles[0].bounds_shape, dtype=torch.int8) if track_bounds else None
+        self._groups: list[tuple[int, int, int]] = []  # sequences [first, past) and their shared tokens
+        self._group_tensors = None
         self.status = zeros(1, dtype=torch.int32)
 
     @property
@@ -123,9 +137,15 @@ class DecodeCache:
             host = self._pinned([r + [-1] * (cols - len(r)) for r in rows])
             handle.table[:, :cols].copy_(host, non_blocking=True)
 
-    def append(self, k: torch.Tensor, v: torch.Tensor, counts=None) -> None:
+    def append(self, k: torch.Tensor, v: torch.Tensor, counts=None,
+               rotation: KVRotation | None = None, positions: torch.Tensor | None = None,
+               q: torch.Tensor | None = None) -> torch.Tensor | None:
         """Rows [n, heads, head_dim] behind what the sequences hold: counts[b] of them to
-        sequence b, one sequence after another (None: the same number each)."""
+        sequence b, one sequence after another (None: the same number each). With ``rotation``
+        keys are rotated on the way, by ``positions`` (int32 [n, axes]; None: the tokens'
+        numbers), and so are the query rows ``q`` of the same tokens, which are returned."""
+        if rotation is None and (q is not None or positions is not None):
+            raise ValueError("positions and q go with a rotation")
         each, counts = counts, self._counts(counts, k.shape[0])
         after = [n + c for n, c in zip(self.lengths, counts)]
         if max(after, default=0) > self.max_tokens:
@@ -136,15 +156,71 @@ class DecodeCache:
             pages = [p + q for p, q in zip(self._pages, new)]
             if any(need):
                 self._write_table(now, pages)
-            kv_append(now, k, v, cu=None if each is None else self._offsets(counts),
-                      new_lens=later.lens, status=self.status)
+            cu = None if each is None else self._offsets(counts)
+            turned = None
+            if rotation is None:
+                kv_append(now, k, v, cu=cu, new_lens=later.lens, status=self.status)
+            else:
+                if q is not None:
+                    turned = torch.empty_like(q, memory_format=torch.contiguous_format)
+                kv_append_rotated(now, k, v, rotation, positions=positions, q=q, q_out=turned, cu=cu,
+                                  new_lens=later.lens, status=self.status)
+            before = now.lens.clone() if self.bounds is not None else None
             now.lens.copy_(later.lens)
         self.lengths, self._pages = after, pages
+        if before is not None:
+            kv_bounds(now, self.bounds, begin=before, status=self.status)
+        return turned
 
-    def load(self, k_store, v_store, counts=None) -> None:
+    def share(self, src: int, sequences) -> int:
+        """Let ``sequences``, which are empty and follow src one after another, begin with the
+        whole pages that sequence src holds; returns how many tokens that is (what src holds
+        behind them they do not get). ``attend`` goes over these pages once for all of them."""
+        wanted = list(sequences)
+        if wanted != list(range(src + 1, src + 1 + len(wanted))) or not wanted or \
+                not 0 <= src < len(self.lengths) or wanted[-1] >= len(self.lengths):
+            raise ValueError("sequences that share follow the first of them one after another")
+        if any(self.lengths[b] for b in wanted):
+            raise ValueError("a sequence that takes shared pages is empty")
+        if any(first < wanted[-1] + 1 and src < past for first, past, _ in self._groups):
+            raise ValueError("a sequence shares one beginning")
+        tokens = self.lengths[src] // self.page_tokens * self.page_tokens
+        begin = self._pages[src][:tokens // self.page_tokens]
+        if not begin:
+            return 0
+        pages = list(self._pages)
+        for b in wanted:
+            pages[b] = list(begin)
+        now = self.cache
+        self._write_table(now, pages)
+        now.lens[wanted[0]:wanted[-1] + 1] = tokens  # (a fill: nothing is sent)
+        for b in wanted:
+            self.lengths[b] = tokens
+        self._pages = pages
+        self._groups = sorted(self._groups + [(src, wanted[-1] + 1, tokens)])
+        self._group_tensors = None
+        return tokens
+
+    def _shared(self):
+        """Offsets of the groups and their shared tokens, on the device; sequences between groups
+        are groups that share nothing."""
+        if self._group_tensors is None:
+            offsets, prefix = [0], []
+            for first, past, tokens in self._groups:
+                if first > offsets[-1]:
+                    offsets.append(first)
+                    prefix.append(0)
+                offsets.append(past)
+                prefix.append(tokens)
+            self._group_tensors = tuple(self._pinned(x).to(self.device, non_blocking=True)
+                                        for x in (offsets, prefix))
+        return self._group_tensors
+
+    def load(self, k_store, v_store, counts=None, rotation: KVRotation | None = None,
+             positions: torch.Tensor | None = None) -> None:
         """Append the rows of two compressed tensors (``offload.CompressedTensor``, a row a
         token of n_heads * head_dim 16- or 32-bit floats): decoded on the GPU, then
-        quantised into the pages."""
+        quantised into the pages, with ``rotation`` rotated before that."""
         from . import BF16, FP16, FP32
         kinds = {BF16: torch.bfloat16, FP16: torch.float16, FP32: torch.float32}
         rows = []
@@ -153,19 +229,44 @@ class DecodeCache:
             store.decompress_into(out)
             rows.append(out.view(kinds[store.dtype]).view(store.n_rows, self.cache.n_heads,
                                                           self.cache.head_dim))
-        self.append(rows[0], rows[1], counts)
+        self.append(rows[0], rows[1], counts, rotation=rotation, positions=positions)
 
     def attend(self, q: torch.Tensor, scale: float, counts=None,
-               lse: torch.Tensor | None = None) -> torch.Tensor:
+               lse: torch.Tensor | None = None, pages: int | None = None) -> torch.Tensor:
         """softmax(scale * q k) v of query rows [n, q_heads, head_dim], counts[b] of them the
-        last tokens of sequence b. Adds their probabilities to the tokens' weights."""
+        last tokens of sequence b. Adds their probabilities to the tokens' weights. With
+        ``pages`` a sequence and head attends over so many of its pages: the first, the rows'
+        own, and those of the highest scores (needs ``track_bounds``; adds no weights).
+        Without weights to add to, beginnings that sequences share are gone over once."""
         each, counts = counts, self._counts(counts, q.shape[0])
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         most, track = max(counts, default=0), self.weights is not None
+        cu = None if each is None else self._offsets(counts)
+        if pages is not None:
+            if self.bounds is None:
+                raise RuntimeError("pages are selected by bounds, which this cache does not track")
+            columns = torch.empty((len(self.lengths), self.cache.n_heads, pages), dtype=torch.int32,
+                                  device=self.device)
+            kv_select(self.cache, self.bounds, q, columns,
+                      self._workspace(kv_select_scratch_bytes(self.cache)), cu_q=cu, max_q=most,
+                      status=self.status)
+            scratch = self._workspace(kv_attention_selected_scratch_bytes(
+                self.cache, q.shape[0], most, q.shape[1], pages))
+            kv_attention_selected(self.cache, columns, q, out, scale, scratch, cu_q=cu, max_q=most,
+                                  lse=lse, status=self.status)
+            return out
+        if self._groups and not track:
+            offsets, prefix = self._shared()
+            rows = max(sum(counts[first:past]) for first, past, _ in self._groups)
+            scratch = self._workspace(kv_attention_shared_scratch_bytes(
+                self.cache, q.shape[0], most, q.shape[1], prefix.numel(), rows))
+            kv_attention_shared(self.cache, q, out, scale, scratch, offsets, prefix, rows, cu_q=cu,
+                                max_q=most, lse=lse, status=self.status)
+            return out
         scratch = self._workspace(kv_attention_scratch_bytes(
             self.cache, q.shape[0], most, q.shape[1], track))
         kv_attention(self.cache, q, out, scale, scratch,
-                     cu_q=None if each is None else self._offsets(counts), max_q=most, lse=lse,
+                     cu_q=cu, max_q=most, lse=lse,
                      weights=self.weights, weights_in=self.weights, decay=self.decay,
                      status=self.status)
         return out
@@ -184,11 +285,13 @@ class DecodeCache:
             into = self._weights_after if budget <= self.max_tokens else None
             kv_evict(now, self.weights, budget, recent, later, scratch, new_weights=into,
                      status=self.status)
-        for p in self._pages:
-            self._free.extend(p)
+        self._free.extend(dict.fromkeys(p for of_one in self._pages for p in of_one))  # shared ones once
+        self._groups, self._group_tensors = [], None  # every sequence has its own now
         if into is not None:
             self.weights, self._weights_after = into, self.weights
         self._handles, self._pages, self.lengths = [later, now], pages, kept
+        if self.bounds is not None:
+            kv_bounds(later, self.bounds, status=self.status)
 
     def read(self, dtype: torch.dtype = torch.bfloat16) -> tuple[torch.Tensor, torch.Tensor]:
         """Every sequence's tokens as rows [batch, longest, heads, head_dim] (zeros past the
