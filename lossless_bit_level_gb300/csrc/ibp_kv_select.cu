@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, ONE ? 5 : 4) kv_score_kernel(co
     if (x >= end) return t;
     const int at = find_sequence(prefix, a.batch, x);
     const uint32_t chunks = (uint32_t)(prefix[at + 1] - prefix[at]) / (uint32_t)c.n_heads;
-    const uint32_t in = (uint32_t)(x - prefix[at]);  // (below 2^30 / 16 pages * 4096 heads / 64)
+    const uint32_t in = (uint32_t)(x - prefix[at]);  // (one float of scratch a page, so far below 2^32)
     t.b = a.b0 + at;
     t.head = (int)(in / chunks);
     t.col = (int)(in % chunks) * CHUNK + warp * 16 + g;

@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
       // no more than tiles; of one beginning, a whole number to each head and block of rows, so
       // that none goes over two (which takes it as long as four tiles more)
       mine = (int)min((int64_t)mine, a.total[0]);
-      if (beginnings == 1 && mine > segments) mine = min((mine + segments - 1) / segments, sms / segments) * segments;
+      const int most = rest == 0 ? sms : sms - 1;
+      if (beginnings == 1 && mine > segments) mine = min((mine + segments - 1) / segments, most / segments) * segments;
       a.active[0] = max(mine, 1);
       a.active[1] = max(a.side[1].ctas / sms * (sms - mine), 1);
     }
