@@ -598,7 +598,7 @@ int ibp_kv_bounds(const ibp_kv_cache *cache, int8_t *d_bounds, const int32_t *d_
  * Of `query`, q, d_cu, n_rows, max_q, q_row_stride, q_head_stride, q_heads and dtype count.
  * pages holds column 0 and the rows' own: at least (max_q - 1 + page_tokens - 1) /
  * page_tokens + 2 (IBP_ERR_ARG). d_scratch: what ibp_kv_select_scratch_bytes gives (16-byte
- * aligned), overwritten. Asynchronous on s, capturable, two launches. */
+ * aligned), overwritten. Asynchronous on s, capturable, one launch or two. */
 int ibp_kv_select_scratch_bytes(const ibp_kv_cache *cache, size_t *bytes);
 int ibp_kv_select(const ibp_kv_cache *cache, const int8_t *d_bounds, const ibp_kv_query *query,
                   int64_t pages, int32_t *d_columns, void *d_scratch, size_t scratch_bytes,

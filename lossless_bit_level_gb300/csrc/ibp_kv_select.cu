@@ -202,6 +202,126 @@ __device__ __forceinline__ uint32_t whole_pair(uint32_t u) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Rows r0 .. r0 + some - 1 of a sequence and K/V head (in whole tiles of 8) in whole numbers, as the
+// lanes hold the second operand: every warp takes some.
+template <int D, int DT, bool ONE, int WARPS>
+__device__ __forceinline__ void rows_in_whole_numbers(const SelectArgs &a, int64_t row0, int head, int r0, int some,
+                                                      int tiles, uint2 (*rows)[D / 8][32], float *unit) {
+  constexpr int STEPS = D / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.q.q_heads / a.c.n_heads;
+          constexpr int BATCH = ONE ? 2 : 4;  // rows of a warp that are asked for at a time
+          for (int r1 = warp; r1 < 8 * tiles; r1 += BATCH * WARPS) {
+            uint2 asked[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              const int r = r1 + k * WARPS, rr = r0 + r;
+              asked[k] = make_uint2(0u, 0u);
+              if (r < some && lane < D / 4)
+                asked[k] = __ldg(reinterpret_cast<const uint2 *>(
+                    static_cast<const char *>(a.q.q) + 2 * ((row0 + rr / group) * a.q.q_row_stride +
+                                                            (head * group + rr % group) * a.q.q_head_stride + 4 * lane)));
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+              const int r = r1 + k * WARPS;
+              if (r >= 8 * tiles) break;
+              float q[4];
+              const uint32_t words[2] = {asked[k].x, asked[k].y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if constexpr (DT == IBP_BF16) {
+                  q[2 * i] = __uint_as_float(words[i] << 16);
+                  q[2 * i + 1] = __uint_as_float(words[i] & 0xFFFF0000u);
+                } else {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&words[i]));
+                  q[2 * i] = f.x;
+                  q[2 * i + 1] = f.y;
+                }
+              }
+              float most = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
+              most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));
+              const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
+              const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
+              if (lane == 0)
+                unit[r] = r < some ? __uint_as_float((uint32_t)(127 - 6 + e) << 23) : __uint_as_float(0x7FFFFFFFu);
+              uint32_t w[2][2];
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                float y[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float z = rintf(q[i + k] * up);
+                  y[k] = z == z ? fminf(fmaxf(z, -127.0f), 127.0f) : 0.0f;
+                }
+                w[0][i / 2] = pack2<IBP_FP16>(fminf(y[0], 0.0f), fminf(y[1], 0.0f));
+                w[1][i / 2] = pack2<IBP_FP16>(fmaxf(y[0], 0.0f), fmaxf(y[1], 0.0f));
+              }
+              if (lane < D / 4) {  // elements 4 lane ..: bytes 16 t + 4 e .. of 64 j
+                const int j = lane / 16, t = lane % 16 / 4, step = 4 * j + lane % 4;
+                rows[r / 8][step][(r % 8) * 4 + t] = make_uint2(w[0][0], w[0][1]);
+                rows[r / 8][STEPS / 2 + step][(r % 8) * 4 + t] = make_uint2(w[1][0], w[1][1]);
+              }
+            }
+          }
+}
+
+// 16 pages' bounds: lane (g, t) holds bytes 16 t .. of pages g and g + 8 (page < 0: none).
+template <int D>
+struct Pages16 {
+  static constexpr int K = 2 * D, STEPS = K / 16;
+  float scale[2];
+  bool there[2];
+  uint4 raw[2][K / 64];
+  __device__ __forceinline__ void load(const SelectArgs &a, const int *page, int head) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      there[h] = page[h] >= 0;
+      const int64_t tile = (int64_t)page[h] * a.c.n_heads + head;
+      scale[h] = there[h] ? __ldg(a.c.k_scales + tile) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < K / 64; ++j)
+        raw[h][j] = there[h] ? __ldg(reinterpret_cast<const uint4 *>(a.bounds + tile * K) + (threadIdx.x & 3) + 4 * j)
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void operand(int step, uint32_t *m) const {  // 16 bytes of both, as fp16
+    const int j = step / 4, e = step % 4;
+    const uint4 r = raw[0][j], q = raw[1][j];
+    const uint32_t u = (e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w) ^ 0x80808080u,
+                   v = (e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w) ^ 0x80808080u;
+    m[0] = whole_pair<0>(u);
+    m[1] = whole_pair<0>(v);
+    m[2] = whole_pair<1>(u);
+    m[3] = whole_pair<1>(v);
+  }
+  // the largest of best and the tiles' scores before the pages' scales
+  template <bool ONE>
+  __device__ __forceinline__ void against(float *best, const uint32_t (*m)[4], int tiles, const uint2 (*rows)[STEPS][32],
+                                          const float *unit) const {
+    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    for (int i = 0; i < tiles; ++i) {
+      float even[4] = {}, odd[4] = {};  // two chains: a chain waits for each of its own
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const uint2 y = rows[i][k][lane];
+        uint32_t w[4];
+        if constexpr (ONE) operand(k, w);
+        const uint32_t *x = ONE ? w : m[ONE ? 0 : k];
+        mma_f16(k & 1 ? odd : even, x[0], x[1], x[2], x[3], y.x, y.y);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        best[k >> 1] = fmaxf(best[k >> 1], (even[k] + odd[k]) * unit[8 * i + 2 * t4 + (k & 1)]);
+    }
+  }
+  // over the lanes of a page, times its scale
+  __device__ __forceinline__ float score(float best, int h) const {
+    best = fmaxf(best, __shfl_xor_sync(FULL, best, 1));
+    best = fmaxf(best, __shfl_xor_sync(FULL, best, 2));
+    return there[h] ? __fmul_rn(best, scale[h]) : -INFINITY;
+  }
+};
+
 // score = scale_k max_r 2^(e_r - 6) sum_d max(n_rd least_d, n_rd largest_d), with the query row
 // r in whole numbers n up to 127 of 2^(e - 6). The inner sum is min(n, 0) . least +
 // max(n, 0) . largest: a matrix product of fp16 numbers whose partial sums are whole and
@@ -260,118 +380,30 @@ __global__ void __launch_bounds__(SCORE_THREADS, ONE ? 5 : 4) kv_score_kernel(co
     const Item t = next;
     const int b = t.b, head = t.head, all = t.n * group, col = t.col, pages = t.pages;
     const int64_t row0 = t.row0;
-    // this warp's 16 pages: lane (g, t) holds bytes 16 t .. of pages g and g + 8
-    int64_t tile[2];
-    float scale[2];
-    uint4 raw[2][K / 64];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      tile[h] = t.page[h] < 0 ? -1 : (int64_t)t.page[h] * c.n_heads + head;
-      scale[h] = t.page[h] < 0 ? 0.0f : __ldg(c.k_scales + tile[h]);
-#pragma unroll
-      for (int j = 0; j < K / 64; ++j)
-        raw[h][j] = tile[h] < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                : __ldg(reinterpret_cast<const uint4 *>(a.bounds + tile[h] * K) + t4 + 4 * j);
-    }
+    Pages16<D> p;
+    p.load(a, t.page, head);
     next = look_up(x + 1);
-    auto operand = [&](int step, uint32_t *m) {  // 16 bytes of both pages, codes as fp16
-      const int j = step / 4, e = step % 4;
-      const uint4 r = raw[0][j], q = raw[1][j];
-      const uint32_t u = (e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w) ^ 0x80808080u,
-                     v = (e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w) ^ 0x80808080u;
-      m[0] = whole_pair<0>(u);
-      m[1] = whole_pair<0>(v);
-      m[2] = whole_pair<1>(u);
-      m[3] = whole_pair<1>(v);
-    };
     uint32_t m[ONE ? 1 : STEPS][4];
     if constexpr (!ONE)
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k) operand(k, m[k]);
+      for (int k = 0; k < STEPS; ++k) p.operand(k, m[k]);
     float best[2] = {-INFINITY, -INFINITY};
     for (int r0 = 0; r0 < all; r0 += HELD) {
       const int some = min(all - r0, HELD), tiles = (some + 7) / 8;
       if (ready_b != b || ready_head != head || all > HELD) {
         __syncthreads();  // the ones before have been read
-        constexpr int BATCH = ONE ? 2 : 4;  // rows of a warp that are asked for at a time
-        for (int r1 = warp; r1 < 8 * tiles; r1 += BATCH * SCORE_WARPS) {
-          uint2 asked[BATCH];
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = r1 + k * SCORE_WARPS, rr = r0 + r;
-            asked[k] = make_uint2(0u, 0u);
-            if (r < some && lane < D / 4)
-              asked[k] = __ldg(reinterpret_cast<const uint2 *>(
-                  static_cast<const char *>(a.q.q) + 2 * ((row0 + rr / group) * a.q.q_row_stride +
-                                                          (head * group + rr % group) * a.q.q_head_stride + 4 * lane)));
-          }
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = r1 + k * SCORE_WARPS;
-            if (r >= 8 * tiles) break;
-            float q[4];
-            const uint32_t words[2] = {asked[k].x, asked[k].y};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if constexpr (DT == IBP_BF16) {
-                q[2 * i] = __uint_as_float(words[i] << 16);
-                q[2 * i + 1] = __uint_as_float(words[i] & 0xFFFF0000u);
-              } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&words[i]));
-                q[2 * i] = f.x;
-                q[2 * i + 1] = f.y;
-              }
-            }
-            float most = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
-            most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));
-            const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
-            const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
-            if (lane == 0)
-              unit[r] = r < some ? __uint_as_float((uint32_t)(127 - 6 + e) << 23) : __uint_as_float(0x7FFFFFFFu);
-            uint32_t w[2][2];
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              float y[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float z = rintf(q[i + k] * up);
-                y[k] = z == z ? fminf(fmaxf(z, -127.0f), 127.0f) : 0.0f;
-              }
-              w[0][i / 2] = pack2<IBP_FP16>(fminf(y[0], 0.0f), fminf(y[1], 0.0f));
-              w[1][i / 2] = pack2<IBP_FP16>(fmaxf(y[0], 0.0f), fmaxf(y[1], 0.0f));
-            }
-            if (lane < D / 4) {  // elements 4 lane ..: bytes 16 t + 4 e .. of 64 j
-              const int j = lane / 16, t = lane % 16 / 4, step = 4 * j + lane % 4;
-              rows[r / 8][step][(r % 8) * 4 + t] = make_uint2(w[0][0], w[0][1]);
-              rows[r / 8][STEPS / 2 + step][(r % 8) * 4 + t] = make_uint2(w[1][0], w[1][1]);
-            }
-          }
-        }
+        rows_in_whole_numbers<D, DT, ONE, SCORE_WARPS>(a, row0, head, r0, some, tiles, rows, unit);
         __syncthreads();
         ready_b = b;
         ready_head = head;
       }
-      for (int i = 0; i < tiles; ++i) {
-        float even[4] = {}, odd[4] = {};  // two chains: a chain waits for each of its own
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-          const uint2 y = rows[i][k][lane];
-          uint32_t *w = m[ONE ? 0 : k];
-          if constexpr (ONE) operand(k, w);
-          mma_f16(k & 1 ? odd : even, w[0], w[1], w[2], w[3], y.x, y.y);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          best[k >> 1] = fmaxf(best[k >> 1], (even[k] + odd[k]) * unit[8 * i + 2 * t4 + (k & 1)]);
-      }
+      p.template against<ONE>(best, m, tiles, rows, unit);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      best[h] = fmaxf(best[h], __shfl_xor_sync(FULL, best[h], 1));
-      best[h] = fmaxf(best[h], __shfl_xor_sync(FULL, best[h], 2));
+      const float score = p.score(best[h], h);
       if (t4 == 0 && col + 8 * h < pages)
-        a.scores[((int64_t)b * c.n_heads + head) * c.table_cols + col + 8 * h] =
-            tile[h] < 0 ? -INFINITY : __fmul_rn(best[h], scale[h]);
+        a.scores[((int64_t)b * c.n_heads + head) * c.table_cols + col + 8 * h] = score;
     }
   }
 }
@@ -394,51 +426,30 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // need-th largest key is found from the top bits of the keys' own range down, 8 at a time (of
 // floats of similar sizes the uppermost bits are the same: counting by those would queue at a
 // few counters), then the keys above it and the first of those equal to it are listed in order.
-__global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_constant__ SelectArgs a) {
-  __shared__ uint32_t keys[KEPT_KEYS];
-  __shared__ uint32_t hist[BINS], warp_sum[PICK_WARPS];
-  __shared__ uint32_t found[2];
-  __shared__ uint2 warp_count[PICK_WARPS];
-  const ibp_kv_cache &c = a.c;
-  const int b = a.b0 + blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
+struct Picking {
+  uint32_t hist[BINS], warp_sum[PICK_WARPS], found[2];
+  uint2 warp_count[PICK_WARPS];
+};
+// key_at(i): of column 1 + i, there for all threads of the block.
+template <typename Keys>
+__device__ __forceinline__ void pick_columns(int32_t *out, int open, int room, Picking &sm, Keys key_at) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t list = (int64_t)b * c.n_heads + head;
-  int32_t *out = a.columns + list * a.pages;
-  int64_t row0;
-  const int n = rows_at(a, b, &row0, nullptr), len = n > 0 ? kv_len(c, b, nullptr) : 0;
-  const PageList p = page_list(c, len, n, a.pages);
-  grid_dependency_wait();
-  for (int i = p.count + tid; i < a.pages; i += PICK_THREADS) out[i] = -1;
-  if (p.count == p.all) {
-    for (int i = tid; i < p.all; i += PICK_THREADS) out[i] = i;
-    return;
-  }
-  // p.all > pages >= first + own: columns 1 .. first_own - 1 compete
-  const int own = p.all - p.first_own, room = a.pages - own - 1, open = p.first_own - 1;
-  if (tid == 0) out[0] = 0;
-  for (int i = tid; i < own; i += PICK_THREADS) out[1 + room + i] = p.first_own + i;
-  const float *scores = a.scores + list * c.table_cols + 1;
-  const bool held = open <= KEPT_KEYS;
-  if (held)
-    for (int i = tid; i < open; i += PICK_THREADS) keys[i] = score_key(__ldcg(scores + i));
-  auto key_at = [&](int i) { return held ? keys[i] : score_key(__ldcg(scores + i)); };
   // A key to a thread while there are few: its rank is counted (62 keys 4.5 us, 5.4 by their bits;
   // 217 keys 6.7 and 5.7).
   if (open <= 128) {
-    __syncthreads();
-    const uint32_t mine = tid < open ? keys[tid] : 0u;
+    const uint32_t mine = tid < open ? key_at(tid) : 0u;
     int rank = 0;
 #pragma unroll 8
     for (int i = 0; i < open; ++i) {
-      const uint32_t other = keys[i];
+      const uint32_t other = key_at(i);
       rank += other > mine || (other == mine && i < tid);
     }
     const bool chosen = tid < open && rank < room;
     const unsigned votes = __ballot_sync(FULL, chosen);
-    if (lane == 0) warp_sum[warp] = __popc(votes);
+    if (lane == 0) sm.warp_sum[warp] = __popc(votes);
     __syncthreads();
     int to = 1 + __popc(votes & ((1u << lane) - 1u));
-    for (int k = 0; k < warp; ++k) to += warp_sum[k];
+    for (int k = 0; k < warp; ++k) to += sm.warp_sum[k];
     if (chosen) out[to] = 1 + tid;
     return;
   }
@@ -451,49 +462,49 @@ __global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_cons
   }
   least = __reduce_min_sync(FULL, least);
   most = __reduce_max_sync(FULL, most);
-  if (lane == 0) warp_count[warp] = make_uint2(least, most);
+  if (lane == 0) sm.warp_count[warp] = make_uint2(least, most);
   __syncthreads();
   for (int k = 0; k < PICK_WARPS; ++k) {
-    least = min(least, warp_count[k].x);
-    most = max(most, warp_count[k].y);
+    least = min(least, sm.warp_count[k].x);
+    most = max(most, sm.warp_count[k].y);
   }
   __syncthreads();  // (its places are used again)
   uint32_t need = (uint32_t)room, value = 0;  // of key - least, from its top bits down
   for (int top = 32 - __clz((int)(most - least)), shift; room > 0 && top > 0; top = shift) {
     shift = max(top - BIN_BITS, 0);
-    for (int i = tid; i < BINS; i += PICK_THREADS) hist[i] = 0;
+    for (int i = tid; i < BINS; i += PICK_THREADS) sm.hist[i] = 0;
     __syncthreads();
     const uint32_t above = top >= 32 ? 0u : value >> top;
     for (int i = tid; i < open; i += PICK_THREADS) {
       const uint32_t d = key_at(i) - least;
-      if ((top >= 32 ? 0u : d >> top) == above) atomicAdd(&hist[(d >> shift) & (BINS - 1)], 1u);
+      if ((top >= 32 ? 0u : d >> top) == above) atomicAdd(&sm.hist[(d >> shift) & (BINS - 1)], 1u);
     }
     __syncthreads();
     // bins from the top, a few to a thread
     constexpr int EACH = BINS / PICK_THREADS;
     uint32_t mine[EACH], sum = 0;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) sum += mine[e] = hist[BINS - 1 - (EACH * tid + e)];
+    for (int e = 0; e < EACH; ++e) sum += mine[e] = sm.hist[BINS - 1 - (EACH * tid + e)];
     uint32_t run = sum;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(FULL, run, o);
       if (lane >= o) run += y;
     }
-    if (lane == 31) warp_sum[warp] = run;
+    if (lane == 31) sm.warp_sum[warp] = run;
     __syncthreads();
     uint32_t before = run - sum;
-    for (int k = 0; k < warp; ++k) before += warp_sum[k];
+    for (int k = 0; k < warp; ++k) before += sm.warp_sum[k];
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       if (before < need && before + mine[e] >= need) {
-        found[0] = (uint32_t)(BINS - 1 - (EACH * tid + e));
-        found[1] = need - before;
+        sm.found[0] = (uint32_t)(BINS - 1 - (EACH * tid + e));
+        sm.found[1] = need - before;
       }
       before += mine[e];
     }
     __syncthreads();
-    value = (shift + BIN_BITS >= 32 ? 0u : value >> (shift + BIN_BITS) << (shift + BIN_BITS)) | found[0] << shift;
-    need = found[1];
+    value = (shift + BIN_BITS >= 32 ? 0u : value >> (shift + BIN_BITS) << (shift + BIN_BITS)) | sm.found[0] << shift;
+    need = sm.found[1];
   }
   const uint32_t prefix = least + value;
   // each warp a stretch of columns: what lies above the threshold and at it
@@ -505,12 +516,12 @@ __global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_cons
     gt += __popc(__ballot_sync(FULL, t0 + lane < last && key > prefix));
     eq += __popc(__ballot_sync(FULL, t0 + lane < last && key == prefix));
   }
-  if (lane == 0) warp_count[warp] = make_uint2(gt, eq);
+  if (lane == 0) sm.warp_count[warp] = make_uint2(gt, eq);
   __syncthreads();
   uint32_t gt_before = 0, eq_before = 0;
   for (int k = 0; k < warp; ++k) {
-    gt_before += warp_count[k].x;
-    eq_before += warp_count[k].y;
+    gt_before += sm.warp_count[k].x;
+    eq_before += sm.warp_count[k].y;
   }
   if (room == 0) return;
   const uint32_t lower = (1u << lane) - 1u;
@@ -526,6 +537,112 @@ __global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_cons
     gt_before += __popc(above_it);
     eq_before += __popc(at_it);
   }
+}
+
+// What needs no score: all columns of a list that holds them, the first and the rows' own of
+// another. Whether others compete.
+__device__ __forceinline__ bool sure_columns(int32_t *out, const PageList &p, int pages) {
+  const int tid = threadIdx.x;
+  for (int i = p.count + tid; i < pages; i += PICK_THREADS) out[i] = -1;
+  if (p.count == p.all) {
+    for (int i = tid; i < p.all; i += PICK_THREADS) out[i] = i;
+    return false;
+  }
+  // p.all > pages >= first + own: columns 1 .. first_own - 1 compete
+  const int own = p.all - p.first_own;
+  if (tid == 0) out[0] = 0;
+  for (int i = tid; i < own; i += PICK_THREADS) out[pages - own + i] = p.first_own + i;
+  return true;
+}
+
+__global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_constant__ SelectArgs a) {
+  __shared__ uint32_t keys[KEPT_KEYS];
+  __shared__ Picking sm;
+  const ibp_kv_cache &c = a.c;
+  const int b = a.b0 + blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads, tid = threadIdx.x;
+  const int64_t list = (int64_t)b * c.n_heads + head;
+  int32_t *out = a.columns + list * a.pages;
+  int64_t row0;
+  const int n = rows_at(a, b, &row0, nullptr), len = n > 0 ? kv_len(c, b, nullptr) : 0;
+  const PageList p = page_list(c, len, n, a.pages);
+  grid_dependency_wait();
+  if (!sure_columns(out, p, a.pages)) return;
+  const int room = a.pages - (p.all - p.first_own) - 1, open = p.first_own - 1;
+  const float *scores = a.scores + list * c.table_cols + 1;
+  const bool held = open <= KEPT_KEYS;
+  if (held)
+    for (int i = tid; i < open; i += PICK_THREADS) keys[i] = score_key(__ldcg(scores + i));
+  __syncthreads();
+  pick_columns(out, open, room, sm, [&](int i) { return held ? keys[i] : score_key(__ldcg(scores + i)); });
+}
+
+// Both for lists of few pages, a block to a (sequence, head): one launch, and no score leaves the
+// SM. Few long lists need more blocks than there are lists.
+constexpr int SHORT_LIST = 1024;
+template <int D, int DT, bool ONE>
+__global__ void __launch_bounds__(PICK_THREADS, 2) kv_select_short_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int STEPS = D / 8, HELD = ONE ? 8 : ROWS;
+  __shared__ uint2 rows[HELD / 8][STEPS][32];
+  __shared__ float unit[HELD];
+  __shared__ uint32_t keys[SHORT_LIST];
+  __shared__ Picking sm;
+  const ibp_kv_cache &c = a.c;
+  const int b = a.b0 + blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  int32_t *status = head == 0 && threadIdx.x == 0 ? a.status : nullptr;
+  int32_t *out = a.columns + ((int64_t)b * c.n_heads + head) * a.pages;
+  int64_t row0;
+  const int n = rows_at(a, b, &row0, status), held = kv_len(c, b, status), all = n * (a.q.q_heads / c.n_heads);
+  const PageList p = page_list(c, n > 0 ? held : 0, n, a.pages);
+  if (!sure_columns(out, p, a.pages)) return;
+  const int room = a.pages - (p.all - p.first_own) - 1, open = p.first_own - 1;
+  const int passes = (p.all + 16 * PICK_WARPS - 1) / (16 * PICK_WARPS);
+  // page ids are looked up two passes ahead of their scores, bounds one
+  auto look_up = [&](int pass, int *page) {
+    const int col = (pass * PICK_WARPS + warp) * 16 + g;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      page[h] = col + 8 * h < p.all ? kv_page(c, b, col + 8 * h, t4 == 0 ? a.status : nullptr) : -1;
+  };
+  Pages16<D> q, next;
+  int page[2];
+  look_up(0, page);
+  next.load(a, page, head);
+  look_up(1, page);
+  for (int pass = 0; pass < passes; ++pass) {
+    const int col = (pass * PICK_WARPS + warp) * 16 + g;
+    q = next;
+    if constexpr (ONE) {  // (more rows need the registers)
+      next.load(a, page, head);
+      look_up(pass + 2, page);
+    }
+    uint32_t m[ONE ? 1 : STEPS][4];
+    if constexpr (!ONE)
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) q.operand(k, m[k]);
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int r0 = 0; r0 < all; r0 += HELD) {
+      const int some = min(all - r0, HELD), tiles = (some + 7) / 8;
+      if (pass == 0 || all > HELD) {
+        __syncthreads();  // the ones before have been read
+        rows_in_whole_numbers<D, DT, ONE, PICK_WARPS>(a, row0, head, r0, some, tiles, rows, unit);
+        __syncthreads();
+      }
+      q.template against<ONE>(best, m, tiles, rows, unit);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float score = q.score(best[h], h);
+      const int at = col + 8 * h - 1;
+      if (t4 == 0 && at >= 0 && at < open) keys[at] = score_key(score);
+    }
+    if constexpr (!ONE) {
+      next.load(a, page, head);
+      look_up(pass + 2, page);
+    }
+  }
+  __syncthreads();
+  pick_columns(out, open, room, sm, [&](int i) { return keys[i]; });
 }
 
 template <int D>
@@ -570,8 +687,23 @@ int launch_kv_select(const ibp_kv_cache &c, const int8_t *d_bounds, const ibp_kv
   a.pages = (int)pages;
   for (a.b0 = 0; a.b0 < c.batch; a.b0 += SLAB_BATCH) {
     a.batch = std::min(c.batch - a.b0, SLAB_BATCH);
-    const int64_t most = (int64_t)a.batch * c.n_heads * ((c.table_cols + CHUNK - 1) / CHUNK);
     const bool one = a.q.max_q * (query.q_heads / c.n_heads) <= 8, bf16 = query.dtype == IBP_BF16;
+    // One kernel where a block is done with its list in two passes of 128 pages, or where there are
+    // lists for all SMs (whole steps in one | two kernels: 256 lists of 64 pages 57 | 62 us, 192 of up
+    // to 219 42 | 48, 8 of 487 24.6 | 22.6).
+    const bool lists = (int64_t)a.batch * c.n_heads >= dev.sm_count;
+    if (c.table_cols <= 2 * 16 * PICK_WARPS || (lists && c.table_cols <= SHORT_LIST)) {
+      const auto kernel =
+          c.head_dim == 64
+              ? (one ? (bf16 ? kv_select_short_kernel<64, IBP_BF16, true> : kv_select_short_kernel<64, IBP_FP16, true>)
+                     : (bf16 ? kv_select_short_kernel<64, IBP_BF16, false> : kv_select_short_kernel<64, IBP_FP16, false>))
+              : (one ? (bf16 ? kv_select_short_kernel<128, IBP_BF16, true> : kv_select_short_kernel<128, IBP_FP16, true>)
+                     : (bf16 ? kv_select_short_kernel<128, IBP_BF16, false> : kv_select_short_kernel<128, IBP_FP16, false>));
+      kernel<<<(unsigned)(a.batch * c.n_heads), PICK_THREADS, 0, s>>>(a);
+      if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+      continue;
+    }
+    const int64_t most = (int64_t)a.batch * c.n_heads * ((c.table_cols + CHUNK - 1) / CHUNK);
     const auto kernel =
         c.head_dim == 64
             ? (one ? (bf16 ? kv_score_kernel<64, IBP_BF16, true> : kv_score_kernel<64, IBP_FP16, true>)

@@ -120,6 +120,21 @@ def test_bounds_selection_and_attention(lens, counts, q_heads, heads, dim, page,
     check_attention(want, q, counts, scale, columns, out, lse)
 
 
+@pytest.mark.parametrize("lens,counts,q_heads,heads,dim,page,code,dtype,pages", CASES)
+def test_selection_through_wide_tables(lens, counts, q_heads, heads, dim, page, code, dtype, pages):
+    """Tables of more than 1024 columns, most of them unused: scores and choice in two kernels."""
+    rng = np.random.default_rng(sum(lens) + dim + pages)
+    want = cache_of(rng, lens, heads, page, dim, code)
+    cache, status = pools(want, rng, cols=1100), status_word()
+    bounds = bounds_of(cache)
+    ibp.kv_bounds(cache, bounds, status=status)
+    check_bounds(want, cache, bounds, [0] * len(lens))
+    q = rounded(1.5 * rng.standard_normal((sum(counts), q_heads, dim)), dtype).cuda()
+    columns = select(cache, bounds, q, counts, pages, status=status)
+    assert int(status.item()) == 0
+    check_columns(want, q, counts, columns)
+
+
 def test_no_offsets_views_and_another_stream():
     rng = np.random.default_rng(2)
     want = cache_of(rng, [500, 260, 90], 2, 16, 64, "int8")
