@@ -391,6 +391,10 @@ __global__ void __launch_bounds__(MAX_THREADS)
     kv_rotate_kernel(const __grid_constant__ RotateArgs a) {
   __shared__ uint32_t sm[2][32];
   grid_launch_dependents();
+  if ((int64_t)blockIdx.x >= a.kv_blocks) {
+    turn_queries<D, DT>(a, (int64_t)blockIdx.x - a.kv_blocks);
+    return;
+  }
   const int T = blockDim.x;
   const int64_t item = blockIdx.x / (2 * a.kv_chunks);
   const int which = (int)(blockIdx.x % (2 * a.kv_chunks)), chunk = which >> 1;
@@ -556,7 +560,13 @@ int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const int64_t at_once = (int64_t)dev.sm_count * std::min(512 / threads, 32);
   a.kv_chunks = (int)std::min<int64_t>(std::max<int64_t>(at_once / (a.items * 2), (a.c.n_heads + 15) / 16),
                                        a.c.n_heads);
-  const int64_t blocks = a.items * 2 * a.kv_chunks, turns = query_blocks(a, TURN_THREADS, 4 * (int64_t)dev.sm_count);
+  a.kv_blocks = a.items * 2 * a.kv_chunks;
+  // Few queries along in the same launch; many in one of their own, which has half the registers
+  // (whole calls with the read back: 3,500 rows of 8 heads of 64, 7 MB, 22.6 us | 26.7 in a launch of
+  // their own; 5,556 rows of 28 heads of 128, 40 MB, 48 | 39).
+  const bool apart = a.q.q && a.r.n_rows * a.q.q_heads * D * (DT == IBP_FP32 ? 4 : 2) > (int64_t)(16 << 20);
+  const int64_t turns = query_blocks(a, apart ? TURN_THREADS : threads, (apart ? 4 : 16) * (int64_t)dev.sm_count);
+  const int64_t blocks = a.kv_blocks + (apart ? 0 : turns);
   if (blocks > 0x7FFFFFFF || turns > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;
   const auto kernel = int8 ? kv_rotate_kernel<D, DT, IBP_KV_INT8> : kv_rotate_kernel<D, DT, IBP_KV_E4M3>;
   const int smem = threads * Ahead<DT>::thread_bytes * Ahead<DT>::stages;
@@ -564,7 +574,7 @@ int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     return IBP_ERR_CUDA;
   kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
-  if (turns > 0 && launch_dependent(kv_turn_kernel<D, DT>, dim3((unsigned)turns), dim3(TURN_THREADS), 0, s, a) != cudaSuccess)
+  if (apart && turns > 0 && launch_dependent(kv_turn_kernel<D, DT>, dim3((unsigned)turns), dim3(TURN_THREADS), 0, s, a) != cudaSuccess)
     return IBP_ERR_CUDA;
   return IBP_OK;
 }
