@@ -624,7 +624,8 @@ int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *que
  * use may be named more than once in calls that only read). A prefix longer than a
  * sequence, or than what the first of its rows sees, counts as far as all rows of the group
  * see it. Each beginning is gone over once for all rows of its group, in slabs of 128
- * sequences. group_rows: the most query rows that the sequences of one group have together;
+ * sequences (unless the tables can hold no more than 64 MB of codes, or a sequence has more
+ * than 64 rows a K/V head: then the call is that of ibp_kv_attention). group_rows: the most query rows that the sequences of one group have together;
  * it chooses the kernel, no result depends on its being right. d_scratch: the size
  * ibp_kv_attention_shared_scratch_bytes gives for the same cache, query shapes and groups.
  * Asynchronous on s, capturable. */

@@ -562,7 +562,7 @@ int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
                                        a.c.n_heads);
   a.kv_blocks = a.items * 2 * a.kv_chunks;
   // Few queries along in the same launch; many in one of their own, which has half the registers
-  // (whole calls with the read back: 3,500 rows of 8 heads of 64, 7 MB, 22.6 us | 26.7 in a launch of
+  // (whole calls with the read back: 3,500 rows of 8 heads of 64, 7 MB, 24.6 us | 26.7 in a launch of
   // their own; 5,556 rows of 28 heads of 128, 40 MB, 48 | 39).
   const bool apart = a.q.q && a.r.n_rows * a.q.q_heads * D * (DT == IBP_FP32 ? 4 : 2) > (int64_t)(16 << 20);
   const int64_t turns = query_blocks(a, apart ? TURN_THREADS : threads, (apart ? 4 : 16) * (int64_t)dev.sm_count);

@@ -400,6 +400,8 @@ int launch_join(const ShareArgs &a, bool share, int64_t blocks, cudaStream_t s) 
 // CTAs of the kernel for few rows in segments of mb.
 int attend_ctas(int mb, const DeviceInfo &dev) { return std::min((mb == 8 ? 3 : 2) * dev.sm_count, MAX_CTAS); }
 
+constexpr int64_t ALONE_BYTES = int64_t(64) << 20;
+
 // How a call is divided: rows of a segment, and whether beginnings go to the kernel for many
 // rows or along with the rest. alone: not divided at all.
 struct Division {
@@ -411,7 +413,12 @@ Division division_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q
   const int64_t group = q_heads / c.n_heads, each = std::min(max_q, n_rows) * group;
   const int64_t all = std::max(std::min(group_rows, n_rows) * group, each);
   Division d;
-  d.alone = each > 64 || n_groups == 0;
+  // Not divided: many rows of every sequence, which arithmetic bounds; and where all that the
+  // tables can hold is read within the time that laying out, a second kernel and joining take
+  // (4 sequences of 777 to 877 tokens, 8 heads of 128, tables of 7 MB: 12 us, 18 divided; 40 of up
+  // to 5,004, 4 heads of 64, 104 MB: 49 us, 41 divided).
+  const int64_t held = (int64_t)c.batch * c.table_cols * c.page_tokens * c.n_heads * 2 * c.head_dim;
+  d.alone = each > 64 || n_groups == 0 || held <= ALONE_BYTES;
   d.many = all > 32;
   d.split = all <= prefill_shape(true).rows;
   d.mb = rows_of(d.many ? each : all);

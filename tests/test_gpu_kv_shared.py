@@ -15,9 +15,10 @@ from test_gpu_kv import check_attention, run_attention, status_word
 pytestmark = pytest.mark.gpu
 
 
-def shared_cache(rng, groups, heads, page, dim, code, spare=2):
+def shared_cache(rng, groups, heads, page, dim, code, spare=2, wide=True):
     """groups: [(prefix, [own tokens of each sequence])]; the plain cache and the same as pools in
-    which a group's whole prefix pages are there once (what would be the others' is NaN scales)."""
+    which a group's whole prefix pages are there once (what would be the others' is NaN scales).
+    wide: tables of so many columns (most of them unused) that the call is divided."""
     lens = [p + t for p, own in groups for t in own]
     want = ref.Cache(len(lens), heads, page, dim, code)
     b = 0
@@ -29,7 +30,8 @@ def shared_cache(rng, groups, heads, page, dim, code, spare=2):
             if t:
                 want.append(b, as_float32(random_rows(rng, t, heads, dim)))
             b += 1
-    cache = pools(want, rng, spare=spare)
+    cols = (64 << 20) // (len(lens) * page * heads * 2 * dim) + 1 if wide else None
+    cache = pools(want, rng, spare=spare, cols=cols)
     b = 0
     for p, own in groups:
         for i in range(1, len(own)):
@@ -85,10 +87,11 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("groups,counts,q_heads,heads,dim,page,code,dtype", CASES)
-def test_shared_beginnings(groups, counts, q_heads, heads, dim, page, code, dtype):
+def test_shared_beginnings(groups, counts, q_heads, heads, dim, page, code, dtype, wide):
     rng = np.random.default_rng(sum(counts) + dim + page + q_heads)
-    want, cache = shared_cache(rng, groups, heads, page, dim, code)
+    want, cache = shared_cache(rng, groups, heads, page, dim, code, wide=wide)
     q = rounded(1.5 * rng.standard_normal((sum(counts), q_heads, dim)), dtype).cuda()
     out, lse = run_shared(cache, groups, q, counts, dim ** -0.5)
     check_attention(want, q, counts, dim ** -0.5, out, lse, None, None)

@@ -50,7 +50,7 @@ def test_several_answers_to_one_prompt(code, page, dim):
     rng = np.random.default_rng(11)
     turns = turn.table(400, dim)
     rotation = ibp.KVRotation(torch.from_numpy(turns).cuda())
-    cache = DecodeCache(n_pages=120, batch=batch, n_heads=heads, head_dim=dim, max_tokens=400, page_tokens=page,
+    cache = DecodeCache(n_pages=120, batch=batch, n_heads=heads, head_dim=dim, max_tokens=65_536, page_tokens=page,
                         code=code, track_weights=False)
     want = ref.Cache(batch, heads, page, dim, code)
     append(cache, want, rng, [150, 0, 0, 0, 0, 33], turns, rotation, heads, q_heads, dim)
