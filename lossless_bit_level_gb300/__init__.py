@@ -22,7 +22,9 @@ packed store (pack_offsets, pack, decompress_gather_packed) and per-position or
 block-position metadata (build_meta_positions, build_meta_block_positions,
 compress_positions, decompress_gather_positions). Beside the codec, an 8-bit paged
 key/value cache for the K/V rows it stores: KVCache, kv_append, kv_read, kv_attention,
-kv_evict (``kvcache.py`` manages one). ``offload.py`` streams compressed
+kv_evict; kv_append_rotated (positions rotated on the way in), kv_attention_shared (beginnings
+that sequences share), kv_bounds, kv_select and kv_attention_selected (a few pages of many)
+(``kvcache.py`` manages one). ``offload.py`` streams compressed
 tensors through device buffers; ``sharded.py`` builds the metadata of a table spread
 over several processes.
 """

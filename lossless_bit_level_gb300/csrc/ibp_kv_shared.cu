@@ -6,6 +6,17 @@
 //   z = log2(2^z_0 + 2^z_1),  out = o_0 2^(z_0 - z) + o_1 2^(z_1 - z).
 // So a beginning is gone over once for the rows of all its sequences together, which fill the
 // matrix unit, where each sequence by itself would read and convert it again.
+//
+// A small kernel lays out the spans; beginnings with more than 32 rows a K/V head go to the kernel
+// for many rows, the rest of each sequence to the one for few, side by side on SMs that the
+// layout shares out; a last kernel joins. (With fewer rows both go through the one for few
+// together: two documents with 64 rows a head each take 92 us with the first way, 104 with the
+// second.) 32 conversations behind 8,192 tokens, 32 query heads on 8 of 128: 48 us (undivided 89;
+// floor 7); 16 answers to documents of 60,001 and 33,333, 32 on 4, e4m3: 76 us (undivided 107;
+// floor 15). What bounds it: a tile takes the kernel for many rows 1.6 us for two halves whatever
+// rows there are (fp16 of its codes made by four warps, shared memory that holds Q and both fp16
+// tiles), 14 us go by before its first scores (layout 3.5, where its stretch begins 3, queries,
+// pages, scales and codes one after another), and joining takes 4 us.
 #include "ibp_kv_attend.cuh"
 
 namespace ibp {
@@ -64,7 +75,8 @@ __device__ __forceinline__ int64_t sum_before(int64_t x, int64_t *warp_sum, int6
   return before + run - x;
 }
 
-// One CTA lays out the spans of up to SHARE_SLAB sequences. A run of sequences of one group
+// One CTA lays out the spans of up to SHARE_SLAB sequences (3.4 us: what it loads depends on one
+// another, and it waits for its sums). A run of sequences of one group
 // shares the whole pages of its prefix that none of its rows may not see; a run of one
 // sequence shares nothing.
 __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __grid_constant__ ShareArgs a) {
