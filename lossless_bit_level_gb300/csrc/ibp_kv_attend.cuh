@@ -130,6 +130,9 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ibp_kv_cache &c = a.c;
   const int group = a.q.q_heads / c.n_heads, cta = blockIdx.x;
+  // SELECTED: launched while the kernel before it ends, most often the one that wrote the lists;
+  // every block waits for that one here, before anything is read or written
+  if constexpr (OVER == Over::SELECTED) grid_dependency_wait();
   if constexpr (OVER != Over::SHARED) grid_launch_dependents();
   // SHARED beside the kernel for many rows, which this one need not wait for before its end: that
   // one let it start once the spans were there
@@ -629,8 +632,13 @@ int launch_shape(AttentionArgs a, const DeviceInfo &dev, cudaStream_t s) {
                ? IBP_OK
                : IBP_ERR_CUDA;
   } else {
-    kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    if constexpr (OVER == Over::SELECTED) {
+      if (launch_dependent(kernel, dim3((unsigned)a.ctas), dim3(THREADS), S::smem, s, a) != cudaSuccess)
+        return IBP_ERR_CUDA;
+    } else {
+      kernel<<<a.ctas, THREADS, S::smem, s>>>(a);
+      if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    }
     const int64_t chunks = SCORES ? (a.score_cols + WEIGHT_TOKENS - 1) / WEIGHT_TOKENS : 0;
     if (launch_dependent(kv_finish_kernel<D, DT, typename S::Plan, SCORES, OVER>,
                          dim3((unsigned)(blocks + chunks), (unsigned)a.c.n_heads, (unsigned)a.batch),

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(BOUNDS_THREADS, 3) kv_bounds_kernel(const __gr
   __shared__ int64_t prefix[SLAB_BATCH + 1];
   const ibp_kv_cache &c = a.c;
   const int P = c.page_tokens, lane = threadIdx.x & 31, piece = lane % PIECES;
+  grid_launch_dependents();
   auto first_page = [&](int b) { return a.begin ? max(__ldg(a.begin + a.b0 + b), 0) / P : 0; };
   if (threadIdx.x < 32)
     count_items(prefix, a.batch, [&](int b) {
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, ONE ? 5 : 4) kv_score_kernel(co
   const ibp_kv_cache &c = a.c;
   const int P = c.page_tokens, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int group = a.q.q_heads / c.n_heads;
+  grid_dependency_wait();  // for the kernel before it, most often that of the bounds
   grid_launch_dependents();
   auto chunks_of = [&](int b, int32_t *status) {
     int64_t row0;
@@ -570,6 +572,7 @@ __global__ void __launch_bounds__(PICK_THREADS) kv_pick_kernel(const __grid_cons
   const int n = rows_at(a, b, &row0, nullptr), len = n > 0 ? kv_len(c, b, nullptr) : 0;
   const PageList p = page_list(c, len, n, a.pages);
   grid_dependency_wait();
+  grid_launch_dependents();
   if (!sure_columns(out, p, a.pages)) return;
   const int room = a.pages - (p.all - p.first_own) - 1, open = p.first_own - 1;
   const float *scores = a.scores + list * c.table_cols + 1;
@@ -594,6 +597,8 @@ __global__ void __launch_bounds__(PICK_THREADS, 2) kv_select_short_kernel(const 
   const int b = a.b0 + blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   int32_t *status = head == 0 && threadIdx.x == 0 ? a.status : nullptr;
+  grid_dependency_wait();  // for the kernel before it, most often that of the bounds
+  grid_launch_dependents();
   int32_t *out = a.columns + ((int64_t)b * c.n_heads + head) * a.pages;
   int64_t row0;
   const int n = rows_at(a, b, &row0, status), held = kv_len(c, b, status), all = n * (a.q.q_heads / c.n_heads);
@@ -703,8 +708,8 @@ int launch_kv_select(const ibp_kv_cache &c, const int8_t *d_bounds, const ibp_kv
                      : (bf16 ? kv_select_short_kernel<64, IBP_BF16, false> : kv_select_short_kernel<64, IBP_FP16, false>))
               : (one ? (bf16 ? kv_select_short_kernel<128, IBP_BF16, true> : kv_select_short_kernel<128, IBP_FP16, true>)
                      : (bf16 ? kv_select_short_kernel<128, IBP_BF16, false> : kv_select_short_kernel<128, IBP_FP16, false>));
-      kernel<<<(unsigned)(a.batch * c.n_heads), PICK_THREADS, 0, s>>>(a);
-      if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+      if (launch_dependent(kernel, dim3((unsigned)(a.batch * c.n_heads)), dim3(PICK_THREADS), 0, s, a) != cudaSuccess)
+        return IBP_ERR_CUDA;
       continue;
     }
     const int64_t most = (int64_t)a.batch * c.n_heads * ((c.table_cols + CHUNK - 1) / CHUNK);
@@ -715,8 +720,7 @@ int launch_kv_select(const ibp_kv_cache &c, const int8_t *d_bounds, const ibp_kv
             : (one ? (bf16 ? kv_score_kernel<128, IBP_BF16, true> : kv_score_kernel<128, IBP_FP16, true>)
                    : (bf16 ? kv_score_kernel<128, IBP_BF16, false> : kv_score_kernel<128, IBP_FP16, false>));
     const int64_t ctas = std::max<int64_t>(std::min<int64_t>(most, dev.sm_count * (one ? 5 : 4)), 1);
-    kernel<<<(unsigned)ctas, SCORE_THREADS, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    if (launch_dependent(kernel, dim3((unsigned)ctas), dim3(SCORE_THREADS), 0, s, a) != cudaSuccess) return IBP_ERR_CUDA;
     if (launch_dependent(kv_pick_kernel, dim3((unsigned)(a.batch * c.n_heads)), dim3(PICK_THREADS), 0, s, a) !=
         cudaSuccess)
       return IBP_ERR_CUDA;
