@@ -362,6 +362,7 @@ template <int D, int DT, typename Plan, bool SCORES, Over OVER = Over::ALL>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
+  if constexpr (OVER == Over::SELECTED) grid_launch_dependents();
   __shared__ float lse2[MB];
   __shared__ Parts where;
   __shared__ int64_t prefix[2];  // tiles before sequence b and in all

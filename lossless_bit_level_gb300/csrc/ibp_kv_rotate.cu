@@ -391,6 +391,7 @@ __device__ __forceinline__ void append_heads(const RotateArgs &a, const AppendPl
 // Rows that queries are rotated in, after (and along with the end of) the kernel that appends.
 template <int D, int DT>
 __global__ void __launch_bounds__(TURN_THREADS, 4) kv_turn_kernel(const __grid_constant__ RotateArgs a) {
+  grid_launch_dependents();
   turn_queries<D, DT>(a, blockIdx.x);
   grid_dependency_wait();  // what comes next in the stream may be ordered behind this grid alone
 }
@@ -505,6 +506,7 @@ __device__ __forceinline__ void append_few(const RotateArgs &a, const AppendPlac
 
 template <int D, int DT, int CODE>
 __global__ void __launch_bounds__(32 * FEW_WARPS) kv_rotate_few_kernel(const __grid_constant__ RotateArgs a) {
+  grid_launch_dependents();
   if ((int64_t)blockIdx.x >= a.kv_blocks) {
     turn_queries<D, DT>(a, (int64_t)blockIdx.x - a.kv_blocks);
     return;

@@ -660,7 +660,8 @@ int launch_bounds_of(BoundsArgs a, const DeviceInfo &dev, cudaStream_t s) {
   for (a.b0 = 0; a.b0 < a.c.batch; a.b0 += SLAB_BATCH) {
     a.batch = std::min(a.c.batch - a.b0, SLAB_BATCH);
     const int64_t most = ((int64_t)a.batch * a.c.n_heads * a.c.table_cols + BOUNDS_THREADS / 32 - 1) / (BOUNDS_THREADS / 32);
-    kernel<<<(unsigned)std::min<int64_t>(most, dev.sm_count * 3), BOUNDS_THREADS, 0, s>>>(a);
+    const int64_t ctas = std::min<int64_t>(most, dev.sm_count * 3);
+    kernel<<<(unsigned)ctas, BOUNDS_THREADS, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
   }
   return IBP_OK;

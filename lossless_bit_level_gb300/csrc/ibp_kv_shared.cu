@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
   const int t = threadIdx.x, b = a.b0 + t, heads = a.c.n_heads, group = a.q.q_heads / heads;
   const int P = a.c.page_tokens;
   const bool live = t < a.batch;
+  grid_dependency_wait();  // for the kernel before it in the stream, which may have let it start
   grid_launch_dependents();
   // the last group that does not begin after the sequence, if it has it
   int mine = -1;
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t x = SHARE ? blockIdx.x : (int64_t)blockIdx.x * JOIN_WARPS + warp, each = a.q.max_q * a.q.q_heads;
   const int i = (int)quotient(x, each), in = (int)(x - i * each), j = in / a.q.q_heads, qh = in % a.q.q_heads;
+  grid_launch_dependents();
   // The spans are there before the kernels that go over them let this one start (loads pass the
   // first-level cache), so that only their results are waited for.
   Span s = {}, from = {};
@@ -506,8 +508,7 @@ int launch_kv_attention_shared(const ibp_kv_cache &c, const ibp_kv_query &query,
     a.batch = std::min(c.batch - a.b0, SHARE_SLAB);
     // of a slab's sequences, two at least have each shared beginning
     a.beginnings = t.beginnings = (int)std::min<int64_t>(n_groups, (a.batch + 1) / 2);
-    kv_share_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return IBP_ERR_CUDA;
+    if (launch_dependent(kv_share_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, a) != cudaSuccess) return IBP_ERR_CUDA;
     if (d.many) {
       t.b0 = 0;
       t.batch = a.beginnings;
