@@ -579,7 +579,8 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
  * IBP_KV_E4M3 code * 127 / 448 rounded down (least) and up (largest); whole numbers in
  * [-127, 127]. Written for the pages of the tokens from d_begin[b] (null or negative: 0) to
  * the length of each sequence, after an append the pages that it touched when d_begin holds
- * the lengths before it; other pages' bounds are left alone. Asynchronous on s, capturable. */
+ * the lengths before it; other pages' bounds are left alone. A page that several sequences name
+ * must hold equally many tokens in each. Asynchronous on s, capturable. */
 int ibp_kv_bounds(const ibp_kv_cache *cache, int8_t *d_bounds, const int32_t *d_begin,
                   int32_t *d_status, ibp_stream_t s);
 
@@ -607,8 +608,8 @@ int ibp_kv_select(const ibp_kv_cache *cache, const int8_t *d_bounds, const ibp_k
 /* Attention over the pages that d_columns ([batch][n_heads][pages], as ibp_kv_select writes it)
  * names, as ibp_kv_attention over the whole cache (without weights: IBP_ERR_ARG). A sequence
  * has the smaller of `pages` and its number of pages as entries; the last of them must be the
- * columns where its rows stand, in order, the others distinct columns before those in any
- * order. A different entry is an IBP_ERR_INDEX and its page is left out. d_scratch: the size
+ * columns where its rows stand, in order, the others columns before those in any order (one that
+ * is named twice counts twice). A different entry is an IBP_ERR_INDEX and its page is left out. d_scratch: the size
  * ibp_kv_attention_selected_scratch_bytes gives. Asynchronous on s, capturable. */
 int ibp_kv_attention_selected_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,
                                             int32_t q_heads, int64_t pages, size_t *bytes);

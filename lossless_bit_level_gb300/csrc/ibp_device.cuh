@@ -183,7 +183,10 @@ __device__ __forceinline__ uint64_t global_ns() {
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation waits here until the kernel before it on the stream has completed
 // and its memory is visible (a no-op for a kernel launched the ordinary way); a
-// kernel lets the next one start launching early with launch_dependents.
+// kernel lets the next one start launching early with launch_dependents. A kernel
+// that another call's may follow does so behind its own wait, so that no grid starts before the
+// one two before it has ended, and only if none of its blocks reads a line that another writes:
+// the next grid's loads might find the old one in the first-level cache.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

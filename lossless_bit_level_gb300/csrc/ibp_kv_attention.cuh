@@ -165,7 +165,7 @@ __device__ __forceinline__ int page_of(const AttentionArgs &a, int b, int head, 
     const int len = kv_len(a.c, a.b0 + b, nullptr), n = sequence_of(a, b, nullptr).n;
     const PageList p = page_list(a.c, len, n, a.pages);
     const int listed =
-        __ldg(a.columns + ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.pages + col);
+        __ldcg(a.columns + ((int64_t)(a.b0 + b) * a.c.n_heads + head) * a.pages + col);
     // the rows' own pages are the list's last, in order; no other entry is one of them, so that
     // no token past the length counts and none that a row does not see
     const int own = p.all - p.first_own, left = p.count - col;
@@ -362,7 +362,6 @@ template <int D, int DT, typename Plan, bool SCORES, Over OVER = Over::ALL>
 __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4 ? 2 : 8)
     kv_finish_kernel(const __grid_constant__ AttentionArgs a, int row_blocks) {
   constexpr int MB = Plan::MB;
-  if constexpr (OVER == Over::SELECTED) grid_launch_dependents();
   __shared__ float lse2[MB];
   __shared__ Parts where;
   __shared__ int64_t prefix[2];  // tiles before sequence b and in all
@@ -401,6 +400,7 @@ __global__ void __launch_bounds__(FINISH_THREADS, (JOIN_AHEAD<Plan, SCORES>) > 4
     __syncthreads();
     const Parts p = where;
     grid_dependency_wait();
+    if constexpr (OVER == Over::SELECTED) grid_launch_dependents();
     if (rows <= 0 || (tiles > 0 && p.first == p.last)) return;
     for (int u = threadIdx.x; u < rows * (D / 4); u += FINISH_THREADS) {
       const int r = u / (D / 4), piece = u % (D / 4), rr = r0 + r;

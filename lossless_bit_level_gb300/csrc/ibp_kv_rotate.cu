@@ -33,6 +33,7 @@ struct RotateArgs {
   int64_t kv_blocks;   // blocks that append; those after them rotate queries
   int q_chunks;        // blocks that share the heads of a query row
   int kv_chunks;       // blocks that share the heads of a page, of K or V
+  bool apart;          // queries are rotated in a launch of their own
   int mixed;           // a unit's pairs are not all on one axis
   int shift;           // log2 of the page size
   int32_t *new_lens, *status;
@@ -391,7 +392,6 @@ __device__ __forceinline__ void append_heads(const RotateArgs &a, const AppendPl
 // Rows that queries are rotated in, after (and along with the end of) the kernel that appends.
 template <int D, int DT>
 __global__ void __launch_bounds__(TURN_THREADS, 4) kv_turn_kernel(const __grid_constant__ RotateArgs a) {
-  grid_launch_dependents();
   turn_queries<D, DT>(a, blockIdx.x);
   grid_dependency_wait();  // what comes next in the stream may be ordered behind this grid alone
 }
@@ -400,7 +400,10 @@ template <int D, int DT, int CODE>
 __global__ void __launch_bounds__(MAX_THREADS)
     kv_rotate_kernel(const __grid_constant__ RotateArgs a) {
   __shared__ uint32_t sm[2][32];
-  grid_launch_dependents();
+  // For the queries' kernel, which reads nothing that this one writes. No other starts before this
+  // one ends: it could hold an old line of scales in its first-level cache, which a block of this
+  // one read for its own head while another's was still to be written.
+  if (a.apart) grid_launch_dependents();
   if ((int64_t)blockIdx.x >= a.kv_blocks) {
     turn_queries<D, DT>(a, (int64_t)blockIdx.x - a.kv_blocks);
     return;
@@ -506,7 +509,6 @@ __device__ __forceinline__ void append_few(const RotateArgs &a, const AppendPlac
 
 template <int D, int DT, int CODE>
 __global__ void __launch_bounds__(32 * FEW_WARPS) kv_rotate_few_kernel(const __grid_constant__ RotateArgs a) {
-  grid_launch_dependents();
   if ((int64_t)blockIdx.x >= a.kv_blocks) {
     turn_queries<D, DT>(a, (int64_t)blockIdx.x - a.kv_blocks);
     return;
@@ -576,7 +578,7 @@ int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   // Few queries along in the same launch; many in one of their own, which has half the registers
   // (whole calls with the read back: 3,500 rows of 8 heads of 64, 7 MB, 24.6 us | 26.7 in a launch of
   // their own; 5,556 rows of 28 heads of 128, 40 MB, 48 | 39).
-  const bool apart = a.q.q && a.r.n_rows * a.q.q_heads * D * (DT == IBP_FP32 ? 4 : 2) > (int64_t)(16 << 20);
+  const bool apart = a.apart = a.q.q && a.r.n_rows * a.q.q_heads * D * (DT == IBP_FP32 ? 4 : 2) > (int64_t)(16 << 20);
   const int64_t turns = query_blocks(a, apart ? TURN_THREADS : threads, (apart ? 4 : 16) * (int64_t)dev.sm_count);
   const int64_t blocks = a.kv_blocks + (apart ? 0 : turns);
   if (blocks > 0x7FFFFFFF || turns > 0x7FFFFFFF) return IBP_ERR_UNSUPPORTED;

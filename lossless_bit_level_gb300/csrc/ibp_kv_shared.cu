@@ -340,7 +340,6 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t x = SHARE ? blockIdx.x : (int64_t)blockIdx.x * JOIN_WARPS + warp, each = a.q.max_q * a.q.q_heads;
   const int i = (int)quotient(x, each), in = (int)(x - i * each), j = in / a.q.q_heads, qh = in % a.q.q_heads;
-  grid_launch_dependents();
   // The spans are there before the kernels that go over them let this one start (loads pass the
   // first-level cache), so that only their results are waited for.
   Span s = {}, from = {};
@@ -354,6 +353,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_share_join_kernel(const __
     rest = where_of(a, 1, s, row, qh);
   }
   grid_dependency_wait();
+  grid_launch_dependents();
   if (!live) return;
   Half<D> h;
   if constexpr (SHARE) {

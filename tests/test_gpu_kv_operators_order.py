@@ -71,3 +71,50 @@ def test_right_behind_a_kernel_that_writes_their_inputs(answers, graph):
         got = [t.clone() for t in outs[4:]]
         for a, b in zip(got, expected[i % 2]):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("q_rows", [False, True])  # queries in a launch of their own behind the keys
+def test_selection_right_behind_an_append_that_raises_scales(q_rows):
+    batch, heads, d, page, old, new = 24, 32, 128, 32, 20, 40
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rows(n, times):
+        return (times * torch.randn((n, heads, d), generator=gen, device="cuda")).to(torch.bfloat16)
+
+    n_pages = 2 * batch
+    codes = [torch.zeros((n_pages, heads, page, d), dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((n_pages, heads), device="cuda") for _ in range(2)]
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").view(batch, 2)
+    lens = [torch.full((batch,), n, dtype=torch.int32, device="cuda") for n in (0, old, old + new)]
+    caches = [ibp.KVCache(*codes, *scales, table, x) for x in lens]
+    turn = ibp.KVRotation(ibp.rotation_table(old + new, d))
+    ibp.kv_append(caches[0], rows(batch * old, 1.0), rows(batch * old, 1.0))
+    start = [t.clone() for t in (*codes, *scales)]
+    k, v, wide = rows(batch * new, 30.0), rows(batch * new, 30.0), rows(batch * new, 1.0)
+    turned = torch.empty_like(wide) if q_rows else None  # (its launch comes between)
+    q, out = rows(batch, 1.0), torch.empty((batch, heads, d), dtype=torch.bfloat16, device="cuda")
+    bounds = torch.zeros(caches[0].bounds_shape, dtype=torch.int8, device="cuda")
+    columns = torch.empty((batch, heads, 2), dtype=torch.int32, device="cuda")
+    one = torch.zeros((batch, heads, 2), dtype=torch.int32, device="cuda") + torch.arange(2, device="cuda").int()
+    scratch = torch.empty(1 << 27, dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        for t, x in zip((*codes, *scales), start):
+            t.copy_(x)
+        ibp.kv_append_rotated(caches[1], k, v, turn, q=wide if q_rows else None, q_out=turned)
+        if wait:
+            torch.cuda.synchronize()
+        ibp.kv_attention_selected(caches[2], one, q, out, 0.1, scratch)
+        if wait:
+            torch.cuda.synchronize()
+        ibp.kv_bounds(caches[2], bounds)
+        ibp.kv_select(caches[2], bounds, q, columns, scratch)
+        return [t.clone() for t in (out, columns, bounds, *scales)]
+
+    expected = run(True)
+    assert (scales[0] > start[2]).any()
+    heavy = torch.randn((4096, 4096), device="cuda")
+    for i in range(20):
+        torch.mm(heavy, heavy, out=heavy.new_empty(heavy.shape))
+        for a, b in zip(run(False), expected):
+            assert torch.equal(a, b), i
