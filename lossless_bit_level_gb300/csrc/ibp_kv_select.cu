@@ -700,7 +700,7 @@ int launch_kv_select(const ibp_kv_cache &c, const int8_t *d_bounds, const ibp_kv
     const bool one = a.q.max_q * (query.q_heads / c.n_heads) <= 8, bf16 = query.dtype == IBP_BF16;
     // One kernel where a block is done with its list in two passes of 128 pages, or where there are
     // lists for all SMs (whole steps in one | two kernels: 256 lists of 64 pages 57 | 62 us, 192 of up
-    // to 219 42 | 48, 8 of 487 24.6 | 22.6).
+    // to 219 42 | 48, 8 of 487 26.6 | 24.6).
     const bool lists = (int64_t)a.batch * c.n_heads >= dev.sm_count;
     if (c.table_cols <= 2 * 16 * PICK_WARPS || (lists && c.table_cols <= SHORT_LIST)) {
       const auto kernel =

@@ -12,7 +12,7 @@
 // layout shares out; a last kernel joins. (With fewer rows both go through the one for few
 // together: two documents with 64 rows a head each take 92 us with the first way, 104 with the
 // second.) 32 conversations behind 8,192 tokens, 32 query heads on 8 of 128: 48 us (undivided 89;
-// floor 7); 16 answers to documents of 60,001 and 33,333, 32 on 4, e4m3: 76 us (undivided 107;
+// floor 7); 16 answers to documents of 60,001 and 33,333, 32 on 4, e4m3: 75 us (undivided 107;
 // floor 15). What bounds it: a tile takes the kernel for many rows 1.6 us for two halves whatever
 // rows there are (fp16 of its codes made by four warps, shared memory that holds Q and both fp16
 // tiles), 14 us go by before its first scores (layout 3.5, where its stretch begins 3, queries,
