@@ -621,13 +621,14 @@ int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *que
  * weights: IBP_ERR_ARG). Group g is the sequences d_groups[g] .. d_groups[g+1] - 1 (d_groups
  * [n_groups + 1] rising within [0, batch], else IBP_ERR_INDEX; sequences of no group share
  * nothing); their first d_prefix[g] tokens are the same, and for the whole pages of these
- * their tables name the same pages (those of the group's first sequence are read; pages in
+ * their tables name the same pages (those of its first sequence with rows are read; pages in
  * use may be named more than once in calls that only read). A prefix longer than a
  * sequence, or than what the first of its rows sees, counts as far as all rows of the group
  * see it. Each beginning is gone over once for all rows of its group, in slabs of 128
  * sequences (unless the tables can hold no more than 64 MB of codes, or a sequence has more
- * than 64 rows a K/V head: then the call is that of ibp_kv_attention). group_rows: the most query rows that the sequences of one group have together;
- * it chooses the kernel, no result depends on its being right. d_scratch: the size
+ * than 64 rows a K/V head: then the call is that of ibp_kv_attention). group_rows: the most
+ * query rows that the sequences of one group have together; it chooses the kernel, no result
+ * depends on its being right. d_scratch: the size
  * ibp_kv_attention_shared_scratch_bytes gives for the same cache, query shapes and groups.
  * Asynchronous on s, capturable. */
 int ibp_kv_attention_shared_scratch_bytes(const ibp_kv_cache *cache, int64_t n_rows, int64_t max_q,

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
     }
   group_of[t] = mine;
   seen[t] = 0x7FFFFFFF;
-  members[t] = first[t] = last[t] = 0;
+  members[t] = last[t] = 0;
+  first[t] = SHARE_SLAB - 1;
   __syncthreads();
   const bool starts = live && (t == 0 || mine < 0 || group_of[t - 1] != mine);
   int64_t runs;
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_share_plan_kernel(const __gri
     if (hi - lo > a.q.max_q) report(a.status, IBP_ERR_INDEX);
     n = (int)min(hi - lo, a.q.max_q);
     len = kv_len(a.c, b, a.status);
-    if (starts) first[run] = t;
-    if (t + 1 == a.batch || mine < 0 || group_of[t + 1] != mine) last[run] = t;
-    if (n > 0) {
+    if (n > 0) {  // (one without rows may hold less than the others share)
+      atomicMin(&first[run], t);
+      atomicMax(&last[run], t);
       const int whole = mine >= 0 ? __ldg(a.prefix + mine) : 0;
       atomicMin(&seen[run], max(min(whole, len - n + 1), 0) / P * P);
       atomicAdd(&members[run], 1);

@@ -252,3 +252,19 @@ def test_the_same_as_undivided():
     plain, plain_lse, _, _ = run_attention(cache, q, [1] * 4, 0.125, weights=False)
     half = 2.0 ** -8  # two roundings to bf16 of values 2^-20 apart
     assert bool(((out.float() - plain.float()).abs() <= 2.1 * half * plain.float().abs() + 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("fill", [-1, 0])
+@pytest.mark.parametrize("times", [1, 5])  # 10 and 50 rows a head
+def test_a_group_whose_first_sequence_is_empty(times, fill):
+    """A slot without rows or tokens at the head of a group: what its table holds is never read."""
+    rng = np.random.default_rng(times)
+    groups = [(320, [0] + [11, 40, 3, 70, 0] * times), (0, [5]), (200, [0, 9, 30])]
+    counts = [0] + [1] * (5 * times) + [2] + [0, 1, 3]
+    want, cache = shared_cache(rng, groups, 2, 32, 128, "int8")
+    for b in (0, 5 * times + 2):
+        cache.table[b] = fill
+        cache.lens[b] = 0
+    q = rounded(rng.standard_normal((sum(counts), 4, 128)), "bf16").cuda()
+    out, lse = run_shared(cache, groups, q, counts, 0.1)
+    check_attention(want, q, counts, 0.1, out, lse, None, None)
