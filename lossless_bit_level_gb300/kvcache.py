@@ -64,6 +64,7 @@ class DecodeCache:
             tuple(zeros(n_pages, n_heads, dtype=torch.float32) for _ in range(2))
         self.max_tokens = cols * page_tokens
         self.lengths = [0] * batch             # as the host knows them
+        self._seen = [0] * batch               # tokens so far, those that were evicted among them
         self._pages: list[list[int]] = [[] for _ in range(batch)]
         self._free = list(range(n_pages - 1, -1, -1))
         # two tables and lengths: a call reads one and writes the other
@@ -137,13 +138,27 @@ class DecodeCache:
             host = self._pinned([r + [-1] * (cols - len(r)) for r in rows])
             handle.table[:, :cols].copy_(host, non_blocking=True)
 
+    def _numbers(self, counts: list[int], axes: int) -> torch.Tensor | None:
+        """Positions [n, axes] of new rows: each its token's number among all that its sequence
+        was given. None while a token's place in the cache says that; where tokens were evicted
+        their places are taken by later ones, and what is kept stays rotated by its own number."""
+        if self._seen == self.lengths:
+            return None
+        host = torch.empty((sum(counts), axes), dtype=torch.int32, pin_memory=self.device.type == "cuda")
+        at = 0
+        for seen, n in zip(self._seen, counts):
+            host[at:at + n] = torch.arange(seen, seen + n, dtype=torch.int32)[:, None]
+            at += n
+        return host.to(self.device, non_blocking=True)
+
     def append(self, k: torch.Tensor, v: torch.Tensor, counts=None,
                rotation: KVRotation | None = None, positions: torch.Tensor | None = None,
                q: torch.Tensor | None = None) -> torch.Tensor | None:
         """Rows [n, heads, head_dim] behind what the sequences hold: counts[b] of them to
         sequence b, one sequence after another (None: the same number each). With ``rotation``
         keys are rotated on the way, by ``positions`` (int32 [n, axes]; None: the tokens'
-        numbers), and so are the query rows ``q`` of the same tokens, which are returned."""
+        numbers among all that their sequences were given, evicted ones counted), and so are the
+        query rows ``q`` of the same tokens, which are returned."""
         if rotation is None and (q is not None or positions is not None):
             raise ValueError("positions and q go with a rotation")
         each, counts = counts, self._counts(counts, k.shape[0])
@@ -161,12 +176,15 @@ class DecodeCache:
             if rotation is None:
                 kv_append(now, k, v, cu=cu, new_lens=later.lens, status=self.status)
             else:
+                if positions is None:
+                    positions = self._numbers(counts, rotation.axes)
                 if q is not None:
                     turned = torch.empty_like(q, memory_format=torch.contiguous_format)
                 kv_append_rotated(now, k, v, rotation, positions=positions, q=q, q_out=turned, cu=cu,
                                   new_lens=later.lens, status=self.status)
             before = now.lens.clone() if self.bounds is not None else None
             now.lens.copy_(later.lens)
+        self._seen = [n + c for n, c in zip(self._seen, counts)]
         self.lengths, self._pages = after, pages
         if before is not None:
             kv_bounds(now, self.bounds, begin=before, status=self.status)
@@ -196,6 +214,9 @@ class DecodeCache:
         now.lens[wanted[0]:wanted[-1] + 1] = tokens  # (a fill: nothing is sent)
         for b in wanted:
             self.lengths[b] = tokens
+            # the least number past all of the shared tokens: places keep the tokens' order in
+            # every head, and src holds so many behind them
+            self._seen[b] = self._seen[src] - (self.lengths[src] - tokens)
         self._pages = pages
         self._groups = sorted(self._groups + [(src, wanted[-1] + 1, tokens)])
         self._group_tensors = None
