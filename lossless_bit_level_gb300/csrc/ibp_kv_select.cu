@@ -241,7 +241,8 @@ __device__ __forceinline__ void rows_in_whole_numbers(const SelectArgs &a, int64
                   q[2 * i + 1] = f.y;
                 }
               }
-              float most = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
+              // (a NaN is not counted; where all four are, the 0 is what is left)
+              float most = fmaxf(fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3]))), 0.0f);
               most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));
               const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
               const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
