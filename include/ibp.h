@@ -509,7 +509,8 @@ typedef struct {
 
 /* Query rows that are rotated with the new rows: row r belongs to the token that row r of K
  * becomes. Same type as K; strides as in ibp_kv_query; out is q itself (with its strides) or
- * memory apart from it and from K and V. */
+ * shares no element with it, and in both cases none with K and V (else IBP_ERR_ARG, also where
+ * rows of another stride than theirs lie in the same stretch of memory). */
 typedef struct {
   const void *q;             /* device, 16-byte aligned */
   void *out;                 /* device, 16-byte aligned */

@@ -94,10 +94,53 @@ int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d
   return launch_kv_append(*cache, *rows, d_new_lens, d_status, reinterpret_cast<cudaStream_t>(s));
 }
 
-// Bytes from the first element of n rows of heads to past the last one.
-static size_t rows_span(int64_t n, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim,
-                        int elem_bytes) {
-  return n > 0 ? (size_t)((n - 1) * row_stride + (heads - 1) * head_stride + dim) * elem_bytes : 0;
+// Elements from the first of n rows of heads to past the last one (what no memory holds is held
+// at 2^60).
+static int64_t rows_span(int64_t n, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim) {
+  const int64_t most = int64_t(1) << 60;
+  if (n <= 0) return 0;
+  if (row_stride > 0 && n - 1 > most / row_stride) return most;
+  return (n - 1) * row_stride + (heads - 1) * head_stride + dim;
+}
+
+// Rows of heads in memory that is read, or written.
+struct HeadRows {
+  const void *at;
+  int64_t row_stride, head_stride, heads;
+};
+
+// Whether n rows of heads of `dim` elements that are written share an element with n rows that are
+// read. Both may lie in one fused tensor, so that the stretches of memory that they span overlap
+// while their elements do not: with one row stride it is the heads' places in a row that count.
+// Rows of different strides in overlapping stretches are taken to share one.
+static bool rows_overlap(const HeadRows &w, const HeadRows &r, int64_t n, int64_t dim, int elem_bytes) {
+  const int64_t n_r = r.row_stride ? n : 1, heads_r = r.head_stride ? r.heads : 1;  // (broadcast: one of them)
+  if (!ranges_overlap(w.at, (size_t)rows_span(n, w.row_stride, w.heads, w.head_stride, dim) * elem_bytes, r.at,
+                      (size_t)rows_span(n_r, r.row_stride, heads_r, r.head_stride, dim) * elem_bytes))
+    return false;
+  if (n > 1 && n_r > 1 && w.row_stride != r.row_stride) return true;
+  const int64_t far = int64_t(1) << 58, row = n > 1 ? w.row_stride : w.heads > 1 ? far - far % w.head_stride : far;
+  const int64_t from = (reinterpret_cast<intptr_t>(r.at) - reinterpret_cast<intptr_t>(w.at)) / elem_bytes;
+  // the common layouts, in a few steps: one's heads behind the other's within a row, or between them
+  const int64_t in_row = from % row + (from % row < 0 ? row : 0);
+  if (in_row >= rows_span(1, 0, w.heads, w.head_stride, dim) &&
+      in_row + rows_span(1, 0, heads_r, r.head_stride, dim) <= row)
+    return false;
+  if (w.heads > 1 && (heads_r == 1 || w.head_stride == r.head_stride) && row % w.head_stride == 0) {
+    const int64_t in_head = in_row % w.head_stride;
+    if (in_head >= dim && in_head + dim <= w.head_stride) return false;
+  }
+  // every head read against every head written, in the rows around it: those k rows on, of which
+  // there are n - 1 forwards and n_r - 1 back
+  for (int64_t i = 0; i < heads_r; ++i)
+    for (int64_t j = 0; j < w.heads; ++j) {
+      const int64_t apart = from + i * r.head_stride - j * w.head_stride, below = apart / row - (apart % row < 0);
+      for (int64_t k = below; k <= below + 1; ++k) {
+        const int64_t held = k < 1 - n_r ? 1 - n_r : k > n - 1 ? n - 1 : k, past = apart - held * row;
+        if (past < dim && -past < dim) return true;
+      }
+    }
+  return false;
 }
 
 int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_rows *rows,
@@ -128,10 +171,14 @@ int ibp_kv_append_rotated(const ibp_kv_cache *cache, const ibp_kv_rows *rows,
     const ibp_kv_turned &q = *queries;
     if (!device_ptr(q.q, 16) || !device_ptr(q.out, 16)) return IBP_ERR_ARG;
     const bool same = q.q == q.out && q.q_row_stride == q.out_row_stride && q.q_head_stride == q.out_head_stride;
-    if (!same && ranges_overlap(q.q, rows_span(rows->n_rows, q.q_row_stride, q.q_heads, q.q_head_stride,
-                                               cache->head_dim, es),
-                                q.out, rows_span(rows->n_rows, q.out_row_stride, q.q_heads, q.out_head_stride,
-                                                 cache->head_dim, es)))
+    const HeadRows out = {q.out, q.out_row_stride, q.out_head_stride, q.q_heads};
+    // queries are written while rows are still read
+    const HeadRows from = {q.q, q.q_row_stride, q.q_head_stride, q.q_heads};
+    const HeadRows k = {rows->k, rows->k_row_stride, rows->k_head_stride, cache->n_heads};
+    const HeadRows v = {rows->v, rows->v_row_stride, rows->v_head_stride, cache->n_heads};
+    if ((!same && rows_overlap(out, from, rows->n_rows, cache->head_dim, es)) ||
+        rows_overlap(out, k, rows->n_rows, cache->head_dim, es) ||
+        rows_overlap(out, v, rows->n_rows, cache->head_dim, es))
       return IBP_ERR_ARG;
   }
   return launch_kv_append_rotated(*cache, *rows, t, queries, d_new_lens, d_status,
