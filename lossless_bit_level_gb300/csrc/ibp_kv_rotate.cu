@@ -429,15 +429,14 @@ __global__ void __launch_bounds__(MAX_THREADS)
   const int per = (a.c.n_heads + a.kv_chunks - 1) / a.kv_chunks, h0 = chunk * per,
             h1 = min(h0 + per, a.c.n_heads);
   if (h0 >= h1) return;
-  const bool covers = T * GROUPS * 16 == D << a.shift;  // (a page of 16 tokens of 64 elements is less than a warp's)
   const bool full = p.t0 >= p.len && p.end - p.t0 >= 1 << a.shift;
   if (which & 1) {
-    if (full && covers)
+    if (full)
       append_heads<D, DT, CODE, false, true>(a, p, h0, h1, sm);
     else
       append_heads<D, DT, CODE, false, false>(a, p, h0, h1, sm);
   } else {
-    if (full && a.t.dim == D && !a.t.interleaved && covers)
+    if (full && a.t.dim == D && !a.t.interleaved)
       append_heads<D, DT, CODE, true, true>(a, p, h0, h1, sm);
     else
       append_heads<D, DT, CODE, true, false>(a, p, h0, h1, sm);
@@ -567,7 +566,7 @@ int launch_code(RotateArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     kernel<<<(unsigned)blocks, threads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? IBP_OK : IBP_ERR_CUDA;
   }
-  const int threads = std::max(P * D / 16 / GROUPS, 32);
+  const int threads = P * D / 16 / GROUPS;  // that hold a page: 32 (16 tokens of 64 elements) to 512
   // Up to 16 heads to a block (8 x 4,096 tokens, 32 heads of 128: 215 us with 8, 207 with 16,
   // 211 with 32). What a block looks up before its first row arrives takes as long as several
   // heads, so no more blocks than run at once where there are few pages.
