@@ -585,7 +585,17 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
 int ibp_kv_bounds(const ibp_kv_cache *cache, int8_t *d_bounds, const int32_t *d_begin,
                   int32_t *d_status, ibp_stream_t s);
 
-/* Selection of pages: for every sequence b and K/V head h, d_columns[b][h][0 .. pages - 1]
+/* Early starts: the first kernel of ibp_kv_select, ibp_kv_attention_selected and
+ * ibp_kv_attention_shared is launched with programmatic stream serialization. Where the kernel
+ * before it on s is one that lets its dependents launch early (griddepcontrol.launch_dependents,
+ * cudaTriggerProgrammaticLaunchCompletion), it starts while that one runs and waits for its end
+ * before it reads or writes anything. What the three calls read they read through the first-level
+ * cache. So a kernel of the caller's that lets them start early must not write, in any block, a
+ * 128-byte line of their inputs that another of its blocks reads, and must itself have waited for
+ * the kernel before it. Kernels that do not ask for this, and all calls of this interface, may
+ * stand before them as they are.
+ *
+ * Selection of pages: for every sequence b and K/V head h, d_columns[b][h][0 .. pages - 1]
  * receives columns of the page table in rising order, then -1: all that the sequence has
  * where these are no more than `pages`, otherwise column 0, those where its query rows stand
  * (positions d_lens[b] - n and on) and of the others those of the highest scores, among equal

@@ -186,7 +186,11 @@ __device__ __forceinline__ uint64_t global_ns() {
 // kernel lets the next one start launching early with launch_dependents. A kernel
 // that another call's may follow does so behind its own wait, so that no grid starts before the
 // one two before it has ended, and only if none of its blocks reads a line that another writes:
-// the next grid's loads might find the old one in the first-level cache.
+// the next grid's loads might find the old one in the first-level cache. (One grid does not: in
+// attention behind shared beginnings the kernel for few rows, beside that for many, lets the
+// joining start without a wait. There the joining may run while the grid two before it does, so
+// all that it takes from either passes the first-level cache (ld.cg), and what orders it behind
+// the kernel for many rows is the wait of the first CTA of the one for few, at its end, alone.)
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

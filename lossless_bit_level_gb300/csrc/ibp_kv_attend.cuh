@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NT, WQ>::per_sm))
   if constexpr (OVER == Over::SELECTED) grid_dependency_wait();
   if constexpr (OVER != Over::SHARED) grid_launch_dependents();
   // SHARED beside the kernel for many rows, which this one need not wait for before its end: that
-  // one let it start once the spans were there
+  // one let it start once the spans were there. The joining may then start while both run: it
+  // reads neither's results, nor the spans, through the first-level cache
   if constexpr (OVER == Over::SHARED) {
     if (!a.beside) grid_dependency_wait();
     grid_launch_dependents();  // the spans are there for the joining too
