@@ -577,8 +577,8 @@ int ibp_kv_attention(const ibp_kv_cache *cache, const ibp_kv_query *query, void 
 /* Bounds of pages, for selecting among them: d_bounds [n_pages][n_heads][2][head_dim] (16-byte
  * aligned) receives the least and the largest K code of each element over the tokens that a
  * page holds, in units of scale * qmax / 127: for IBP_KV_INT8 the codes (-127 for -128), for
- * IBP_KV_E4M3 code * 127 / 448 rounded down (least) and up (largest); whole numbers in
- * [-127, 127]. Written for the pages of the tokens from d_begin[b] (null or negative: 0) to
+ * IBP_KV_E4M3 code * 127 / 448 rounded down (least) and up (largest; a NaN counts as 448 of its
+ * sign); whole numbers in [-127, 127]. Written for the pages of the tokens from d_begin[b] (null or negative: 0) to
  * the length of each sequence, after an append the pages that it touched when d_begin holds
  * the lengths before it; other pages' bounds are left alone. A page that several sequences name
  * must hold equally many tokens in each. Asynchronous on s, capturable. */
