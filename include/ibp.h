@@ -494,7 +494,8 @@ int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *rows, int32_t *d
  * i of a head's first dim elements is (i, i + dim/2), or (2i, 2i + 1) when interleaved is not
  * 0; the rest of the head stays as it is. dim is a multiple of 16 from 16 to head_dim. A row
  * has a position on each of `axes` (1 to 4) axes, d_positions [n_rows][axes]; null: its
- * token's number in the sequence on every axis. Pair i goes by the position on axis[i]
+ * token's place in the cache (d_lens[b] and on) on every axis, which is its number in the
+ * sequence until ibp_kv_evict leaves fewer tokens than there were: pass positions from then on. Pair i goes by the position on axis[i]
  * (axis[0 .. dim/2 - 1] < axes), so any layout of time, height and width is a matter of
  * axis[]. A pair (x, y) becomes (x c - y s, y c + x s), every product and sum rounded to
  * single precision. A position outside [0, n_positions) is held within it, with
@@ -637,7 +638,12 @@ int ibp_kv_attention_selected(const ibp_kv_cache *cache, const ibp_kv_query *que
  * sequence, or than what the first of its rows sees, counts as far as all rows of the group
  * see it. Each beginning is gone over once for all rows of its group, in slabs of 128
  * sequences (unless the tables can hold no more than 64 MB of codes, or a sequence has more
- * than 64 rows a K/V head: then the call is that of ibp_kv_attention). group_rows: the most
+ * than 64 rows a K/V head: then the call is that of ibp_kv_attention, and groups and prefixes are
+ * not looked at). Dividing takes 6 to 10 us more before it gains anything: for short sequences
+ * pass tables (table_cols) no wider than they need, or call ibp_kv_attention. Give pieces of
+ * prompts a call of their own: one sequence of many rows leaves all undivided. A member of a group
+ * whose first row sees less than a page of the prefix leaves the group nothing to share: let it
+ * stand outside. group_rows: the most
  * query rows that the sequences of one group have together; it chooses the kernel, no result
  * depends on its being right. d_scratch: the size
  * ibp_kv_attention_shared_scratch_bytes gives for the same cache, query shapes and groups.

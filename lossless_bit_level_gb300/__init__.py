@@ -692,7 +692,8 @@ def kv_append_rotated(cache: KVCache, k: torch.Tensor, v: torch.Tensor, rotation
                       stream=None) -> None:
     """ibp_kv_append_rotated: ``kv_append`` with ``rotation`` applied to ``k`` on the way, and
     to the query rows ``q`` ([n_rows, q_heads, head_dim], k's type), which go to ``q_out``
-    (None: q itself). ``positions``: int32 [n_rows, axes] (None: each row's token number)."""
+    (None: q itself). ``positions``: int32 [n_rows, axes] (None: each row's place in the cache,
+    which after an eviction is not its token's number any more)."""
     kr, kh = _head_rows(k, cache, cache.n_heads, "k")
     vr, vh = _head_rows(v, cache, cache.n_heads, "v")
     n = k.shape[0]

@@ -431,7 +431,11 @@ Division division_of(const ibp_kv_cache &c, int64_t n_rows, int64_t max_q, int q
   // Not divided: many rows of every sequence, which arithmetic bounds; and where all that the
   // tables can hold is read within the time that laying out, a second kernel and joining take
   // (4 sequences of 777 to 877 tokens, 8 heads of 128, tables of 7 MB: 12 us, 18 divided; 40 of up
-  // to 5,004, 4 heads of 64, 104 MB: 49 us, 41 divided).
+  // to 5,004, 4 heads of 64, 104 MB: 49 us, 41 divided). It goes by what the tables can hold, as
+  // the lengths are on the device: through tables that are wide for what is held little is
+  // divided too and takes the longer way (those 4 behind tables for 65,536 tokens 18.6 us, 32
+  // conversations behind 777 tokens 29 where 21 undivided; 8 behind 8,192 36 and 31; behind 60,001
+  // 86 and 145).
   const int64_t held = (int64_t)c.batch * c.table_cols * c.page_tokens * c.n_heads * 2 * c.head_dim;
   d.alone = each > 64 || n_groups == 0 || held <= ALONE_BYTES;
   d.many = all > 32;

@@ -193,7 +193,9 @@ class DecodeCache:
     def share(self, src: int, sequences) -> int:
         """Let ``sequences``, which are empty and follow src one after another, begin with the
         whole pages that sequence src holds; returns how many tokens that is (what src holds
-        behind them they do not get). ``attend`` goes over these pages once for all of them."""
+        behind them they do not get). ``attend`` goes over these pages once for all of them where
+        the cache tracks no weights (``track_weights=False``); with weights, which are each
+        sequence's own and begin at 0, every sequence is gone over by itself."""
         wanted = list(sequences)
         if wanted != list(range(src + 1, src + 1 + len(wanted))) or not wanted or \
                 not 0 <= src < len(self.lengths) or wanted[-1] >= len(self.lengths):
