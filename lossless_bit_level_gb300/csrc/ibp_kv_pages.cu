@@ -29,15 +29,15 @@ __global__ void __launch_bounds__(Tile<P, D>::threads)
     int below = 0;
     for (int k0 = 0; k0 < c.batch; k0 += T) {
       const int k = k0 + (int)threadIdx.x;
-      below += __syncthreads_count(k < c.batch && first_item(r, k, page_shift(P)) <= item);
+      below += __syncthreads_count(k < c.batch && first_item(r, k, FixedPage<P>()) <= item);
     }
     b = max(below - 1, 0);
-    nth = item - first_item(r, b, page_shift(P));
+    nth = item - first_item(r, b, FixedPage<P>());
   } else {
     b = (int)(item / items_each);
     nth = item - items_each * b;
   }
-  const AppendPlace p = place_of(c, r, each, b, nth, page_shift(P), head == 0 && !is_v && threadIdx.x == 0,
+  const AppendPlace p = place_of(c, r, each, b, nth, FixedPage<P>(), head == 0 && !is_v && threadIdx.x == 0,
                                     new_lens, status);
   if (p.page < 0) return;
   const int64_t lo = p.lo, t0 = p.t0, end = p.end;
@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(32 * FEW_WARPS)
   if (r.d_cu) {
     int below = 0;
     for (int k0 = 0; k0 < c.batch; k0 += 32)
-      below += __popc(__ballot_sync(FULL, k0 + lane < c.batch && first_item(r, k0 + lane, page_shift(P)) <= item));
+      below += __popc(__ballot_sync(FULL, k0 + lane < c.batch && first_item(r, k0 + lane, FixedPage<P>()) <= item));
     b = max(below - 1, 0);
-    nth = item - first_item(r, b, page_shift(P));
+    nth = item - first_item(r, b, FixedPage<P>());
   } else {
     b = (int)(item / items_each);
     nth = item - items_each * b;
   }
-  const AppendPlace p = place_of(c, r, each, b, nth, page_shift(P), which == 0 && lane == 0, new_lens, status);
+  const AppendPlace p = place_of(c, r, each, b, nth, FixedPage<P>(), which == 0 && lane == 0, new_lens, status);
   if (p.page < 0) return;
   const char *src = static_cast<const char *>(is_v ? r.v : r.k);
   const int64_t row_stride = is_v ? r.v_row_stride : r.k_row_stride;

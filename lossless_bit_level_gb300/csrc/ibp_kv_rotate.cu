@@ -416,14 +416,14 @@ __global__ void __launch_bounds__(MAX_THREADS)
     int below = 0;  // starts rise with b: the last one that is not past the item
     for (int k0 = 0; k0 < a.c.batch; k0 += T) {
       const int k = k0 + (int)threadIdx.x;
-      below += __syncthreads_count(k < a.c.batch && first_item(a.r, k, a.shift) <= item);
+      below += __syncthreads_count(k < a.c.batch && first_item(a.r, k, ShiftedPage{a.shift}) <= item);
     }
     i.b = max(below - 1, 0);
-    i.nth = item - first_item(a.r, i.b, a.shift);
+    i.nth = item - first_item(a.r, i.b, ShiftedPage{a.shift});
   } else {
     i = even_item(a, item);
   }
-  const AppendPlace p = place_of(a.c, a.r, a.each, i.b, i.nth, a.shift, which == 0 && threadIdx.x == 0,
+  const AppendPlace p = place_of(a.c, a.r, a.each, i.b, i.nth, ShiftedPage{a.shift}, which == 0 && threadIdx.x == 0,
                                  a.new_lens, a.status);
   if (p.page < 0) return;
   const int per = (a.c.n_heads + a.kv_chunks - 1) / a.kv_chunks, h0 = chunk * per,
@@ -521,14 +521,14 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) kv_rotate_few_kernel(const __g
   if (a.r.d_cu) {
     int below = 0;
     for (int k0 = 0; k0 < a.c.batch; k0 += 32)
-      below += __popc(__ballot_sync(FULL, k0 + lane < a.c.batch && first_item(a.r, k0 + lane, a.shift) <= item));
+      below += __popc(__ballot_sync(FULL, k0 + lane < a.c.batch && first_item(a.r, k0 + lane, ShiftedPage{a.shift}) <= item));
     i.b = max(below - 1, 0);
-    i.nth = item - first_item(a.r, i.b, a.shift);
+    i.nth = item - first_item(a.r, i.b, ShiftedPage{a.shift});
   } else {
     i = even_item(a, item);
   }
   const AppendPlace p =
-      place_of(a.c, a.r, a.each, i.b, i.nth, a.shift, which == 0 && lane == 0, a.new_lens, a.status);
+      place_of(a.c, a.r, a.each, i.b, i.nth, ShiftedPage{a.shift}, which == 0 && lane == 0, a.new_lens, a.status);
   if (p.page < 0) return;
   if (which & 1)
     append_few<D, DT, CODE, false>(a, p, head, lane);
